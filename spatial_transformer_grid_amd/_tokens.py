@@ -1,0 +1,323 @@
+"""ctypes binding of libgsample's token operators (include/gsample_tokens.h).
+
+Argument marshalling only, as in _binding: layer normalisation, dropout and
+attention with a relative position bias, forward and backward.  Tensors may be
+strided where the library takes strides; the last axis is made contiguous.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+
+from ._binding import (GS_F32, _check, _device_tensor, _I, _P, _ptr, _stream, _torch,
+                       dtype_code)
+from ._binding import lib as _library
+
+_I64 = ctypes.c_int64
+_F = ctypes.c_float
+_U32 = ctypes.c_uint32
+_U64 = ctypes.c_uint64
+_S3 = ctypes.c_int64 * 3
+_PI64 = ctypes.POINTER(ctypes.c_int64)
+
+
+class AttentionDesc(ctypes.Structure):
+    """gs_attention_desc"""
+
+    _fields_ = ([("dtype", _I), ("table_dtype", _I)]
+                + [(n, _I64) for n in ("batch", "q_heads", "kv_heads", "q_len", "kv_len", "head_dim")]
+                + [(n + "_stride", _S3) for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")]
+                + [("scale", _F), ("causal", _I), ("q_from_end", _I), ("q_position", _I64),
+                   ("num_buckets", _I), ("max_distance", _I), ("bidirectional", _I), ("ratio", _F),
+                   ("call", _U32), ("seed", _U64)])
+
+
+_PDESC = ctypes.POINTER(AttentionDesc)
+
+# C entry points and their argument types (mirrors include/gsample_tokens.h)
+TOKEN_SIGNATURES = {
+    "gs_layer_norm": ([_P, _I, _I64, _I64, _I64, _P, _P, _I, _F, _P, _I64, _P, _P, _P], _I),
+    "gs_layer_norm_backward": ([_P, _P, _I, _I64, _I64, _I64, _I64, _P, _I, _P, _P, _P, _I64, _P, _P,
+                                _P, _I64, _P], _I),
+    "gs_layer_norm_backward_workspace_size": ([_I64, _I64, _PI64], _I),
+    "gs_dropout": ([_P, _I, _I64, _P, _F, _U64, _U32, _P, _P], _I),
+    "gs_relative_bucket": ([_I64, _I, _I, _I, ctypes.POINTER(_I)], _I),
+    "gs_attention": ([_PDESC, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P], _I),
+    "gs_attention_workspace_size": ([_PDESC, _PI64], _I),
+    "gs_attention_backward": ([_PDESC] + [_P] * 13 + [_I64, _P], _I),
+    "gs_attention_backward_workspace_size": ([_PDESC, _PI64], _I),
+}
+
+_typed = None
+
+
+def token_lib():
+    """The loaded libgsample with the token entry points' argument types set."""
+    global _typed
+    if _typed is None:
+        handle = _library()
+        for name, (args, res) in TOKEN_SIGNATURES.items():
+            fn = getattr(handle, name)
+            fn.argtypes = args
+            fn.restype = res
+        _typed = handle
+    return _typed
+
+
+def _tensor(t, name, dtype=None, shape=None):
+    """`t` on the GPU with a contiguous last axis, its type and shape checked."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must have element type %s" % (name, dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s" % (name, tuple(shape)))
+    return t if t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+def _like(t):
+    """A new tensor laid out like `t` (a broadcast axis or a gap is not kept), its last axis contiguous."""
+    torch = _torch()
+    if 0 not in t.stride():
+        new = torch.empty_like(t)
+        if new.shape[-1] <= 1 or new.stride(-1) == 1:
+            return new
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _output(out, like, dense):
+    """`out` checked, or a new tensor: contiguous where `dense`, else laid out like `like`."""
+    if out is None:
+        return _torch().empty(like.shape, dtype=like.dtype, device=like.device) if dense else _like(like)
+    if not out.is_cuda or out.shape != like.shape or out.dtype != like.dtype or (
+            not out.is_contiguous() if dense else out.shape[-1] > 1 and out.stride(-1) != 1):
+        raise ValueError("out must be a %s GPU tensor of shape %s and type %s"
+                         % ("contiguous" if dense else "(last axis contiguous)", tuple(like.shape), like.dtype))
+    return out
+
+
+def _rows(t):
+    """`t` as rows of its last axis that one stride separates (copied where none does) and that stride."""
+    flat = t.reshape(-1, t.shape[-1]) if t.numel() else t.contiguous()
+    n = t.shape[-1]
+    return flat, (flat.stride(0) if flat.dim() == 2 and flat.shape[0] > 1 else n)
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=device) if need else None
+    if workspace is None or workspace.numel() == 0:
+        return None, None, 0
+    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def _norm_params(X, scale, bias):
+    cols = X.shape[-1]
+    scale = _device_tensor(scale, "scale")
+    for name, t in (("scale", scale), ("bias", bias)):
+        if t is not None and tuple(t.shape) != (cols,):
+            raise ValueError("%s must have shape (%d,)" % (name, cols))
+    if scale.dtype != X.dtype and scale.dtype != _torch().float32:
+        raise TypeError("scale must have X's element type or float32")
+    if bias is not None:
+        bias = _device_tensor(bias, "bias")
+        if bias.dtype != scale.dtype:
+            raise TypeError("bias must have scale's element type")
+    return scale, bias
+
+
+def layer_norm(X, scale, bias=None, epsilon: float = 1e-5, return_stats: bool = False, out=None,
+               stream=None):
+    """Layer normalisation over the last axis of X (gs_layer_norm).
+
+    scale and bias have X's element type or float32.  With `return_stats` the
+    mean and inverse standard deviation of each row are returned too (float32,
+    X's shape without its last axis): layer_norm_backward takes them."""
+    torch = _torch()
+    X = _tensor(X, "X")
+    if X.dim() < 1:
+        raise ValueError("X needs an axis")
+    scale, bias = _norm_params(X, scale, bias)
+    x, xs = _rows(X)
+    cols = X.shape[-1]
+    rows = math.prod(X.shape[:-1])
+    Y = _output(out, X, True)
+    mean = inv_std = None
+    if return_stats:
+        mean = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
+        inv_std = torch.empty_like(mean)
+    st = token_lib().gs_layer_norm(
+        _ptr(x), dtype_code(X), rows, cols, xs, _ptr(scale), _ptr(bias), dtype_code(scale),
+        float(epsilon), _ptr(Y), cols, _ptr(mean), _ptr(inv_std),
+        _stream(stream, X.device))
+    _check(st, "gs_layer_norm")
+    return (Y, mean, inv_std) if return_stats else Y
+
+
+def layer_norm_backward(dY, X, scale, mean, inv_std, stream=None, workspace=None):
+    """Gradients (dX, dscale, dbias) of layer_norm (gs_layer_norm_backward).
+    `workspace`: device scratch; None takes it from torch's allocator."""
+    torch = _torch()
+    X = _tensor(X, "X")
+    dY = _tensor(dY, "dY", X.dtype, X.shape)
+    scale, _ = _norm_params(X, scale, None)
+    cols = X.shape[-1]
+    rows = math.prod(X.shape[:-1])
+    for name, t in (("mean", mean), ("inv_std", inv_std)):
+        if t.dtype != torch.float32 or t.numel() != rows or not t.is_cuda:
+            raise ValueError("%s must be a float32 GPU tensor with an element per row" % name)
+    mean, inv_std = mean.contiguous(), inv_std.contiguous()
+    x, xs = _rows(X)
+    dy, dys = _rows(dY)
+    dX = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    dscale, dbias = torch.empty_like(scale), torch.empty_like(scale)
+    need = _I64(0)
+    _check(token_lib().gs_layer_norm_backward_workspace_size(rows, cols, ctypes.byref(need)),
+           "gs_layer_norm_backward_workspace_size")
+    workspace, ws, ws_bytes = _workspace(workspace, need.value, X.device)
+    st = token_lib().gs_layer_norm_backward(
+        _ptr(dy), _ptr(x), dtype_code(X), rows, cols, dys, xs, _ptr(scale), dtype_code(scale),
+        _ptr(mean), _ptr(inv_std), _ptr(dX), cols, _ptr(dscale), _ptr(dbias), ws, ws_bytes,
+        _stream(stream, X.device))
+    _check(st, "gs_layer_norm_backward")
+    return dX, dscale, dbias
+
+
+def dropout(X, ratio: float, seed: int, call: int = 0, residual=None, out=None, stream=None):
+    """residual + dropout(X) (gs_dropout); the mask follows from seed, call and
+    an element's place in X.  The gradient with respect to X is
+    dropout(dY, ratio, seed, call); with respect to the residual it is dY."""
+    X = _device_tensor(X, "X")
+    if residual is not None:
+        residual = _device_tensor(residual, "residual")
+        if residual.dtype != X.dtype or residual.shape != X.shape:
+            raise ValueError("residual must have X's shape and element type")
+    Y = _output(out, X, True)
+    st = token_lib().gs_dropout(_ptr(X), dtype_code(X), X.numel(), _ptr(residual), float(ratio),
+                                int(seed) & (2 ** 64 - 1), int(call) & (2 ** 32 - 1), _ptr(Y),
+                                _stream(stream, X.device))
+    _check(st, "gs_dropout")
+    return Y
+
+
+def relative_bucket(r: int, num_buckets: int, max_distance: int = 128, bidirectional: int = 1) -> int:
+    """Bucket of key position minus query position (gs_relative_bucket)."""
+    got = _I(0)
+    _check(token_lib().gs_relative_bucket(int(r), int(num_buckets), int(max_distance),
+                                          int(bidirectional), ctypes.byref(got)), "gs_relative_bucket")
+    return got.value
+
+
+def _strides(t):
+    # the stride of an axis of one element addresses nothing
+    s, n = t.stride(), t.shape
+    return _S3(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
+
+
+def _attention_inputs(Q, K, V, scale, causal, kv_lengths, table, max_distance, bidirectional,
+                      q_position, ratio, seed, call):
+    """Checked tensors of an attention call and its descriptor, without O's strides."""
+    torch = _torch()
+    if Q.dim() != 4 or K.dim() != 4:
+        raise ValueError("Q and K must have shape (batch, heads, length, head_dim)")
+    Q = _tensor(Q, "Q")
+    K = _tensor(K, "K", Q.dtype)
+    if K.shape[0] != Q.shape[0] or K.shape[3] != Q.shape[3]:
+        raise ValueError("K must share Q's batch and head_dim")
+    V = _tensor(V, "V", Q.dtype, K.shape)
+    B, H, Lq, D = Q.shape
+    if kv_lengths is not None:
+        kv_lengths = _tensor(kv_lengths, "kv_lengths", torch.int32, (B,)).contiguous()
+    d = AttentionDesc()
+    d.dtype = dtype_code(Q)
+    d.batch, d.q_heads, d.q_len, d.head_dim = B, H, Lq, D
+    d.kv_heads, d.kv_len = K.shape[1], K.shape[2]
+    d.q_stride, d.k_stride, d.v_stride = _strides(Q), _strides(K), _strides(V)
+    d.scale = 1.0 / math.sqrt(D) if scale is None and D else float(scale or 0.0)
+    d.causal = int(causal)
+    if isinstance(q_position, str):
+        if q_position != "end":
+            raise ValueError('q_position must be a number or "end"')
+        d.q_from_end = 1
+    else:
+        d.q_position = int(q_position)
+    if table is not None:
+        table = _device_tensor(table, "table")
+        if table.dim() != 2 or table.shape[1] != H:
+            raise ValueError("table must have shape (buckets, %d)" % H)
+        if table.dtype != Q.dtype and table.dtype != torch.float32:
+            raise TypeError("table must have Q's element type or float32")
+        if table.shape[0] < 2:
+            raise ValueError("table needs two buckets or more")
+        d.table_dtype = dtype_code(table)
+        d.num_buckets, d.max_distance, d.bidirectional = table.shape[0], int(max_distance), int(bidirectional)
+    else:
+        d.table_dtype = GS_F32
+    d.ratio, d.seed, d.call = float(ratio), int(seed) & (2 ** 64 - 1), int(call) & (2 ** 32 - 1)
+    return Q, K, V, kv_lengths, table, d
+
+
+def attention(Q, K, V, scale=None, causal: int = 0, kv_lengths=None, table=None,
+              max_distance: int = 128, bidirectional: int = 1, q_position=0, ratio: float = 0.0,
+              seed: int = 0, call: int = 0, return_lse: bool = False, out=None, stream=None,
+              workspace=None):
+    """Attention with a relative position bias (gs_attention).
+
+    Q (batch, heads, length, head_dim), K and V (batch, kv_heads, kv_length,
+    head_dim), of any strides with a contiguous last axis: a (batch, length,
+    heads, head_dim) tensor is passed as its transpose(1, 2).  `scale` defaults
+    to 1 / sqrt(head_dim).  `kv_lengths` (int32, batch): keys each sequence
+    holds.  `table` (buckets, heads): the learned bias.  `q_position`: position
+    of query 0 among the keys, or "end" where the queries are the last of each
+    sequence (a cache is read).  O is laid out like Q.  With `return_lse` the
+    log-sum-exp of the scores (float32, batch x heads x length) is returned
+    too: attention_backward takes it."""
+    torch = _torch()
+    Q, K, V, kv_lengths, table, d = _attention_inputs(
+        Q, K, V, scale, causal, kv_lengths, table, max_distance, bidirectional, q_position, ratio,
+        seed, call)
+    O = _output(out, Q, False)
+    d.o_stride = _strides(O)
+    lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device) if return_lse else None
+    if workspace is None:
+        need = _I64(0)
+        _check(token_lib().gs_attention_workspace_size(ctypes.byref(d), ctypes.byref(need)),
+               "gs_attention_workspace_size")
+        workspace, ws, ws_bytes = _workspace(None, need.value, Q.device)
+    else:
+        workspace, ws, ws_bytes = _workspace(workspace, 0, Q.device)
+    st = token_lib().gs_attention(ctypes.byref(d), _ptr(Q), _ptr(K), _ptr(V), _ptr(kv_lengths),
+                                  _ptr(table), _ptr(O), _ptr(lse), ws, ws_bytes,
+                                  _stream(stream, Q.device))
+    _check(st, "gs_attention")
+    return (O, lse) if return_lse else O
+
+
+def attention_backward(dO, Q, K, V, O, lse, scale=None, causal: int = 0, kv_lengths=None, table=None,
+                       max_distance: int = 128, bidirectional: int = 1, q_position=0,
+                       ratio: float = 0.0, seed: int = 0, call: int = 0, stream=None,
+                       workspace=None):
+    """Gradients (dQ, dK, dV, dtable) of attention (gs_attention_backward) from
+    its inputs, its O and its lse; dtable is None without a table."""
+    torch = _torch()
+    Q, K, V, kv_lengths, table, d = _attention_inputs(
+        Q, K, V, scale, causal, kv_lengths, table, max_distance, bidirectional, q_position, ratio,
+        seed, call)
+    O = _tensor(O, "O", Q.dtype, Q.shape)
+    dO = _tensor(dO, "dO", Q.dtype, Q.shape)
+    lse = _tensor(lse, "lse", torch.float32, Q.shape[:3]).contiguous()
+    dQ, dK, dV = _like(Q), _like(K), _like(V)
+    dtable = torch.empty_like(table) if table is not None else None
+    d.o_stride, d.do_stride = _strides(O), _strides(dO)
+    d.dq_stride, d.dk_stride, d.dv_stride = _strides(dQ), _strides(dK), _strides(dV)
+    need = _I64(0)
+    _check(token_lib().gs_attention_backward_workspace_size(ctypes.byref(d), ctypes.byref(need)),
+           "gs_attention_backward_workspace_size")
+    workspace, ws, ws_bytes = _workspace(workspace, need.value, Q.device)
+    st = token_lib().gs_attention_backward(
+        ctypes.byref(d), _ptr(dO), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse), _ptr(kv_lengths),
+        _ptr(table), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dtable), ws, ws_bytes,
+        _stream(stream, Q.device))
+    _check(st, "gs_attention_backward")
+    return dQ, dK, dV, dtable

@@ -26,7 +26,8 @@ LIB = os.path.join(PKG, "libgsample.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["gs_kernels.hip", "gs_gather.hip", "gs_resize.hip", "gs_nd.hip", "gs_deform.hip",
-           "gs_noalloc.hip", "gs_api.cpp"]
+           "gs_noalloc.hip", "gs_api.cpp", "gs_norm.hip", "gs_dropout.hip", "gs_attention.hip",
+           "gs_attention_bwd.hip", "gs_tokens_api.cpp"]
 
 FLAGS = [
     "--offload-arch=gfx950",

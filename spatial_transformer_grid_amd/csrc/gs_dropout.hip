@@ -1,0 +1,63 @@
+// gs_dropout.hip -- dropout from a counter-based generator, with an optional
+// residual: Y = residual + dropout(X).
+//
+// A lane takes eight consecutive elements: one generator call.  Bound by
+// memory: one read of X (and of the residual), one write of Y.
+#include "gs_tokens.hpp"
+
+namespace gs {
+
+namespace {
+
+template <typename T, bool RES>
+__global__ __launch_bounds__(256) void dropout_kernel(DropoutParams p) {
+    typedef typename T::raw_t raw_t;
+    const raw_t *X = (const raw_t *)p.X, *R = (const raw_t *)p.residual;
+    raw_t *Y = (raw_t *)p.Y;
+    const int64_t blocks = (p.count + 7) >> 3;
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < blocks; n += (int64_t)gridDim.x * 256) {
+        const int64_t at = 8 * n;
+        const int left = (int)(p.count - at < 8 ? p.count - at : 8);
+        const bool vec = p.vec && left == 8;
+        Frag<T> x = frag_global<T>(X + at, 0, left, true, vec), r;
+        if constexpr (RES) r = frag_global<T>(R + at, 0, left, true, vec);
+        const u32x4 rnd =
+            philox((uint32_t)n, (uint32_t)(n >> 32), 0, p.call, p.seed_lo, p.seed_hi);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = kept(rnd, j, p.threshold) ? frag_get<T>(x, j) * p.keep_scale : 0.0f;
+            if constexpr (RES) v[j] += frag_get<T>(r, j);
+        }
+        if (vec) {
+            const Frag<T> y = frag_pack<T>(v);
+#pragma unroll
+            for (int i = 0; i < T::bytes / 2; ++i) *(u32x4 *)(Y + at + i * (16 / T::bytes)) = y.w[i];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < left) Y[at + j] = to_bits<T>(v[j]);
+        }
+    }
+}
+
+template <typename T>
+int launch_t(const DropoutParams &p, hipStream_t stream) {
+    const int64_t blocks = ((p.count + 7) / 8 + 255) / 256;
+    const dim3 grid((unsigned)(blocks < 16384 ? blocks : 16384));
+    if (p.residual)
+        hipLaunchKernelGGL((dropout_kernel<T, true>), grid, dim3(256), 0, stream, p);
+    else
+        hipLaunchKernelGGL((dropout_kernel<T, false>), grid, dim3(256), 0, stream, p);
+    return (int)hipGetLastError();
+}
+
+}  // namespace
+
+int launch_dropout(const DropoutParams &p, int dtype, hipStream_t stream) {
+    if (dtype == 0) return launch_t<F32>(p, stream);
+    if (dtype == 1) return launch_t<F16>(p, stream);
+    return launch_t<BF16>(p, stream);
+}
+
+}  // namespace gs
