@@ -8,56 +8,114 @@
 // A wave owns 32 queries.  It computes S^T = K Q^T, so a lane holds one
 // query's scores: the softmax needs no exchange but one with lane + 32, and
 // the probabilities are already the B operand of O^T += V^T P^T (a_row).
+//
+// Two forms.  Where 128-query blocks fill the chip, the four waves of a block
+// share each tile of keys, two buffers deep.  Where they do not, a block has 32
+// queries and its waves take every fourth key tile, each into LDS of its own
+// without block barriers, and add up at the end; if that is still too few
+// blocks, the key axis is also split over blocks and attention_combine joins
+// them.  There the rows may be the queries of all the heads that share a key
+// head, so that the cache is read once.
 #include "gs_tokens.hpp"
 
 namespace gs {
 
 namespace {
 
-constexpr int kKeys = 64;   // keys of an LDS tile
-
-template <typename T, int DP>
+template <typename T, int DP, bool FEW>
 struct FwdGeo {
+    static constexpr int KEYS = FEW || T::bytes == 4 ? 32 : 64;   // keys of an LDS tile
     static constexpr int PITCH = DP + 16 / T::bytes;
-    static constexpr int tile_elems = kKeys * PITCH;
-    static constexpr int fixed_bytes = 2 * tile_elems * T::bytes;
+    static constexpr int tile_elems = KEYS * PITCH;
+    // two buffers of K and V, or one of each wave's own
+    static constexpr int fixed_bytes = (FEW ? 4 : 2) * 2 * tile_elems * T::bytes;
+    static constexpr int SUM = DP + 4;                            // floats of a row of a wave's O
+    static_assert(!FEW || 4 * 32 * SUM * 4 <= fixed_bytes, "the waves' sums take the tiles' place");
 };
 
-template <typename T, int DP, bool DROP>
-__global__ __launch_bounds__(256) void attention_forward(AttnParams p) {
-    typedef typename T::raw_t raw_t;
-    typedef FwdGeo<T, DP> Geo;
-    constexpr int PITCH = Geo::PITCH;
-    extern __shared__ __align__(16) unsigned char smem[];
-    raw_t *Ks = (raw_t *)smem;
-    raw_t *Vs = Ks + Geo::tile_elems;
-    float *lut = (float *)(smem + Geo::fixed_bytes);
+// A new maximum is taken up only where a score passes the old one by more than
+// this (base 2): the probabilities then stay below 2^kSlack, far from the
+// largest fp16 value, and O is not scaled again with each small step.
+constexpr float kSlack = 8.0f;
 
-    const int lb = xcd_contiguous_block(p.nblocks);
-    if (lb >= p.nblocks) return;
-    int tile = lb % p.tiles;
-    const int bh = lb / p.tiles;
-    if (p.causal) tile = p.tiles - 1 - tile;        // the longest rows first
-    const int b = bh / p.H, h = bh - b * p.H, hk = h / p.G;
+template <typename T, int DP, bool DROP, bool FEW>
+__global__ __launch_bounds__(256, FEW && T::bytes == 4 && DP > 64 ? 1 : 2) void attention_forward(AttnParams p) {
+    typedef typename T::raw_t raw_t;
+    typedef FwdGeo<T, DP, FEW> Geo;
+    constexpr int PITCH = Geo::PITCH, KEYS = Geo::KEYS, U = KEYS / 32, NT = FEW ? 64 : 256;
+    extern __shared__ __align__(16) unsigned char smem[];
+    float *luts = (float *)(smem + Geo::fixed_bytes);
+    __shared__ float stat[4][2][32];                 // FEW: maximum and sum of each wave
+
+    int unit, tile, part;
+    if (!block_place(p, !FEW, unit, tile, part)) return;
     const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    // the lane's row: query qi of head h
+    int b, h, hk, g = 0, qi, rows;
+    const int row = FEW ? tile * 32 + (lane & 31) : tile * kAttnRows + wave * 32 + (lane & 31);
+    if (FEW && p.pack) {
+        b = unit / p.Hkv;
+        hk = unit - b * p.Hkv;
+        rows = p.G * p.Lq;
+        g = row < rows ? row / p.Lq : 0;
+        qi = row < rows ? row - g * p.Lq : 0;
+        h = hk * p.G + g;
+    } else {
+        b = unit / p.H;
+        h = unit - b * p.H;
+        hk = h / p.G;
+        rows = p.Lq;
+        qi = row;
+    }
+    const bool live = row < rows;
     const int len = sequence_length(p, b);
     const int first = p.from_end ? len - p.Lq : p.first;
-    const int q0 = tile * kAttnQueries + wave * 32;
-    const int qi = q0 + (lane & 31);
     const int pos = first + qi;
-    const int block_last = first + min((tile + 1) * kAttnQueries, p.Lq) - 1;
-    const int end = p.causal ? min(len, block_last + 1) : len;
+    // positions of the wave's rows, and the last one of the block's
+    const int row0 = FEW ? tile * 32 : tile * kAttnRows + wave * 32;
+    const int wave_first = FEW && p.pack ? first : first + row0;
+    const int wave_last = FEW && p.pack ? first + p.Lq - 1 : wave_first + 31;
+    const int block_last =
+        FEW && p.pack ? wave_last : first + min(FEW ? row0 + 32 : (tile + 1) * kAttnRows, p.Lq) - 1;
+    const int end = min(p.causal ? min(len, block_last + 1) : len, FEW ? (part + 1) * p.chunk : len);
+    const int begin = FEW ? part * p.chunk + wave * KEYS : 0;
+    constexpr int STEP = FEW ? 4 * KEYS : KEYS;
     const bool vec = p.vec;
 
     const raw_t *kb = (const raw_t *)p.k + (int64_t)b * p.ks[0] + (int64_t)hk * p.ks[1];
     const raw_t *vb = (const raw_t *)p.v + (int64_t)b * p.vs[0] + (int64_t)hk * p.vs[1];
     const raw_t *qrow =
         (const raw_t *)p.q + (int64_t)b * p.qs[0] + (int64_t)h * p.qs[1] + (int64_t)qi * p.qs[2];
+    const int tt = FEW ? lane : t;
+    raw_t *Kt = (raw_t *)smem + (FEW ? wave * 2 * Geo::tile_elems : 0);
+    TileCopy<T, DP, KEYS, NT, PITCH> kc, vc;
+    if (begin < end) {
+        kc.fetch(kb, p.ks[2], begin, end, p.D, vec, tt);
+        vc.fetch(vb, p.vs[2], begin, end, p.D, vec, tt);
+    }
+    // a negative scale moves into Q: the maximum of the scores is then that of the products
+    const float scale2 = fabsf(p.scale2);
     Frag<T> qf[DP / 16];
 #pragma unroll
-    for (int s = 0; s < DP / 16; ++s) qf[s] = frag_global<T>(qrow, 16 * s + 8 * half, p.D, qi < p.Lq, vec);
-    if (p.lut) fill_lut<T>(p, h, lut, (uint16_t *)(lut + p.lut), t, 256);
+    for (int s = 0; s < DP / 16; ++s) {
+        qf[s] = frag_global<T>(qrow, 16 * s + 8 * half, p.D, live, vec);
+        if (p.scale2 < 0.0f) frag_negate<T>(qf[s]);
+    }
+    const float *lut = luts;
+    float bias_lo = 0.0f, bias_hi = 0.0f;
+    if (p.lut) {
+        const int heads = FEW && p.pack ? p.G : 1;
+        uint16_t *starts = (uint16_t *)(luts + heads * p.lut);
+        for (int i = t; i < p.side; i += 256) starts[i] = p.starts[i];
+        __syncthreads();
+        for (int i = 0; i < heads; ++i)
+            fill_lut<T>(p, FEW && p.pack ? hk * p.G + i : h, luts + i * p.lut, starts, t, 256);
+        __syncthreads();
+        lut = luts + (FEW ? g * p.lut : 0);
+        bias_lo = lut[0];
+        bias_hi = lut[p.lut - 1];
+    }
 
     f32x16 acc[DP / 32];
 #pragma unroll
@@ -65,97 +123,214 @@ __global__ __launch_bounds__(256) void attention_forward(AttnParams p) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
     float m = -INFINITY, l = 0.0f;
+    const uint32_t below = (p.threshold - 1) * 0x10001u;
 
-    TileCopy<T, DP, kKeys, 256, PITCH> copy;
-    for (int k0 = 0; k0 < end; k0 += kKeys) {
-        __syncthreads();
-        copy.fetch(kb, p.ks[2], k0, end, p.D, vec, t);
-        copy.put(Ks, t);
-        copy.fetch(vb, p.vs[2], k0, end, p.D, vec, t);
-        copy.put(Vs, t);
-        __syncthreads();
-        const int wave_first = first + q0, wave_last = wave_first + 31;
-        if (q0 >= p.Lq || (p.causal && k0 > wave_last)) continue;
-
-        float s[32];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            f32x16 st;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) st[r] = 0.0f;
-            const raw_t *row = Ks + (32 * u + a_row(lane & 31)) * PITCH + 8 * half;
-#pragma unroll
-            for (int x = 0; x < DP / 16; ++x) mma<T>(st, frag_lds<T>(row + 16 * x), qf[x]);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[16 * u + r] = st[r];
+    if (begin < end) {
+        kc.put(Kt, tt);
+        vc.put(Kt + Geo::tile_elems, tt);
+    }
+    for (int k0 = begin, n = 0; k0 < end; k0 += STEP, ++n) {
+        const raw_t *Ks = Kt + (FEW ? 0 : (n & 1) * 2 * Geo::tile_elems);
+        const raw_t *Vs = Ks + Geo::tile_elems;
+        tile_sync<FEW>();
+        const bool more = k0 + STEP < end;
+        if (more) {
+            kc.fetch(kb, p.ks[2], k0 + STEP, end, p.D, vec, tt);
+            vc.fetch(vb, p.vs[2], k0 + STEP, end, p.D, vec, tt);
         }
-        // s[16 u + 8 x + j]: key k0 + 32 u + 16 x + 8 half + j of this lane's query
-        const int key0 = k0 + 8 * half;
-        if (p.lut) {
+        if (FEW || (row0 < p.Lq && !(p.causal && k0 > wave_last))) {
+            float s[16 * U];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                s[i] = fmaf(s[i], p.scale2, lut[lut_index(p, key0 + 16 * (i >> 3) + (i & 7) - pos)]);
-        } else {
+            for (int u = 0; u < U; ++u) {
+                f32x16 st;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] *= p.scale2;
-        }
-        if (k0 + kKeys > end || (p.causal && k0 + kKeys - 1 > wave_first)) {
-            const int seen = p.causal ? min(end, pos + 1) : end;
+                for (int r = 0; r < 16; ++r) st[r] = 0.0f;
+                const raw_t *krow = Ks + (32 * u + a_row(lane & 31)) * PITCH + 8 * half;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (key0 + 16 * (i >> 3) + (i & 7) >= seen) s[i] = -INFINITY;
-        }
-        float top = m;
+                for (int x = 0; x < DP / 16; ++x) mma<T>(st, frag_lds<T>(krow + 16 * x), qf[x]);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i]);
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float base = top == -INFINITY ? 0.0f : top;
-        const float alpha = __builtin_amdgcn_exp2f(m - base);
-        m = top;
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            s[i] = __builtin_amdgcn_exp2f(s[i] - base);
-            sum += s[i];
-        }
-        l = fmaf(l, alpha, sum);
-#pragma unroll
-        for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[d][r] *= alpha;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            if constexpr (DROP) {
-                const u32x4 rnd = philox((uint32_t)(key0 + 16 * x) >> 3, (uint32_t)qi, (uint32_t)bh, p.call,
-                                         p.seed_lo, p.seed_hi);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s[8 * x + j] = kept(rnd, j, p.threshold) ? s[8 * x + j] : 0.0f;
+                for (int r = 0; r < 16; ++r) s[16 * u + r] = st[r];
             }
-            const Frag<T> pf = frag_pack<T>(s + 8 * x);
+            // s[8 x + j]: key k0 + 16 x + 8 half + j of this lane's query, a score
+            // once multiplied by mul, with c added
+            const int key0 = k0 + 8 * half;
+            float mul = scale2, c = 0.0f;
+            const int cls = bias_class(p, k0 - wave_last, k0 + KEYS - 1 - wave_first);
+            const bool edge = k0 + KEYS > end || (p.causal && k0 + KEYS - 1 > wave_first);
+            if (cls == 1) c = bias_lo;
+            if (cls == 2) c = bias_hi;
+            // fp32 rounds every score before the maximum leaves it, so that the
+            // largest one's probability is 1 exactly; elsewhere the probability's
+            // own rounding hides the difference
+            if (cls == 0 || edge || T::bytes == 4) {
+                if (cls == 0) {
+                    const float *at = lut + (key0 - pos + p.border + kLutPad);
 #pragma unroll
-            for (int d = 0; d < DP / 32; ++d)
-                mma<T>(acc[d], frag_lds_transposed<T, PITCH>(Vs, 16 * x, 32 * d, lane), pf);
+                    for (int i = 0; i < 16 * U; ++i) s[i] = fmaf(s[i], mul, at[16 * (i >> 3) + (i & 7)]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16 * U; ++i) s[i] = fmaf(s[i], mul, c);
+                }
+                mul = 1.0f;
+                c = 0.0f;
+                if (edge) {
+                    const int seen = (p.causal ? min(end, pos + 1) : end) - key0;
+#pragma unroll
+                    for (int i = 0; i < 16 * U; ++i)
+                        if (16 * (i >> 3) + (i & 7) >= seen) s[i] = -INFINITY;
+                }
+            }
+            float top = s[0];
+#pragma unroll
+            for (int i = 1; i < 16 * U; ++i) top = fmaxf(top, s[i]);
+            top = fmaf(top, mul, c);
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (__any(top > m + kSlack)) {
+                const float next = fmaxf(m, top);
+                const float alpha = next == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - next);
+                m = next;
+                l *= alpha;
+#pragma unroll
+                for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[d][r] *= alpha;
+            }
+            c -= m == -INFINITY ? 0.0f : m;
+            float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 16 * U; ++i) {
+                s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], mul, c));
+                sum[i & 1] += s[i];
+            }
+            l += sum[0] + sum[1];
+#pragma unroll
+            for (int x = 0; x < 2 * U; ++x) {
+                u32x4 rnd;
+                if constexpr (DROP)
+                    rnd = philox((uint32_t)(key0 + 16 * x) >> 3, (uint32_t)qi, (uint32_t)(b * p.H + h), p.call,
+                                 p.seed_lo, p.seed_hi);
+                if constexpr (DROP && T::bytes == 4) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[8 * x + j] = kept(rnd, j, p.threshold) ? s[8 * x + j] : 0.0f;
+                }
+                Frag<T> pf = frag_pack<T>(s + 8 * x);
+                if constexpr (DROP && T::bytes == 2) frag_keep<T>(pf, rnd, below);
+#pragma unroll
+                for (int d = 0; d < DP / 32; ++d)
+                    mma<T>(acc[d], frag_lds_transposed<T, PITCH>(Vs, 16 * x, 32 * d, lane), pf);
+            }
+        }
+        if (more) {
+            if (FEW) tile_sync<true>();
+            raw_t *next = Kt + (FEW ? 0 : ((n + 1) & 1) * 2 * Geo::tile_elems);
+            kc.put(next, tt);
+            vc.put(next + Geo::tile_elems, tt);
         }
     }
     l += __shfl_xor(l, 32);
-    if (qi >= p.Lq) return;
-    const float norm = l > 0.0f || l != l ? p.keep_scale / l : 0.0f;
-    raw_t *orow = (raw_t *)p.o + (int64_t)b * p.os[0] + (int64_t)h * p.os[1] + (int64_t)qi * p.os[2];
+    if constexpr (!FEW) {
+        if (!live) return;
+        const float norm = l > 0.0f || l != l ? p.keep_scale / l : 0.0f;
+        raw_t *orow = (raw_t *)p.o + (int64_t)b * p.os[0] + (int64_t)h * p.os[1] + (int64_t)qi * p.os[2];
 #pragma unroll
-    for (int d = 0; d < DP / 32; ++d)
+        for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
-        for (int r = 0; r < 16; r += 4)
-            store4<T>(orow, 32 * d + 2 * r + 4 * half, p.D, vec, acc[d][r] * norm, acc[d][r + 1] * norm,
-                      acc[d][r + 2] * norm, acc[d][r + 3] * norm);
-    if (p.lse && half == 0)
-        p.lse[(int64_t)bh * p.Lq + qi] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+            for (int r = 0; r < 16; r += 4)
+                store4<T>(orow, 32 * d + 2 * r + 4 * half, p.D, vec, acc[d][r] * norm, acc[d][r + 1] * norm,
+                          acc[d][r + 2] * norm, acc[d][r + 3] * norm);
+        if (p.lse && half == 0)
+            p.lse[(int64_t)unit * p.Lq + qi] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    } else {
+        // the waves' O, l under a common maximum, added in the order of the waves
+        if (half == 0) {
+            stat[wave][0][lane] = m;
+            stat[wave][1][lane] = l;
+        }
+        __syncthreads();
+        const int col = lane & 31;
+        const float all = fmaxf(fmaxf(stat[0][0][col], stat[1][0][col]), fmaxf(stat[2][0][col], stat[3][0][col]));
+        const float alpha = all == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - all);
+        float *sums = (float *)smem;
+        float *mine = sums + (wave * 32 + col) * Geo::SUM + 4 * half;
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4)
+                *(tokens_f32x4 *)(mine + 32 * d + 2 * r) = tokens_f32x4{acc[d][r] * alpha, acc[d][r + 1] * alpha,
+                                                                       acc[d][r + 2] * alpha, acc[d][r + 3] * alpha};
+        __syncthreads();
+        for (int i = t; i < 32 * (DP / 4); i += 256) {
+            const int r = i / (DP / 4), at = (i - r * (DP / 4)) * 4;
+            const int rr = tile * 32 + r;
+            if (rr >= rows || at >= p.D) continue;
+            float big = stat[0][0][r], lr = 0.0f;
+#pragma unroll
+            for (int w = 1; w < 4; ++w) big = fmaxf(big, stat[w][0][r]);
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                if (big != -INFINITY) lr = fmaf(stat[w][1][r], __builtin_amdgcn_exp2f(stat[w][0][r] - big), lr);
+            tokens_f32x4 v = *(const tokens_f32x4 *)(sums + r * Geo::SUM + at);
+#pragma unroll
+            for (int w = 1; w < 4; ++w) v += *(const tokens_f32x4 *)(sums + (w * 32 + r) * Geo::SUM + at);
+            const int64_t flat = (int64_t)unit * rows + rr;       // (b, h, qi) in either order of the rows
+            if (p.splits > 1) {
+                const int64_t all_rows = (int64_t)p.B * p.H * p.Lq, dr = split_row(p.D);
+                float *out = p.split + ((int64_t)part * all_rows + flat) * dr;
+                *(tokens_f32x4 *)(out + at) = v;
+                if (at == 0) {
+                    float *st = p.split + (int64_t)p.splits * all_rows * dr + ((int64_t)part * all_rows + flat) * 2;
+                    st[0] = big;
+                    st[1] = lr;
+                }
+                continue;
+            }
+            const float norm = lr > 0.0f || lr != lr ? p.keep_scale / lr : 0.0f;
+            const int64_t bh = flat / p.Lq;
+            const int bb = (int)(bh / p.H), hh = (int)(bh - (int64_t)bb * p.H), q = (int)(flat - bh * p.Lq);
+            raw_t *orow = (raw_t *)p.o + (int64_t)bb * p.os[0] + (int64_t)hh * p.os[1] + (int64_t)q * p.os[2];
+            store4<T>(orow, at, p.D, vec, v[0] * norm, v[1] * norm, v[2] * norm, v[3] * norm);
+            if (p.lse && at == 0) p.lse[flat] = lr == 0.0f ? -INFINITY : (big + __builtin_amdgcn_logf(lr)) * kLn2;
+        }
+    }
 }
 
-template <typename T, int DP>
-int launch_dp(const AttnParams &p, hipStream_t stream) {
-    const int smem = FwdGeo<T, DP>::fixed_bytes + p.lut * 4 + (p.lut ? p.side * 2 : 0);
+// O and lse from the parts of the key axis, a wave a row: the parts' O and
+// sums under their common maximum, added in the order of the parts.
+template <typename T>
+__global__ __launch_bounds__(256) void attention_combine(AttnParams p) {
+    typedef typename T::raw_t raw_t;
+    const int64_t rows = (int64_t)p.B * p.H * p.Lq;
+    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (r >= rows) return;
+    const int lane = threadIdx.x & 63, dr = split_row(p.D);
+    const float *st = p.split + (int64_t)p.splits * rows * dr;
+    float big = -INFINITY;
+    for (int i = 0; i < p.splits; ++i) big = fmaxf(big, st[(i * rows + r) * 2]);
+    float l = 0.0f, v[2] = {0.0f, 0.0f};
+    const int c0 = lane < p.D ? lane : 0, c1 = lane + 64 < p.D ? lane + 64 : 0;
+    if (big != -INFINITY)
+        for (int i = 0; i < p.splits; ++i) {
+            const int64_t at = i * rows + r;
+            const float w = __builtin_amdgcn_exp2f(st[at * 2] - big);
+            l = fmaf(st[at * 2 + 1], w, l);
+            v[0] = fmaf(p.split[at * dr + c0], w, v[0]);
+            v[1] = fmaf(p.split[at * dr + c1], w, v[1]);
+        }
+    const float norm = l > 0.0f || l != l ? p.keep_scale / l : 0.0f;
+    const int64_t bh = r / p.Lq;
+    const int b = (int)(bh / p.H), h = (int)(bh - (int64_t)b * p.H), q = (int)(r - bh * p.Lq);
+    raw_t *orow = (raw_t *)p.o + (int64_t)b * p.os[0] + (int64_t)h * p.os[1] + (int64_t)q * p.os[2];
+    if (lane < p.D) orow[lane] = to_bits<T>(v[0] * norm);
+    if (lane + 64 < p.D) orow[lane + 64] = to_bits<T>(v[1] * norm);
+    if (p.lse && lane == 0) p.lse[r] = l == 0.0f ? -INFINITY : (big + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+template <typename T, int DP, bool DROP, bool FEW>
+int launch_form(const AttnParams &p, hipStream_t stream) {
+    const int heads = p.pack ? p.G : 1;
+    const int smem = FwdGeo<T, DP, FEW>::fixed_bytes + heads * p.lut * 4 + (p.lut ? p.side * 2 : 0);
     const dim3 grid((p.nblocks + 7) / 8 * 8);
-    void (*const fn)(AttnParams) = p.threshold ? attention_forward<T, DP, true> : attention_forward<T, DP, false>;
+    void (*const fn)(AttnParams) = attention_forward<T, DP, DROP, FEW>;
     if (smem > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void *)fn, hipFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != hipSuccess) return (int)e;
@@ -164,20 +339,65 @@ int launch_dp(const AttnParams &p, hipStream_t stream) {
     return (int)hipGetLastError();
 }
 
+template <typename T, int DP>
+int launch_dp(const AttnParams &p, bool few, hipStream_t stream) {
+    if (few) return p.threshold ? launch_form<T, DP, true, true>(p, stream) : launch_form<T, DP, false, true>(p, stream);
+    return p.threshold ? launch_form<T, DP, true, false>(p, stream) : launch_form<T, DP, false, false>(p, stream);
+}
+
 template <typename T>
-int launch_t(const AttnParams &p, hipStream_t stream) {
-    if (p.D <= 32) return launch_dp<T, 32>(p, stream);
-    if (p.D <= 64) return launch_dp<T, 64>(p, stream);
-    if (p.D <= 96) return launch_dp<T, 96>(p, stream);
-    return launch_dp<T, 128>(p, stream);
+int launch_t(const AttnParams &p, bool few, hipStream_t stream) {
+    const int dp = padded_dim(p.D);
+    const int e = dp == 32   ? launch_dp<T, 32>(p, few, stream)
+                  : dp == 64 ? launch_dp<T, 64>(p, few, stream)
+                  : dp == 96 ? launch_dp<T, 96>(p, few, stream)
+                             : launch_dp<T, 128>(p, few, stream);
+    if (e || p.splits <= 1) return e;
+    const int64_t rows = (int64_t)p.B * p.H * p.Lq;
+    hipLaunchKernelGGL(attention_combine<T>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
+    return (int)hipGetLastError();
 }
 
 }  // namespace
 
-int launch_attention(const AttnParams &p, int dtype, hipStream_t stream) {
-    if (dtype == 0) return launch_t<F32>(p, stream);
-    if (dtype == 1) return launch_t<F16>(p, stream);
-    return launch_t<BF16>(p, stream);
+// The 32-row form where 128-row blocks would leave compute units without one.
+AttnPlan plan_forward(const AttnParams &p, int, bool workspace) {
+    AttnPlan a = {};
+    a.splits = 1;
+    a.units = p.B * p.H;
+    a.tiles = (p.Lq + kAttnRows - 1) / kAttnRows;
+    a.chunk = p.Lk;
+    a.few = (int64_t)a.units * a.tiles < 256;
+    if (!a.few) return a;
+    // tables of all heads that share a key head take at most 16 KiB of LDS
+    if (p.G > 1 && p.G * (int64_t)p.Lq <= 32 && (int64_t)p.G * p.lut * 4 <= 16384) {
+        a.pack = 1;
+        a.units = p.B * p.Hkv;
+    }
+    a.tiles = a.pack ? 1 : (p.Lq + 31) / 32;
+    const int64_t blocks = (int64_t)a.units * a.tiles;
+    if (!workspace || blocks >= 512 || blocks == 0) return a;
+    int64_t splits = (1024 + blocks - 1) / blocks;
+    if (splits > p.Lk / 256) splits = p.Lk / 256;    // two tiles a wave at least
+    if (splits <= 1) return a;
+    a.chunk = (int)(((p.Lk + splits - 1) / splits + 127) / 128 * 128);
+    a.splits = (p.Lk + a.chunk - 1) / a.chunk;
+    a.split_floats = (int64_t)a.splits * p.B * p.H * p.Lq * (split_row(p.D) + 2);
+    return a;
+}
+
+int launch_attention(const AttnParams &p0, int dtype, hipStream_t stream) {
+    AttnParams p = p0;
+    const AttnPlan a = plan_forward(p, dtype, p.split != nullptr);
+    p.pack = a.pack;
+    p.splits = a.splits;
+    p.chunk = a.chunk;
+    p.tiles = a.tiles;
+    p.units = a.units;
+    p.nblocks = a.units * a.tiles * a.splits;
+    if (dtype == 0) return launch_t<F32>(p, a.few, stream);
+    if (dtype == 1) return launch_t<F16>(p, a.few, stream);
+    return launch_t<BF16>(p, a.few, stream);
 }
 
 }  // namespace gs

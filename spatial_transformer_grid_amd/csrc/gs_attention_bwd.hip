@@ -11,14 +11,14 @@
 // and a fixed order of summation; the price is the scores and dO V^T twice,
 // seven products in place of the five of a single pass that would add dQ with
 // atomics, in an order that varies.
+//
+// keep_scale is left out of dS until the last scaling: M is then 0 or 1 and
+// delta is divided by keep_scale.
 #include "gs_tokens.hpp"
 
 namespace gs {
 
 namespace {
-
-constexpr int kKeys = 64;      // keys of an LDS tile (dQ)
-constexpr int kRows = 64;      // queries of an LDS tile (dK, dV)
 
 // Sums of dS by distance, per wave: one copy for each half of the wave, so
 // that no two lanes of an instruction add to one address (the lanes of a half
@@ -27,10 +27,17 @@ constexpr int kRows = 64;      // queries of an LDS tile (dK, dV)
 // do not depend on timing.
 __host__ __device__ constexpr int near_pitch(int lut) { return (lut + 31) / 64 * 64 + 32; }
 
-template <typename T, int DP>
+// Geometry of both kernels: `ROWS` rows of the axis that is walked in an LDS
+// tile, two buffers of two tensors, or one of each wave's own (FEW).
+template <typename T, int DP, bool FEW>
 struct BwdGeo {
+    static constexpr int ROWS = FEW || T::bytes == 4 || DP > 64 ? 32 : 64;
     static constexpr int PITCH = DP + 16 / T::bytes;
-    static constexpr int tile_bytes = 2 * kKeys * PITCH * T::bytes;
+    static constexpr int tile_elems = ROWS * PITCH;
+    static constexpr int copies = FEW ? 4 : 2;
+    static constexpr int tile_bytes = copies * 2 * tile_elems * T::bytes;
+    static constexpr int SUM = DP + 4;
+    static_assert(!FEW || 4 * 32 * SUM * 4 <= tile_bytes, "the waves' sums take the tiles' place");
 };
 
 __device__ __forceinline__ void lds_add(float *p, float v) {
@@ -43,39 +50,64 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
-template <typename T, int DP, bool DROP>
-__global__ __launch_bounds__(256) void attention_backward_q(AttnParams p) {
+// A wave's 32-row result (transposed: the lane's column is its row) into LDS.
+template <int DP, int SUM>
+__device__ __forceinline__ void put_sums(float *sums, const f32x16 *acc, int wave, int lane) {
+    float *mine = sums + (wave * 32 + (lane & 31)) * SUM + 4 * (lane >> 5);
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+            *(tokens_f32x4 *)(mine + 32 * d + 2 * r) =
+                tokens_f32x4{acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]};
+}
+
+template <int SUM>
+__device__ __forceinline__ tokens_f32x4 add_sums(const float *sums, int r, int at) {
+    tokens_f32x4 v = *(const tokens_f32x4 *)(sums + r * SUM + at);
+#pragma unroll
+    for (int w = 1; w < 4; ++w) v += *(const tokens_f32x4 *)(sums + (w * 32 + r) * SUM + at);
+    return v;
+}
+
+template <typename T, int DP, bool DROP, bool FEW>
+__global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnParams p) {
     typedef typename T::raw_t raw_t;
-    typedef BwdGeo<T, DP> Geo;
-    constexpr int PITCH = Geo::PITCH;
+    typedef BwdGeo<T, DP, FEW> Geo;
+    constexpr int PITCH = Geo::PITCH, KEYS = Geo::ROWS, NT = FEW ? 64 : 256;
     extern __shared__ __align__(16) unsigned char smem[];
-    raw_t *Ks = (raw_t *)smem;
-    raw_t *Vs = Ks + kKeys * PITCH;
     float *lut = (float *)(smem + Geo::tile_bytes);
     const int pitch = near_pitch(p.lut);
     float *near = lut + (p.lut + 3) / 4 * 4;         // [wave][half][pitch]
-    float *far = near + (p.lut ? 8 * pitch : 0);     // [wave][2]
+    float *far = near + (p.part ? 8 * pitch : 0);    // [wave][2]
     uint16_t *starts = (uint16_t *)(far + 8);
 
-    const int lb = xcd_contiguous_block(p.nblocks);
-    if (lb >= p.nblocks) return;
-    int tile = lb % p.tiles;
-    const int bh = lb / p.tiles;
-    if (p.causal) tile = p.tiles - 1 - tile;
-    const int b = bh / p.H, h = bh - b * p.H, hk = h / p.G;
+    int unit, tile, part;
+    if (!block_place(p, !FEW, unit, tile, part)) return;
+    const int b = unit / p.H, h = unit - b * p.H, hk = h / p.G;
     const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int len = sequence_length(p, b);
     const int first = p.from_end ? len - p.Lq : p.first;
-    const int q0 = tile * kAttnQueries + wave * 32;
+    const int q0 = FEW ? tile * 32 : tile * kAttnRows + wave * 32;
     const int qi = q0 + (lane & 31);
     const int pos = first + qi;
-    const int block_last = first + min((tile + 1) * kAttnQueries, p.Lq) - 1;
+    const int block_last = first + min(FEW ? q0 + 32 : (tile + 1) * kAttnRows, p.Lq) - 1;
     const int end = p.causal ? min(len, block_last + 1) : len;
+    const int wave_first = first + q0, wave_last = wave_first + 31;
+    const int begin = FEW ? wave * KEYS : 0;
+    constexpr int STEP = FEW ? 4 * KEYS : KEYS;
     const bool vec = p.vec, live = qi < p.Lq;
 
     const raw_t *kb = (const raw_t *)p.k + (int64_t)b * p.ks[0] + (int64_t)hk * p.ks[1];
     const raw_t *vb = (const raw_t *)p.v + (int64_t)b * p.vs[0] + (int64_t)hk * p.vs[1];
+    const int tt = FEW ? lane : t;
+    raw_t *Kt = (raw_t *)smem + (FEW ? wave * 2 * Geo::tile_elems : 0);
+    TileCopy<T, DP, KEYS, NT, PITCH> kc, vc;
+    if (begin < end) {
+        kc.fetch(kb, p.ks[2], begin, end, p.D, vec, tt);
+        vc.fetch(vb, p.vs[2], begin, end, p.D, vec, tt);
+    }
     Frag<T> qf[DP / 16], gf[DP / 16];
     float delta = 0.0f;
     {
@@ -96,18 +128,26 @@ __global__ __launch_bounds__(256) void attention_backward_q(AttnParams p) {
         }
     }
     delta += __shfl_xor(delta, 32);
-    float lse2 = INFINITY;                           // 2^(s - inf) = 0: no key seen
+    float minus_lse = -INFINITY;                     // 2^(s - inf) = 0: no key seen
     if (live) {
-        const int64_t at = (int64_t)bh * p.Lq + qi;
+        const int64_t at = (int64_t)unit * p.Lq + qi;
         const float v = p.lse[at];
-        if (v != -INFINITY) lse2 = v * kLog2e;
-        if (half == 0) p.delta[at] = delta;
+        if (v != -INFINITY) minus_lse = -v * kLog2e;
+        if (half == 0 && (!FEW || wave == 0)) p.delta[at] = delta;
     }
+    delta = delta / p.keep_scale;
+    float bias_lo = 0.0f, bias_hi = 0.0f;
     if (p.lut) {
+        for (int i = t; i < p.side; i += 256) starts[i] = p.starts[i];
+        if (p.part)
+            for (int i = t; i < 8 * pitch; i += 256) near[i] = 0.0f;
+        __syncthreads();
         fill_lut<T>(p, h, lut, starts, t, 256);
-        for (int i = t; i < 8 * pitch; i += 256) near[i] = 0.0f;
+        __syncthreads();
+        bias_lo = lut[0];
+        bias_hi = lut[p.lut - 1];
     }
-    float far_lo = 0.0f, far_hi = 0.0f;              // distances at or past the borders
+    float far_lo = 0.0f, far_hi = 0.0f;              // distances at or past the last change
     float *mine = near + (wave * 2 + half) * pitch;
 
     f32x16 acc[DP / 32];
@@ -116,20 +156,23 @@ __global__ __launch_bounds__(256) void attention_backward_q(AttnParams p) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
 
-    TileCopy<T, DP, kKeys, 256, PITCH> copy;
-    for (int k0 = 0; k0 < end; k0 += kKeys) {
-        __syncthreads();
-        copy.fetch(kb, p.ks[2], k0, end, p.D, vec, t);
-        copy.put(Ks, t);
-        copy.fetch(vb, p.vs[2], k0, end, p.D, vec, t);
-        copy.put(Vs, t);
-        __syncthreads();
-        const int wave_first = first + q0, wave_last = wave_first + 31;
-        if (q0 >= p.Lq) continue;
+    if (begin < end) {
+        kc.put(Kt, tt);
+        vc.put(Kt + Geo::tile_elems, tt);
+    }
+    for (int k0 = begin, n = 0; k0 < end; k0 += STEP, ++n) {
+        const raw_t *Ks = Kt + (FEW ? 0 : (n & 1) * 2 * Geo::tile_elems);
+        const raw_t *Vs = Ks + Geo::tile_elems;
+        tile_sync<FEW>();
+        const bool more = k0 + STEP < end;
+        if (more) {
+            kc.fetch(kb, p.ks[2], k0 + STEP, end, p.D, vec, tt);
+            vc.fetch(vb, p.vs[2], k0 + STEP, end, p.D, vec, tt);
+        }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < KEYS / 32; ++u) {
             const int ku = k0 + 32 * u;              // this 32-key part
-            if (ku >= end || (p.causal && ku > wave_last)) continue;
+            if (q0 >= p.Lq || ku >= end || (p.causal && ku > wave_last)) continue;
             f32x16 st, dp;
 #pragma unroll
             for (int r = 0; r < 16; ++r) st[r] = dp[r] = 0.0f;
@@ -140,43 +183,50 @@ __global__ __launch_bounds__(256) void attention_backward_q(AttnParams p) {
                 mma<T>(dp, frag_lds<T>(Vs + row + 16 * x), gf[x]);
             }
             const int key0 = ku + 8 * half;
+            const int cls = bias_class(p, ku - wave_last, ku + 31 - wave_first);
+            float e[16];
+            if (cls == 0) {
+                const float *at = lut + (key0 - pos + p.border + kLutPad);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    e[i] = __builtin_amdgcn_exp2f(fmaf(st[i], p.scale2, at[16 * (i >> 3) + (i & 7)]) + minus_lse);
+            } else {
+                const float c = minus_lse + (cls == 1 ? bias_lo : cls == 2 ? bias_hi : 0.0f);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(st[i], p.scale2, c));
+            }
             float ds[16];
-            const bool edge = ku + 32 > end || (p.causal && ku + 31 > wave_first);
-            const int seen = p.causal ? min(end, pos + 1) : end;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 u32x4 rnd;
                 if constexpr (DROP)
-                    rnd = philox((uint32_t)(key0 + 16 * x) >> 3, (uint32_t)qi, (uint32_t)bh, p.call, p.seed_lo,
+                    rnd = philox((uint32_t)(key0 + 16 * x) >> 3, (uint32_t)qi, (uint32_t)unit, p.call, p.seed_lo,
                                  p.seed_hi);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int i = 8 * x + j, key = key0 + 16 * x + j;
-                    float s = st[i] * p.scale2;
-                    if (p.lut) s = fmaf(st[i], p.scale2, lut[lut_index(p, key - pos)]);
-                    float e = __builtin_amdgcn_exp2f(s - lse2);
-                    if (edge && key >= seen) e = 0.0f;
+                    const int i = 8 * x + j;
                     float g = dp[i];
-                    if constexpr (DROP) g = kept(rnd, j, p.threshold) ? g * p.keep_scale : 0.0f;
-                    ds[i] = e * (g - delta);
+                    if constexpr (DROP) g = kept(rnd, j, p.threshold) ? g : 0.0f;
+                    ds[i] = e[i] * (g - delta);
                 }
             }
-            if (p.lut) {
-                const int rel_lo = ku - wave_last, rel_hi = ku + 31 - wave_first;
-                float sum = 0.0f;
-                if (rel_lo >= p.lut - p.border || rel_hi <= -p.border) {
+            if (ku + 32 > end || (p.causal && ku + 31 > wave_first)) {
+                const int seen = (p.causal ? min(end, pos + 1) : end) - key0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (16 * (i >> 3) + (i & 7) >= seen) ds[i] = 0.0f;
+            }
+            if (p.part) {
+                if (cls == 0) {
+                    float *at = mine + (key0 - pos + p.border + kLutPad);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) lds_add(at + 16 * (i >> 3) + (i & 7), ds[i]);
+                } else {
+                    float sum = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) sum += (ds[i] + ds[i + 1]) + (ds[i + 2] + ds[i + 3]);
-                    if (rel_hi <= -p.border) far_lo += sum;
+                    if (cls == 1) far_lo += sum;
                     else far_hi += sum;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int at = key0 + 16 * (i >> 3) + (i & 7) - pos + p.border;
-                        if (at <= 0) far_lo += ds[i];
-                        else if (at >= p.lut - (p.bidirectional ? 1 : 0)) far_hi += ds[i];
-                        else lds_add(mine + at, ds[i]);
-                    }
                 }
             }
 #pragma unroll
@@ -187,17 +237,39 @@ __global__ __launch_bounds__(256) void attention_backward_q(AttnParams p) {
                     mma<T>(acc[d], frag_lds_transposed<T, PITCH>(Ks, 32 * u + 16 * x, 32 * d, lane), df);
             }
         }
+        if (more) {
+            if (FEW) tile_sync<true>();
+            raw_t *next = Kt + (FEW ? 0 : ((n + 1) & 1) * 2 * Geo::tile_elems);
+            kc.put(next, tt);
+            vc.put(next + Geo::tile_elems, tt);
+        }
     }
-    if (live) {
-        raw_t *drow = (raw_t *)p.dq + (int64_t)b * p.dqs[0] + (int64_t)h * p.dqs[1] + (int64_t)qi * p.dqs[2];
+    const float scale = p.scale * p.keep_scale;
+    if constexpr (!FEW) {
+        if (live) {
+            raw_t *drow = (raw_t *)p.dq + (int64_t)b * p.dqs[0] + (int64_t)h * p.dqs[1] + (int64_t)qi * p.dqs[2];
 #pragma unroll
-        for (int d = 0; d < DP / 32; ++d)
+            for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
-            for (int r = 0; r < 16; r += 4)
-                store4<T>(drow, 32 * d + 2 * r + 4 * half, p.D, vec, acc[d][r] * p.scale, acc[d][r + 1] * p.scale,
-                          acc[d][r + 2] * p.scale, acc[d][r + 3] * p.scale);
+                for (int r = 0; r < 16; r += 4)
+                    store4<T>(drow, 32 * d + 2 * r + 4 * half, p.D, vec, acc[d][r] * scale, acc[d][r + 1] * scale,
+                              acc[d][r + 2] * scale, acc[d][r + 3] * scale);
+        }
+    } else {
+        float *sums = (float *)smem;
+        __syncthreads();
+        put_sums<DP, Geo::SUM>(sums, acc, wave, lane);
+        __syncthreads();
+        for (int i = t; i < 32 * (DP / 4); i += 256) {
+            const int r = i / (DP / 4), at = (i - r * (DP / 4)) * 4;
+            if (q0 + r >= p.Lq) continue;
+            const tokens_f32x4 v = add_sums<Geo::SUM>(sums, r, at);
+            raw_t *drow =
+                (raw_t *)p.dq + (int64_t)b * p.dqs[0] + (int64_t)h * p.dqs[1] + (int64_t)(q0 + r) * p.dqs[2];
+            store4<T>(drow, at, p.D, vec, v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
+        }
     }
-    if (!p.lut || !p.part) return;
+    if (!p.part) return;
     far_lo = wave_sum(far_lo);
     far_hi = wave_sum(far_hi);
     if (lane == 0) {
@@ -205,52 +277,50 @@ __global__ __launch_bounds__(256) void attention_backward_q(AttnParams p) {
         far[wave * 2 + 1] = far_hi;
     }
     __syncthreads();
-    // bucket n of a side holds distances starts[n] .. starts[n + 1] - 1; the
-    // last one lies wholly in the far sums.  Without the other side a key
-    // after the query counts as distance 0 (the far sum of that direction).
+    // bucket n of a side holds distances starts[n] .. starts[n + 1] - 1, the
+    // last one all that follow.  Without the other side a key after the query
+    // counts as distance 0.
     float *out = p.part + (((int64_t)h * p.B + b) * p.tiles + tile) * p.buckets;
     for (int n = t; n < p.buckets; n += 256) {
         const bool after = n >= p.side;              // the side of keys after the query
         const int m = after ? n - p.side : n;
+        const bool last = m == p.side - 1;
         float sum = 0.0f;
-        if (m == p.side - 1) {
+        if (last)
             for (int w = 0; w < 4; ++w) sum += far[2 * w + (after ? 1 : 0)];
-        } else {
-            for (int d = max((int)starts[m], after ? 1 : 0); d < (int)starts[m + 1]; ++d) {
-                const int at = p.border + (after ? d : -d);
-                for (int w = 0; w < 8; ++w) sum += near[w * pitch + at];
-            }
-        }
-        if (!p.bidirectional && m == 0)
+        const int lo = max((int)starts[m], after ? 1 : 0), hi = last ? p.border + kLutPad + 1 : starts[m + 1];
+        for (int d = lo; d < hi; ++d)
+            for (int w = 0; w < 8; ++w) sum += near[w * pitch + p.border + kLutPad + (after ? d : -d)];
+        if (!p.bidirectional && m == 0) {
             for (int w = 0; w < 4; ++w) sum += far[2 * w + 1];
-        out[n] = sum;
+            for (int d = 1; d <= kLutPad; ++d)
+                for (int w = 0; w < 8; ++w) sum += near[w * pitch + p.border + kLutPad + d];
+        }
+        out[n] = sum * p.keep_scale;
     }
 }
 
-template <typename T, int DP, bool DROP>
-__global__ __launch_bounds__(256) void attention_backward_kv(AttnParams p) {
+template <typename T, int DP, bool DROP, bool FEW>
+__global__ __launch_bounds__(256, FEW || T::bytes == 4 ? 1 : 2) void attention_backward_kv(AttnParams p) {
     typedef typename T::raw_t raw_t;
-    typedef BwdGeo<T, DP> Geo;
-    constexpr int PITCH = Geo::PITCH;
+    typedef BwdGeo<T, DP, FEW> Geo;
+    constexpr int PITCH = Geo::PITCH, ROWS = Geo::ROWS, NT = FEW ? 64 : 256;
     extern __shared__ __align__(16) unsigned char smem[];
-    raw_t *Qs = (raw_t *)smem;
-    raw_t *Gs = Qs + kRows * PITCH;
-    float *lse2s = (float *)(smem + Geo::tile_bytes);
-    float *deltas = lse2s + kRows;
-    unsigned char *masks = (unsigned char *)(deltas + kRows);   // [wave][4][32]
+    // per copy of a tile: minus lse without and with the biases of the two ends, delta
+    float *row_stats = (float *)(smem + Geo::tile_bytes);
+    unsigned char *masks = (unsigned char *)(row_stats + Geo::copies * 4 * ROWS);   // [wave][4][32]
     float *lut = (float *)(masks + 512);
     uint16_t *starts = (uint16_t *)(lut + (p.lut + 3) / 4 * 4);
 
-    const int lb = xcd_contiguous_block(p.nblocks);
-    if (lb >= p.nblocks) return;
-    const int tile = lb % p.tiles;
-    const int bk = lb / p.tiles;
-    const int b = bk / p.Hkv, hk = bk - b * p.Hkv;
+    int unit, tile, part;
+    if (!block_place(p, false, unit, tile, part)) return;
+    const int b = unit / p.Hkv, hk = unit - b * p.Hkv;
     const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int len = sequence_length(p, b);
     const int first = p.from_end ? len - p.Lq : p.first;
-    const int k0 = tile * kAttnQueries + wave * 32;
+    const int block0 = FEW ? tile * 32 : tile * kAttnRows;
+    const int k0 = FEW ? block0 : block0 + wave * 32;
     const int key = k0 + (lane & 31);
     const bool vec = p.vec, live = key < len;
 
@@ -269,43 +339,78 @@ __global__ __launch_bounds__(256) void attention_backward_kv(AttnParams p) {
     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dk[d][r] = dv[d][r] = 0.0f;
+    if (p.lut)
+        for (int i = t; i < p.side; i += 256) starts[i] = p.starts[i];
 
-    // queries before q_begin see no key of this block
-    const int q_begin =
-        p.causal ? max(0, tile * kAttnQueries - first) / kRows * kRows : 0;
-    const int q_end = tile * kAttnQueries < len ? p.Lq : 0;
-    TileCopy<T, DP, kRows, 256, PITCH> copy;
+    // queries before q_begin see no key of this block; the block's part is a
+    // range of the (head, query tile) pairs that are left
+    const int q_begin = p.causal ? max(0, block0 - first) / ROWS * ROWS : 0;
+    const int q_tiles = block0 < len && q_begin < p.Lq ? (p.Lq - q_begin + ROWS - 1) / ROWS : 0;
+    const int64_t pairs = (int64_t)p.G * q_tiles;
+    const int64_t p0 = pairs * part / p.splits, p1 = pairs * (part + 1) / p.splits;
+    const int tt = FEW ? lane : t;
+    raw_t *Qt = (raw_t *)smem + (FEW ? wave * 2 * Geo::tile_elems : 0);
+    float *stats = row_stats + (FEW ? wave * 4 * ROWS : 0);
+    unsigned char *mask = masks + wave * 128;
+    TileCopy<T, DP, ROWS, NT, PITCH> qc, gc;
+    const float keep_inv = 1.0f / p.keep_scale;
+
     for (int g = 0; g < p.G; ++g) {
+        const int64_t base = (int64_t)g * q_tiles;
+        const int t0 = (int)max(p0 - base, (int64_t)0), t1 = (int)min(p1 - base, (int64_t)q_tiles);
+        if (t0 >= t1) continue;
         const int h = hk * p.G + g, bh = b * p.H + h;
         const raw_t *qb = (const raw_t *)p.q + (int64_t)b * p.qs[0] + (int64_t)h * p.qs[1];
         const raw_t *gb = (const raw_t *)p.d_o + (int64_t)b * p.dos[0] + (int64_t)h * p.dos[1];
+        __syncthreads();
+        float bias_lo = 0.0f, bias_hi = 0.0f;
         if (p.lut) {
-            __syncthreads();
             fill_lut<T>(p, h, lut, starts, t, 256);
+            __syncthreads();
+            bias_lo = lut[0];
+            bias_hi = lut[p.lut - 1];
         }
-        for (int q0 = q_begin; q0 < q_end; q0 += kRows) {
-            __syncthreads();
-            copy.fetch(qb, p.qs[2], q0, p.Lq, p.D, vec, t);
-            copy.put(Qs, t);
-            copy.fetch(gb, p.dos[2], q0, p.Lq, p.D, vec, t);
-            copy.put(Gs, t);
-            if (t < kRows) {
-                const int64_t at = (int64_t)bh * p.Lq + q0 + t;
-                float e = INFINITY, d = 0.0f;
-                if (q0 + t < p.Lq) {
-                    const float v = p.lse[at];
-                    if (v != -INFINITY) e = v * kLog2e;
-                    d = p.delta[at];
-                }
-                lse2s[t] = e;
-                deltas[t] = d;
+        float lse = 0.0f, delta = 0.0f;              // of row tt of the tile in flight
+        const auto fetch = [&](int q0) {
+            qc.fetch(qb, p.qs[2], q0, p.Lq, p.D, vec, tt);
+            gc.fetch(gb, p.dos[2], q0, p.Lq, p.D, vec, tt);
+            if (tt < ROWS) {
+                const bool in = q0 + tt < p.Lq;
+                const int64_t at = (int64_t)bh * p.Lq + q0 + tt;
+                lse = in ? p.lse[at] : -INFINITY;
+                delta = in ? p.delta[at] : 0.0f;
             }
-            __syncthreads();
-            if (k0 >= len) continue;
+        };
+        const auto put = [&](int copy) {
+            raw_t *to = Qt + copy * 2 * Geo::tile_elems;
+            qc.put(to, tt);
+            gc.put(to + Geo::tile_elems, tt);
+            if (tt < ROWS) {
+                float *s = stats + copy * 4 * ROWS;
+                const float e = lse == -INFINITY ? -INFINITY : -lse * kLog2e;   // 2^(s - inf) = 0: no key seen
+                s[tt] = e;
+                s[ROWS + tt] = e + bias_lo;
+                s[2 * ROWS + tt] = e + bias_hi;
+                s[3 * ROWS + tt] = delta * keep_inv;
+            }
+        };
+        constexpr int STEP = FEW ? 4 : 1;
+        const int begin = FEW ? t0 + wave : t0;
+        if (begin < t1) {
+            fetch(q_begin + begin * ROWS);
+            put(0);
+        }
+        for (int n = begin, it = 0; n < t1; n += STEP, ++it) {
+            const int q0 = q_begin + n * ROWS, copy = FEW ? 0 : it & 1;
+            const raw_t *Qs = Qt + copy * 2 * Geo::tile_elems, *Gs = Qs + Geo::tile_elems;
+            const float *rs = stats + copy * 4 * ROWS;
+            tile_sync<FEW>();
+            const bool more = n + STEP < t1;
+            if (more) fetch(q0 + STEP * ROWS);
 #pragma unroll
-            for (int u = 0; u < kRows / 32; ++u) {
+            for (int u = 0; u < ROWS / 32; ++u) {
                 const int qu = q0 + 32 * u;          // this 32-query part
-                if (qu >= p.Lq || (p.causal && first + qu + 31 < k0)) continue;
+                if (k0 >= len || qu >= p.Lq || (p.causal && first + qu + 31 < k0)) continue;
                 f32x16 st, dp;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) st[r] = dp[r] = 0.0f;
@@ -315,48 +420,55 @@ __global__ __launch_bounds__(256) void attention_backward_kv(AttnParams p) {
                     mma<T>(st, frag_lds<T>(Qs + row + 16 * x), kf[x]);
                     mma<T>(dp, frag_lds<T>(Gs + row + 16 * x), vf[x]);
                 }
-                unsigned char *mask = masks + wave * 128;
                 if constexpr (DROP) {
                     // this lane's two calls: query qu + lane % 32, keys
                     // k0 + 16 half .. + 15; one byte of kept bits each
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    tile_sync<true>();
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const int oct = 2 * half + n;
+                    for (int n2 = 0; n2 < 2; ++n2) {
+                        const int oct = 2 * half + n2;
                         const u32x4 rnd = philox((uint32_t)(k0 >> 3) + oct, (uint32_t)(qu + (lane & 31)),
                                                  (uint32_t)bh, p.call, p.seed_lo, p.seed_hi);
-                        uint32_t bits = 0;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) bits |= kept(rnd, j, p.threshold) ? 1u << j : 0u;
-                        mask[oct * 32 + (lane & 31)] = (unsigned char)bits;
+                        mask[oct * 32 + (lane & 31)] = (unsigned char)kept_byte(rnd, (p.threshold - 1) * 0x10001u);
                     }
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                    __builtin_amdgcn_wave_barrier();
+                    tile_sync<true>();
                 }
+                const int cls = bias_class(p, k0 - (first + qu + 31), k0 + 31 - (first + qu));
                 const bool edge = k0 + 32 > len || (p.causal && first + qu < k0 + 31);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int r0 = 32 * u + 16 * x + 8 * half;   // this lane's eight queries
-                    const int pos0 = first + q0 + r0;
-                    u32x2 bits = {0, 0};
-                    if constexpr (DROP)
-                        bits = *(const u32x2 *)(mask + ((lane & 31) >> 3) * 32 + 16 * x + 8 * half);
+                    const float *ml = rs + (cls == 1 ? ROWS : cls == 2 ? 2 * ROWS : 0) + r0;
+                    const float *dl = rs + 3 * ROWS + r0;
                     float pd[8], ds[8];
+                    if (cls == 0) {
+                        const float *at = lut + (key - first - q0 - r0 + p.border + kLutPad);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int i = 8 * x + j;
-                        float s = st[i] * p.scale2;
-                        if (p.lut) s = fmaf(st[i], p.scale2, lut[lut_index(p, key - (pos0 + j))]);
-                        float e = __builtin_amdgcn_exp2f(s - lse2s[r0 + j]);
-                        if (edge && (key >= len || (p.causal && key > pos0 + j))) e = 0.0f;
-                        float g = dp[i], f = e;
-                        if constexpr (DROP) {
-                            const bool keep = bits[j >> 2] >> (8 * (j & 3) + (lane & 7)) & 1u;
-                            g = keep ? g * p.keep_scale : 0.0f;
-                            f = keep ? e : 0.0f;
+                        for (int j = 0; j < 8; ++j) pd[j] = fmaf(st[8 * x + j], p.scale2, at[-j]) + ml[j];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) pd[j] = fmaf(st[8 * x + j], p.scale2, ml[j]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) pd[j] = __builtin_amdgcn_exp2f(pd[j]);
+                    if constexpr (DROP) {
+                        u32x2 bits = *(const u32x2 *)(mask + ((lane & 31) >> 3) * 32 + 16 * x + 8 * half);
+                        bits = (bits >> (uint32_t)(lane & 7)) & 0x01010101u;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float keep = (float)(bits[j >> 2] >> (8 * (j & 3)) & 0xffu);
+                            ds[j] = pd[j] * fmaf(dp[8 * x + j], keep, -dl[j]);
+                            pd[j] *= keep;
                         }
-                        pd[j] = f;
-                        ds[j] = e * (g - deltas[r0 + j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) ds[j] = pd[j] * (dp[8 * x + j] - dl[j]);
+                    }
+                    if (edge) {
+                        const int hidden = p.causal ? key - (first + q0 + r0) : 0;   // queries before the key
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (!live || j < hidden) pd[j] = ds[j] = 0.0f;
                     }
                     const Frag<T> pf = frag_pack<T>(pd), df = frag_pack<T>(ds);
 #pragma unroll
@@ -366,20 +478,82 @@ __global__ __launch_bounds__(256) void attention_backward_kv(AttnParams p) {
                     }
                 }
             }
+            if (more) {
+                if (FEW) tile_sync<true>();
+                put(FEW ? 0 : (it + 1) & 1);
+            }
         }
     }
-    if (key >= p.Lk) return;
-    raw_t *dkrow = (raw_t *)p.dk + (int64_t)b * p.dks[0] + (int64_t)hk * p.dks[1] + (int64_t)key * p.dks[2];
-    raw_t *dvrow = (raw_t *)p.dv + (int64_t)b * p.dvs[0] + (int64_t)hk * p.dvs[1] + (int64_t)key * p.dvs[2];
-    const float sk = p.scale, sv = p.keep_scale;
+    const float sk = p.scale * p.keep_scale, sv = p.keep_scale;
+    if constexpr (FEW) {
+        float *sums = (float *)smem;
 #pragma unroll
-    for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-            const int col = 32 * d + 2 * r + 4 * half;
-            store4<T>(dkrow, col, p.D, vec, dk[d][r] * sk, dk[d][r + 1] * sk, dk[d][r + 2] * sk, dk[d][r + 3] * sk);
-            store4<T>(dvrow, col, p.D, vec, dv[d][r] * sv, dv[d][r + 1] * sv, dv[d][r + 2] * sv, dv[d][r + 3] * sv);
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+            put_sums<DP, Geo::SUM>(sums, which ? dv : dk, wave, lane);
+            __syncthreads();
+            const float scale = which ? sv : sk;
+            const int64_t *s = which ? p.dvs : p.dks;
+            raw_t *to = (raw_t *)(which ? p.dv : p.dk) + (int64_t)b * s[0] + (int64_t)hk * s[1];
+            for (int i = t; i < 32 * (DP / 4); i += 256) {
+                const int r = i / (DP / 4), at = (i - r * (DP / 4)) * 4;
+                if (k0 + r >= p.Lk) continue;
+                const tokens_f32x4 v = add_sums<Geo::SUM>(sums, r, at);
+                store4<T>(to + (int64_t)(k0 + r) * s[2], at, p.D, vec, v[0] * scale, v[1] * scale, v[2] * scale,
+                          v[3] * scale);
+            }
         }
+    } else {
+        if (key >= p.Lk) return;
+        if (p.splits > 1) {
+            // this part's sums: (part, b, hk, key), dK then dV
+            const int dr = split_row(p.D);
+            float *out = p.split + (((int64_t)part * p.units + unit) * p.Lk + key) * 2 * dr;
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4) {
+                    const int col = 32 * d + 2 * r + 4 * half;
+                    if (col >= p.D) continue;
+                    *(tokens_f32x4 *)(out + col) = tokens_f32x4{dk[d][r], dk[d][r + 1], dk[d][r + 2], dk[d][r + 3]};
+                    *(tokens_f32x4 *)(out + dr + col) =
+                        tokens_f32x4{dv[d][r], dv[d][r + 1], dv[d][r + 2], dv[d][r + 3]};
+                }
+            return;
+        }
+        raw_t *dkrow = (raw_t *)p.dk + (int64_t)b * p.dks[0] + (int64_t)hk * p.dks[1] + (int64_t)key * p.dks[2];
+        raw_t *dvrow = (raw_t *)p.dv + (int64_t)b * p.dvs[0] + (int64_t)hk * p.dvs[1] + (int64_t)key * p.dvs[2];
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const int col = 32 * d + 2 * r + 4 * half;
+                store4<T>(dkrow, col, p.D, vec, dk[d][r] * sk, dk[d][r + 1] * sk, dk[d][r + 2] * sk,
+                          dk[d][r + 3] * sk);
+                store4<T>(dvrow, col, p.D, vec, dv[d][r] * sv, dv[d][r + 1] * sv, dv[d][r + 2] * sv,
+                          dv[d][r + 3] * sv);
+            }
+    }
+}
+
+// dK and dV from the sums of the parts, added in their order: a thread takes
+// four columns of a row.
+template <typename T>
+__global__ __launch_bounds__(256) void attention_backward_join(AttnParams p) {
+    typedef typename T::raw_t raw_t;
+    const int dr = split_row(p.D), quads = 2 * dr / 4;
+    const int64_t rows = (int64_t)p.units * p.Lk, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = i / quads;
+    if (row >= rows) return;
+    const int at = (int)(i - row * quads) * 4;
+    tokens_f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < p.splits; ++s) v += *(const tokens_f32x4 *)(p.split + (s * rows + row) * 2 * dr + at);
+    const bool second = at >= dr;
+    const float scale = second ? p.keep_scale : p.scale * p.keep_scale;
+    const int64_t unit = row / p.Lk, key = row - unit * p.Lk, b = unit / p.Hkv, hk = unit - b * p.Hkv;
+    const int64_t *st = second ? p.dvs : p.dks;
+    raw_t *to = (raw_t *)(second ? p.dv : p.dk) + b * st[0] + hk * st[1] + key * st[2];
+    store4<T>(to, second ? at - dr : at, p.D, p.vec, v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
 }
 
 // dtable[n][h]: the sums of one head over sequences and query tiles, in
@@ -403,58 +577,125 @@ __global__ __launch_bounds__(256) void attention_backward_table(AttnParams p) {
     else ((typename T::raw_t *)p.dtable)[at] = to_bits<T>(v);
 }
 
-int big_lds(void (*fn)(AttnParams), int smem) {
-    return smem > 65536
-               ? (int)hipFuncSetAttribute((const void *)fn, hipFuncAttributeMaxDynamicSharedMemorySize, smem)
-               : 0;
+template <typename T, int DP, bool FEW>
+int q_lds(const AttnParams &p, bool table) {
+    return BwdGeo<T, DP, FEW>::tile_bytes + (p.lut + 3) / 4 * 16 + (table ? 8 * near_pitch(p.lut) * 4 : 0) + 32 +
+           p.side * 2;
+}
+
+template <typename T, int DP, bool FEW>
+int kv_lds(const AttnParams &p) {
+    return BwdGeo<T, DP, FEW>::tile_bytes + BwdGeo<T, DP, FEW>::copies * 4 * BwdGeo<T, DP, FEW>::ROWS * 4 + 512 +
+           (p.lut + 3) / 4 * 16 + p.side * 2;
+}
+
+int launch(void (*fn)(AttnParams), const AttnParams &p, int smem, hipStream_t stream) {
+    if (smem > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void *)fn, hipFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != hipSuccess) return (int)e;
+    }
+    hipLaunchKernelGGL(fn, dim3((p.nblocks + 7) / 8 * 8), dim3(256), smem, stream, p);
+    return (int)hipGetLastError();
+}
+
+void take_plan(AttnParams &p, const AttnPlan &a) {
+    p.splits = a.splits;
+    p.tiles = a.tiles;
+    p.units = a.units;
+    p.nblocks = a.units * a.tiles * a.splits;
 }
 
 template <typename T, int DP>
-int launch_dp(const AttnParams &p0, hipStream_t stream) {
+int launch_dp(const AttnParams &p0, int dtype, hipStream_t stream) {
     AttnParams p = p0;
-    const int lut = p.lut ? (p.lut + 3) / 4 * 16 : 0;
-    if (p.Lq > 0) {
-        p.tiles = (p.Lq + kAttnQueries - 1) / kAttnQueries;
-        p.nblocks = p.B * p.H * p.tiles;
-        const int smem = BwdGeo<T, DP>::tile_bytes + lut + (p.lut ? 8 * near_pitch(p.lut) * 4 : 0) + 32 + p.side * 2;
-        void (*const fn)(AttnParams) =
-            p.threshold ? attention_backward_q<T, DP, true> : attention_backward_q<T, DP, false>;
-        if (const int e = big_lds(fn, smem)) return e;
-        hipLaunchKernelGGL(fn, dim3((p.nblocks + 7) / 8 * 8), dim3(256), smem, stream, p);
-        if (const int e = (int)hipGetLastError()) return e;
+    const bool drop = p.threshold != 0;
+    AttnPlan a = plan_backward_q(p, dtype);
+    take_plan(p, a);
+    if (p.nblocks > 0) {
+        const bool table = p.part != nullptr;
+        const int e = a.few ? launch(drop ? attention_backward_q<T, DP, true, true> : attention_backward_q<T, DP, false, true>,
+                                     p, q_lds<T, DP, true>(p, table), stream)
+                            : launch(drop ? attention_backward_q<T, DP, true, false> : attention_backward_q<T, DP, false, false>,
+                                     p, q_lds<T, DP, false>(p, table), stream);
+        if (e) return e;
     }
     if (p.dtable && p.buckets) {
-        p.tiles = (p.Lq + kAttnQueries - 1) / kAttnQueries;
         hipLaunchKernelGGL(attention_backward_table<T>, dim3(p.buckets * p.H), dim3(256), 0, stream, p);
         if (const int e = (int)hipGetLastError()) return e;
     }
-    if (p.Lk > 0) {
-        p.tiles = (p.Lk + kAttnQueries - 1) / kAttnQueries;
-        p.nblocks = p.B * p.Hkv * p.tiles;
-        const int smem = BwdGeo<T, DP>::tile_bytes + 2 * kRows * 4 + 512 + lut + p.side * 2;
-        void (*const fn)(AttnParams) =
-            p.threshold ? attention_backward_kv<T, DP, true> : attention_backward_kv<T, DP, false>;
-        if (const int e = big_lds(fn, smem)) return e;
-        hipLaunchKernelGGL(fn, dim3((p.nblocks + 7) / 8 * 8), dim3(256), smem, stream, p);
-        if (const int e = (int)hipGetLastError()) return e;
-    }
-    return 0;
+    a = plan_backward_kv(p, dtype);
+    take_plan(p, a);
+    if (p.nblocks == 0) return 0;
+    const int e = a.few ? launch(drop ? attention_backward_kv<T, DP, true, true> : attention_backward_kv<T, DP, false, true>,
+                                 p, kv_lds<T, DP, true>(p), stream)
+                        : launch(drop ? attention_backward_kv<T, DP, true, false> : attention_backward_kv<T, DP, false, false>,
+                                 p, kv_lds<T, DP, false>(p), stream);
+    if (e || p.splits <= 1) return e;
+    const int64_t threads = (int64_t)p.units * p.Lk * (split_row(p.D) / 2);
+    hipLaunchKernelGGL(attention_backward_join<T>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, p);
+    return (int)hipGetLastError();
 }
 
 template <typename T>
-int launch_t(const AttnParams &p, hipStream_t stream) {
-    if (p.D <= 32) return launch_dp<T, 32>(p, stream);
-    if (p.D <= 64) return launch_dp<T, 64>(p, stream);
-    if (p.D <= 96) return launch_dp<T, 96>(p, stream);
-    return launch_dp<T, 128>(p, stream);
+int launch_t(const AttnParams &p, int dtype, hipStream_t stream) {
+    const int dp = padded_dim(p.D);
+    if (dp == 32) return launch_dp<T, 32>(p, dtype, stream);
+    if (dp == 64) return launch_dp<T, 64>(p, dtype, stream);
+    if (dp == 96) return launch_dp<T, 96>(p, dtype, stream);
+    return launch_dp<T, 128>(p, dtype, stream);
+}
+
+// LDS of the 32-row form of the dQ kernel.
+int few_q_lds(const AttnParams &p, int dtype) {
+    const int dp = padded_dim(p.D);
+    if (dtype == 0)
+        return dp == 32   ? q_lds<F32, 32, true>(p, true)
+               : dp == 64 ? q_lds<F32, 64, true>(p, true)
+               : dp == 96 ? q_lds<F32, 96, true>(p, true)
+                          : q_lds<F32, 128, true>(p, true);
+    return dp == 32   ? q_lds<F16, 32, true>(p, true)
+           : dp == 64 ? q_lds<F16, 64, true>(p, true)
+           : dp == 96 ? q_lds<F16, 96, true>(p, true)
+                      : q_lds<F16, 128, true>(p, true);
 }
 
 }  // namespace
 
+AttnPlan plan_backward_q(const AttnParams &p, int dtype) {
+    AttnPlan a = {};
+    a.splits = 1;
+    a.units = p.B * p.H;
+    a.tiles = (p.Lq + kAttnRows - 1) / kAttnRows;
+    a.few = (int64_t)a.units * a.tiles < 256 && few_q_lds(p, dtype) <= kMaxLds;
+    if (a.few) a.tiles = (p.Lq + 31) / 32;
+    return a;
+}
+
+AttnPlan plan_backward_kv(const AttnParams &p, int dtype) {
+    AttnPlan a = {};
+    a.splits = 1;
+    a.units = p.B * p.Hkv;
+    a.tiles = (p.Lk + kAttnRows - 1) / kAttnRows;
+    const int64_t blocks = (int64_t)a.units * a.tiles;
+    if (blocks == 0 || blocks >= 512) return a;
+    if (blocks < 64) {
+        a.few = true;
+        a.tiles = (p.Lk + 31) / 32;
+        return a;
+    }
+    const int64_t pairs = (int64_t)p.G * ((p.Lq + 63) / 64);
+    int64_t splits = (768 + blocks - 1) / blocks;
+    if (splits > pairs / 8) splits = pairs / 8;
+    if (splits <= 1) return a;
+    a.splits = (int)splits;
+    a.split_floats = splits * a.units * p.Lk * 2 * split_row(p.D);
+    return a;
+}
+
 int launch_attention_backward(const AttnParams &p, int dtype, hipStream_t stream) {
-    if (dtype == 0) return launch_t<F32>(p, stream);
-    if (dtype == 1) return launch_t<F16>(p, stream);
-    return launch_t<BF16>(p, stream);
+    if (dtype == 0) return launch_t<F32>(p, dtype, stream);
+    if (dtype == 1) return launch_t<F16>(p, dtype, stream);
+    return launch_t<BF16>(p, dtype, stream);
 }
 
 }  // namespace gs

@@ -42,7 +42,7 @@ struct AttnParams {
     const int32_t *lengths;
     float *delta;             // backward: (B, H, Lq) row sums of dO * O
     float *part;              // backward: (H, B * q_tiles, buckets) sums of dS
-    float *split;             // forward, split keys: partial O, then (max, sum)
+    float *split;             // sums of the parts of a split axis (see each kernel)
     int64_t qs[3], ks[3], vs[3], os[3], dos[3], dqs[3], dks[3], dvs[3];
     int B, H, Hkv, G, Lq, Lk, D;
     int causal, from_end, first;
@@ -52,11 +52,23 @@ struct AttnParams {
     uint32_t threshold, seed_lo, seed_hi, call;
     float keep_scale;
     int vec;                  // rows of every tensor allow 16-byte accesses
-    int tiles;                // query tiles (key tiles in the dK / dV kernel)
-    int splits;               // forward, few queries: parts of the key axis
+    int tiles;                // row tiles of a unit (a head of a sequence)
+    int units;
+    int pack;                 // forward, few queries: rows are the queries of all heads of a key head
+    int splits, chunk;        // parts of the split axis; keys of a part
     int nblocks;
     uint16_t starts[kMaxBuckets];  // first distance of each bucket of one side
 };
+
+// How an attention call is laid out on the chip.
+struct AttnPlan {
+    bool few;                 // 32-row blocks whose waves split the other axis
+    int pack, splits, chunk, tiles, units;
+    int64_t split_floats;     // of workspace
+};
+AttnPlan plan_forward(const AttnParams &p, int dtype, bool workspace);
+AttnPlan plan_backward_q(const AttnParams &p, int dtype);
+AttnPlan plan_backward_kv(const AttnParams &p, int dtype);
 
 // Launchers; 0 or the hipError_t of the launch.  `dtype` 0 f32, 1 f16, 2 bf16.
 int launch_layer_norm(const NormParams &p, int dtype, hipStream_t stream);
@@ -66,7 +78,19 @@ int launch_dropout(const DropoutParams &p, int dtype, hipStream_t stream);
 int launch_attention(const AttnParams &p, int dtype, hipStream_t stream);
 int launch_attention_backward(const AttnParams &p, int dtype, hipStream_t stream);
 
-constexpr int kAttnQueries = 128;    // queries of a block, keys of a dK / dV block
+constexpr int kAttnRows = 128;       // rows of a block: four waves of 32
+constexpr int kMaxLds = 163840;      // bytes of LDS of a compute unit
+
+// Entries of the distance table: the relative positions between the changes of
+// bucket, and kLutPad past either end.
+constexpr int kLutPad = 96;
+
+__host__ __device__ inline int lut_entries(int border, int bidirectional) {
+    return (bidirectional ? 2 * border : border) + 1 + 2 * kLutPad;
+}
+
+inline int padded_dim(int D) { return (D + 31) / 32 * 32; }
+__host__ __device__ inline int split_row(int D) { return (D + 3) / 4 * 4; }   // floats of a row of partial sums
 
 }  // namespace gs
 
@@ -94,22 +118,36 @@ __device__ __forceinline__ typename T::raw_t to_bits(float v) {
 }
 
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw 2011): ten rounds of two 32 x 32
-// -> 64-bit products each.  What bounds it is the rate of the 32-bit integer
-// multiplier, a quarter of the vector rate; one call serves eight elements.
+// -> 64-bit products, whose key words are the same for every lane, each
+// followed by one three-way exclusive or.  One call serves eight elements.
 __device__ __forceinline__ u32x4 philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3,
                                         uint32_t k0, uint32_t k1) {
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-        const uint32_t n0 = (uint32_t)(b >> 32) ^ c1 ^ k0, n2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c0 = __builtin_amdgcn_bitop3_b32((uint32_t)(b >> 32), c1, k0, 0x96);
+        c2 = __builtin_amdgcn_bitop3_b32((uint32_t)(a >> 32), c3, k1, 0x96);
         c1 = (uint32_t)b;
         c3 = (uint32_t)a;
-        c0 = n0;
-        c2 = n2;
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
     }
     return u32x4{c0, c1, c2, c3};
+}
+
+// 1 in each 16-bit half of a generator word that keeps its element, else 0;
+// `below` holds threshold - 1 (threshold > 0) in both halves.
+__device__ __forceinline__ uint32_t kept_pair(uint32_t w, uint32_t below) {
+    uint32_t d;
+    __asm__("v_pk_sub_u16 %0, %1, %2 clamp\n\tv_pk_min_u16 %0, %0, 1 op_sel_hi:[1,0]" : "=v"(d) : "v"(w), "s"(below));
+    return d;
+}
+
+// One bit for each of a call's eight elements, 1 where it is kept.
+__device__ __forceinline__ uint32_t kept_byte(const u32x4 &r, uint32_t below) {
+    const uint32_t x = kept_pair(r[0], below) | kept_pair(r[1], below) << 2 | kept_pair(r[2], below) << 4 |
+                       kept_pair(r[3], below) << 6;
+    return x | x >> 15;
 }
 
 // Number e (0..7) of a call: low half of the first word first.
@@ -150,6 +188,25 @@ __device__ __forceinline__ Frag<T> frag_pack(const float *v) {
         f.w[0] = __builtin_bit_cast(u32x4, x);
     }
     return f;
+}
+
+template <typename T>
+__device__ __forceinline__ void frag_negate(Frag<T> &f) {
+#pragma unroll
+    for (int n = 0; n < T::bytes / 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.w[n][i] ^= T::bytes == 4 ? 0x80000000u : 0x80008000u;
+}
+
+// Zeros where the generator drops an element (16-bit types): each half of a
+// word times 1 or 0, as integers.
+template <typename T>
+__device__ __forceinline__ void frag_keep(Frag<T> &f, const u32x4 &rnd, uint32_t below) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f.w[0][i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(u16x2, (uint32_t)f.w[0][i]) *
+                                                     __builtin_bit_cast(u16x2, kept_pair(rnd[i], below)));
 }
 
 // acc (32 x 32) += A (32 x 16) B (16 x 32).  Lane l holds row l % 32 of A and
@@ -257,19 +314,29 @@ __device__ __forceinline__ Frag<T> frag_lds(const typename T::raw_t *p) {
 }
 
 // A operand of a transposed tile: lane l gets column col0 + l % 32 of LDS
-// rows row0 + 8 (l / 32) .. + 7.  A lane reads each element on its own.
+// rows row0 + 8 (l / 32) .. + 7.  16-bit elements go through the transposing
+// LDS read: sixteen lanes name four rows of sixteen columns, four elements
+// each, and each gets one column of the four rows.  A lane reads four-byte
+// elements on their own.
 template <typename T, int PITCH>
 __device__ __forceinline__ Frag<T> frag_lds_transposed(const typename T::raw_t *lds, int row0, int col0,
                                                        int lane) {
     Frag<T> f;
-    const typename T::raw_t *p = lds + (row0 + 8 * (lane >> 5)) * PITCH + col0 + (lane & 31);
     if constexpr (T::bytes == 4) {
+        const typename T::raw_t *p = lds + (row0 + 8 * (lane >> 5)) * PITCH + col0 + (lane & 31);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f.w[j >> 2][j & 3] = p[j * PITCH];
     } else {
+        typedef __attribute__((address_space(3))) s16v4 *lds_s16v4;
+        const typename T::raw_t *p = lds + (row0 + 8 * (lane >> 5) + ((lane >> 2) & 3)) * PITCH + col0 +
+                                     (lane & 16) + 4 * (lane & 3);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            f.w[0][j] = (uint32_t)p[2 * j * PITCH] | (uint32_t)p[(2 * j + 1) * PITCH] << 16;
+        for (int n = 0; n < 2; ++n) {
+            const u32x2 v = __builtin_bit_cast(
+                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16v4)(p + 4 * n * PITCH)));
+            f.w[0][2 * n] = v[0];
+            f.w[0][2 * n + 1] = v[1];
+        }
     }
     return f;
 }
@@ -310,21 +377,17 @@ __device__ __forceinline__ int bucket_of(const uint16_t *starts, int side, int d
     return lo;
 }
 
-// A relative position's place in the distance table: -border .. border
-// (bidirectional) or -border .. 0; beyond them the bucket no longer changes.
-__device__ __forceinline__ int lut_index(const AttnParams &p, int rel) {
-    return min(max(rel + p.border, 0), p.lut - 1);
-}
-
-// Fills lut[index] = bias of head h, times log2(e) (the scores are kept in
-// base 2), for every place of the distance table.
+// The distance table of a head in LDS: entry rel + border + kLutPad is the
+// bias of relative position rel, times log2(e) (the scores are kept in base
+// 2), from kLutPad positions before the first distance of the last bucket to
+// as many past the last change.  A tile that touches a change of bucket reads
+// it without limits on the index; any other tile has one bias, that of its end
+// of the table.
 template <typename T>
-__device__ __forceinline__ void fill_lut(const AttnParams &p, int h, float *lut, uint16_t *starts, int t,
+__device__ __forceinline__ void fill_lut(const AttnParams &p, int h, float *lut, const uint16_t *starts, int t,
                                          int nt) {
-    for (int i = t; i < p.side; i += nt) starts[i] = p.starts[i];
-    __syncthreads();
     for (int i = t; i < p.lut; i += nt) {
-        const int rel = i - p.border;
+        const int rel = i - p.border - kLutPad;
         int b = bucket_of(starts, p.side, rel < 0 ? -rel : (p.bidirectional ? rel : 0));
         if (p.bidirectional && rel > 0) b += p.side;
         const size_t at = (size_t)b * p.H + h;
@@ -335,11 +398,51 @@ __device__ __forceinline__ void fill_lut(const AttnParams &p, int h, float *lut,
     }
 }
 
-// Blocks of one XCD (every eighth of the launch) take consecutive logical
-// blocks: the tiles of one head read the same K and V from one L2.
-__device__ __forceinline__ int xcd_contiguous_block(int n) {
-    const int per = (n + 7) >> 3;
-    return (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+// Which bias the relative positions lo .. hi have: 0 the table's, entry by
+// entry; 1 that of its first entry; 2 that of its last; 3 none.
+__device__ __forceinline__ int bias_class(const AttnParams &p, int lo, int hi) {
+    if (!p.lut) return 3;
+    if (hi <= -p.border) return 1;
+    return lo >= (p.bidirectional ? p.border : 0) ? 2 : 0;
+}
+
+// Writes of a tile by the threads that share it, before its reads by them (and
+// the reverse): a block's, or one wave's own.
+template <bool WAVE>
+__device__ __forceinline__ void tile_sync() {
+    if constexpr (WAVE) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    } else {
+        __syncthreads();
+    }
+}
+
+// Row tile and unit of a block.  The eighth of the launch that an XCD runs
+// takes whole units where eight divides them: their tiles read the same keys
+// from one L2.  With a causal mask the longest tiles come first, then, from the
+// middle on, the shortest, so that the tiles that a compute unit holds at once
+// add up to about the same work; `longest_last` tells which end is long.
+__device__ __forceinline__ bool block_place(const AttnParams &p, bool longest_last, int &unit, int &tile, int &part) {
+    const int per = (p.nblocks + 7) >> 3;
+    const int x = blockIdx.x & 7, i = (int)(blockIdx.x >> 3);
+    int n = x * per + i;                             // (unit, tile, part), part fastest
+    if (p.causal && (p.units & 7) == 0 && p.splits == 1) {
+        const int u = p.units >> 3, step = i / u;
+        unit = x * u + (i - step * u);
+        const int half = (p.tiles + 1) >> 1;
+        tile = step < half ? step : p.tiles - 1 - (step - half);
+        if (longest_last) tile = p.tiles - 1 - tile;
+        part = 0;
+        return true;
+    }
+    if (n >= p.nblocks) return false;
+    part = n % p.splits;
+    n /= p.splits;
+    tile = n % p.tiles;
+    unit = n / p.tiles;
+    if (p.causal && longest_last) tile = p.tiles - 1 - tile;
+    return true;
 }
 
 __device__ __forceinline__ int sequence_length(const AttnParams &p, int b) {

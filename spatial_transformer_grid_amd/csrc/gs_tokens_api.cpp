@@ -100,14 +100,13 @@ int attention_setup(const gs_attention_desc *d, bool backward, gs::AttnParams &p
         p.buckets = d->num_buckets;
         p.bidirectional = d->bidirectional;
         p.border = p.starts[p.side - 1];
-        p.lut = (p.bidirectional ? 2 * p.border : p.border) + 1;
+        p.lut = gs::lut_entries(p.border, p.bidirectional);
         p.table_f32 = d->table_dtype == GS_F32;
     }
     if (d->head_dim > 128 || d->q_len > kMaxPosition || d->kv_len > kMaxPosition || d->q_position > kMaxPosition ||
         d->q_position < -kMaxPosition || d->batch > kInt32Max || d->q_heads > kMaxHeads || d->kv_heads > kMaxHeads)
         return GS_ERR_TOO_LARGE;
-    const int64_t tile = gs::kAttnQueries;
-    const int64_t tiles = (d->q_len + tile - 1) / tile, ktiles = (d->kv_len + tile - 1) / tile;
+    const int64_t tiles = (d->q_len + 31) / 32, ktiles = (d->kv_len + 31) / 32;
     const int64_t pairs = d->batch * d->q_heads, kv_pairs = d->batch * d->kv_heads;
     if (pairs > kMaxBlocks || pairs * tiles > kMaxBlocks || kv_pairs > kMaxBlocks || kv_pairs * ktiles > kMaxBlocks)
         return GS_ERR_TOO_LARGE;
@@ -136,8 +135,8 @@ int attention_setup(const gs_attention_desc *d, bool backward, gs::AttnParams &p
     p.seed_lo = (uint32_t)d->seed;
     p.seed_hi = (uint32_t)(d->seed >> 32);
     p.call = d->call;
+    p.units = (int)pairs;
     p.tiles = (int)tiles;
-    p.nblocks = (int)(pairs * tiles);
     const int epc = 16 / dtype_bytes(d->dtype);
     p.vec = p.D % epc == 0 && strides_vec(p.qs, epc) && strides_vec(p.ks, epc) && strides_vec(p.vs, epc) &&
             strides_vec(p.os, epc);
@@ -147,8 +146,19 @@ int attention_setup(const gs_attention_desc *d, bool backward, gs::AttnParams &p
     return GS_OK;
 }
 
-int64_t backward_bytes(const gs::AttnParams &p) {
-    return round_ws((int64_t)p.B * p.H * p.Lq * 4) + round_ws((int64_t)p.B * p.H * p.tiles * p.buckets * 4);
+// Workspace of a backward call: delta, the query tiles' sums for the table, the
+// parts' sums of dK and dV; each 256-byte aligned.
+struct BackwardSpace {
+    int64_t part, split, bytes;
+};
+
+BackwardSpace backward_space(const gs::AttnParams &p, int dtype) {
+    const gs::AttnPlan q = gs::plan_backward_q(p, dtype), kv = gs::plan_backward_kv(p, dtype);
+    BackwardSpace s;
+    s.part = round_ws((int64_t)p.B * p.H * p.Lq * 4);
+    s.split = s.part + round_ws((int64_t)p.B * p.H * q.tiles * p.buckets * 4);
+    s.bytes = s.split + round_ws(kv.split_floats * 4);
+    return s;
 }
 
 }  // namespace
@@ -269,7 +279,7 @@ int gs_attention_workspace_size(const gs_attention_desc *desc, int64_t *bytes) {
     gs::AttnParams p;
     const int rc = attention_setup(desc, false, p);
     if (rc != GS_OK) return rc;
-    *bytes = 0;
+    *bytes = p.units * (int64_t)p.tiles == 0 ? 0 : round_ws(gs::plan_forward(p, desc->dtype, true).split_floats * 4);
     return GS_OK;
 }
 
@@ -279,7 +289,7 @@ int gs_attention(const gs_attention_desc *desc, const void *Q, const void *K, co
     const int rc = attention_setup(desc, false, p);
     if (rc != GS_OK) return rc;
     if (workspace_bytes < 0 || (workspace && (uintptr_t)workspace % kWsAlign)) return GS_ERR_ATTR;
-    if (p.nblocks == 0) return GS_OK;
+    if (p.units == 0 || p.tiles == 0) return GS_OK;
     if (!Q || !O || (p.Lk > 0 && (!K || !V)) || (p.buckets && !table)) return GS_ERR_NULL;
     p.q = Q;
     p.k = K;
@@ -289,6 +299,8 @@ int gs_attention(const gs_attention_desc *desc, const void *Q, const void *K, co
     p.o = O;
     p.lse = lse;
     p.vec = p.vec && aligned16(Q) && aligned16(K) && aligned16(V) && aligned16(O);
+    const int64_t need = gs::plan_forward(p, desc->dtype, true).split_floats * 4;
+    if (workspace && workspace_bytes >= need) p.split = (float *)workspace;
     return hip_status(gs::launch_attention(p, desc->dtype, (hipStream_t)stream));
 }
 
@@ -297,7 +309,7 @@ int gs_attention_backward_workspace_size(const gs_attention_desc *desc, int64_t 
     gs::AttnParams p;
     const int rc = attention_setup(desc, true, p);
     if (rc != GS_OK) return rc;
-    *bytes = backward_bytes(p);
+    *bytes = backward_space(p, desc->dtype).bytes;
     return GS_OK;
 }
 
@@ -311,11 +323,12 @@ int gs_attention_backward(const gs_attention_desc *desc, const void *dO, const v
     if (p.B == 0 || p.H == 0) {
         if (!p.H || !dtable || !p.buckets) return GS_OK;
     }
-    const bool queries = p.nblocks > 0, keys = (int64_t)p.B * p.Hkv * p.Lk > 0;
+    const bool queries = p.units > 0 && p.tiles > 0, keys = (int64_t)p.B * p.Hkv * p.Lk > 0;
     if (queries && (!dO || !Q || !O || !lse || !dQ)) return GS_ERR_NULL;
     if (keys && (!K || !V || !dK || !dV)) return GS_ERR_NULL;
     if (p.buckets && queries && !table) return GS_ERR_NULL;
-    const int64_t need = backward_bytes(p);
+    const BackwardSpace space = backward_space(p, desc->dtype);
+    const int64_t need = space.bytes;
     if (need > 0) {
         if (!workspace) return GS_ERR_NULL;
         if (workspace_bytes < need || (uintptr_t)workspace % kWsAlign) return GS_ERR_ATTR;
@@ -333,7 +346,8 @@ int gs_attention_backward(const gs_attention_desc *desc, const void *dO, const v
     p.dv = dV;
     p.dtable = p.buckets ? dtable : nullptr;
     p.delta = (float *)workspace;
-    p.part = p.dtable && workspace ? (float *)((char *)workspace + round_ws((int64_t)p.B * p.H * p.Lq * 4)) : nullptr;
+    p.part = p.dtable && workspace ? (float *)((char *)workspace + space.part) : nullptr;
+    p.split = (float *)((char *)workspace + space.split);
     p.vec = p.vec && aligned16(Q) && aligned16(K) && aligned16(V) && aligned16(O) && aligned16(dO) && aligned16(dQ) &&
             aligned16(dK) && aligned16(dV);
     return hip_status(gs::launch_attention_backward(p, desc->dtype, (hipStream_t)stream));
