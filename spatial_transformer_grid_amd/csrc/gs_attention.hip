@@ -25,12 +25,11 @@ namespace {
 template <typename T, int DP, bool FEW>
 struct FwdGeo {
     static constexpr int KEYS = FEW || T::bytes == 4 ? 32 : 64;   // keys of an LDS tile
-    static constexpr int PITCH = DP + 16 / T::bytes;
-    static constexpr int tile_elems = KEYS * PITCH;
-    // two buffers of K and V, or one of each wave's own
-    static constexpr int fixed_bytes = (FEW ? 4 : 2) * 2 * tile_elems * T::bytes;
+    static constexpr int tile_elems = KEYS * DP;
     static constexpr int SUM = DP + 4;                            // floats of a row of a wave's O
-    static_assert(!FEW || 4 * 32 * SUM * 4 <= fixed_bytes, "the waves' sums take the tiles' place");
+    // two buffers of K and V, or one of each wave's own, whose place the waves' O takes
+    static constexpr int tile_bytes = (FEW ? 4 : 2) * 2 * tile_elems * T::bytes;
+    static constexpr int fixed_bytes = FEW && 4 * 32 * SUM * 4 > tile_bytes ? 4 * 32 * SUM * 4 : tile_bytes;
 };
 
 // A new maximum is taken up only where a score passes the old one by more than
@@ -42,7 +41,7 @@ template <typename T, int DP, bool DROP, bool FEW>
 __global__ __launch_bounds__(256, FEW && T::bytes == 4 && DP > 64 ? 1 : 2) void attention_forward(AttnParams p) {
     typedef typename T::raw_t raw_t;
     typedef FwdGeo<T, DP, FEW> Geo;
-    constexpr int PITCH = Geo::PITCH, KEYS = Geo::KEYS, U = KEYS / 32, NT = FEW ? 64 : 256;
+    constexpr int KEYS = Geo::KEYS, U = KEYS / 32, NT = FEW ? 64 : 256;
     extern __shared__ __align__(16) unsigned char smem[];
     float *luts = (float *)(smem + Geo::fixed_bytes);
     __shared__ float stat[4][2][32];                 // FEW: maximum and sum of each wave
@@ -89,10 +88,26 @@ __global__ __launch_bounds__(256, FEW && T::bytes == 4 && DP > 64 ? 1 : 2) void 
         (const raw_t *)p.q + (int64_t)b * p.qs[0] + (int64_t)h * p.qs[1] + (int64_t)qi * p.qs[2];
     const int tt = FEW ? lane : t;
     raw_t *Kt = (raw_t *)smem + (FEW ? wave * 2 * Geo::tile_elems : 0);
-    TileCopy<T, DP, KEYS, NT, PITCH> kc, vc;
+    TileCopy<T, DP, KEYS, NT> kc, vc;
+    const bool async = !FEW && p.async;
+    const auto load = [&](raw_t *to, int k0) {      // the block's form: the whole way into LDS
+        if (async) {
+            kc.load(to, kb, p.ks[2], k0, end, p.D, tt);
+            vc.load(to + Geo::tile_elems, vb, p.vs[2], k0, end, p.D, tt);
+        } else {
+            kc.fetch(kb, p.ks[2], k0, end, p.D, vec, tt);
+            kc.put(to, tt);
+            vc.fetch(vb, p.vs[2], k0, end, p.D, vec, tt);
+            vc.put(to + Geo::tile_elems, tt);
+        }
+    };
     if (begin < end) {
-        kc.fetch(kb, p.ks[2], begin, end, p.D, vec, tt);
-        vc.fetch(vb, p.vs[2], begin, end, p.D, vec, tt);
+        if constexpr (FEW) {
+            kc.fetch(kb, p.ks[2], begin, end, p.D, vec, tt);
+            vc.fetch(vb, p.vs[2], begin, end, p.D, vec, tt);
+        } else {
+            load(Kt, begin);
+        }
     }
     // a negative scale moves into Q: the maximum of the scores is then that of the products
     const float scale2 = fabsf(p.scale2);
@@ -125,18 +140,24 @@ __global__ __launch_bounds__(256, FEW && T::bytes == 4 && DP > 64 ? 1 : 2) void 
     float m = -INFINITY, l = 0.0f;
     const uint32_t below = (p.threshold - 1) * 0x10001u;
 
-    if (begin < end) {
-        kc.put(Kt, tt);
-        vc.put(Kt + Geo::tile_elems, tt);
-    }
+    if constexpr (FEW)
+        if (begin < end) {
+            kc.put(Kt, tt);
+            vc.put(Kt + Geo::tile_elems, tt);
+        }
     for (int k0 = begin, n = 0; k0 < end; k0 += STEP, ++n) {
         const raw_t *Ks = Kt + (FEW ? 0 : (n & 1) * 2 * Geo::tile_elems);
         const raw_t *Vs = Ks + Geo::tile_elems;
+        if (!FEW) async_wait();
         tile_sync<FEW>();
         const bool more = k0 + STEP < end;
         if (more) {
-            kc.fetch(kb, p.ks[2], k0 + STEP, end, p.D, vec, tt);
-            vc.fetch(vb, p.vs[2], k0 + STEP, end, p.D, vec, tt);
+            if constexpr (FEW) {
+                kc.fetch(kb, p.ks[2], k0 + STEP, end, p.D, vec, tt);
+                vc.fetch(vb, p.vs[2], k0 + STEP, end, p.D, vec, tt);
+            } else {
+                load(Kt + ((n + 1) & 1) * 2 * Geo::tile_elems, k0 + STEP);
+            }
         }
         if (FEW || (row0 < p.Lq && !(p.causal && k0 > wave_last))) {
             float s[16 * U];
@@ -145,9 +166,9 @@ __global__ __launch_bounds__(256, FEW && T::bytes == 4 && DP > 64 ? 1 : 2) void 
                 f32x16 st;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) st[r] = 0.0f;
-                const raw_t *krow = Ks + (32 * u + a_row(lane & 31)) * PITCH + 8 * half;
 #pragma unroll
-                for (int x = 0; x < DP / 16; ++x) mma<T>(st, frag_lds<T>(krow + 16 * x), qf[x]);
+                for (int x = 0; x < DP / 16; ++x)
+                    mma<T>(st, frag_lds<T, DP>(Ks, 32 * u + a_row(lane & 31), 16 * x + 8 * half), qf[x]);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[16 * u + r] = st[r];
             }
@@ -217,15 +238,15 @@ __global__ __launch_bounds__(256, FEW && T::bytes == 4 && DP > 64 ? 1 : 2) void 
                 if constexpr (DROP && T::bytes == 2) frag_keep<T>(pf, rnd, below);
 #pragma unroll
                 for (int d = 0; d < DP / 32; ++d)
-                    mma<T>(acc[d], frag_lds_transposed<T, PITCH>(Vs, 16 * x, 32 * d, lane), pf);
+                    mma<T>(acc[d], frag_lds_transposed<T, DP>(Vs, 16 * x, 32 * d, lane), pf);
             }
         }
-        if (more) {
-            if (FEW) tile_sync<true>();
-            raw_t *next = Kt + (FEW ? 0 : ((n + 1) & 1) * 2 * Geo::tile_elems);
-            kc.put(next, tt);
-            vc.put(next + Geo::tile_elems, tt);
-        }
+        if constexpr (FEW)
+            if (more) {
+                tile_sync<true>();
+                kc.put(Kt, tt);
+                vc.put(Kt + Geo::tile_elems, tt);
+            }
     }
     l += __shfl_xor(l, 32);
     if constexpr (!FEW) {
@@ -360,14 +381,15 @@ int launch_t(const AttnParams &p, bool few, hipStream_t stream) {
 
 }  // namespace
 
-// The 32-row form where 128-row blocks would leave compute units without one.
+// The 32-row form where 128-row blocks would leave compute units without one,
+// or would be mostly empty.
 AttnPlan plan_forward(const AttnParams &p, int, bool workspace) {
     AttnPlan a = {};
     a.splits = 1;
     a.units = p.B * p.H;
     a.tiles = (p.Lq + kAttnRows - 1) / kAttnRows;
     a.chunk = p.Lk;
-    a.few = (int64_t)a.units * a.tiles < 256;
+    a.few = p.Lq <= 32 || (int64_t)a.units * a.tiles < 256;
     if (!a.few) return a;
     // tables of all heads that share a key head take at most 16 KiB of LDS
     if (p.G > 1 && p.G * (int64_t)p.Lq <= 32 && (int64_t)p.G * p.lut * 4 <= 16384) {

@@ -20,29 +20,26 @@ namespace gs {
 
 namespace {
 
-// Sums of dS by distance, per wave: one copy for each half of the wave, so
-// that no two lanes of an instruction add to one address (the lanes of a half
-// hold different queries and the same key, hence different distances).  An
-// LDS add without return keeps the order of a wave's instructions, so the sums
-// do not depend on timing.
-__host__ __device__ constexpr int near_pitch(int lut) { return (lut + 31) / 64 * 64 + 32; }
+// Sums of dS by distance.  A wave writes a 32 x 32 part of dS to LDS, a query a
+// row of 64 floats whose second half stays zero; lane d then adds up the
+// diagonal key - query = d - 31, an element a row (what lies left or right of
+// a row's 32 are the zeros of the row before or its own), and adds the sum to
+// the wave's entry for that distance.  LDS adds by atomics in the place of the
+// 32 reads cost about 180 cycles an instruction.
+constexpr int kDiagonal = 32 + 32 * 64;              // floats of a wave
 
 // Geometry of both kernels: `ROWS` rows of the axis that is walked in an LDS
 // tile, two buffers of two tensors, or one of each wave's own (FEW).
 template <typename T, int DP, bool FEW>
 struct BwdGeo {
     static constexpr int ROWS = FEW || T::bytes == 4 || DP > 64 ? 32 : 64;
-    static constexpr int PITCH = DP + 16 / T::bytes;
-    static constexpr int tile_elems = ROWS * PITCH;
+    static constexpr int tile_elems = ROWS * DP;
     static constexpr int copies = FEW ? 4 : 2;
-    static constexpr int tile_bytes = copies * 2 * tile_elems * T::bytes;
     static constexpr int SUM = DP + 4;
-    static_assert(!FEW || 4 * 32 * SUM * 4 <= tile_bytes, "the waves' sums take the tiles' place");
+    static constexpr int own_bytes = copies * 2 * tile_elems * T::bytes;
+    // (FEW: the waves' sums take the tiles' place)
+    static constexpr int tile_bytes = FEW && 4 * 32 * SUM * 4 > own_bytes ? 4 * 32 * SUM * 4 : own_bytes;
 };
-
-__device__ __forceinline__ void lds_add(float *p, float v) {
-    __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-}
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -74,12 +71,12 @@ template <typename T, int DP, bool DROP, bool FEW>
 __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnParams p) {
     typedef typename T::raw_t raw_t;
     typedef BwdGeo<T, DP, FEW> Geo;
-    constexpr int PITCH = Geo::PITCH, KEYS = Geo::ROWS, NT = FEW ? 64 : 256;
+    constexpr int KEYS = Geo::ROWS, NT = FEW ? 64 : 256;
     extern __shared__ __align__(16) unsigned char smem[];
     float *lut = (float *)(smem + Geo::tile_bytes);
-    const int pitch = near_pitch(p.lut);
-    float *near = lut + (p.lut + 3) / 4 * 4;         // [wave][half][pitch]
-    float *far = near + (p.part ? 8 * pitch : 0);    // [wave][2]
+    float *diagonals = lut + (p.lut + 3) / 4 * 4;    // [wave][kDiagonal]
+    float *near = diagonals + (p.part ? 4 * kDiagonal : 0);   // [wave][lut]
+    float *far = near + (p.part ? 4 * p.lut : 0);    // [wave][2]
     uint16_t *starts = (uint16_t *)(far + 8);
 
     int unit, tile, part;
@@ -103,10 +100,26 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
     const raw_t *vb = (const raw_t *)p.v + (int64_t)b * p.vs[0] + (int64_t)hk * p.vs[1];
     const int tt = FEW ? lane : t;
     raw_t *Kt = (raw_t *)smem + (FEW ? wave * 2 * Geo::tile_elems : 0);
-    TileCopy<T, DP, KEYS, NT, PITCH> kc, vc;
+    TileCopy<T, DP, KEYS, NT> kc, vc;
+    const bool async = !FEW && p.async;
+    const auto load = [&](raw_t *to, int k0) {      // the block's form: the whole way into LDS
+        if (async) {
+            kc.load(to, kb, p.ks[2], k0, end, p.D, tt);
+            vc.load(to + Geo::tile_elems, vb, p.vs[2], k0, end, p.D, tt);
+        } else {
+            kc.fetch(kb, p.ks[2], k0, end, p.D, vec, tt);
+            kc.put(to, tt);
+            vc.fetch(vb, p.vs[2], k0, end, p.D, vec, tt);
+            vc.put(to + Geo::tile_elems, tt);
+        }
+    };
     if (begin < end) {
-        kc.fetch(kb, p.ks[2], begin, end, p.D, vec, tt);
-        vc.fetch(vb, p.vs[2], begin, end, p.D, vec, tt);
+        if constexpr (FEW) {
+            kc.fetch(kb, p.ks[2], begin, end, p.D, vec, tt);
+            vc.fetch(vb, p.vs[2], begin, end, p.D, vec, tt);
+        } else {
+            load(Kt, begin);
+        }
     }
     Frag<T> qf[DP / 16], gf[DP / 16];
     float delta = 0.0f;
@@ -140,7 +153,7 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
     if (p.lut) {
         for (int i = t; i < p.side; i += 256) starts[i] = p.starts[i];
         if (p.part)
-            for (int i = t; i < 8 * pitch; i += 256) near[i] = 0.0f;
+            for (int i = t; i < 4 * (kDiagonal + p.lut); i += 256) diagonals[i] = 0.0f;
         __syncthreads();
         fill_lut<T>(p, h, lut, starts, t, 256);
         __syncthreads();
@@ -148,7 +161,7 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
         bias_hi = lut[p.lut - 1];
     }
     float far_lo = 0.0f, far_hi = 0.0f;              // distances at or past the last change
-    float *mine = near + (wave * 2 + half) * pitch;
+    float *diagonal = diagonals + wave * kDiagonal + 32, *mine = near + wave * p.lut;
 
     f32x16 acc[DP / 32];
 #pragma unroll
@@ -156,18 +169,24 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
 
-    if (begin < end) {
-        kc.put(Kt, tt);
-        vc.put(Kt + Geo::tile_elems, tt);
-    }
+    if constexpr (FEW)
+        if (begin < end) {
+            kc.put(Kt, tt);
+            vc.put(Kt + Geo::tile_elems, tt);
+        }
     for (int k0 = begin, n = 0; k0 < end; k0 += STEP, ++n) {
         const raw_t *Ks = Kt + (FEW ? 0 : (n & 1) * 2 * Geo::tile_elems);
         const raw_t *Vs = Ks + Geo::tile_elems;
+        if (!FEW) async_wait();
         tile_sync<FEW>();
         const bool more = k0 + STEP < end;
         if (more) {
-            kc.fetch(kb, p.ks[2], k0 + STEP, end, p.D, vec, tt);
-            vc.fetch(vb, p.vs[2], k0 + STEP, end, p.D, vec, tt);
+            if constexpr (FEW) {
+                kc.fetch(kb, p.ks[2], k0 + STEP, end, p.D, vec, tt);
+                vc.fetch(vb, p.vs[2], k0 + STEP, end, p.D, vec, tt);
+            } else {
+                load(Kt + ((n + 1) & 1) * 2 * Geo::tile_elems, k0 + STEP);
+            }
         }
 #pragma unroll
         for (int u = 0; u < KEYS / 32; ++u) {
@@ -176,11 +195,11 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
             f32x16 st, dp;
 #pragma unroll
             for (int r = 0; r < 16; ++r) st[r] = dp[r] = 0.0f;
-            const int row = (32 * u + a_row(lane & 31)) * PITCH + 8 * half;
+            const int row = 32 * u + a_row(lane & 31);
 #pragma unroll
             for (int x = 0; x < DP / 16; ++x) {
-                mma<T>(st, frag_lds<T>(Ks + row + 16 * x), qf[x]);
-                mma<T>(dp, frag_lds<T>(Vs + row + 16 * x), gf[x]);
+                mma<T>(st, frag_lds<T, DP>(Ks, row, 16 * x + 8 * half), qf[x]);
+                mma<T>(dp, frag_lds<T, DP>(Vs, row, 16 * x + 8 * half), gf[x]);
             }
             const int key0 = ku + 8 * half;
             const int cls = bias_class(p, ku - wave_last, ku + 31 - wave_first);
@@ -218,9 +237,17 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
             }
             if (p.part) {
                 if (cls == 0) {
-                    float *at = mine + (key0 - pos + p.border + kLutPad);
+                    float *row = diagonal + (lane & 31) * 64 + 8 * half;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) lds_add(at + 16 * (i >> 3) + (i & 7), ds[i]);
+                    for (int i = 0; i < 16; i += 4)
+                        *(tokens_f32x4 *)(row + 16 * (i >> 3) + (i & 7)) =
+                            tokens_f32x4{ds[i], ds[i + 1], ds[i + 2], ds[i + 3]};
+                    tile_sync<true>();
+                    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) sum[q & 1] += diagonal[lane - 31 + 65 * q];
+                    mine[ku - wave_first - 31 + lane + p.border + kLutPad] += sum[0] + sum[1];
+                    tile_sync<true>();
                 } else {
                     float sum = 0.0f;
 #pragma unroll
@@ -234,15 +261,15 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
                 const Frag<T> df = frag_pack<T>(ds + 8 * x);
 #pragma unroll
                 for (int d = 0; d < DP / 32; ++d)
-                    mma<T>(acc[d], frag_lds_transposed<T, PITCH>(Ks, 32 * u + 16 * x, 32 * d, lane), df);
+                    mma<T>(acc[d], frag_lds_transposed<T, DP>(Ks, 32 * u + 16 * x, 32 * d, lane), df);
             }
         }
-        if (more) {
-            if (FEW) tile_sync<true>();
-            raw_t *next = Kt + (FEW ? 0 : ((n + 1) & 1) * 2 * Geo::tile_elems);
-            kc.put(next, tt);
-            vc.put(next + Geo::tile_elems, tt);
-        }
+        if constexpr (FEW)
+            if (more) {
+                tile_sync<true>();
+                kc.put(Kt, tt);
+                vc.put(Kt + Geo::tile_elems, tt);
+            }
     }
     const float scale = p.scale * p.keep_scale;
     if constexpr (!FEW) {
@@ -290,11 +317,11 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
             for (int w = 0; w < 4; ++w) sum += far[2 * w + (after ? 1 : 0)];
         const int lo = max((int)starts[m], after ? 1 : 0), hi = last ? p.border + kLutPad + 1 : starts[m + 1];
         for (int d = lo; d < hi; ++d)
-            for (int w = 0; w < 8; ++w) sum += near[w * pitch + p.border + kLutPad + (after ? d : -d)];
+            for (int w = 0; w < 4; ++w) sum += near[w * p.lut + p.border + kLutPad + (after ? d : -d)];
         if (!p.bidirectional && m == 0) {
             for (int w = 0; w < 4; ++w) sum += far[2 * w + 1];
             for (int d = 1; d <= kLutPad; ++d)
-                for (int w = 0; w < 8; ++w) sum += near[w * pitch + p.border + kLutPad + d];
+                for (int w = 0; w < 4; ++w) sum += near[w * p.lut + p.border + kLutPad + d];
         }
         out[n] = sum * p.keep_scale;
     }
@@ -304,7 +331,7 @@ template <typename T, int DP, bool DROP, bool FEW>
 __global__ __launch_bounds__(256, FEW || T::bytes == 4 ? 1 : 2) void attention_backward_kv(AttnParams p) {
     typedef typename T::raw_t raw_t;
     typedef BwdGeo<T, DP, FEW> Geo;
-    constexpr int PITCH = Geo::PITCH, ROWS = Geo::ROWS, NT = FEW ? 64 : 256;
+    constexpr int ROWS = Geo::ROWS, NT = FEW ? 64 : 256;
     extern __shared__ __align__(16) unsigned char smem[];
     // per copy of a tile: minus lse without and with the biases of the two ends, delta
     float *row_stats = (float *)(smem + Geo::tile_bytes);
@@ -352,7 +379,8 @@ __global__ __launch_bounds__(256, FEW || T::bytes == 4 ? 1 : 2) void attention_b
     raw_t *Qt = (raw_t *)smem + (FEW ? wave * 2 * Geo::tile_elems : 0);
     float *stats = row_stats + (FEW ? wave * 4 * ROWS : 0);
     unsigned char *mask = masks + wave * 128;
-    TileCopy<T, DP, ROWS, NT, PITCH> qc, gc;
+    TileCopy<T, DP, ROWS, NT> qc, gc;
+    const bool async = !FEW && p.async;
     const float keep_inv = 1.0f / p.keep_scale;
 
     for (int g = 0; g < p.G; ++g) {
@@ -371,9 +399,7 @@ __global__ __launch_bounds__(256, FEW || T::bytes == 4 ? 1 : 2) void attention_b
             bias_hi = lut[p.lut - 1];
         }
         float lse = 0.0f, delta = 0.0f;              // of row tt of the tile in flight
-        const auto fetch = [&](int q0) {
-            qc.fetch(qb, p.qs[2], q0, p.Lq, p.D, vec, tt);
-            gc.fetch(gb, p.dos[2], q0, p.Lq, p.D, vec, tt);
+        const auto fetch_stats = [&](int q0) {
             if (tt < ROWS) {
                 const bool in = q0 + tt < p.Lq;
                 const int64_t at = (int64_t)bh * p.Lq + q0 + tt;
@@ -381,10 +407,7 @@ __global__ __launch_bounds__(256, FEW || T::bytes == 4 ? 1 : 2) void attention_b
                 delta = in ? p.delta[at] : 0.0f;
             }
         };
-        const auto put = [&](int copy) {
-            raw_t *to = Qt + copy * 2 * Geo::tile_elems;
-            qc.put(to, tt);
-            gc.put(to + Geo::tile_elems, tt);
+        const auto put_stats = [&](int copy) {
             if (tt < ROWS) {
                 float *s = stats + copy * 4 * ROWS;
                 const float e = lse == -INFINITY ? -INFINITY : -lse * kLog2e;   // 2^(s - inf) = 0: no key seen
@@ -394,19 +417,51 @@ __global__ __launch_bounds__(256, FEW || T::bytes == 4 ? 1 : 2) void attention_b
                 s[3 * ROWS + tt] = delta * keep_inv;
             }
         };
+        const auto fetch = [&](int q0) {            // one wave's form
+            qc.fetch(qb, p.qs[2], q0, p.Lq, p.D, vec, tt);
+            gc.fetch(gb, p.dos[2], q0, p.Lq, p.D, vec, tt);
+            fetch_stats(q0);
+        };
+        const auto put = [&]() {
+            qc.put(Qt, tt);
+            gc.put(Qt + Geo::tile_elems, tt);
+            put_stats(0);
+        };
+        const auto load = [&](int copy, int q0) {   // the block's form: the whole way into LDS
+            raw_t *to = Qt + copy * 2 * Geo::tile_elems;
+            fetch_stats(q0);
+            if (async) {
+                qc.load(to, qb, p.qs[2], q0, p.Lq, p.D, tt);
+                gc.load(to + Geo::tile_elems, gb, p.dos[2], q0, p.Lq, p.D, tt);
+            } else {
+                qc.fetch(qb, p.qs[2], q0, p.Lq, p.D, vec, tt);
+                qc.put(to, tt);
+                gc.fetch(gb, p.dos[2], q0, p.Lq, p.D, vec, tt);
+                gc.put(to + Geo::tile_elems, tt);
+            }
+        };
         constexpr int STEP = FEW ? 4 : 1;
         const int begin = FEW ? t0 + wave : t0;
         if (begin < t1) {
-            fetch(q_begin + begin * ROWS);
-            put(0);
+            if constexpr (FEW) {
+                fetch(q_begin + begin * ROWS);
+                put();
+            } else {
+                load(0, q_begin + begin * ROWS);
+                put_stats(0);
+            }
         }
         for (int n = begin, it = 0; n < t1; n += STEP, ++it) {
             const int q0 = q_begin + n * ROWS, copy = FEW ? 0 : it & 1;
             const raw_t *Qs = Qt + copy * 2 * Geo::tile_elems, *Gs = Qs + Geo::tile_elems;
             const float *rs = stats + copy * 4 * ROWS;
+            if (!FEW) async_wait();
             tile_sync<FEW>();
             const bool more = n + STEP < t1;
-            if (more) fetch(q0 + STEP * ROWS);
+            if (more) {
+                if constexpr (FEW) fetch(q0 + STEP * ROWS);
+                else load((it + 1) & 1, q0 + STEP * ROWS);
+            }
 #pragma unroll
             for (int u = 0; u < ROWS / 32; ++u) {
                 const int qu = q0 + 32 * u;          // this 32-query part
@@ -414,11 +469,11 @@ __global__ __launch_bounds__(256, FEW || T::bytes == 4 ? 1 : 2) void attention_b
                 f32x16 st, dp;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) st[r] = dp[r] = 0.0f;
-                const int row = (32 * u + a_row(lane & 31)) * PITCH + 8 * half;
+                const int row = 32 * u + a_row(lane & 31);
 #pragma unroll
                 for (int x = 0; x < DP / 16; ++x) {
-                    mma<T>(st, frag_lds<T>(Qs + row + 16 * x), kf[x]);
-                    mma<T>(dp, frag_lds<T>(Gs + row + 16 * x), vf[x]);
+                    mma<T>(st, frag_lds<T, DP>(Qs, row, 16 * x + 8 * half), kf[x]);
+                    mma<T>(dp, frag_lds<T, DP>(Gs, row, 16 * x + 8 * half), vf[x]);
                 }
                 if constexpr (DROP) {
                     // this lane's two calls: query qu + lane % 32, keys
@@ -473,14 +528,18 @@ __global__ __launch_bounds__(256, FEW || T::bytes == 4 ? 1 : 2) void attention_b
                     const Frag<T> pf = frag_pack<T>(pd), df = frag_pack<T>(ds);
 #pragma unroll
                     for (int d = 0; d < DP / 32; ++d) {
-                        mma<T>(dv[d], frag_lds_transposed<T, PITCH>(Gs, 32 * u + 16 * x, 32 * d, lane), pf);
-                        mma<T>(dk[d], frag_lds_transposed<T, PITCH>(Qs, 32 * u + 16 * x, 32 * d, lane), df);
+                        mma<T>(dv[d], frag_lds_transposed<T, DP>(Gs, 32 * u + 16 * x, 32 * d, lane), pf);
+                        mma<T>(dk[d], frag_lds_transposed<T, DP>(Qs, 32 * u + 16 * x, 32 * d, lane), df);
                     }
                 }
             }
             if (more) {
-                if (FEW) tile_sync<true>();
-                put(FEW ? 0 : (it + 1) & 1);
+                if constexpr (FEW) {
+                    tile_sync<true>();
+                    put();
+                } else {
+                    put_stats((it + 1) & 1);
+                }
             }
         }
     }
@@ -579,7 +638,7 @@ __global__ __launch_bounds__(256) void attention_backward_table(AttnParams p) {
 
 template <typename T, int DP, bool FEW>
 int q_lds(const AttnParams &p, bool table) {
-    return BwdGeo<T, DP, FEW>::tile_bytes + (p.lut + 3) / 4 * 16 + (table ? 8 * near_pitch(p.lut) * 4 : 0) + 32 +
+    return BwdGeo<T, DP, FEW>::tile_bytes + (p.lut + 3) / 4 * 16 + (table ? 4 * (kDiagonal + p.lut) * 4 : 0) + 32 +
            p.side * 2;
 }
 

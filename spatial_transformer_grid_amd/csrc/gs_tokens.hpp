@@ -52,6 +52,7 @@ struct AttnParams {
     uint32_t threshold, seed_lo, seed_hi, call;
     float keep_scale;
     int vec;                  // rows of every tensor allow 16-byte accesses
+    int async;                // and their tiles asynchronous loads
     int tiles;                // row tiles of a unit (a head of a sequence)
     int units;
     int pack;                 // forward, few queries: rows are the queries of all heads of a key head
@@ -238,16 +239,43 @@ __device__ __forceinline__ int a_row(int m) {
     return 16 * (m >> 4) + 8 * ((m >> 2) & 1) + 4 * ((m >> 3) & 1) + (m & 3);
 }
 
-// Rows row0 .. row0 + ROWS - 1 of a strided tensor into registers, in 16-byte
-// chunks over NT threads, zeros outside rows < limit and columns < D; put()
-// writes them to LDS rows of PITCH elements.
-template <typename T, int DP, int ROWS, int NT, int PITCH>
+// An LDS tile: rows of DP elements without gaps (an asynchronous load writes a
+// wave's 16-byte chunks one after another), whose chunks change places by row
+// so that neither of two reads meets a bank twice: the 16-byte reads of eight
+// consecutive lanes, which lie in rows r .. r + 3 and r + 8 .. r + 11 (a_row),
+// and the transposing read, whose 32 lanes cover 64 bytes of rows r .. r + 3.
+template <typename T, int DP>
+struct Tile {
+    static constexpr int EPC = 16 / T::bytes;       // elements of a chunk
+    static constexpr int CPR = DP / EPC;            // chunks of a row
+    __device__ __forceinline__ static int turn(int row) {
+        if constexpr (T::bytes == 4) return (row & 3) | (row >> 1 & 4);
+        if constexpr (DP == 128) return (row & 3) << 2 | (row >> 3 & 1);
+        if constexpr (DP == 64) return (row & 2) << 1 | (row >> 3 & 1);
+        return row >> 3 & 1;
+    }
+    // element offset of the chunk that holds column col
+    __device__ __forceinline__ static int chunk(int row, int col) {
+        return row * DP + ((col / EPC) ^ turn(row)) * EPC;
+    }
+};
+
+__device__ __forceinline__ void async_wait() { __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Rows row0 .. row0 + ROWS - 1 of a strided tensor on their way into an LDS
+// tile, in 16-byte chunks over NT threads, zeros outside rows < limit and
+// columns < D: through registers (fetch, then put), or by asynchronous loads
+// that write LDS by themselves (load, then async_wait).
+template <typename T, int DP, int ROWS, int NT>
 struct TileCopy {
     typedef typename T::raw_t raw_t;
-    static constexpr int EPC = 16 / T::bytes;
-    static constexpr int CPR = DP / EPC;
+    typedef Tile<T, DP> L;
+    static constexpr int EPC = L::EPC, CPR = L::CPR;
     static constexpr int N = (ROWS * CPR + NT - 1) / NT;
+    static_assert(ROWS * CPR % 64 == 0, "a wave has a whole step or none");
     u32x4 reg[N];
+
+    __device__ __forceinline__ static bool inside(int c) { return ROWS * CPR % NT == 0 || c < ROWS * CPR; }
 
     __device__ __forceinline__ void fetch(const raw_t *base, int64_t stride, int row0, int limit, int D,
                                           bool vec, int t) {
@@ -255,7 +283,7 @@ struct TileCopy {
         for (int n = 0; n < N; ++n) {
             const int c = t + n * NT, r = c / CPR, col = (c - r * CPR) * EPC;
             u32x4 v = {0, 0, 0, 0};
-            if ((ROWS * CPR % NT == 0 || c < ROWS * CPR) && row0 + r < limit && col < D) {
+            if (inside(c) && row0 + r < limit && col < D) {
                 const raw_t *src = base + (int64_t)(row0 + r) * stride + col;
                 if (vec) {
                     v = *(const u32x4 *)src;
@@ -273,7 +301,25 @@ struct TileCopy {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int c = t + n * NT, r = c / CPR, col = (c - r * CPR) * EPC;
-            if (ROWS * CPR % NT == 0 || c < ROWS * CPR) *(u32x4 *)(lds + r * PITCH + col) = reg[n];
+            if (inside(c)) *(u32x4 *)(lds + L::chunk(r, col)) = reg[n];
+        }
+    }
+    // A lane's chunk lands at its own place of the tile, so it is the source
+    // column that changes place.  Reads outside the range of the descriptor
+    // give zeros.  The caller has checked that ROWS rows span less than 2 GiB.
+    __device__ __forceinline__ static void load(raw_t *lds, const raw_t *base, int64_t stride, int row0, int limit,
+                                                int D, int t) {
+        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)(base + (int64_t)row0 * stride), 0, 0x7fffffff, 0x00027000);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int c = t + n * NT, r = c / CPR, col = ((c - r * CPR) ^ L::turn(r)) * EPC;
+            const uint32_t at =
+                row0 + r < limit && col < D ? (uint32_t)(r * (int)stride + col) * T::bytes : 0x80000000u;
+            if (inside(c))
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rsrc, (__attribute__((address_space(3))) void *)(lds + ((t & ~63) + n * NT) * EPC), 16, (int)at, 0,
+                    0, 0);
         }
     }
 };
@@ -304,12 +350,13 @@ __device__ __forceinline__ Frag<T> frag_global(const typename T::raw_t *row, int
     return f;
 }
 
-// Eight elements from an LDS row (16-byte aligned).
-template <typename T>
-__device__ __forceinline__ Frag<T> frag_lds(const typename T::raw_t *p) {
+// Eight elements of an LDS tile from column col (a multiple of 8) of a row.
+template <typename T, int DP>
+__device__ __forceinline__ Frag<T> frag_lds(const typename T::raw_t *lds, int row, int col) {
     Frag<T> f;
 #pragma unroll
-    for (int n = 0; n < T::bytes / 2; ++n) f.w[n] = *(const u32x4 *)(p + n * (16 / T::bytes));
+    for (int n = 0; n < T::bytes / 2; ++n)
+        f.w[n] = *(const u32x4 *)(lds + Tile<T, DP>::chunk(row, col + n * Tile<T, DP>::EPC));
     return f;
 }
 
@@ -318,22 +365,23 @@ __device__ __forceinline__ Frag<T> frag_lds(const typename T::raw_t *p) {
 // LDS read: sixteen lanes name four rows of sixteen columns, four elements
 // each, and each gets one column of the four rows.  A lane reads four-byte
 // elements on their own.
-template <typename T, int PITCH>
+template <typename T, int DP>
 __device__ __forceinline__ Frag<T> frag_lds_transposed(const typename T::raw_t *lds, int row0, int col0,
                                                        int lane) {
     Frag<T> f;
     if constexpr (T::bytes == 4) {
-        const typename T::raw_t *p = lds + (row0 + 8 * (lane >> 5)) * PITCH + col0 + (lane & 31);
+        const int col = col0 + (lane & 31);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f.w[j >> 2][j & 3] = p[j * PITCH];
+        for (int j = 0; j < 8; ++j)
+            f.w[j >> 2][j & 3] = lds[Tile<T, DP>::chunk(row0 + 8 * (lane >> 5) + j, col) + (col & 3)];
     } else {
         typedef __attribute__((address_space(3))) s16v4 *lds_s16v4;
-        const typename T::raw_t *p = lds + (row0 + 8 * (lane >> 5) + ((lane >> 2) & 3)) * PITCH + col0 +
-                                     (lane & 16) + 4 * (lane & 3);
+        const int row = row0 + 8 * (lane >> 5) + (lane >> 2 & 3), col = col0 + (lane & 16) + 4 * (lane & 3);
+        const typename T::raw_t *p = lds + Tile<T, DP>::chunk(row, col) + (col & 4);
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < 2; ++n) {   // four rows on, the chunks' places are the same
             const u32x2 v = __builtin_bit_cast(
-                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16v4)(p + 4 * n * PITCH)));
+                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16v4)(p + 4 * n * DP)));
             f.w[0][2 * n] = v[0];
             f.w[0][2 * n + 1] = v[1];
         }

@@ -146,6 +146,10 @@ int attention_setup(const gs_attention_desc *d, bool backward, gs::AttnParams &p
     return GS_OK;
 }
 
+// Rows of a tile that an asynchronous load reaches from its first by a 32-bit
+// byte offset.
+bool stride_async(int64_t s) { return s <= (int64_t(1) << 22); }
+
 // Workspace of a backward call: delta, the query tiles' sums for the table, the
 // parts' sums of dK and dV; each 256-byte aligned.
 struct BackwardSpace {
@@ -299,6 +303,7 @@ int gs_attention(const gs_attention_desc *desc, const void *Q, const void *K, co
     p.o = O;
     p.lse = lse;
     p.vec = p.vec && aligned16(Q) && aligned16(K) && aligned16(V) && aligned16(O);
+    p.async = p.vec && stride_async(p.ks[2]) && stride_async(p.vs[2]);
     const int64_t need = gs::plan_forward(p, desc->dtype, true).split_floats * 4;
     if (workspace && workspace_bytes >= need) p.split = (float *)workspace;
     return hip_status(gs::launch_attention(p, desc->dtype, (hipStream_t)stream));
@@ -350,6 +355,8 @@ int gs_attention_backward(const gs_attention_desc *desc, const void *dO, const v
     p.split = (float *)((char *)workspace + space.split);
     p.vec = p.vec && aligned16(Q) && aligned16(K) && aligned16(V) && aligned16(O) && aligned16(dO) && aligned16(dQ) &&
             aligned16(dK) && aligned16(dV);
+    p.async = p.vec && stride_async(p.ks[2]) && stride_async(p.vs[2]) && stride_async(p.qs[2]) &&
+              stride_async(p.dos[2]);
     return hip_status(gs::launch_attention_backward(p, desc->dtype, (hipStream_t)stream));
 }
 
