@@ -21,12 +21,14 @@ namespace gs {
 namespace {
 
 // Sums of dS by distance.  A wave writes a 32 x 32 part of dS to LDS, a query a
-// row of 64 floats whose second half stays zero; lane d then adds up the
-// diagonal key - query = d - 31, an element a row (what lies left or right of
-// a row's 32 are the zeros of the row before or its own), and adds the sum to
-// the wave's entry for that distance.  LDS adds by atomics in the place of the
+// row of kDiagonalRow floats of which the last 36 stay zero; lane d then adds
+// up the diagonal key - query = d - 31, an element a row (what lies left or
+// right of a row's 32 are the zeros of the row before or its own), and adds the
+// sum to the wave's entry for that distance.  The row length spreads the rows
+// over the banks.  LDS adds by atomics in the place of the
 // 32 reads cost about 180 cycles an instruction.
-constexpr int kDiagonal = 32 + 32 * 64;              // floats of a wave
+constexpr int kDiagonalRow = 68;
+constexpr int kDiagonal = 32 + 32 * kDiagonalRow;    // floats of a wave
 
 // Geometry of both kernels: `ROWS` rows of the axis that is walked in an LDS
 // tile, two buffers of two tensors, or one of each wave's own (FEW).
@@ -237,7 +239,7 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
             }
             if (p.part) {
                 if (cls == 0) {
-                    float *row = diagonal + (lane & 31) * 64 + 8 * half;
+                    float *row = diagonal + (lane & 31) * kDiagonalRow + 8 * half;
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
                         *(tokens_f32x4 *)(row + 16 * (i >> 3) + (i & 7)) =
@@ -245,7 +247,7 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
                     tile_sync<true>();
                     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) sum[q & 1] += diagonal[lane - 31 + 65 * q];
+                    for (int q = 0; q < 32; ++q) sum[q & 1] += diagonal[lane - 31 + (kDiagonalRow + 1) * q];
                     mine[ku - wave_first - 31 + lane + p.border + kLutPad] += sum[0] + sum[1];
                     tile_sync<true>();
                 } else {
@@ -328,7 +330,7 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
 }
 
 template <typename T, int DP, bool DROP, bool FEW>
-__global__ __launch_bounds__(256, FEW || T::bytes == 4 ? 1 : 2) void attention_backward_kv(AttnParams p) {
+__global__ __launch_bounds__(256, FEW || T::bytes == 4 || DP > 64 ? 1 : 2) void attention_backward_kv(AttnParams p) {
     typedef typename T::raw_t raw_t;
     typedef BwdGeo<T, DP, FEW> Geo;
     constexpr int ROWS = Geo::ROWS, NT = FEW ? 64 : 256;

@@ -241,18 +241,20 @@ __device__ __forceinline__ int a_row(int m) {
 
 // An LDS tile: rows of DP elements without gaps (an asynchronous load writes a
 // wave's 16-byte chunks one after another), whose chunks change places by row
-// so that neither of two reads meets a bank twice: the 16-byte reads of eight
-// consecutive lanes, which lie in rows r .. r + 3 and r + 8 .. r + 11 (a_row),
-// and the transposing read, whose 32 lanes cover 64 bytes of rows r .. r + 3.
+// so that neither of two reads meets a bank twice.  The 64 banks of four bytes
+// serve sixteen lanes of a 16-byte read at once, which lie in one chunk column
+// of sixteen rows (a_row), and 32 lanes of a transposing read, which cover
+// four chunks, an aligned group, of rows r .. r + 3, r a multiple of four.
 template <typename T, int DP>
 struct Tile {
     static constexpr int EPC = 16 / T::bytes;       // elements of a chunk
     static constexpr int CPR = DP / EPC;            // chunks of a row
     __device__ __forceinline__ static int turn(int row) {
-        if constexpr (T::bytes == 4) return (row & 3) | (row >> 1 & 4);
-        if constexpr (DP == 128) return (row & 3) << 2 | (row >> 3 & 1);
-        if constexpr (DP == 64) return (row & 2) << 1 | (row >> 3 & 1);
-        return row >> 3 & 1;
+        if constexpr (T::bytes == 4) return CPR % 16 == 0 ? row & 15 : row >> 1 & 7;
+        const int low = row >> 2 & 3;
+        if constexpr (DP == 128) return (row & 3) << 2 | low;
+        if constexpr (DP == 64) return (row & 2) << 1 | low;
+        return low;
     }
     // element offset of the chunk that holds column col
     __device__ __forceinline__ static int chunk(int row, int col) {
@@ -377,11 +379,10 @@ __device__ __forceinline__ Frag<T> frag_lds_transposed(const typename T::raw_t *
     } else {
         typedef __attribute__((address_space(3))) s16v4 *lds_s16v4;
         const int row = row0 + 8 * (lane >> 5) + (lane >> 2 & 3), col = col0 + (lane & 16) + 4 * (lane & 3);
-        const typename T::raw_t *p = lds + Tile<T, DP>::chunk(row, col) + (col & 4);
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {   // four rows on, the chunks' places are the same
-            const u32x2 v = __builtin_bit_cast(
-                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16v4)(p + 4 * n * DP)));
+        for (int n = 0; n < 2; ++n) {
+            const typename T::raw_t *p = lds + Tile<T, DP>::chunk(row + 4 * n, col) + (col & 4);
+            const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16v4)p));
             f.w[0][2 * n] = v[0];
             f.w[0][2 * n + 1] = v[1];
         }
