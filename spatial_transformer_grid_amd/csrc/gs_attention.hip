@@ -27,8 +27,10 @@ struct FwdGeo {
     static constexpr int KEYS = FEW || T::bytes == 4 ? 32 : 64;   // keys of an LDS tile
     static constexpr int tile_elems = KEYS * DP;
     static constexpr int SUM = DP + 4;                            // floats of a row of a wave's O
-    // two buffers of K and V, or one of each wave's own, whose place the waves' O takes
-    static constexpr int tile_bytes = (FEW ? 4 : 2) * 2 * tile_elems * T::bytes;
+    // two buffers of K and V, a block's or each wave's own (one, where two would
+    // leave a compute unit with one block); the waves' O takes their place
+    static constexpr int bufs = FEW && DP * T::bytes > 128 ? 1 : 2;
+    static constexpr int tile_bytes = (FEW ? 4 : 1) * bufs * 2 * tile_elems * T::bytes;
     static constexpr int fixed_bytes = FEW && 4 * 32 * SUM * 4 > tile_bytes ? 4 * 32 * SUM * 4 : tile_bytes;
 };
 
@@ -38,7 +40,7 @@ struct FwdGeo {
 constexpr float kSlack = 8.0f;
 
 template <typename T, int DP, bool DROP, bool FEW>
-__global__ __launch_bounds__(256, FEW && T::bytes == 4 && DP > 64 ? 1 : 2) void attention_forward(AttnParams p) {
+__global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attention_forward(AttnParams p) {
     typedef typename T::raw_t raw_t;
     typedef FwdGeo<T, DP, FEW> Geo;
     constexpr int KEYS = Geo::KEYS, U = KEYS / 32, NT = FEW ? 64 : 256;
@@ -87,28 +89,12 @@ __global__ __launch_bounds__(256, FEW && T::bytes == 4 && DP > 64 ? 1 : 2) void 
     const raw_t *qrow =
         (const raw_t *)p.q + (int64_t)b * p.qs[0] + (int64_t)h * p.qs[1] + (int64_t)qi * p.qs[2];
     const int tt = FEW ? lane : t;
-    raw_t *Kt = (raw_t *)smem + (FEW ? wave * 2 * Geo::tile_elems : 0);
-    TileCopy<T, DP, KEYS, NT> kc, vc;
-    const bool async = !FEW && p.async;
-    const auto load = [&](raw_t *to, int k0) {      // the block's form: the whole way into LDS
-        if (async) {
-            kc.load(to, kb, p.ks[2], k0, end, p.D, tt);
-            vc.load(to + Geo::tile_elems, vb, p.vs[2], k0, end, p.D, tt);
-        } else {
-            kc.fetch(kb, p.ks[2], k0, end, p.D, vec, tt);
-            kc.put(to, tt);
-            vc.fetch(vb, p.vs[2], k0, end, p.D, vec, tt);
-            vc.put(to + Geo::tile_elems, tt);
-        }
+    raw_t *Kt = (raw_t *)smem + (FEW ? wave * Geo::bufs * 2 * Geo::tile_elems : 0);
+    const auto load = [&](raw_t *to, int k0) {
+        copy_tile<T, DP, KEYS, NT>(to, kb, p.ks[2], k0, end, p.D, p.async, vec, tt);
+        copy_tile<T, DP, KEYS, NT>(to + Geo::tile_elems, vb, p.vs[2], k0, end, p.D, p.async, vec, tt);
     };
-    if (begin < end) {
-        if constexpr (FEW) {
-            kc.fetch(kb, p.ks[2], begin, end, p.D, vec, tt);
-            vc.fetch(vb, p.vs[2], begin, end, p.D, vec, tt);
-        } else {
-            load(Kt, begin);
-        }
-    }
+    if (begin < end) load(Kt, begin);
     // a negative scale moves into Q: the maximum of the scores is then that of the products
     const float scale2 = fabsf(p.scale2);
     Frag<T> qf[DP / 16];
@@ -140,38 +126,29 @@ __global__ __launch_bounds__(256, FEW && T::bytes == 4 && DP > 64 ? 1 : 2) void 
     float m = -INFINITY, l = 0.0f;
     const uint32_t below = (p.threshold - 1) * 0x10001u;
 
-    if constexpr (FEW)
-        if (begin < end) {
-            kc.put(Kt, tt);
-            vc.put(Kt + Geo::tile_elems, tt);
-        }
     for (int k0 = begin, n = 0; k0 < end; k0 += STEP, ++n) {
-        const raw_t *Ks = Kt + (FEW ? 0 : (n & 1) * 2 * Geo::tile_elems);
+        const raw_t *Ks = Kt + (Geo::bufs == 2 ? (n & 1) * 2 * Geo::tile_elems : 0);
         const raw_t *Vs = Ks + Geo::tile_elems;
-        if (!FEW) async_wait();
+        async_wait();
         tile_sync<FEW>();
         const bool more = k0 + STEP < end;
-        if (more) {
-            if constexpr (FEW) {
-                kc.fetch(kb, p.ks[2], k0 + STEP, end, p.D, vec, tt);
-                vc.fetch(vb, p.vs[2], k0 + STEP, end, p.D, vec, tt);
-            } else {
-                load(Kt + ((n + 1) & 1) * 2 * Geo::tile_elems, k0 + STEP);
-            }
-        }
+        if (Geo::bufs == 2 && more) load(Kt + ((n + 1) & 1) * 2 * Geo::tile_elems, k0 + STEP);
         if (FEW || (row0 < p.Lq && !(p.causal && k0 > wave_last))) {
             float s[16 * U];
+            f32x16 st[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                f32x16 st;
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) st[r] = 0.0f;
+                for (int r = 0; r < 16; ++r) st[u][r] = 0.0f;
+            pipelined<T, U * (DP / 16), T::bytes == 4 ? 1 : DP == 32 ? 2 : DP == 96 ? 3 : 4>(
+                [&](int i) {
+                    return frag_lds<T, DP>(Ks, 32 * (i % U) + a_row(lane & 31), 16 * (i / U) + 8 * half);
+                },
+                [&](int i, const Frag<T> &a) { mma<T>(st[i % U], a, qf[i / U]); });
 #pragma unroll
-                for (int x = 0; x < DP / 16; ++x)
-                    mma<T>(st, frag_lds<T, DP>(Ks, 32 * u + a_row(lane & 31), 16 * x + 8 * half), qf[x]);
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[16 * u + r] = st[r];
-            }
+                for (int r = 0; r < 16; ++r) s[16 * u + r] = st[u][r];
             // s[8 x + j]: key k0 + 16 x + 8 half + j of this lane's query, a score
             // once multiplied by mul, with c added
             const int key0 = k0 + 8 * half;
@@ -224,6 +201,7 @@ __global__ __launch_bounds__(256, FEW && T::bytes == 4 && DP > 64 ? 1 : 2) void 
                 sum[i & 1] += s[i];
             }
             l += sum[0] + sum[1];
+            Frag<T> pf[2 * U];
 #pragma unroll
             for (int x = 0; x < 2 * U; ++x) {
                 u32x4 rnd;
@@ -234,19 +212,17 @@ __global__ __launch_bounds__(256, FEW && T::bytes == 4 && DP > 64 ? 1 : 2) void 
 #pragma unroll
                     for (int j = 0; j < 8; ++j) s[8 * x + j] = kept(rnd, j, p.threshold) ? s[8 * x + j] : 0.0f;
                 }
-                Frag<T> pf = frag_pack<T>(s + 8 * x);
-                if constexpr (DROP && T::bytes == 2) frag_keep<T>(pf, rnd, below);
-#pragma unroll
-                for (int d = 0; d < DP / 32; ++d)
-                    mma<T>(acc[d], frag_lds_transposed<T, DP>(Vs, 16 * x, 32 * d, lane), pf);
+                pf[x] = frag_pack<T>(s + 8 * x);
+                if constexpr (DROP && T::bytes == 2) frag_keep<T>(pf[x], rnd, below);
             }
+            pipelined<T, 2 * U * (DP / 32), T::bytes == 4 ? 1 : DP / 32>(
+                [&](int i) { return frag_lds_transposed<T, DP>(Vs, 16 * (i / (DP / 32)), 32 * (i % (DP / 32)), lane); },
+                [&](int i, const Frag<T> &a) { mma<T>(acc[i % (DP / 32)], a, pf[i / (DP / 32)]); });
         }
-        if constexpr (FEW)
-            if (more) {
-                tile_sync<true>();
-                kc.put(Kt, tt);
-                vc.put(Kt + Geo::tile_elems, tt);
-            }
+        if (Geo::bufs == 1 && more) {
+            tile_sync<true>();
+            load(Kt, k0 + STEP);
+        }
     }
     l += __shfl_xor(l, 32);
     if constexpr (!FEW) {

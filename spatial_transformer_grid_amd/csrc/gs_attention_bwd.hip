@@ -31,12 +31,14 @@ constexpr int kDiagonalRow = 68;
 constexpr int kDiagonal = 32 + 32 * kDiagonalRow;    // floats of a wave
 
 // Geometry of both kernels: `ROWS` rows of the axis that is walked in an LDS
-// tile, two buffers of two tensors, or one of each wave's own (FEW).
+// tile, two buffers of two tensors, a block's or each wave's own (FEW; one
+// where two would take more than half of the LDS).
 template <typename T, int DP, bool FEW>
 struct BwdGeo {
     static constexpr int ROWS = FEW || T::bytes == 4 || DP > 64 ? 32 : 64;
     static constexpr int tile_elems = ROWS * DP;
-    static constexpr int copies = FEW ? 4 : 2;
+    static constexpr int bufs = FEW && DP * T::bytes > 128 ? 1 : 2;       // of a block, or of a wave
+    static constexpr int copies = (FEW ? 4 : 1) * bufs;
     static constexpr int SUM = DP + 4;
     static constexpr int own_bytes = copies * 2 * tile_elems * T::bytes;
     // (FEW: the waves' sums take the tiles' place)
@@ -70,7 +72,7 @@ __device__ __forceinline__ tokens_f32x4 add_sums(const float *sums, int r, int a
 }
 
 template <typename T, int DP, bool DROP, bool FEW>
-__global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnParams p) {
+__global__ __launch_bounds__(256, (FEW || T::bytes == 4) && DP > 64 ? 1 : 2) void attention_backward_q(AttnParams p) {
     typedef typename T::raw_t raw_t;
     typedef BwdGeo<T, DP, FEW> Geo;
     constexpr int KEYS = Geo::ROWS, NT = FEW ? 64 : 256;
@@ -101,28 +103,12 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
     const raw_t *kb = (const raw_t *)p.k + (int64_t)b * p.ks[0] + (int64_t)hk * p.ks[1];
     const raw_t *vb = (const raw_t *)p.v + (int64_t)b * p.vs[0] + (int64_t)hk * p.vs[1];
     const int tt = FEW ? lane : t;
-    raw_t *Kt = (raw_t *)smem + (FEW ? wave * 2 * Geo::tile_elems : 0);
-    TileCopy<T, DP, KEYS, NT> kc, vc;
-    const bool async = !FEW && p.async;
-    const auto load = [&](raw_t *to, int k0) {      // the block's form: the whole way into LDS
-        if (async) {
-            kc.load(to, kb, p.ks[2], k0, end, p.D, tt);
-            vc.load(to + Geo::tile_elems, vb, p.vs[2], k0, end, p.D, tt);
-        } else {
-            kc.fetch(kb, p.ks[2], k0, end, p.D, vec, tt);
-            kc.put(to, tt);
-            vc.fetch(vb, p.vs[2], k0, end, p.D, vec, tt);
-            vc.put(to + Geo::tile_elems, tt);
-        }
+    raw_t *Kt = (raw_t *)smem + (FEW ? wave * Geo::bufs * 2 * Geo::tile_elems : 0);
+    const auto load = [&](raw_t *to, int k0) {
+        copy_tile<T, DP, KEYS, NT>(to, kb, p.ks[2], k0, end, p.D, p.async, vec, tt);
+        copy_tile<T, DP, KEYS, NT>(to + Geo::tile_elems, vb, p.vs[2], k0, end, p.D, p.async, vec, tt);
     };
-    if (begin < end) {
-        if constexpr (FEW) {
-            kc.fetch(kb, p.ks[2], begin, end, p.D, vec, tt);
-            vc.fetch(vb, p.vs[2], begin, end, p.D, vec, tt);
-        } else {
-            load(Kt, begin);
-        }
-    }
+    if (begin < end) load(Kt, begin);
     Frag<T> qf[DP / 16], gf[DP / 16];
     float delta = 0.0f;
     {
@@ -171,25 +157,13 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
 
-    if constexpr (FEW)
-        if (begin < end) {
-            kc.put(Kt, tt);
-            vc.put(Kt + Geo::tile_elems, tt);
-        }
     for (int k0 = begin, n = 0; k0 < end; k0 += STEP, ++n) {
-        const raw_t *Ks = Kt + (FEW ? 0 : (n & 1) * 2 * Geo::tile_elems);
+        const raw_t *Ks = Kt + (Geo::bufs == 2 ? (n & 1) * 2 * Geo::tile_elems : 0);
         const raw_t *Vs = Ks + Geo::tile_elems;
-        if (!FEW) async_wait();
+        async_wait();
         tile_sync<FEW>();
         const bool more = k0 + STEP < end;
-        if (more) {
-            if constexpr (FEW) {
-                kc.fetch(kb, p.ks[2], k0 + STEP, end, p.D, vec, tt);
-                vc.fetch(vb, p.vs[2], k0 + STEP, end, p.D, vec, tt);
-            } else {
-                load(Kt + ((n + 1) & 1) * 2 * Geo::tile_elems, k0 + STEP);
-            }
-        }
+        if (Geo::bufs == 2 && more) load(Kt + ((n + 1) & 1) * 2 * Geo::tile_elems, k0 + STEP);
 #pragma unroll
         for (int u = 0; u < KEYS / 32; ++u) {
             const int ku = k0 + 32 * u;              // this 32-key part
@@ -198,11 +172,9 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
 #pragma unroll
             for (int r = 0; r < 16; ++r) st[r] = dp[r] = 0.0f;
             const int row = 32 * u + a_row(lane & 31);
-#pragma unroll
-            for (int x = 0; x < DP / 16; ++x) {
-                mma<T>(st, frag_lds<T, DP>(Ks, row, 16 * x + 8 * half), qf[x]);
-                mma<T>(dp, frag_lds<T, DP>(Vs, row, 16 * x + 8 * half), gf[x]);
-            }
+            pipelined<T, 2 * (DP / 16), T::bytes == 4 ? 1 : 4>(
+                [&](int i) { return frag_lds<T, DP>(i & 1 ? Vs : Ks, row, 8 * (i & ~1) + 8 * half); },
+                [&](int i, const Frag<T> &a) { mma<T>(i & 1 ? dp : st, a, i & 1 ? gf[i >> 1] : qf[i >> 1]); });
             const int key0 = ku + 8 * half;
             const int cls = bias_class(p, ku - wave_last, ku + 31 - wave_first);
             float e[16];
@@ -258,20 +230,17 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
                     else far_hi += sum;
                 }
             }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const Frag<T> df = frag_pack<T>(ds + 8 * x);
-#pragma unroll
-                for (int d = 0; d < DP / 32; ++d)
-                    mma<T>(acc[d], frag_lds_transposed<T, DP>(Ks, 32 * u + 16 * x, 32 * d, lane), df);
-            }
+            const Frag<T> df[2] = {frag_pack<T>(ds), frag_pack<T>(ds + 8)};
+            pipelined<T, 2 * (DP / 32), T::bytes == 4 ? 1 : DP / 32>(
+                [&](int i) {
+                    return frag_lds_transposed<T, DP>(Ks, 32 * u + 16 * (i / (DP / 32)), 32 * (i % (DP / 32)), lane);
+                },
+                [&](int i, const Frag<T> &a) { mma<T>(acc[i % (DP / 32)], a, df[i / (DP / 32)]); });
         }
-        if constexpr (FEW)
-            if (more) {
-                tile_sync<true>();
-                kc.put(Kt, tt);
-                vc.put(Kt + Geo::tile_elems, tt);
-            }
+        if (Geo::bufs == 1 && more) {
+            tile_sync<true>();
+            load(Kt, k0 + STEP);
+        }
     }
     const float scale = p.scale * p.keep_scale;
     if constexpr (!FEW) {
@@ -330,7 +299,7 @@ __global__ __launch_bounds__(256, FEW ? 1 : 2) void attention_backward_q(AttnPar
 }
 
 template <typename T, int DP, bool DROP, bool FEW>
-__global__ __launch_bounds__(256, FEW || T::bytes == 4 || DP > 64 ? 1 : 2) void attention_backward_kv(AttnParams p) {
+__global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void attention_backward_kv(AttnParams p) {
     typedef typename T::raw_t raw_t;
     typedef BwdGeo<T, DP, FEW> Geo;
     constexpr int ROWS = Geo::ROWS, NT = FEW ? 64 : 256;
@@ -378,11 +347,9 @@ __global__ __launch_bounds__(256, FEW || T::bytes == 4 || DP > 64 ? 1 : 2) void 
     const int64_t pairs = (int64_t)p.G * q_tiles;
     const int64_t p0 = pairs * part / p.splits, p1 = pairs * (part + 1) / p.splits;
     const int tt = FEW ? lane : t;
-    raw_t *Qt = (raw_t *)smem + (FEW ? wave * 2 * Geo::tile_elems : 0);
-    float *stats = row_stats + (FEW ? wave * 4 * ROWS : 0);
+    raw_t *Qt = (raw_t *)smem + (FEW ? wave * Geo::bufs * 2 * Geo::tile_elems : 0);
+    float *stats = row_stats + (FEW ? wave * Geo::bufs * 4 * ROWS : 0);
     unsigned char *mask = masks + wave * 128;
-    TileCopy<T, DP, ROWS, NT> qc, gc;
-    const bool async = !FEW && p.async;
     const float keep_inv = 1.0f / p.keep_scale;
 
     for (int g = 0; g < p.G; ++g) {
@@ -419,51 +386,26 @@ __global__ __launch_bounds__(256, FEW || T::bytes == 4 || DP > 64 ? 1 : 2) void 
                 s[3 * ROWS + tt] = delta * keep_inv;
             }
         };
-        const auto fetch = [&](int q0) {            // one wave's form
-            qc.fetch(qb, p.qs[2], q0, p.Lq, p.D, vec, tt);
-            gc.fetch(gb, p.dos[2], q0, p.Lq, p.D, vec, tt);
-            fetch_stats(q0);
-        };
-        const auto put = [&]() {
-            qc.put(Qt, tt);
-            gc.put(Qt + Geo::tile_elems, tt);
-            put_stats(0);
-        };
-        const auto load = [&](int copy, int q0) {   // the block's form: the whole way into LDS
+        const auto load = [&](int copy, int q0) {
             raw_t *to = Qt + copy * 2 * Geo::tile_elems;
             fetch_stats(q0);
-            if (async) {
-                qc.load(to, qb, p.qs[2], q0, p.Lq, p.D, tt);
-                gc.load(to + Geo::tile_elems, gb, p.dos[2], q0, p.Lq, p.D, tt);
-            } else {
-                qc.fetch(qb, p.qs[2], q0, p.Lq, p.D, vec, tt);
-                qc.put(to, tt);
-                gc.fetch(gb, p.dos[2], q0, p.Lq, p.D, vec, tt);
-                gc.put(to + Geo::tile_elems, tt);
-            }
+            copy_tile<T, DP, ROWS, NT>(to, qb, p.qs[2], q0, p.Lq, p.D, p.async, vec, tt);
+            copy_tile<T, DP, ROWS, NT>(to + Geo::tile_elems, gb, p.dos[2], q0, p.Lq, p.D, p.async, vec, tt);
         };
         constexpr int STEP = FEW ? 4 : 1;
         const int begin = FEW ? t0 + wave : t0;
         if (begin < t1) {
-            if constexpr (FEW) {
-                fetch(q_begin + begin * ROWS);
-                put();
-            } else {
-                load(0, q_begin + begin * ROWS);
-                put_stats(0);
-            }
+            load(0, q_begin + begin * ROWS);
+            put_stats(0);
         }
         for (int n = begin, it = 0; n < t1; n += STEP, ++it) {
-            const int q0 = q_begin + n * ROWS, copy = FEW ? 0 : it & 1;
+            const int q0 = q_begin + n * ROWS, copy = Geo::bufs == 2 ? it & 1 : 0;
             const raw_t *Qs = Qt + copy * 2 * Geo::tile_elems, *Gs = Qs + Geo::tile_elems;
             const float *rs = stats + copy * 4 * ROWS;
-            if (!FEW) async_wait();
+            async_wait();
             tile_sync<FEW>();
             const bool more = n + STEP < t1;
-            if (more) {
-                if constexpr (FEW) fetch(q0 + STEP * ROWS);
-                else load((it + 1) & 1, q0 + STEP * ROWS);
-            }
+            if (Geo::bufs == 2 && more) load((it + 1) & 1, q0 + STEP * ROWS);
 #pragma unroll
             for (int u = 0; u < ROWS / 32; ++u) {
                 const int qu = q0 + 32 * u;          // this 32-query part
@@ -472,11 +414,9 @@ __global__ __launch_bounds__(256, FEW || T::bytes == 4 || DP > 64 ? 1 : 2) void 
 #pragma unroll
                 for (int r = 0; r < 16; ++r) st[r] = dp[r] = 0.0f;
                 const int row = 32 * u + a_row(lane & 31);
-#pragma unroll
-                for (int x = 0; x < DP / 16; ++x) {
-                    mma<T>(st, frag_lds<T, DP>(Qs, row, 16 * x + 8 * half), kf[x]);
-                    mma<T>(dp, frag_lds<T, DP>(Gs, row, 16 * x + 8 * half), vf[x]);
-                }
+                pipelined<T, 2 * (DP / 16), T::bytes == 4 ? 1 : 4>(
+                    [&](int i) { return frag_lds<T, DP>(i & 1 ? Gs : Qs, row, 8 * (i & ~1) + 8 * half); },
+                    [&](int i, const Frag<T> &a) { mma<T>(i & 1 ? dp : st, a, i & 1 ? vf[i >> 1] : kf[i >> 1]); });
                 if constexpr (DROP) {
                     // this lane's two calls: query qu + lane % 32, keys
                     // k0 + 16 half .. + 15; one byte of kept bits each
@@ -492,6 +432,7 @@ __global__ __launch_bounds__(256, FEW || T::bytes == 4 || DP > 64 ? 1 : 2) void 
                 }
                 const int cls = bias_class(p, k0 - (first + qu + 31), k0 + 31 - (first + qu));
                 const bool edge = k0 + 32 > len || (p.causal && first + qu < k0 + 31);
+                Frag<T> pf[2], df[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int r0 = 32 * u + 16 * x + 8 * half;   // this lane's eight queries
@@ -527,21 +468,26 @@ __global__ __launch_bounds__(256, FEW || T::bytes == 4 || DP > 64 ? 1 : 2) void 
                         for (int j = 0; j < 8; ++j)
                             if (!live || j < hidden) pd[j] = ds[j] = 0.0f;
                     }
-                    const Frag<T> pf = frag_pack<T>(pd), df = frag_pack<T>(ds);
-#pragma unroll
-                    for (int d = 0; d < DP / 32; ++d) {
-                        mma<T>(dv[d], frag_lds_transposed<T, DP>(Gs, 32 * u + 16 * x, 32 * d, lane), pf);
-                        mma<T>(dk[d], frag_lds_transposed<T, DP>(Qs, 32 * u + 16 * x, 32 * d, lane), df);
-                    }
+                    pf[x] = frag_pack<T>(pd);
+                    df[x] = frag_pack<T>(ds);
                 }
+                // i: (16 queries, 32 columns, dV or dK)
+                pipelined<T, 4 * (DP / 32), T::bytes == 4 ? 1 : 4>(
+                    [&](int i) {
+                        return frag_lds_transposed<T, DP>(i & 1 ? Qs : Gs, 32 * u + 16 * (i / (DP / 16)),
+                                                          32 * (i / 2 % (DP / 32)), lane);
+                    },
+                    [&](int i, const Frag<T> &a) {
+                        mma<T>(i & 1 ? dk[i / 2 % (DP / 32)] : dv[i / 2 % (DP / 32)], a,
+                               i & 1 ? df[i / (DP / 16)] : pf[i / (DP / 16)]);
+                    });
             }
             if (more) {
-                if constexpr (FEW) {
+                if (Geo::bufs == 1) {
                     tile_sync<true>();
-                    put();
-                } else {
-                    put_stats((it + 1) & 1);
+                    load(0, q0 + STEP * ROWS);
                 }
+                put_stats(Geo::bufs == 2 ? (it + 1) & 1 : 0);
             }
         }
     }

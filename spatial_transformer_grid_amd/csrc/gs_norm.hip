@@ -5,6 +5,12 @@
 // and g = dy scale: dx = inv_std (g - mean(g) - xh mean(g xh)); dscale and
 // dbias are sums over rows, made in parts (one per block, its rows in order)
 // and added up by a second kernel, so that the order is fixed.
+//
+// Both are bound by memory, so each row is read once and stays in registers
+// between its passes: NT threads hold E elements each (a wave up to 2048
+// columns, a block of 256 threads up to 8192, one of 1024 up to 32768), and
+// what belongs to a column (scale, bias, the sums of dscale and dbias) stays
+// there from row to row.  Wider rows take the loops over memory at the end.
 #include "gs_tokens.hpp"
 
 namespace gs {
@@ -17,13 +23,33 @@ __device__ __forceinline__ float wave_total(float v) {
     return v;
 }
 
-// Sum over the 256 threads of a block; `red` holds 4 floats.
-__device__ __forceinline__ float block_total(float v, float *red) {
-    v = wave_total(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+// Sums over the NT threads of a row, two at once; `red` holds 2 NT / 64 floats.
+template <int NT>
+__device__ __forceinline__ void row_totals(float &a, float &b, float *red) {
+    a = wave_total(a);
+    b = wave_total(b);
+    if constexpr (NT > 64) {
+        constexpr int W = NT / 64;
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) {
+            red[threadIdx.x >> 6] = a;
+            red[W + (threadIdx.x >> 6)] = b;
+        }
+        __syncthreads();
+        a = b = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            a += red[w];
+            b += red[W + w];
+        }
+    }
+}
+
+template <int NT>
+__device__ __forceinline__ float row_total(float v, float *red) {
+    float none = 0.0f;
+    row_totals<NT>(v, none, red);
+    return v;
 }
 
 template <typename T>
@@ -32,26 +58,220 @@ __device__ __forceinline__ float param(const void *v, int64_t i, int f32) {
     return T::from_raw(((const typename T::raw_t *)v)[i]);
 }
 
-// One block per row, the row read three times (from the cache after the first).
-template <typename T>
-__global__ __launch_bounds__(256) void layer_norm_rows(NormParams p) {
+// A thread's E elements of a row: eight neighbours of every chunk t + NT j where
+// rows allow 16-byte accesses (VEC), else the elements t + NT j.
+template <int NT, bool VEC>
+__device__ __forceinline__ int column(int t, int e) {
+    return VEC ? 8 * (t + NT * (e >> 3)) + (e & 7) : t + NT * e;
+}
+
+template <typename T, int NT, int E, bool VEC>
+__device__ __forceinline__ void load_row(const typename T::raw_t *row, int cols, int t, float *v) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int e = 0; e < E; e += 8) {
+            const int c = column<NT, true>(t, e);
+            const Frag<T> f = frag_global<T>(row, c, cols, c < cols, true);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[e + j] = frag_get<T>(f, j);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int c = column<NT, false>(t, e);
+            v[e] = c < cols ? T::from_raw(row[c]) : 0.0f;
+        }
+    }
+}
+
+template <typename T, int NT, int E, bool VEC>
+__device__ __forceinline__ void store_row(typename T::raw_t *row, int cols, int t, const float *v) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int e = 0; e < E; e += 8) {
+            const int c = column<NT, true>(t, e);
+            const Frag<T> f = frag_pack<T>(v + e);
+            if (c < cols)
+#pragma unroll
+                for (int i = 0; i < T::bytes / 2; ++i) *(u32x4 *)(row + c + i * (16 / T::bytes)) = f.w[i];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int c = column<NT, false>(t, e);
+            if (c < cols) row[c] = to_bits<T>(v[e]);
+        }
+    }
+}
+
+template <typename T, int NT, int E, bool VEC>
+__device__ __forceinline__ void load_params(const void *src, int f32, int cols, int t, float *v) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int c = column<NT, VEC>(t, e);
+        v[e] = src && c < cols ? param<T>(src, c, f32) : 0.0f;
+    }
+}
+
+constexpr int block_threads(int nt) { return nt < 256 ? 256 : nt; }
+
+template <typename T, int NT, int E, bool VEC>
+__global__ __launch_bounds__(block_threads(NT)) void layer_norm_rows(NormParams p) {
     typedef typename T::raw_t raw_t;
-    __shared__ float red[4];
+    constexpr int ROWS = block_threads(NT) / NT;    // rows of a block at a time
+    __shared__ float red[2 * NT / 64];
+    const int t = threadIdx.x % NT, cols = p.cols;
+    const float inv_n = 1.0f / (float)cols;
+    float w[E], b[E];
+    load_params<T, NT, E, VEC>(p.scale, p.param_f32, cols, t, w);
+    load_params<T, NT, E, VEC>(p.bias, p.param_f32, cols, t, b);
+    for (int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / NT; r < p.rows; r += (int64_t)gridDim.x * ROWS) {
+        float x[E];
+        load_row<T, NT, E, VEC>((const raw_t *)p.X + r * p.x_stride, cols, t, x);
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += x[e];
+        const float mean = row_total<NT>(s, red) * inv_n;
+        s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            x[e] -= mean;
+            if (column<NT, VEC>(t, e) < cols) s = fmaf(x[e], x[e], s);
+        }
+        const float inv = 1.0f / sqrtf(row_total<NT>(s, red) * inv_n + p.epsilon);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = fmaf(x[e] * inv, w[e], b[e]);
+        store_row<T, NT, E, VEC>((raw_t *)p.Y + r * p.y_stride, cols, t, x);
+        if (t == 0) {
+            if (p.mean) p.mean[r] = mean;
+            if (p.inv_std) p.inv_std[r] = inv;
+        }
+    }
+}
+
+// Block `part` takes the rows of one part: dx of each, and their sums of dy xh
+// and dy, which the groups of threads add up in order at the end.
+template <typename T, int NT, int E, bool VEC>
+__global__ __launch_bounds__(block_threads(NT)) void layer_norm_backward_rows(NormParams p) {
+    typedef typename T::raw_t raw_t;
+    constexpr int ROWS = block_threads(NT) / NT;
+    __shared__ float red[2 * NT / 64];
+    __shared__ float sums[ROWS > 1 ? ROWS * NT * 8 : 1];
+    const int t = threadIdx.x % NT, group = threadIdx.x / NT, cols = p.cols;
+    const float inv_n = 1.0f / (float)cols;
+    float w[E], ds[E], db[E];
+    load_params<T, NT, E, VEC>(p.scale, p.param_f32, cols, t, w);
+#pragma unroll
+    for (int e = 0; e < E; ++e) ds[e] = db[e] = 0.0f;
+    const int64_t r0 = p.rows * (int64_t)blockIdx.x / gridDim.x, r1 = p.rows * (int64_t)(blockIdx.x + 1) / gridDim.x;
+    for (int64_t r = r0 + group; r < r1; r += ROWS) {
+        float x[E], g[E];
+        load_row<T, NT, E, VEC>((const raw_t *)p.X + r * p.x_stride, cols, t, x);
+        load_row<T, NT, E, VEC>((const raw_t *)p.dY + r * p.dy_stride, cols, t, g);
+        const float mean = p.mean[r], inv = p.inv_std[r];
+        float a = 0.0f, c = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            x[e] = (x[e] - mean) * inv;
+            ds[e] = fmaf(g[e], x[e], ds[e]);
+            db[e] += g[e];
+            g[e] *= w[e];                            // 0 past the row's end, with w
+            a += g[e];
+            c = fmaf(g[e], x[e], c);
+        }
+        row_totals<NT>(a, c, red);
+        a *= inv_n;
+        c *= inv_n;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = inv * (g[e] - a - x[e] * c);
+        store_row<T, NT, E, VEC>((raw_t *)p.dX + r * p.dx_stride, cols, t, x);
+    }
+    if (!p.dscale) return;
+    float *out = p.partial + (int64_t)blockIdx.x * 2 * cols;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        float *v = which ? db : ds;
+        if constexpr (ROWS > 1) {
+            // eight elements of every thread at a time
+#pragma unroll
+            for (int e = 0; e < E; e += 8) {
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sums[(group * 8 + j) * NT + t] = v[e + j];
+                __syncthreads();
+                if (group == 0)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float s = v[e + j];
+#pragma unroll
+                        for (int i = 1; i < ROWS; ++i) s += sums[(i * 8 + j) * NT + t];
+                        const int c = column<NT, VEC>(t, e + j);
+                        if (c < cols) out[which * (int64_t)cols + c] = s;
+                    }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int c = column<NT, VEC>(t, e);
+                if (c < cols) out[which * (int64_t)cols + c] = v[e];
+            }
+        }
+    }
+}
+
+// dscale and dbias from the parts: 64 of the 2 cols columns a block, sixteen
+// waves with a range of the parts each, added in order.
+template <typename T>
+__global__ __launch_bounds__(1024) void layer_norm_param_sums(NormParams p) {
+    __shared__ float red[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t both = 2 * (int64_t)p.cols, c = (int64_t)blockIdx.x * 64 + lane;
+    float s = 0.0f;
+    if (c < both) {
+        const int i0 = p.parts * wave / 16, i1 = p.parts * (wave + 1) / 16;
+        const float *v = p.partial + c;
+        int i = i0;
+        for (; i + 8 <= i1; i += 8) {
+            float a[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] = v[(i + j) * both];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += a[j];
+        }
+        for (; i < i1; ++i) s += v[i * both];
+    }
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave || c >= both) return;
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += red[w][lane];
+    void *const out = c < p.cols ? p.dscale : p.dbias;
+    const int64_t at = c < p.cols ? c : c - p.cols;
+    if (p.param_f32) ((float *)out)[at] = s;
+    else ((typename T::raw_t *)out)[at] = to_bits<T>(s);
+}
+
+// ------------------------------------------- rows past 32768 columns
+
+template <typename T>
+__global__ __launch_bounds__(1024) void layer_norm_wide(NormParams p) {
+    typedef typename T::raw_t raw_t;
+    __shared__ float red[32];
     const int t = threadIdx.x;
     const float inv_n = 1.0f / (float)p.cols;
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const raw_t *x = (const raw_t *)p.X + r * p.x_stride;
         raw_t *y = (raw_t *)p.Y + r * p.y_stride;
         float s = 0.0f;
-        for (int c = t; c < p.cols; c += 256) s += T::from_raw(x[c]);
-        const float mean = block_total(s, red) * inv_n;
+        for (int c = t; c < p.cols; c += 1024) s += T::from_raw(x[c]);
+        const float mean = row_total<1024>(s, red) * inv_n;
         s = 0.0f;
-        for (int c = t; c < p.cols; c += 256) {
+        for (int c = t; c < p.cols; c += 1024) {
             const float d = T::from_raw(x[c]) - mean;
             s = fmaf(d, d, s);
         }
-        const float inv = 1.0f / sqrtf(block_total(s, red) * inv_n + p.epsilon);
-        for (int c = t; c < p.cols; c += 256) {
+        const float inv = 1.0f / sqrtf(row_total<1024>(s, red) * inv_n + p.epsilon);
+        for (int c = t; c < p.cols; c += 1024) {
             const float xh = (T::from_raw(x[c]) - mean) * inv;
             const float b = p.bias ? param<T>(p.bias, c, p.param_f32) : 0.0f;
             y[c] = to_bits<T>(fmaf(xh, param<T>(p.scale, c, p.param_f32), b));
@@ -64,9 +284,9 @@ __global__ __launch_bounds__(256) void layer_norm_rows(NormParams p) {
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void layer_norm_dx_rows(NormParams p) {
+__global__ __launch_bounds__(1024) void layer_norm_dx_wide(NormParams p) {
     typedef typename T::raw_t raw_t;
-    __shared__ float red[4];
+    __shared__ float red[32];
     const int t = threadIdx.x;
     const float inv_n = 1.0f / (float)p.cols;
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
@@ -75,14 +295,15 @@ __global__ __launch_bounds__(256) void layer_norm_dx_rows(NormParams p) {
         raw_t *dx = (raw_t *)p.dX + r * p.dx_stride;
         const float mean = p.mean[r], inv = p.inv_std[r];
         float a = 0.0f, b = 0.0f;
-        for (int c = t; c < p.cols; c += 256) {
+        for (int c = t; c < p.cols; c += 1024) {
             const float g = T::from_raw(dy[c]) * param<T>(p.scale, c, p.param_f32);
             a += g;
             b = fmaf(g, (T::from_raw(x[c]) - mean) * inv, b);
         }
-        a = block_total(a, red) * inv_n;
-        b = block_total(b, red) * inv_n;
-        for (int c = t; c < p.cols; c += 256) {
+        row_totals<1024>(a, b, red);
+        a *= inv_n;
+        b *= inv_n;
+        for (int c = t; c < p.cols; c += 1024) {
             const float g = T::from_raw(dy[c]) * param<T>(p.scale, c, p.param_f32);
             const float xh = (T::from_raw(x[c]) - mean) * inv;
             dx[c] = to_bits<T>(inv * (g - a - xh * b));
@@ -90,10 +311,9 @@ __global__ __launch_bounds__(256) void layer_norm_dx_rows(NormParams p) {
     }
 }
 
-// Partial sums of dscale and dbias: block (c, part) owns 256 columns and the
-// rows of one part.
+// Sums of one part's rows: block (c, part) owns 256 columns.
 template <typename T>
-__global__ __launch_bounds__(256) void layer_norm_dparam_parts(NormParams p) {
+__global__ __launch_bounds__(256) void layer_norm_params_wide(NormParams p) {
     typedef typename T::raw_t raw_t;
     const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (c >= p.cols) return;
@@ -110,49 +330,77 @@ __global__ __launch_bounds__(256) void layer_norm_dparam_parts(NormParams p) {
     p.partial[((int64_t)part * 2 + 1) * p.cols + c] = db;
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void layer_norm_dparam_sum(NormParams p) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= p.cols) return;
-    float s[2] = {0.0f, 0.0f};
-    for (int part = 0; part < p.parts; ++part)
-        for (int i = 0; i < 2; ++i) s[i] += p.partial[((int64_t)part * 2 + i) * p.cols + c];
-    void *const out[2] = {p.dscale, p.dbias};
-    for (int i = 0; i < 2; ++i) {
-        if (p.param_f32) ((float *)out[i])[c] = s[i];
-        else ((typename T::raw_t *)out[i])[c] = to_bits<T>(s[i]);
+// --------------------------------------------------------------- launches
+
+constexpr int kWidest = 32768;       // columns of a row that stays in registers
+
+// Rows of a block at a time.
+int block_rows(int64_t cols) { return cols <= 2048 ? 4 : 1; }
+
+template <typename T, int NT, int E>
+void rows_form(const NormParams &p, bool backward, hipStream_t stream) {
+    constexpr int B = block_threads(NT);
+    if (backward) {
+        const dim3 grid((unsigned)p.parts);
+        if (p.vec) hipLaunchKernelGGL((layer_norm_backward_rows<T, NT, E, true>), grid, dim3(B), 0, stream, p);
+        else hipLaunchKernelGGL((layer_norm_backward_rows<T, NT, E, false>), grid, dim3(B), 0, stream, p);
+        return;
     }
+    const int64_t blocks = (p.rows + B / NT - 1) / (B / NT);
+    const dim3 grid((unsigned)(blocks < 1024 ? blocks : 1024));    // four blocks a compute unit
+    if (p.vec) hipLaunchKernelGGL((layer_norm_rows<T, NT, E, true>), grid, dim3(B), 0, stream, p);
+    else hipLaunchKernelGGL((layer_norm_rows<T, NT, E, false>), grid, dim3(B), 0, stream, p);
+}
+
+template <typename T>
+int rows_launch(const NormParams &p, bool backward, hipStream_t stream) {
+    if (p.cols <= 512) rows_form<T, 64, 8>(p, backward, stream);
+    else if (p.cols <= 1024) rows_form<T, 64, 16>(p, backward, stream);
+    else if (p.cols <= 2048) rows_form<T, 64, 32>(p, backward, stream);
+    else if (p.cols <= 4096) rows_form<T, 256, 16>(p, backward, stream);
+    else if (p.cols <= 8192) rows_form<T, 256, 32>(p, backward, stream);
+    else if (p.cols <= 16384) rows_form<T, 1024, 16>(p, backward, stream);
+    else rows_form<T, 1024, 32>(p, backward, stream);
+    return (int)hipGetLastError();
 }
 
 template <typename T>
 int forward(const NormParams &p, hipStream_t stream) {
-    const dim3 grid((unsigned)(p.rows < 65536 ? p.rows : 65536));
-    hipLaunchKernelGGL(layer_norm_rows<T>, grid, dim3(256), 0, stream, p);
+    if (p.cols <= kWidest) return rows_launch<T>(p, false, stream);
+    hipLaunchKernelGGL(layer_norm_wide<T>, dim3((unsigned)(p.rows < 1024 ? p.rows : 1024)), dim3(1024), 0, stream, p);
     return (int)hipGetLastError();
 }
 
 template <typename T>
 int backward(const NormParams &p, hipStream_t stream) {
-    const unsigned cb = (unsigned)((p.cols + 255) / 256);
-    if (p.rows > 0) {
-        const dim3 grid((unsigned)(p.rows < 65536 ? p.rows : 65536));
-        hipLaunchKernelGGL(layer_norm_dx_rows<T>, grid, dim3(256), 0, stream, p);
+    if (p.rows > 0 && p.cols <= kWidest) {
+        if (const int e = rows_launch<T>(p, true, stream)) return e;
+    } else if (p.rows > 0) {
+        const dim3 grid((unsigned)(p.rows < 1024 ? p.rows : 1024));
+        hipLaunchKernelGGL(layer_norm_dx_wide<T>, grid, dim3(1024), 0, stream, p);
         if (const int e = (int)hipGetLastError()) return e;
+        if (p.dscale) {
+            const dim3 parts((unsigned)((p.cols + 255) / 256), (unsigned)p.parts);
+            hipLaunchKernelGGL(layer_norm_params_wide<T>, parts, dim3(256), 0, stream, p);
+            if (const int e = (int)hipGetLastError()) return e;
+        }
     }
     if (!p.dscale) return 0;
-    if (p.parts > 0) {
-        hipLaunchKernelGGL(layer_norm_dparam_parts<T>, dim3(cb, (unsigned)p.parts), dim3(256), 0, stream, p);
-        if (const int e = (int)hipGetLastError()) return e;
-    }
-    hipLaunchKernelGGL(layer_norm_dparam_sum<T>, dim3(cb), dim3(256), 0, stream, p);
+    const dim3 grid((unsigned)((2 * (int64_t)p.cols + 63) / 64));
+    hipLaunchKernelGGL(layer_norm_param_sums<T>, grid, dim3(1024), 0, stream, p);
     return (int)hipGetLastError();
 }
 
 }  // namespace
 
+// Two blocks a compute unit, fewer where their sums would pass 32 MiB.
 int layer_norm_parts(int64_t rows, int64_t cols) {
-    (void)cols;
-    return (int)(rows < 64 ? rows : 64);
+    if (rows == 0) return 0;
+    int64_t n = (rows + block_rows(cols) - 1) / block_rows(cols);
+    const int64_t most = (int64_t(1) << 22) / cols;
+    if (n > 512) n = 512;
+    if (n > most) n = most < 1 ? 1 : most;
+    return (int)n;
 }
 
 int launch_layer_norm(const NormParams &p, int dtype, hipStream_t stream) {

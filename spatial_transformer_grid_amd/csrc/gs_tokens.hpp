@@ -264,53 +264,21 @@ struct Tile {
 
 __device__ __forceinline__ void async_wait() { __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// Rows row0 .. row0 + ROWS - 1 of a strided tensor on their way into an LDS
-// tile, in 16-byte chunks over NT threads, zeros outside rows < limit and
-// columns < D: through registers (fetch, then put), or by asynchronous loads
-// that write LDS by themselves (load, then async_wait).
+// Rows row0 .. row0 + ROWS - 1 of a strided tensor into an LDS tile, in 16-byte
+// chunks over the NT threads that share it, zeros outside rows < limit and
+// columns < D.  `async`: by loads that write LDS by themselves (async_wait,
+// then tile_sync, before the tile is read), which leaves the registers to the
+// products.  A lane's chunk lands at its own place of the tile, so it is the
+// source column that changes place; reads outside the range of the descriptor
+// give zeros, and ROWS rows span less than 2 GiB.  Otherwise through registers.
 template <typename T, int DP, int ROWS, int NT>
-struct TileCopy {
+__device__ __forceinline__ void copy_tile(typename T::raw_t *lds, const typename T::raw_t *base, int64_t stride,
+                                          int row0, int limit, int D, bool async, bool vec, int t) {
     typedef typename T::raw_t raw_t;
     typedef Tile<T, DP> L;
-    static constexpr int EPC = L::EPC, CPR = L::CPR;
-    static constexpr int N = (ROWS * CPR + NT - 1) / NT;
+    constexpr int EPC = L::EPC, CPR = L::CPR, N = (ROWS * CPR + NT - 1) / NT;
     static_assert(ROWS * CPR % 64 == 0, "a wave has a whole step or none");
-    u32x4 reg[N];
-
-    __device__ __forceinline__ static bool inside(int c) { return ROWS * CPR % NT == 0 || c < ROWS * CPR; }
-
-    __device__ __forceinline__ void fetch(const raw_t *base, int64_t stride, int row0, int limit, int D,
-                                          bool vec, int t) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int c = t + n * NT, r = c / CPR, col = (c - r * CPR) * EPC;
-            u32x4 v = {0, 0, 0, 0};
-            if (inside(c) && row0 + r < limit && col < D) {
-                const raw_t *src = base + (int64_t)(row0 + r) * stride + col;
-                if (vec) {
-                    v = *(const u32x4 *)src;
-                } else {
-                    raw_t e[EPC];
-#pragma unroll
-                    for (int j = 0; j < EPC; ++j) e[j] = col + j < D ? src[j] : raw_t(0);
-                    __builtin_memcpy(&v, e, 16);
-                }
-            }
-            reg[n] = v;
-        }
-    }
-    __device__ __forceinline__ void put(raw_t *lds, int t) const {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int c = t + n * NT, r = c / CPR, col = (c - r * CPR) * EPC;
-            if (inside(c)) *(u32x4 *)(lds + L::chunk(r, col)) = reg[n];
-        }
-    }
-    // A lane's chunk lands at its own place of the tile, so it is the source
-    // column that changes place.  Reads outside the range of the descriptor
-    // give zeros.  The caller has checked that ROWS rows span less than 2 GiB.
-    __device__ __forceinline__ static void load(raw_t *lds, const raw_t *base, int64_t stride, int row0, int limit,
-                                                int D, int t) {
+    if (async) {
         const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
             (void *)(base + (int64_t)row0 * stride), 0, 0x7fffffff, 0x00027000);
 #pragma unroll
@@ -318,13 +286,31 @@ struct TileCopy {
             const int c = t + n * NT, r = c / CPR, col = ((c - r * CPR) ^ L::turn(r)) * EPC;
             const uint32_t at =
                 row0 + r < limit && col < D ? (uint32_t)(r * (int)stride + col) * T::bytes : 0x80000000u;
-            if (inside(c))
+            if (ROWS * CPR % NT == 0 || c < ROWS * CPR)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
                     rsrc, (__attribute__((address_space(3))) void *)(lds + ((t & ~63) + n * NT) * EPC), 16, (int)at, 0,
                     0, 0);
         }
+        return;
     }
-};
+#pragma unroll 1
+    for (int c = t; c < ROWS * CPR; c += NT) {
+        const int r = c / CPR, col = (c - r * CPR) * EPC;
+        u32x4 v = {0, 0, 0, 0};
+        if (row0 + r < limit && col < D) {
+            const raw_t *src = base + (int64_t)(row0 + r) * stride + col;
+            if (vec) {
+                v = *(const u32x4 *)src;
+            } else {
+                raw_t e[EPC];
+#pragma unroll
+                for (int j = 0; j < EPC; ++j) e[j] = col + j < D ? src[j] : raw_t(0);
+                __builtin_memcpy(&v, e, 16);
+            }
+        }
+        *(u32x4 *)(lds + L::chunk(r, col)) = v;
+    }
+}
 
 // Eight elements from column col of a global row (zeros at and past D).
 template <typename T>
@@ -388,6 +374,36 @@ __device__ __forceinline__ Frag<T> frag_lds_transposed(const typename T::raw_t *
         }
     }
     return f;
+}
+
+// N products whose A operands are read from LDS, GROUP at a time: a group is
+// read while the one before is multiplied.  Left alone the compiler reads each
+// operand right before its product and waits for it, and a wave stands still
+// for the latency of LDS each time.  Vector arithmetic may move across the
+// fences (mask 0x406), memory and matrix instructions may not.  GROUP 0 leaves
+// the order to the compiler: where registers are short, or memory is the bound.
+template <typename T, int N, int GROUP, typename Read, typename Multiply>
+__device__ __forceinline__ void pipelined(const Read &read, const Multiply &multiply) {
+    if constexpr (GROUP == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) multiply(i, read(i));
+    } else {
+    static_assert(N % GROUP == 0, "whole groups");
+    Frag<T> a[2][GROUP];
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) a[0][i] = read(i);
+#pragma unroll
+    for (int g = 0; g < N / GROUP; ++g) {
+        if (g + 1 < N / GROUP) {
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i) a[(g + 1) & 1][i] = read((g + 1) * GROUP + i);
+        }
+        __builtin_amdgcn_sched_barrier(0x406);
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) multiply(g * GROUP + i, a[g & 1][i]);
+        __builtin_amdgcn_sched_barrier(0x406);
+    }
+    }
 }
 
 // Four consecutive elements of an output row.
