@@ -119,17 +119,23 @@ def _torch():
     return torch
 
 
+_codes = {}
+
+
 def dtype_code(t) -> int:
-    torch = _torch()
-    codes = {torch.float32: GS_F32, torch.float16: GS_F16, torch.bfloat16: GS_BF16,
-             torch.float64: GS_F64, torch.int8: GS_I8, torch.uint8: GS_U8, torch.int16: GS_I16,
-             torch.int32: GS_I32, torch.int64: GS_I64}
-    for name, code in (("uint16", GS_U16), ("uint32", GS_U32), ("uint64", GS_U64)):
-        if hasattr(torch, name):
-            codes[getattr(torch, name)] = code
-    if t.dtype not in codes:
+    if not _codes:
+        torch = _torch()
+        codes = {torch.float32: GS_F32, torch.float16: GS_F16, torch.bfloat16: GS_BF16,
+                 torch.float64: GS_F64, torch.int8: GS_I8, torch.uint8: GS_U8, torch.int16: GS_I16,
+                 torch.int32: GS_I32, torch.int64: GS_I64}
+        for name, code in (("uint16", GS_U16), ("uint32", GS_U32), ("uint64", GS_U64)):
+            if hasattr(torch, name):
+                codes[getattr(torch, name)] = code
+        _codes.update(codes)
+    code = _codes.get(t.dtype)
+    if code is None:
         raise TypeError("unsupported element type %s" % t.dtype)
-    return codes[t.dtype]
+    return code
 
 
 def _device_tensor(t, name):

@@ -10,8 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 
-from ._binding import (GS_F32, _check, _device_tensor, _I, _P, _ptr, _stream, _torch,
-                       dtype_code)
+from ._binding import GS_F32, GS_OK, _check, _device_tensor, _I, _P, _ptr, _stream, _torch, dtype_code
 from ._binding import lib as _library
 
 _I64 = ctypes.c_int64
@@ -34,6 +33,7 @@ class AttentionDesc(ctypes.Structure):
 
 
 _PDESC = ctypes.POINTER(AttentionDesc)
+_MASK32, _MASK64 = 2 ** 32 - 1, 2 ** 64 - 1
 
 # C entry points and their argument types (mirrors include/gsample_tokens.h)
 TOKEN_SIGNATURES = {
@@ -89,7 +89,11 @@ def _like(t):
 def _output(out, like, dense):
     """`out` checked, or a new tensor: contiguous where `dense`, else laid out like `like`."""
     if out is None:
-        return _torch().empty(like.shape, dtype=like.dtype, device=like.device) if dense else _like(like)
+        if not dense:
+            return _like(like)
+        torch = _torch()
+        return torch.empty_like(like) if like.is_contiguous() else torch.empty(
+            like.shape, dtype=like.dtype, device=like.device)
     if not out.is_cuda or out.shape != like.shape or out.dtype != like.dtype or (
             not out.is_contiguous() if dense else out.shape[-1] > 1 and out.stride(-1) != 1):
         raise ValueError("out must be a %s GPU tensor of shape %s and type %s"
@@ -99,17 +103,35 @@ def _output(out, like, dense):
 
 def _rows(t):
     """`t` as rows of its last axis that one stride separates (copied where none does) and that stride."""
-    flat = t.reshape(-1, t.shape[-1]) if t.numel() else t.contiguous()
     n = t.shape[-1]
+    if t.is_contiguous():
+        return t, n
+    flat = t.reshape(-1, n) if t.numel() else t.contiguous()
     return flat, (flat.stride(0) if flat.dim() == 2 and flat.shape[0] > 1 else n)
 
 
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_handle(stream, device):
+    """The hipStream_t of `stream`, or of the device's current stream.  A call of a few microseconds is
+    made of such steps, so the handle is read without a stream object around it."""
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _workspace(workspace, need, device):
+    """The scratch tensor (kept alive by the caller until the launch), its address and its bytes."""
     if workspace is None:
-        workspace = _torch().empty(need, dtype=_torch().uint8, device=device) if need else None
-    if workspace is None or workspace.numel() == 0:
+        if not need:
+            return None, None, 0
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+        return workspace, workspace.data_ptr(), need
+    if workspace.numel() == 0:
         return None, None, 0
-    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _norm_params(X, scale, bias):
@@ -141,17 +163,17 @@ def layer_norm(X, scale, bias=None, epsilon: float = 1e-5, return_stats: bool = 
     scale, bias = _norm_params(X, scale, bias)
     x, xs = _rows(X)
     cols = X.shape[-1]
-    rows = math.prod(X.shape[:-1])
+    rows = X.numel() // cols if cols else math.prod(X.shape[:-1])
     Y = _output(out, X, True)
     mean = inv_std = None
     if return_stats:
         mean = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
         inv_std = torch.empty_like(mean)
     st = token_lib().gs_layer_norm(
-        _ptr(x), dtype_code(X), rows, cols, xs, _ptr(scale), _ptr(bias), dtype_code(scale),
-        float(epsilon), _ptr(Y), cols, _ptr(mean), _ptr(inv_std),
-        _stream(stream, X.device))
-    _check(st, "gs_layer_norm")
+        x.data_ptr(), dtype_code(X), rows, cols, xs, scale.data_ptr(), _address(bias), dtype_code(scale),
+        epsilon, Y.data_ptr(), cols, _address(mean), _address(inv_std), _stream_handle(stream, X.device))
+    if st != GS_OK:
+        _check(st, "gs_layer_norm")
     return (Y, mean, inv_std) if return_stats else Y
 
 
@@ -170,16 +192,16 @@ def layer_norm_backward(dY, X, scale, mean, inv_std, stream=None, workspace=None
     mean, inv_std = mean.contiguous(), inv_std.contiguous()
     x, xs = _rows(X)
     dy, dys = _rows(dY)
-    dX = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    dX = _output(None, X, True)
     dscale, dbias = torch.empty_like(scale), torch.empty_like(scale)
     need = _I64(0)
     _check(token_lib().gs_layer_norm_backward_workspace_size(rows, cols, ctypes.byref(need)),
            "gs_layer_norm_backward_workspace_size")
     workspace, ws, ws_bytes = _workspace(workspace, need.value, X.device)
     st = token_lib().gs_layer_norm_backward(
-        _ptr(dy), _ptr(x), dtype_code(X), rows, cols, dys, xs, _ptr(scale), dtype_code(scale),
-        _ptr(mean), _ptr(inv_std), _ptr(dX), cols, _ptr(dscale), _ptr(dbias), ws, ws_bytes,
-        _stream(stream, X.device))
+        dy.data_ptr(), x.data_ptr(), dtype_code(X), rows, cols, dys, xs, scale.data_ptr(), dtype_code(scale),
+        mean.data_ptr(), inv_std.data_ptr(), dX.data_ptr(), cols, dscale.data_ptr(), dbias.data_ptr(), ws,
+        ws_bytes, _stream_handle(stream, X.device))
     _check(st, "gs_layer_norm_backward")
     return dX, dscale, dbias
 
@@ -194,10 +216,11 @@ def dropout(X, ratio: float, seed: int, call: int = 0, residual=None, out=None, 
         if residual.dtype != X.dtype or residual.shape != X.shape:
             raise ValueError("residual must have X's shape and element type")
     Y = _output(out, X, True)
-    st = token_lib().gs_dropout(_ptr(X), dtype_code(X), X.numel(), _ptr(residual), float(ratio),
-                                int(seed) & (2 ** 64 - 1), int(call) & (2 ** 32 - 1), _ptr(Y),
-                                _stream(stream, X.device))
-    _check(st, "gs_dropout")
+    st = token_lib().gs_dropout(X.data_ptr(), dtype_code(X), X.numel(), _address(residual), ratio,
+                                int(seed) & _MASK64, int(call) & _MASK32, Y.data_ptr(),
+                                _stream_handle(stream, X.device))
+    if st != GS_OK:
+        _check(st, "gs_dropout")
     return Y
 
 
@@ -211,8 +234,8 @@ def relative_bucket(r: int, num_buckets: int, max_distance: int = 128, bidirecti
 
 def _strides(t):
     # the stride of an axis of one element addresses nothing
-    s, n = t.stride(), t.shape
-    return _S3(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
+    (a, b, c, _), (i, j, k, _) = t.stride(), t.shape
+    return a if i > 1 else 0, b if j > 1 else 0, c if k > 1 else 0
 
 
 def _attention_inputs(Q, K, V, scale, causal, kv_lengths, table, max_distance, bidirectional,
@@ -254,7 +277,7 @@ def _attention_inputs(Q, K, V, scale, causal, kv_lengths, table, max_distance, b
         d.num_buckets, d.max_distance, d.bidirectional = table.shape[0], int(max_distance), int(bidirectional)
     else:
         d.table_dtype = GS_F32
-    d.ratio, d.seed, d.call = float(ratio), int(seed) & (2 ** 64 - 1), int(call) & (2 ** 32 - 1)
+    d.ratio, d.seed, d.call = ratio, int(seed) & _MASK64, int(call) & _MASK32
     return Q, K, V, kv_lengths, table, d
 
 
@@ -287,10 +310,11 @@ def attention(Q, K, V, scale=None, causal: int = 0, kv_lengths=None, table=None,
         workspace, ws, ws_bytes = _workspace(None, need.value, Q.device)
     else:
         workspace, ws, ws_bytes = _workspace(workspace, 0, Q.device)
-    st = token_lib().gs_attention(ctypes.byref(d), _ptr(Q), _ptr(K), _ptr(V), _ptr(kv_lengths),
-                                  _ptr(table), _ptr(O), _ptr(lse), ws, ws_bytes,
-                                  _stream(stream, Q.device))
-    _check(st, "gs_attention")
+    st = token_lib().gs_attention(ctypes.byref(d), Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+                                  _address(kv_lengths), _address(table), O.data_ptr(), _address(lse), ws,
+                                  ws_bytes, _stream_handle(stream, Q.device))
+    if st != GS_OK:
+        _check(st, "gs_attention")
     return (O, lse) if return_lse else O
 
 
@@ -316,8 +340,8 @@ def attention_backward(dO, Q, K, V, O, lse, scale=None, causal: int = 0, kv_leng
            "gs_attention_backward_workspace_size")
     workspace, ws, ws_bytes = _workspace(workspace, need.value, Q.device)
     st = token_lib().gs_attention_backward(
-        ctypes.byref(d), _ptr(dO), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse), _ptr(kv_lengths),
-        _ptr(table), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dtable), ws, ws_bytes,
-        _stream(stream, Q.device))
+        ctypes.byref(d), dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
+        lse.data_ptr(), _address(kv_lengths), _address(table), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(),
+        _address(dtable), ws, ws_bytes, _stream_handle(stream, Q.device))
     _check(st, "gs_attention_backward")
     return dQ, dK, dV, dtable

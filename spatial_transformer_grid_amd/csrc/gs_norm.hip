@@ -106,10 +106,13 @@ __device__ __forceinline__ void store_row(typename T::raw_t *row, int cols, int 
 
 template <typename T, int NT, int E, bool VEC>
 __device__ __forceinline__ void load_params(const void *src, int f32, int cols, int t, float *v) {
+    if (!src) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int c = column<NT, VEC>(t, e);
-        v[e] = src && c < cols ? param<T>(src, c, f32) : 0.0f;
+        for (int e = 0; e < E; ++e) v[e] = 0.0f;
+    } else if (f32) {
+        load_row<F32, NT, E, VEC>((const uint32_t *)src, cols, t, v);
+    } else {
+        load_row<T, NT, E, VEC>((const typename T::raw_t *)src, cols, t, v);
     }
 }
 
