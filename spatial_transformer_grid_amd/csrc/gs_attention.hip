@@ -22,16 +22,21 @@ namespace gs {
 
 namespace {
 
-template <typename T, int DP, bool FEW>
+// WS: into how many parts (1 or 4) the waves of a block split the keys; a block
+// has 128 / WS rows.
+template <typename T, int DP, int WS>
 struct FwdGeo {
+    static constexpr bool FEW = WS == 4;
+    static constexpr int ROWS = kAttnRows / WS;
     static constexpr int KEYS = FEW || T::bytes == 4 ? 32 : 64;   // keys of an LDS tile
+    static constexpr int U = KEYS / 32;
     static constexpr int tile_elems = KEYS * DP;
     static constexpr int SUM = DP + 4;                            // floats of a row of a wave's O
     // two buffers of K and V, a block's or each wave's own (one, where two would
     // leave a compute unit with one block); the waves' O takes their place
     static constexpr int bufs = FEW && DP * T::bytes > 128 ? 1 : 2;
     static constexpr int tile_bytes = (FEW ? 4 : 1) * bufs * 2 * tile_elems * T::bytes;
-    static constexpr int fixed_bytes = FEW && 4 * 32 * SUM * 4 > tile_bytes ? 4 * 32 * SUM * 4 : tile_bytes;
+    static constexpr int fixed_bytes = WS > 1 && 128 * SUM * 4 > tile_bytes ? 128 * SUM * 4 : tile_bytes;
 };
 
 // A new maximum is taken up only where a score passes the old one by more than
@@ -39,22 +44,24 @@ struct FwdGeo {
 // largest fp16 value, and O is not scaled again with each small step.
 constexpr float kSlack = 8.0f;
 
-template <typename T, int DP, bool DROP, bool FEW>
+template <typename T, int DP, bool DROP, int WS>
 __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attention_forward(AttnParams p) {
     typedef typename T::raw_t raw_t;
-    typedef FwdGeo<T, DP, FEW> Geo;
-    constexpr int KEYS = Geo::KEYS, U = KEYS / 32, NT = FEW ? 64 : 256;
+    typedef FwdGeo<T, DP, WS> Geo;
+    constexpr bool FEW = Geo::FEW;
+    constexpr int KEYS = Geo::KEYS, U = Geo::U, ROWS = Geo::ROWS, NT = FEW ? 64 : 256;
     extern __shared__ __align__(16) unsigned char smem[];
     float *luts = (float *)(smem + Geo::fixed_bytes);
-    __shared__ float stat[4][2][32];                 // FEW: maximum and sum of each wave
+    __shared__ float stat[WS][2][ROWS];              // maximum and sum of each part
 
     int unit, tile, part;
     if (!block_place(p, !FEW, unit, tile, part)) return;
     const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int rg = wave % (4 / WS), wp = wave / (4 / WS);   // the wave's 32 rows, its part of the keys
     // the lane's row: query qi of head h
     int b, h, hk, g = 0, qi, rows;
-    const int row = FEW ? tile * 32 + (lane & 31) : tile * kAttnRows + wave * 32 + (lane & 31);
+    const int row0 = tile * ROWS + rg * 32, row = row0 + (lane & 31);
     if (FEW && p.pack) {
         b = unit / p.Hkv;
         hk = unit - b * p.Hkv;
@@ -74,11 +81,10 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
     const int first = p.from_end ? len - p.Lq : p.first;
     const int pos = first + qi;
     // positions of the wave's rows, and the last one of the block's
-    const int row0 = FEW ? tile * 32 : tile * kAttnRows + wave * 32;
     const int wave_first = FEW && p.pack ? first : first + row0;
     const int wave_last = FEW && p.pack ? first + p.Lq - 1 : wave_first + 31;
     const int block_last =
-        FEW && p.pack ? wave_last : first + min(FEW ? row0 + 32 : (tile + 1) * kAttnRows, p.Lq) - 1;
+        FEW && p.pack ? wave_last : first + min((tile + 1) * ROWS, p.Lq) - 1;
     const int end = min(p.causal ? min(len, block_last + 1) : len, FEW ? (part + 1) * p.chunk : len);
     const int begin = FEW ? part * p.chunk + wave * KEYS : 0;
     constexpr int STEP = FEW ? 4 * KEYS : KEYS;
@@ -145,6 +151,17 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
                     return frag_lds<T, DP>(Ks, 32 * (i % U) + a_row(lane & 31), 16 * (i / U) + 8 * half);
                 },
                 [&](int i, const Frag<T> &a) { mma<T>(st[i % U], a, qf[i / U]); });
+            // the generator runs while the products do
+            u32x4 rnd[2 * U];
+            if constexpr (DROP)
+#pragma unroll
+                for (int x = 0; x < 2 * U; ++x) {
+                    rnd[x] = philox((uint32_t)(k0 + 8 * half + 16 * x) >> 3, (uint32_t)qi, (uint32_t)(b * p.H + h),
+                                    p.call, p.seed_lo, p.seed_hi);
+                    if constexpr (T::bytes == 2)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) rnd[x][i] = kept_pair(rnd[x][i], below);
+                }
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -162,9 +179,11 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
             // own rounding hides the difference
             if (cls == 0 || edge || T::bytes == 4) {
                 if (cls == 0) {
-                    const float *at = lut + (key0 - pos + p.border + kLutPad);
+                    float bias[16 * U];
+                    read_all<16 * U>(lut + (key0 - pos + p.border + kLutPad), bias,
+                                     [](int i) { return 16 * (i >> 3) + (i & 7); });
 #pragma unroll
-                    for (int i = 0; i < 16 * U; ++i) s[i] = fmaf(s[i], mul, at[16 * (i >> 3) + (i & 7)]);
+                    for (int i = 0; i < 16 * U; ++i) s[i] = fmaf(s[i], mul, bias[i]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16 * U; ++i) s[i] = fmaf(s[i], mul, c);
@@ -172,6 +191,7 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
                 mul = 1.0f;
                 c = 0.0f;
                 if (edge) {
+                    rare<16 * U>(s);
                     const int seen = (p.causal ? min(end, pos + 1) : end) - key0;
 #pragma unroll
                     for (int i = 0; i < 16 * U; ++i)
@@ -182,7 +202,7 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
 #pragma unroll
             for (int i = 1; i < 16 * U; ++i) top = fmaxf(top, s[i]);
             top = fmaf(top, mul, c);
-            top = fmaxf(top, __shfl_xor(top, 32));
+            top = fmaxf(top, other_half(top));
             if (__any(top > m + kSlack)) {
                 const float next = fmaxf(m, top);
                 const float alpha = next == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - next);
@@ -204,16 +224,12 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
             Frag<T> pf[2 * U];
 #pragma unroll
             for (int x = 0; x < 2 * U; ++x) {
-                u32x4 rnd;
-                if constexpr (DROP)
-                    rnd = philox((uint32_t)(key0 + 16 * x) >> 3, (uint32_t)qi, (uint32_t)(b * p.H + h), p.call,
-                                 p.seed_lo, p.seed_hi);
                 if constexpr (DROP && T::bytes == 4) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s[8 * x + j] = kept(rnd, j, p.threshold) ? s[8 * x + j] : 0.0f;
+                    for (int j = 0; j < 8; ++j) s[8 * x + j] = kept(rnd[x], j, p.threshold) ? s[8 * x + j] : 0.0f;
                 }
                 pf[x] = frag_pack<T>(s + 8 * x);
-                if constexpr (DROP && T::bytes == 2) frag_keep<T>(pf[x], rnd, below);
+                if constexpr (DROP && T::bytes == 2) frag_keep<T>(pf[x], rnd[x]);
             }
             pipelined<T, 2 * U * (DP / 32), T::bytes == 4 ? 1 : DP / 32>(
                 [&](int i) { return frag_lds_transposed<T, DP>(Vs, 16 * (i / (DP / 32)), 32 * (i % (DP / 32)), lane); },
@@ -225,7 +241,7 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
         }
     }
     l += __shfl_xor(l, 32);
-    if constexpr (!FEW) {
+    if constexpr (WS == 1) {
         if (!live) return;
         const float norm = l > 0.0f || l != l ? p.keep_scale / l : 0.0f;
         raw_t *orow = (raw_t *)p.o + (int64_t)b * p.os[0] + (int64_t)h * p.os[1] + (int64_t)qi * p.os[2];
@@ -238,17 +254,19 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
         if (p.lse && half == 0)
             p.lse[(int64_t)unit * p.Lq + qi] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
     } else {
-        // the waves' O, l under a common maximum, added in the order of the waves
+        // the parts' O and l under a common maximum, added in the order of the parts
+        const int col = rg * 32 + (lane & 31);
         if (half == 0) {
-            stat[wave][0][lane] = m;
-            stat[wave][1][lane] = l;
+            stat[wp][0][col] = m;
+            stat[wp][1][col] = l;
         }
         __syncthreads();
-        const int col = lane & 31;
-        const float all = fmaxf(fmaxf(stat[0][0][col], stat[1][0][col]), fmaxf(stat[2][0][col], stat[3][0][col]));
+        float all = stat[0][0][col];
+#pragma unroll
+        for (int w = 1; w < WS; ++w) all = fmaxf(all, stat[w][0][col]);
         const float alpha = all == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - all);
         float *sums = (float *)smem;
-        float *mine = sums + (wave * 32 + col) * Geo::SUM + 4 * half;
+        float *mine = sums + (wp * ROWS + col) * Geo::SUM + 4 * half;
 #pragma unroll
         for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
@@ -256,19 +274,19 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
                 *(tokens_f32x4 *)(mine + 32 * d + 2 * r) = tokens_f32x4{acc[d][r] * alpha, acc[d][r + 1] * alpha,
                                                                        acc[d][r + 2] * alpha, acc[d][r + 3] * alpha};
         __syncthreads();
-        for (int i = t; i < 32 * (DP / 4); i += 256) {
+        for (int i = t; i < ROWS * (DP / 4); i += 256) {
             const int r = i / (DP / 4), at = (i - r * (DP / 4)) * 4;
-            const int rr = tile * 32 + r;
+            const int rr = tile * ROWS + r;
             if (rr >= rows || at >= p.D) continue;
             float big = stat[0][0][r], lr = 0.0f;
 #pragma unroll
-            for (int w = 1; w < 4; ++w) big = fmaxf(big, stat[w][0][r]);
+            for (int w = 1; w < WS; ++w) big = fmaxf(big, stat[w][0][r]);
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
+            for (int w = 0; w < WS; ++w)
                 if (big != -INFINITY) lr = fmaf(stat[w][1][r], __builtin_amdgcn_exp2f(stat[w][0][r] - big), lr);
             tokens_f32x4 v = *(const tokens_f32x4 *)(sums + r * Geo::SUM + at);
 #pragma unroll
-            for (int w = 1; w < 4; ++w) v += *(const tokens_f32x4 *)(sums + (w * 32 + r) * Geo::SUM + at);
+            for (int w = 1; w < WS; ++w) v += *(const tokens_f32x4 *)(sums + (w * ROWS + r) * Geo::SUM + at);
             const int64_t flat = (int64_t)unit * rows + rr;       // (b, h, qi) in either order of the rows
             if (p.splits > 1) {
                 const int64_t all_rows = (int64_t)p.B * p.H * p.Lq, dr = split_row(p.D);
@@ -322,12 +340,12 @@ __global__ __launch_bounds__(256) void attention_combine(AttnParams p) {
     if (p.lse && lane == 0) p.lse[r] = l == 0.0f ? -INFINITY : (big + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-template <typename T, int DP, bool DROP, bool FEW>
+template <typename T, int DP, bool DROP, int WS>
 int launch_form(const AttnParams &p, hipStream_t stream) {
     const int heads = p.pack ? p.G : 1;
-    const int smem = FwdGeo<T, DP, FEW>::fixed_bytes + heads * p.lut * 4 + (p.lut ? p.side * 2 : 0);
+    const int smem = FwdGeo<T, DP, WS>::fixed_bytes + heads * p.lut * 4 + (p.lut ? p.side * 2 : 0);
     const dim3 grid((p.nblocks + 7) / 8 * 8);
-    void (*const fn)(AttnParams) = attention_forward<T, DP, DROP, FEW>;
+    void (*const fn)(AttnParams) = attention_forward<T, DP, DROP, WS>;
     if (smem > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void *)fn, hipFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != hipSuccess) return (int)e;
@@ -336,19 +354,24 @@ int launch_form(const AttnParams &p, hipStream_t stream) {
     return (int)hipGetLastError();
 }
 
+template <typename T, int DP, int WS>
+int launch_ws(const AttnParams &p, hipStream_t stream) {
+    return p.threshold ? launch_form<T, DP, true, WS>(p, stream) : launch_form<T, DP, false, WS>(p, stream);
+}
+
 template <typename T, int DP>
-int launch_dp(const AttnParams &p, bool few, hipStream_t stream) {
-    if (few) return p.threshold ? launch_form<T, DP, true, true>(p, stream) : launch_form<T, DP, false, true>(p, stream);
-    return p.threshold ? launch_form<T, DP, true, false>(p, stream) : launch_form<T, DP, false, false>(p, stream);
+int launch_dp(const AttnParams &p, int ways, hipStream_t stream) {
+    if (ways == 4) return launch_ws<T, DP, 4>(p, stream);
+    return launch_ws<T, DP, 1>(p, stream);
 }
 
 template <typename T>
-int launch_t(const AttnParams &p, bool few, hipStream_t stream) {
+int launch_t(const AttnParams &p, int ways, hipStream_t stream) {
     const int dp = padded_dim(p.D);
-    const int e = dp == 32   ? launch_dp<T, 32>(p, few, stream)
-                  : dp == 64 ? launch_dp<T, 64>(p, few, stream)
-                  : dp == 96 ? launch_dp<T, 96>(p, few, stream)
-                             : launch_dp<T, 128>(p, few, stream);
+    const int e = dp == 32   ? launch_dp<T, 32>(p, ways, stream)
+                  : dp == 64 ? launch_dp<T, 64>(p, ways, stream)
+                  : dp == 96 ? launch_dp<T, 96>(p, ways, stream)
+                             : launch_dp<T, 128>(p, ways, stream);
     if (e || p.splits <= 1) return e;
     const int64_t rows = (int64_t)p.B * p.H * p.Lq;
     hipLaunchKernelGGL(attention_combine<T>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
@@ -365,8 +388,9 @@ AttnPlan plan_forward(const AttnParams &p, int, bool workspace) {
     a.units = p.B * p.H;
     a.tiles = (p.Lq + kAttnRows - 1) / kAttnRows;
     a.chunk = p.Lk;
-    a.few = p.Lq <= 32 || (int64_t)a.units * a.tiles < 256;
-    if (!a.few) return a;
+    const int64_t full = (int64_t)a.units * a.tiles;
+    a.ways = p.Lq <= 32 || full < 256 ? 4 : 1;
+    if (a.ways == 1) return a;
     // tables of all heads that share a key head take at most 16 KiB of LDS
     if (p.G > 1 && p.G * (int64_t)p.Lq <= 32 && (int64_t)p.G * p.lut * 4 <= 16384) {
         a.pack = 1;
@@ -393,9 +417,9 @@ int launch_attention(const AttnParams &p0, int dtype, hipStream_t stream) {
     p.tiles = a.tiles;
     p.units = a.units;
     p.nblocks = a.units * a.tiles * a.splits;
-    if (dtype == 0) return launch_t<F32>(p, a.few, stream);
-    if (dtype == 1) return launch_t<F16>(p, a.few, stream);
-    return launch_t<BF16>(p, a.few, stream);
+    if (dtype == 0) return launch_t<F32>(p, a.ways, stream);
+    if (dtype == 1) return launch_t<F16>(p, a.ways, stream);
+    return launch_t<BF16>(p, a.ways, stream);
 }
 
 }  // namespace gs

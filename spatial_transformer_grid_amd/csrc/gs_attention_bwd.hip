@@ -30,19 +30,22 @@ namespace {
 constexpr int kDiagonalRow = 68;
 constexpr int kDiagonal = 32 + 32 * kDiagonalRow;    // floats of a wave
 
-// Geometry of both kernels: `ROWS` rows of the axis that is walked in an LDS
-// tile, two buffers of two tensors, a block's or each wave's own (FEW; one
-// where two would take more than half of the LDS).
-template <typename T, int DP, bool FEW>
+// Geometry of both kernels.  WS: into how many parts (1 or 4) the waves of a block
+// split the axis that is walked; a block has BLOCK = 128 / WS rows of the other.  ROWS
+// rows of the walked axis in an LDS tile, two buffers of two tensors, a block's
+// or each wave's own (FEW; one where two would take more than half of the LDS).
+template <typename T, int DP, int WS>
 struct BwdGeo {
+    static constexpr bool FEW = WS == 4;
+    static constexpr int BLOCK = kAttnRows / WS;
     static constexpr int ROWS = FEW || T::bytes == 4 || DP > 64 ? 32 : 64;
     static constexpr int tile_elems = ROWS * DP;
     static constexpr int bufs = FEW && DP * T::bytes > 128 ? 1 : 2;       // of a block, or of a wave
     static constexpr int copies = (FEW ? 4 : 1) * bufs;
     static constexpr int SUM = DP + 4;
     static constexpr int own_bytes = copies * 2 * tile_elems * T::bytes;
-    // (FEW: the waves' sums take the tiles' place)
-    static constexpr int tile_bytes = FEW && 4 * 32 * SUM * 4 > own_bytes ? 4 * 32 * SUM * 4 : own_bytes;
+    // (WS > 1: the parts' sums take the tiles' place)
+    static constexpr int tile_bytes = WS > 1 && 128 * SUM * 4 > own_bytes ? 128 * SUM * 4 : own_bytes;
 };
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -51,10 +54,11 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
-// A wave's 32-row result (transposed: the lane's column is its row) into LDS.
+// A wave's 32-row result (transposed: the lane's column is its row) into LDS,
+// from row `row` of its part on.
 template <int DP, int SUM>
-__device__ __forceinline__ void put_sums(float *sums, const f32x16 *acc, int wave, int lane) {
-    float *mine = sums + (wave * 32 + (lane & 31)) * SUM + 4 * (lane >> 5);
+__device__ __forceinline__ void put_sums(float *sums, const f32x16 *acc, int row, int lane) {
+    float *mine = sums + (row + (lane & 31)) * SUM + 4 * (lane >> 5);
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
@@ -63,19 +67,20 @@ __device__ __forceinline__ void put_sums(float *sums, const f32x16 *acc, int wav
                 tokens_f32x4{acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]};
 }
 
-template <int SUM>
+template <int SUM, int WS>
 __device__ __forceinline__ tokens_f32x4 add_sums(const float *sums, int r, int at) {
     tokens_f32x4 v = *(const tokens_f32x4 *)(sums + r * SUM + at);
 #pragma unroll
-    for (int w = 1; w < 4; ++w) v += *(const tokens_f32x4 *)(sums + (w * 32 + r) * SUM + at);
+    for (int w = 1; w < WS; ++w) v += *(const tokens_f32x4 *)(sums + (w * (128 / WS) + r) * SUM + at);
     return v;
 }
 
-template <typename T, int DP, bool DROP, bool FEW>
-__global__ __launch_bounds__(256, (FEW || T::bytes == 4) && DP > 64 ? 1 : 2) void attention_backward_q(AttnParams p) {
+template <typename T, int DP, bool DROP, int WS>
+__global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2) void attention_backward_q(AttnParams p) {
     typedef typename T::raw_t raw_t;
-    typedef BwdGeo<T, DP, FEW> Geo;
-    constexpr int KEYS = Geo::ROWS, NT = FEW ? 64 : 256;
+    typedef BwdGeo<T, DP, WS> Geo;
+    constexpr bool FEW = Geo::FEW;
+    constexpr int KEYS = Geo::ROWS, BLOCK = Geo::BLOCK, NT = FEW ? 64 : 256;
     extern __shared__ __align__(16) unsigned char smem[];
     float *lut = (float *)(smem + Geo::tile_bytes);
     float *diagonals = lut + (p.lut + 3) / 4 * 4;    // [wave][kDiagonal]
@@ -90,10 +95,11 @@ __global__ __launch_bounds__(256, (FEW || T::bytes == 4) && DP > 64 ? 1 : 2) voi
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int len = sequence_length(p, b);
     const int first = p.from_end ? len - p.Lq : p.first;
-    const int q0 = FEW ? tile * 32 : tile * kAttnRows + wave * 32;
+    const int rg = wave % (4 / WS), wp = wave / (4 / WS);   // the wave's 32 rows, its part of the keys
+    const int q0 = tile * BLOCK + rg * 32;
     const int qi = q0 + (lane & 31);
     const int pos = first + qi;
-    const int block_last = first + min(FEW ? q0 + 32 : (tile + 1) * kAttnRows, p.Lq) - 1;
+    const int block_last = first + min((tile + 1) * BLOCK, p.Lq) - 1;
     const int end = p.causal ? min(len, block_last + 1) : len;
     const int wave_first = first + q0, wave_last = wave_first + 31;
     const int begin = FEW ? wave * KEYS : 0;
@@ -134,7 +140,7 @@ __global__ __launch_bounds__(256, (FEW || T::bytes == 4) && DP > 64 ? 1 : 2) voi
         const int64_t at = (int64_t)unit * p.Lq + qi;
         const float v = p.lse[at];
         if (v != -INFINITY) minus_lse = -v * kLog2e;
-        if (half == 0 && (!FEW || wave == 0)) p.delta[at] = delta;
+        if (half == 0 && wp == 0) p.delta[at] = delta;
     }
     delta = delta / p.keep_scale;
     float bias_lo = 0.0f, bias_hi = 0.0f;
@@ -176,13 +182,21 @@ __global__ __launch_bounds__(256, (FEW || T::bytes == 4) && DP > 64 ? 1 : 2) voi
                 [&](int i) { return frag_lds<T, DP>(i & 1 ? Vs : Ks, row, 8 * (i & ~1) + 8 * half); },
                 [&](int i, const Frag<T> &a) { mma<T>(i & 1 ? dp : st, a, i & 1 ? gf[i >> 1] : qf[i >> 1]); });
             const int key0 = ku + 8 * half;
+            u32x4 rnd[2];                            // the generator runs while the products do
+            if constexpr (DROP)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    rnd[x] = philox((uint32_t)(key0 + 16 * x) >> 3, (uint32_t)qi, (uint32_t)unit, p.call, p.seed_lo,
+                                    p.seed_hi);
             const int cls = bias_class(p, ku - wave_last, ku + 31 - wave_first);
             float e[16];
             if (cls == 0) {
-                const float *at = lut + (key0 - pos + p.border + kLutPad);
+                float bias[16];
+                read_all<16>(lut + (key0 - pos + p.border + kLutPad), bias,
+                             [](int i) { return 16 * (i >> 3) + (i & 7); });
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    e[i] = __builtin_amdgcn_exp2f(fmaf(st[i], p.scale2, at[16 * (i >> 3) + (i & 7)]) + minus_lse);
+                    e[i] = __builtin_amdgcn_exp2f(fmaf(st[i], p.scale2, bias[i]) + minus_lse);
             } else {
                 const float c = minus_lse + (cls == 1 ? bias_lo : cls == 2 ? bias_hi : 0.0f);
 #pragma unroll
@@ -191,19 +205,16 @@ __global__ __launch_bounds__(256, (FEW || T::bytes == 4) && DP > 64 ? 1 : 2) voi
             float ds[16];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                u32x4 rnd;
-                if constexpr (DROP)
-                    rnd = philox((uint32_t)(key0 + 16 * x) >> 3, (uint32_t)qi, (uint32_t)unit, p.call, p.seed_lo,
-                                 p.seed_hi);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int i = 8 * x + j;
                     float g = dp[i];
-                    if constexpr (DROP) g = kept(rnd, j, p.threshold) ? g : 0.0f;
+                    if constexpr (DROP) g = kept(rnd[x], j, p.threshold) ? g : 0.0f;
                     ds[i] = e[i] * (g - delta);
                 }
             }
             if (ku + 32 > end || (p.causal && ku + 31 > wave_first)) {
+                rare<16>(ds);
                 const int seen = (p.causal ? min(end, pos + 1) : end) - key0;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -219,7 +230,13 @@ __global__ __launch_bounds__(256, (FEW || T::bytes == 4) && DP > 64 ? 1 : 2) voi
                     tile_sync<true>();
                     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) sum[q & 1] += diagonal[lane - 31 + (kDiagonalRow + 1) * q];
+                    for (int q = 0; q < 32; q += 16) {
+                        float v[16];
+                        read_all<16>(diagonal + lane - 31 + (kDiagonalRow + 1) * q, v,
+                                     [](int i) { return (kDiagonalRow + 1) * i; });
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sum[i & 1] += v[i];
+                    }
                     mine[ku - wave_first - 31 + lane + p.border + kLutPad] += sum[0] + sum[1];
                     tile_sync<true>();
                 } else {
@@ -243,7 +260,7 @@ __global__ __launch_bounds__(256, (FEW || T::bytes == 4) && DP > 64 ? 1 : 2) voi
         }
     }
     const float scale = p.scale * p.keep_scale;
-    if constexpr (!FEW) {
+    if constexpr (WS == 1) {
         if (live) {
             raw_t *drow = (raw_t *)p.dq + (int64_t)b * p.dqs[0] + (int64_t)h * p.dqs[1] + (int64_t)qi * p.dqs[2];
 #pragma unroll
@@ -256,14 +273,13 @@ __global__ __launch_bounds__(256, (FEW || T::bytes == 4) && DP > 64 ? 1 : 2) voi
     } else {
         float *sums = (float *)smem;
         __syncthreads();
-        put_sums<DP, Geo::SUM>(sums, acc, wave, lane);
+        put_sums<DP, Geo::SUM>(sums, acc, wp * BLOCK + rg * 32, lane);
         __syncthreads();
-        for (int i = t; i < 32 * (DP / 4); i += 256) {
-            const int r = i / (DP / 4), at = (i - r * (DP / 4)) * 4;
-            if (q0 + r >= p.Lq) continue;
-            const tokens_f32x4 v = add_sums<Geo::SUM>(sums, r, at);
-            raw_t *drow =
-                (raw_t *)p.dq + (int64_t)b * p.dqs[0] + (int64_t)h * p.dqs[1] + (int64_t)(q0 + r) * p.dqs[2];
+        for (int i = t; i < BLOCK * (DP / 4); i += 256) {
+            const int r = i / (DP / 4), at = (i - r * (DP / 4)) * 4, q = tile * BLOCK + r;
+            if (q >= p.Lq) continue;
+            const tokens_f32x4 v = add_sums<Geo::SUM, WS>(sums, r, at);
+            raw_t *drow = (raw_t *)p.dq + (int64_t)b * p.dqs[0] + (int64_t)h * p.dqs[1] + (int64_t)q * p.dqs[2];
             store4<T>(drow, at, p.D, vec, v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
         }
     }
@@ -298,11 +314,12 @@ __global__ __launch_bounds__(256, (FEW || T::bytes == 4) && DP > 64 ? 1 : 2) voi
     }
 }
 
-template <typename T, int DP, bool DROP, bool FEW>
+template <typename T, int DP, bool DROP, int WS>
 __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void attention_backward_kv(AttnParams p) {
     typedef typename T::raw_t raw_t;
-    typedef BwdGeo<T, DP, FEW> Geo;
-    constexpr int ROWS = Geo::ROWS, NT = FEW ? 64 : 256;
+    typedef BwdGeo<T, DP, WS> Geo;
+    constexpr bool FEW = Geo::FEW;
+    constexpr int ROWS = Geo::ROWS, BLOCK = Geo::BLOCK, NT = FEW ? 64 : 256;
     extern __shared__ __align__(16) unsigned char smem[];
     // per copy of a tile: minus lse without and with the biases of the two ends, delta
     float *row_stats = (float *)(smem + Geo::tile_bytes);
@@ -317,8 +334,8 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int len = sequence_length(p, b);
     const int first = p.from_end ? len - p.Lq : p.first;
-    const int block0 = FEW ? tile * 32 : tile * kAttnRows;
-    const int k0 = FEW ? block0 : block0 + wave * 32;
+    const int rg = wave % (4 / WS), wp = wave / (4 / WS);   // the wave's 32 rows, its part of the queries
+    const int block0 = tile * BLOCK, k0 = block0 + rg * 32;
     const int key = k0 + (lane & 31);
     const bool vec = p.vec, live = key < len;
 
@@ -440,9 +457,11 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
                     const float *dl = rs + 3 * ROWS + r0;
                     float pd[8], ds[8];
                     if (cls == 0) {
-                        const float *at = lut + (key - first - q0 - r0 + p.border + kLutPad);
+                        float bias[8];
+                        read_all<8>(lut + (key - first - q0 - r0 + p.border + kLutPad), bias,
+                                    [](int j) { return -j; });
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) pd[j] = fmaf(st[8 * x + j], p.scale2, at[-j]) + ml[j];
+                        for (int j = 0; j < 8; ++j) pd[j] = fmaf(st[8 * x + j], p.scale2, bias[j]) + ml[j];
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) pd[j] = fmaf(st[8 * x + j], p.scale2, ml[j]);
@@ -452,17 +471,21 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
                     if constexpr (DROP) {
                         u32x2 bits = *(const u32x2 *)(mask + ((lane & 31) >> 3) * 32 + 16 * x + 8 * half);
                         bits = (bits >> (uint32_t)(lane & 7)) & 0x01010101u;
+                        const float keep[8] = {byte_float<0>(bits[0]), byte_float<1>(bits[0]), byte_float<2>(bits[0]),
+                                               byte_float<3>(bits[0]), byte_float<0>(bits[1]), byte_float<1>(bits[1]),
+                                               byte_float<2>(bits[1]), byte_float<3>(bits[1])};
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float keep = (float)(bits[j >> 2] >> (8 * (j & 3)) & 0xffu);
-                            ds[j] = pd[j] * fmaf(dp[8 * x + j], keep, -dl[j]);
-                            pd[j] *= keep;
+                            ds[j] = pd[j] * fmaf(dp[8 * x + j], keep[j], -dl[j]);
+                            pd[j] *= keep[j];
                         }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) ds[j] = pd[j] * (dp[8 * x + j] - dl[j]);
                     }
                     if (edge) {
+                        rare<8>(pd);
+                        rare<8>(ds);
                         const int hidden = p.causal ? key - (first + q0 + r0) : 0;   // queries before the key
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
@@ -492,21 +515,21 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
         }
     }
     const float sk = p.scale * p.keep_scale, sv = p.keep_scale;
-    if constexpr (FEW) {
+    if constexpr (WS > 1) {
         float *sums = (float *)smem;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             __syncthreads();
-            put_sums<DP, Geo::SUM>(sums, which ? dv : dk, wave, lane);
+            put_sums<DP, Geo::SUM>(sums, which ? dv : dk, wp * BLOCK + rg * 32, lane);
             __syncthreads();
             const float scale = which ? sv : sk;
             const int64_t *s = which ? p.dvs : p.dks;
             raw_t *to = (raw_t *)(which ? p.dv : p.dk) + (int64_t)b * s[0] + (int64_t)hk * s[1];
-            for (int i = t; i < 32 * (DP / 4); i += 256) {
-                const int r = i / (DP / 4), at = (i - r * (DP / 4)) * 4;
-                if (k0 + r >= p.Lk) continue;
-                const tokens_f32x4 v = add_sums<Geo::SUM>(sums, r, at);
-                store4<T>(to + (int64_t)(k0 + r) * s[2], at, p.D, vec, v[0] * scale, v[1] * scale, v[2] * scale,
+            for (int i = t; i < BLOCK * (DP / 4); i += 256) {
+                const int r = i / (DP / 4), at = (i - r * (DP / 4)) * 4, row = block0 + r;
+                if (row >= p.Lk) continue;
+                const tokens_f32x4 v = add_sums<Geo::SUM, WS>(sums, r, at);
+                store4<T>(to + (int64_t)row * s[2], at, p.D, vec, v[0] * scale, v[1] * scale, v[2] * scale,
                           v[3] * scale);
             }
         }
@@ -584,15 +607,16 @@ __global__ __launch_bounds__(256) void attention_backward_table(AttnParams p) {
     else ((typename T::raw_t *)p.dtable)[at] = to_bits<T>(v);
 }
 
-template <typename T, int DP, bool FEW>
+template <typename T, int DP, int WS>
 int q_lds(const AttnParams &p, bool table) {
-    return BwdGeo<T, DP, FEW>::tile_bytes + (p.lut + 3) / 4 * 16 + (table ? 4 * (kDiagonal + p.lut) * 4 : 0) + 32 +
+    return BwdGeo<T, DP, WS>::tile_bytes + (p.lut + 3) / 4 * 16 + (table ? 4 * (kDiagonal + p.lut) * 4 : 0) + 32 +
            p.side * 2;
 }
 
-template <typename T, int DP, bool FEW>
+template <typename T, int DP, int WS>
 int kv_lds(const AttnParams &p) {
-    return BwdGeo<T, DP, FEW>::tile_bytes + BwdGeo<T, DP, FEW>::copies * 4 * BwdGeo<T, DP, FEW>::ROWS * 4 + 512 +
+    typedef BwdGeo<T, DP, WS> Geo;
+    return Geo::tile_bytes + Geo::copies * 4 * Geo::ROWS * 4 + 512 +
            (p.lut + 3) / 4 * 16 + p.side * 2;
 }
 
@@ -612,19 +636,25 @@ void take_plan(AttnParams &p, const AttnPlan &a) {
     p.nblocks = a.units * a.tiles * a.splits;
 }
 
+template <typename T, int DP, int WS>
+int launch_q(const AttnParams &p, hipStream_t stream) {
+    return launch(p.threshold ? attention_backward_q<T, DP, true, WS> : attention_backward_q<T, DP, false, WS>, p,
+                  q_lds<T, DP, WS>(p, p.part != nullptr), stream);
+}
+
+template <typename T, int DP, int WS>
+int launch_kv(const AttnParams &p, hipStream_t stream) {
+    return launch(p.threshold ? attention_backward_kv<T, DP, true, WS> : attention_backward_kv<T, DP, false, WS>, p,
+                  kv_lds<T, DP, WS>(p), stream);
+}
+
 template <typename T, int DP>
 int launch_dp(const AttnParams &p0, int dtype, hipStream_t stream) {
     AttnParams p = p0;
-    const bool drop = p.threshold != 0;
     AttnPlan a = plan_backward_q(p, dtype);
     take_plan(p, a);
     if (p.nblocks > 0) {
-        const bool table = p.part != nullptr;
-        const int e = a.few ? launch(drop ? attention_backward_q<T, DP, true, true> : attention_backward_q<T, DP, false, true>,
-                                     p, q_lds<T, DP, true>(p, table), stream)
-                            : launch(drop ? attention_backward_q<T, DP, true, false> : attention_backward_q<T, DP, false, false>,
-                                     p, q_lds<T, DP, false>(p, table), stream);
-        if (e) return e;
+        if (const int e = a.ways == 4 ? launch_q<T, DP, 4>(p, stream) : launch_q<T, DP, 1>(p, stream)) return e;
     }
     if (p.dtable && p.buckets) {
         hipLaunchKernelGGL(attention_backward_table<T>, dim3(p.buckets * p.H), dim3(256), 0, stream, p);
@@ -633,10 +663,7 @@ int launch_dp(const AttnParams &p0, int dtype, hipStream_t stream) {
     a = plan_backward_kv(p, dtype);
     take_plan(p, a);
     if (p.nblocks == 0) return 0;
-    const int e = a.few ? launch(drop ? attention_backward_kv<T, DP, true, true> : attention_backward_kv<T, DP, false, true>,
-                                 p, kv_lds<T, DP, true>(p), stream)
-                        : launch(drop ? attention_backward_kv<T, DP, true, false> : attention_backward_kv<T, DP, false, false>,
-                                 p, kv_lds<T, DP, false>(p), stream);
+    const int e = a.ways == 4 ? launch_kv<T, DP, 4>(p, stream) : launch_kv<T, DP, 1>(p, stream);
     if (e || p.splits <= 1) return e;
     const int64_t threads = (int64_t)p.units * p.Lk * (split_row(p.D) / 2);
     hipLaunchKernelGGL(attention_backward_join<T>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, p);
@@ -656,14 +683,14 @@ int launch_t(const AttnParams &p, int dtype, hipStream_t stream) {
 int few_q_lds(const AttnParams &p, int dtype) {
     const int dp = padded_dim(p.D);
     if (dtype == 0)
-        return dp == 32   ? q_lds<F32, 32, true>(p, true)
-               : dp == 64 ? q_lds<F32, 64, true>(p, true)
-               : dp == 96 ? q_lds<F32, 96, true>(p, true)
-                          : q_lds<F32, 128, true>(p, true);
-    return dp == 32   ? q_lds<F16, 32, true>(p, true)
-           : dp == 64 ? q_lds<F16, 64, true>(p, true)
-           : dp == 96 ? q_lds<F16, 96, true>(p, true)
-                      : q_lds<F16, 128, true>(p, true);
+        return dp == 32   ? q_lds<F32, 32, 4>(p, true)
+               : dp == 64 ? q_lds<F32, 64, 4>(p, true)
+               : dp == 96 ? q_lds<F32, 96, 4>(p, true)
+                          : q_lds<F32, 128, 4>(p, true);
+    return dp == 32   ? q_lds<F16, 32, 4>(p, true)
+           : dp == 64 ? q_lds<F16, 64, 4>(p, true)
+           : dp == 96 ? q_lds<F16, 96, 4>(p, true)
+                      : q_lds<F16, 128, 4>(p, true);
 }
 
 }  // namespace
@@ -672,26 +699,22 @@ AttnPlan plan_backward_q(const AttnParams &p, int dtype) {
     AttnPlan a = {};
     a.splits = 1;
     a.units = p.B * p.H;
-    a.tiles = (p.Lq + kAttnRows - 1) / kAttnRows;
-    a.few = (int64_t)a.units * a.tiles < 256 && few_q_lds(p, dtype) <= kMaxLds;
-    if (a.few) a.tiles = (p.Lq + 31) / 32;
+    const int64_t full = (int64_t)a.units * ((p.Lq + kAttnRows - 1) / kAttnRows);
+    a.ways = full < 256 && few_q_lds(p, dtype) <= kMaxLds ? 4 : 1;
+    a.tiles = (p.Lq + kAttnRows / a.ways - 1) / (kAttnRows / a.ways);
     return a;
 }
 
-AttnPlan plan_backward_kv(const AttnParams &p, int dtype) {
+AttnPlan plan_backward_kv(const AttnParams &p, int) {
     AttnPlan a = {};
     a.splits = 1;
     a.units = p.B * p.Hkv;
-    a.tiles = (p.Lk + kAttnRows - 1) / kAttnRows;
-    const int64_t blocks = (int64_t)a.units * a.tiles;
-    if (blocks == 0 || blocks >= 512) return a;
-    if (blocks < 64) {
-        a.few = true;
-        a.tiles = (p.Lk + 31) / 32;
-        return a;
-    }
+    const int64_t full = (int64_t)a.units * ((p.Lk + kAttnRows - 1) / kAttnRows);
+    a.ways = full < 64 ? 4 : 1;
+    a.tiles = (p.Lk + kAttnRows / a.ways - 1) / (kAttnRows / a.ways);
+    if (full == 0 || full >= 512 || a.ways == 4) return a;
     const int64_t pairs = (int64_t)p.G * ((p.Lq + 63) / 64);
-    int64_t splits = (768 + blocks - 1) / blocks;
+    int64_t splits = (768 + full - 1) / full;
     if (splits > pairs / 8) splits = pairs / 8;
     if (splits <= 1) return a;
     a.splits = (int)splits;

@@ -63,7 +63,7 @@ struct AttnParams {
 
 // How an attention call is laid out on the chip.
 struct AttnPlan {
-    bool few;                 // 32-row blocks whose waves split the other axis
+    int ways;                 // parts of the other axis that a block's waves take: 128 / ways rows a block
     int pack, splits, chunk, tiles, units;
     int64_t split_floats;     // of workspace
 };
@@ -200,14 +200,42 @@ __device__ __forceinline__ void frag_negate(Frag<T> &f) {
 }
 
 // Zeros where the generator drops an element (16-bit types): each half of a
-// word times 1 or 0, as integers.
+// word times 1 or 0, as integers.  (As asm: the compiler would take the words
+// apart into selected halves and put them together again.)
 template <typename T>
-__device__ __forceinline__ void frag_keep(Frag<T> &f, const u32x4 &rnd, uint32_t below) {
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void frag_keep(Frag<T> &f, const u32x4 &kept) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        f.w[0][i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(u16x2, (uint32_t)f.w[0][i]) *
-                                                     __builtin_bit_cast(u16x2, kept_pair(rnd[i], below)));
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w = f.w[0][i];
+        __asm__("v_pk_mul_lo_u16 %0, %0, %1" : "+v"(w) : "v"(kept[i]));
+        f.w[0][i] = w;
+    }
+}
+
+// Byte n of a word as a float.
+template <int N>
+__device__ __forceinline__ float byte_float(uint32_t w) {
+    float f;
+    if constexpr (N == 0) __asm__("v_cvt_f32_ubyte0_e32 %0, %1" : "=v"(f) : "v"(w));
+    else if constexpr (N == 1) __asm__("v_cvt_f32_ubyte1_e32 %0, %1" : "=v"(f) : "v"(w));
+    else if constexpr (N == 2) __asm__("v_cvt_f32_ubyte2_e32 %0, %1" : "=v"(f) : "v"(w));
+    else __asm__("v_cvt_f32_ubyte3_e32 %0, %1" : "=v"(f) : "v"(w));
+    return f;
+}
+
+// The value of lane ^ 32.
+__device__ __forceinline__ float other_half(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v),
+                                                    false, false);
+    return __builtin_bit_cast(float, (uint32_t)((threadIdx.x & 32) ? r[0] : r[1]));
+}
+
+// Keeps a branch that few tiles take a branch: what it does to the N values is
+// not computed beforehand and selected.
+template <int N>
+__device__ __forceinline__ void rare(float *v) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) __asm__ volatile("" : "+v"(v[i]));
 }
 
 // acc (32 x 32) += A (32 x 16) B (16 x 32).  Lane l holds row l % 32 of A and
@@ -379,9 +407,9 @@ __device__ __forceinline__ Frag<T> frag_lds_transposed(const typename T::raw_t *
 // N products whose A operands are read from LDS, GROUP at a time: a group is
 // read while the one before is multiplied.  Left alone the compiler reads each
 // operand right before its product and waits for it, and a wave stands still
-// for the latency of LDS each time.  Vector arithmetic may move across the
-// fences (mask 0x406), memory and matrix instructions may not.  GROUP 0 leaves
-// the order to the compiler: where registers are short, or memory is the bound.
+// for the latency of LDS each time.  Nothing moves across the fences: arithmetic
+// that follows in the source runs while the last products are under way, not
+// before the first.  GROUP 0 leaves the order to the compiler.
 template <typename T, int N, int GROUP, typename Read, typename Multiply>
 __device__ __forceinline__ void pipelined(const Read &read, const Multiply &multiply) {
     if constexpr (GROUP == 0) {
@@ -398,10 +426,10 @@ __device__ __forceinline__ void pipelined(const Read &read, const Multiply &mult
 #pragma unroll
             for (int i = 0; i < GROUP; ++i) a[(g + 1) & 1][i] = read((g + 1) * GROUP + i);
         }
-        __builtin_amdgcn_sched_barrier(0x406);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) multiply(g * GROUP + i, a[g & 1][i]);
-        __builtin_amdgcn_sched_barrier(0x406);
+        __builtin_amdgcn_sched_barrier(0);
     }
     }
 }
@@ -461,6 +489,14 @@ __device__ __forceinline__ void fill_lut(const AttnParams &p, int h, float *lut,
         else v = T::from_raw(((const typename T::raw_t *)p.table)[at]);
         lut[i] = v * kLog2e;
     }
+}
+
+// N entries of an LDS table, all on their way before the first is used.
+template <int N, typename Index>
+__device__ __forceinline__ void read_all(const float *at, float *v, const Index &index) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = at[index(i)];
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // Which bias the relative positions lo .. hi have: 0 the table's, entry by

@@ -265,6 +265,24 @@ def test_attention_table_in_fp32(gs, dtype, causal):
                     table_type="f32")
 
 
+# many heads of short sequences: enough rows that blocks take 64 or 128 of them
+MANY = [  # B, H, Hkv, Lq, Lk, D
+    (16, 16, 16, 40, 70, 64), (32, 33, 11, 35, 65, 32), (9, 30, 15, 130, 97, 64), (37, 14, 14, 200, 131, 16),
+    (4, 128, 64, 64, 64, 128), (70, 15, 5, 37, 97, 96), (5, 52, 52, 129, 257, 24), (33, 32, 32, 33, 150, 127),
+]
+
+
+@pytest.mark.parametrize("shape", MANY)
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("causal", [0, 1])
+def test_attention_of_many_heads(gs, shape, dtype, causal):
+    B, H, Hkv, Lq, Lk, D = shape
+    lengths = [Lk - b * Lk // B for b in range(B)]
+    lengths[-1] = 0
+    check_attention(gs, *shape, dtype, causal=causal, position="end" if causal else 3, lengths=lengths, buckets=8,
+                    distance=24, both=1 - causal, ratio=0.15 * causal, by_position=bool(causal))
+
+
 DECODES = [(1, 8, 8, 1, 77, 64), (3, 8, 2, 1, 300, 128), (2, 8, 1, 1, 1000, 64), (1, 5, 1, 2, 2049, 40),
            (2, 4, 4, 5, 130, 63), (1, 40, 1, 1, 515, 96), (1, 12, 3, 4, 700, 32), (4, 2, 2, 1, 1, 128),
            (1, 1, 1, 1, 5000, 128), (1, 32, 4, 9, 400, 128)]
