@@ -34,11 +34,13 @@ constexpr int kDiagonal = 32 + 32 * kDiagonalRow;    // floats of a wave
 // split the axis that is walked; a block has BLOCK = 128 / WS rows of the other.  ROWS
 // rows of the walked axis in an LDS tile, two buffers of two tensors, a block's
 // or each wave's own (FEW; one where two would take more than half of the LDS).
-template <typename T, int DP, int WS>
+template <typename T, int DP, int WS, bool KV>
 struct BwdGeo {
     static constexpr bool FEW = WS == 4;
     static constexpr int BLOCK = kAttnRows / WS;
-    static constexpr int ROWS = FEW || T::bytes == 4 || DP > 64 ? 32 : 64;
+    // (64 rows of 128 columns leave a compute unit one block: no loss to the
+    // dK / dV kernel, whose registers allow no more, and fewer barriers)
+    static constexpr int ROWS = FEW || T::bytes == 4 || (!KV && DP > 64) ? 32 : 64;
     static constexpr int tile_elems = ROWS * DP;
     static constexpr int bufs = FEW && DP * T::bytes > 128 ? 1 : 2;       // of a block, or of a wave
     static constexpr int copies = (FEW ? 4 : 1) * bufs;
@@ -78,7 +80,7 @@ __device__ __forceinline__ tokens_f32x4 add_sums(const float *sums, int r, int a
 template <typename T, int DP, bool DROP, int WS>
 __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2) void attention_backward_q(AttnParams p) {
     typedef typename T::raw_t raw_t;
-    typedef BwdGeo<T, DP, WS> Geo;
+    typedef BwdGeo<T, DP, WS, false> Geo;
     constexpr bool FEW = Geo::FEW;
     constexpr int KEYS = Geo::ROWS, BLOCK = Geo::BLOCK, NT = FEW ? 64 : 256;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -89,7 +91,7 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
     uint16_t *starts = (uint16_t *)(far + 8);
 
     int unit, tile, part;
-    if (!block_place(p, !FEW, unit, tile, part)) return;
+    if (!block_place(p, !FEW, p.G, unit, tile, part)) return;
     const int b = unit / p.H, h = unit - b * p.H, hk = h / p.G;
     const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -291,25 +293,33 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
         far[wave * 2 + 1] = far_hi;
     }
     __syncthreads();
+    for (int i = t; i < p.lut; i += 256)
+        near[i] = (near[i] + near[p.lut + i]) + (near[2 * p.lut + i] + near[3 * p.lut + i]);
+    __syncthreads();
     // bucket n of a side holds distances starts[n] .. starts[n + 1] - 1, the
     // last one all that follow.  Without the other side a key after the query
-    // counts as distance 0.
+    // counts as distance 0.  Eight lanes a bucket: the last ones are long.
     float *out = p.part + (((int64_t)h * p.B + b) * p.tiles + tile) * p.buckets;
-    for (int n = t; n < p.buckets; n += 256) {
+    const float *zero = near + p.border + kLutPad;   // of distance 0
+    for (int n0 = 0; n0 < p.buckets; n0 += 32) {
+        const int n = n0 + (t >> 3), e = t & 7;
         const bool after = n >= p.side;              // the side of keys after the query
         const int m = after ? n - p.side : n;
-        const bool last = m == p.side - 1;
+        const bool last = m == p.side - 1, in = n < p.buckets;
         float sum = 0.0f;
+        if (in) {
+            const int lo = max((int)starts[m], after ? 1 : 0), hi = last ? p.border + kLutPad + 1 : starts[m + 1];
+            for (int d = lo + e; d < hi; d += 8) sum += zero[after ? d : -d];
+            if (!p.bidirectional && m == 0)
+                for (int d = 1 + e; d <= kLutPad; d += 8) sum += zero[d];
+        }
+#pragma unroll
+        for (int s = 1; s < 8; s <<= 1) sum += __shfl_xor(sum, s);
+        if (!in || e) continue;
         if (last)
             for (int w = 0; w < 4; ++w) sum += far[2 * w + (after ? 1 : 0)];
-        const int lo = max((int)starts[m], after ? 1 : 0), hi = last ? p.border + kLutPad + 1 : starts[m + 1];
-        for (int d = lo; d < hi; ++d)
-            for (int w = 0; w < 4; ++w) sum += near[w * p.lut + p.border + kLutPad + (after ? d : -d)];
-        if (!p.bidirectional && m == 0) {
+        if (!p.bidirectional && m == 0)
             for (int w = 0; w < 4; ++w) sum += far[2 * w + 1];
-            for (int d = 1; d <= kLutPad; ++d)
-                for (int w = 0; w < 4; ++w) sum += near[w * p.lut + p.border + kLutPad + d];
-        }
         out[n] = sum * p.keep_scale;
     }
 }
@@ -317,7 +327,7 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
 template <typename T, int DP, bool DROP, int WS>
 __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void attention_backward_kv(AttnParams p) {
     typedef typename T::raw_t raw_t;
-    typedef BwdGeo<T, DP, WS> Geo;
+    typedef BwdGeo<T, DP, WS, true> Geo;
     constexpr bool FEW = Geo::FEW;
     constexpr int ROWS = Geo::ROWS, BLOCK = Geo::BLOCK, NT = FEW ? 64 : 256;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -328,7 +338,7 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
     uint16_t *starts = (uint16_t *)(lut + (p.lut + 3) / 4 * 4);
 
     int unit, tile, part;
-    if (!block_place(p, false, unit, tile, part)) return;
+    if (!block_place(p, false, 1, unit, tile, part)) return;
     const int b = unit / p.Hkv, hk = unit - b * p.Hkv;
     const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -529,6 +539,12 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
                 const int r = i / (DP / 4), at = (i - r * (DP / 4)) * 4, row = block0 + r;
                 if (row >= p.Lk) continue;
                 const tokens_f32x4 v = add_sums<Geo::SUM, WS>(sums, r, at);
+                if (p.splits > 1) {
+                    const int dr = split_row(p.D);
+                    if (at < p.D)
+                        *(tokens_f32x4 *)(p.split + ((((int64_t)part * p.units + unit) * p.Lk + row) * 2 + which) * dr + at) = v;
+                    continue;
+                }
                 store4<T>(to + (int64_t)row * s[2], at, p.D, vec, v[0] * scale, v[1] * scale, v[2] * scale,
                           v[3] * scale);
             }
@@ -609,13 +625,13 @@ __global__ __launch_bounds__(256) void attention_backward_table(AttnParams p) {
 
 template <typename T, int DP, int WS>
 int q_lds(const AttnParams &p, bool table) {
-    return BwdGeo<T, DP, WS>::tile_bytes + (p.lut + 3) / 4 * 16 + (table ? 4 * (kDiagonal + p.lut) * 4 : 0) + 32 +
+    return BwdGeo<T, DP, WS, false>::tile_bytes + (p.lut + 3) / 4 * 16 + (table ? 4 * (kDiagonal + p.lut) * 4 : 0) + 32 +
            p.side * 2;
 }
 
 template <typename T, int DP, int WS>
 int kv_lds(const AttnParams &p) {
-    typedef BwdGeo<T, DP, WS> Geo;
+    typedef BwdGeo<T, DP, WS, true> Geo;
     return Geo::tile_bytes + Geo::copies * 4 * Geo::ROWS * 4 + 512 +
            (p.lut + 3) / 4 * 16 + p.side * 2;
 }
@@ -705,17 +721,23 @@ AttnPlan plan_backward_q(const AttnParams &p, int dtype) {
     return a;
 }
 
-AttnPlan plan_backward_kv(const AttnParams &p, int) {
+// Where the blocks are too few, parts of the (head, query tile) pairs go to
+// blocks of their own, as long as a wave keeps a tile: as many as run at once,
+// one a compute unit where registers or LDS allow no two.  16 heads of 4096
+// queries on four key heads of 128 columns: 2 parts 400 us, 6 parts 434 us.
+AttnPlan plan_backward_kv(const AttnParams &p, int dtype) {
     AttnPlan a = {};
     a.splits = 1;
     a.units = p.B * p.Hkv;
     const int64_t full = (int64_t)a.units * ((p.Lk + kAttnRows - 1) / kAttnRows);
     a.ways = full < 64 ? 4 : 1;
     a.tiles = (p.Lk + kAttnRows / a.ways - 1) / (kAttnRows / a.ways);
-    if (full == 0 || full >= 512 || a.ways == 4) return a;
-    const int64_t pairs = (int64_t)p.G * ((p.Lq + 63) / 64);
-    int64_t splits = (768 + full - 1) / full;
-    if (splits > pairs / 8) splits = pairs / 8;
+    const int64_t blocks = (int64_t)a.units * a.tiles, tile = a.ways == 4 ? 32 : 64;
+    const int64_t room = (padded_dim(p.D) > (dtype == 0 ? 32 : 64) ? 256 : 512);
+    if (blocks == 0 || 2 * blocks > room) return a;
+    const int64_t pairs = (int64_t)p.G * ((p.Lq + tile - 1) / tile);
+    int64_t splits = room / blocks;
+    if (splits > pairs / (a.ways == 4 ? 4 : 8)) splits = pairs / (a.ways == 4 ? 4 : 8);
     if (splits <= 1) return a;
     a.splits = (int)splits;
     a.split_floats = splits * a.units * p.Lk * 2 * split_row(p.D);

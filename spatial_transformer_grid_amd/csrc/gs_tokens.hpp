@@ -519,29 +519,42 @@ __device__ __forceinline__ void tile_sync() {
     }
 }
 
-// Row tile and unit of a block.  The eighth of the launch that an XCD runs
-// takes whole units where eight divides them: their tiles read the same keys
-// from one L2.  With a causal mask the longest tiles come first, then, from the
+// Row tile, unit and part of a block.  The eighth of the launch that an XCD runs
+// takes whole groups of `group` units (the heads that read one key head) where
+// eight divides the groups: their tiles read the same keys from one L2.  An XCD
+// gets every eighth group, so that sequences of different lengths spread over
+// all of them.  With a causal mask the longest tiles come first, then, from the
 // middle on, the shortest, so that the tiles that a compute unit holds at once
 // add up to about the same work; `longest_last` tells which end is long.
-__device__ __forceinline__ bool block_place(const AttnParams &p, bool longest_last, int &unit, int &tile, int &part) {
-    const int per = (p.nblocks + 7) >> 3;
+__device__ __forceinline__ bool block_place(const AttnParams &p, bool longest_last, int group, int &unit, int &tile,
+                                            int &part) {
     const int x = blockIdx.x & 7, i = (int)(blockIdx.x >> 3);
-    int n = x * per + i;                             // (unit, tile, part), part fastest
-    if (p.causal && (p.units & 7) == 0 && p.splits == 1) {
-        const int u = p.units >> 3, step = i / u;
-        unit = x * u + (i - step * u);
-        const int half = (p.tiles + 1) >> 1;
-        tile = step < half ? step : p.tiles - 1 - (step - half);
-        if (longest_last) tile = p.tiles - 1 - tile;
-        part = 0;
-        return true;
+    const bool whole = p.units % (8 * group) == 0;
+    if (whole) {
+        const int u = p.units >> 3;
+        int local;
+        if (p.causal && p.splits == 1) {
+            const int step = i / u;
+            local = i - step * u;
+            const int half = (p.tiles + 1) >> 1;
+            tile = step < half ? step : p.tiles - 1 - (step - half);
+            part = 0;
+        } else {
+            int n = i;                               // (unit, tile, part), part fastest
+            part = n % p.splits;
+            n /= p.splits;
+            tile = n % p.tiles;
+            local = n / p.tiles;
+        }
+        unit = (local / group * 8 + x) * group + local % group;
+    } else {
+        int n = x * ((p.nblocks + 7) >> 3) + i;
+        if (n >= p.nblocks) return false;
+        part = n % p.splits;
+        n /= p.splits;
+        tile = n % p.tiles;
+        unit = n / p.tiles;
     }
-    if (n >= p.nblocks) return false;
-    part = n % p.splits;
-    n /= p.splits;
-    tile = n % p.tiles;
-    unit = n / p.tiles;
     if (p.causal && longest_last) tile = p.tiles - 1 - tile;
     return true;
 }
