@@ -319,17 +319,29 @@ __global__ __launch_bounds__(256) void attention_combine(AttnParams p) {
     if (r >= rows) return;
     const int lane = threadIdx.x & 63, dr = split_row(p.D);
     const float *st = p.split + (int64_t)p.splits * rows * dr;
+    // a lane a part for the statistics
     float big = -INFINITY;
-    for (int i = 0; i < p.splits; ++i) big = fmaxf(big, st[(i * rows + r) * 2]);
+    for (int i = lane; i < p.splits; i += 64) big = fmaxf(big, st[(i * rows + r) * 2]);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) big = fmaxf(big, __shfl_xor(big, x));
     float l = 0.0f, v[2] = {0.0f, 0.0f};
     const int c0 = lane < p.D ? lane : 0, c1 = lane + 64 < p.D ? lane + 64 : 0;
     if (big != -INFINITY)
-        for (int i = 0; i < p.splits; ++i) {
-            const int64_t at = i * rows + r;
-            const float w = __builtin_amdgcn_exp2f(st[at * 2] - big);
-            l = fmaf(st[at * 2 + 1], w, l);
-            v[0] = fmaf(p.split[at * dr + c0], w, v[0]);
-            v[1] = fmaf(p.split[at * dr + c1], w, v[1]);
+        for (int i0 = 0; i0 < p.splits; i0 += 64) {
+            const int left = min(64, p.splits - i0);
+            float w = 0.0f, mine = 0.0f;
+            if (lane < left) {
+                const int64_t at = ((i0 + lane) * rows + r) * 2;
+                w = __builtin_amdgcn_exp2f(st[at] - big);
+                mine = st[at + 1];
+            }
+            for (int i = 0; i < left; ++i) {
+                const float wi = __shfl(w, i);
+                const float *o = p.split + ((i0 + i) * rows + r) * dr;
+                l = fmaf(__shfl(mine, i), wi, l);
+                v[0] = fmaf(o[c0], wi, v[0]);
+                v[1] = fmaf(o[c1], wi, v[1]);
+            }
         }
     const float norm = l > 0.0f || l != l ? p.keep_scale / l : 0.0f;
     const int64_t bh = r / p.Lq;

@@ -6,11 +6,20 @@
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = (P M)^T dO,
 //   dtable[n] = sum of dS_ij over the pairs whose distance is in bucket n.
 // P is computed again from the scores and lse.  Two kernels: one per query
-// tile (dQ, delta, the table's sums), one per key tile (dK, dV, over all
-// query heads that share the key head).  Each output element has one writer
+// tile (dQ, delta), one per key tile (dK, dV, the table's sums, over all query
+// heads that share the key head).  Each output element has one writer
 // and a fixed order of summation; the price is the scores and dO V^T twice,
 // seven products in place of the five of a single pass that would add dQ with
 // atomics, in an order that varies.
+//
+// O has been rounded, so that dO . O is delta only to that rounding, and what is
+// wrong in it does not cancel where many dS of a query are added up (a bucket
+// that holds most keys: its sum is that of the few others, negated).  But the
+// exact dS of a query add up to 0, so the sum of those computed with dO . O
+// tells delta exactly: the dQ kernel corrects it for the dK / dV kernel, which
+// therefore makes the table's sums, and where a block sees at most kExactKeys
+// keys, where the rounding of O counts most, it goes over the keys once more
+// with the corrected delta for its own dQ.
 //
 // keep_scale is left out of dS until the last scaling: M is then 0 or 1 and
 // delta is divided by keep_scale.
@@ -20,9 +29,11 @@ namespace gs {
 
 namespace {
 
-// Sums of dS by distance.  A wave writes a 32 x 32 part of dS to LDS, a query a
+constexpr int kExactKeys = 256;
+
+// Sums of dS by distance.  A wave writes a 32 x 32 part of dS to LDS, a key a
 // row of kDiagonalRow floats of which the last 36 stay zero; lane d then adds
-// up the diagonal key - query = d - 31, an element a row (what lies left or
+// up the diagonal query - key = d - 31, an element a row (what lies left or
 // right of a row's 32 are the zeros of the row before or its own), and adds the
 // sum to the wave's entry for that distance.  The row length spreads the rows
 // over the banks.  LDS adds by atomics in the place of the
@@ -85,10 +96,8 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
     constexpr int KEYS = Geo::ROWS, BLOCK = Geo::BLOCK, NT = FEW ? 64 : 256;
     extern __shared__ __align__(16) unsigned char smem[];
     float *lut = (float *)(smem + Geo::tile_bytes);
-    float *diagonals = lut + (p.lut + 3) / 4 * 4;    // [wave][kDiagonal]
-    float *near = diagonals + (p.part ? 4 * kDiagonal : 0);   // [wave][lut]
-    float *far = near + (p.part ? 4 * p.lut : 0);    // [wave][2]
-    uint16_t *starts = (uint16_t *)(far + 8);
+    uint16_t *starts = (uint16_t *)(lut + (p.lut + 3) / 4 * 4);
+    __shared__ float row_sums[WS][BLOCK];
 
     int unit, tile, part;
     if (!block_place(p, !FEW, p.G, unit, tile, part)) return;
@@ -142,125 +151,114 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
         const int64_t at = (int64_t)unit * p.Lq + qi;
         const float v = p.lse[at];
         if (v != -INFINITY) minus_lse = -v * kLog2e;
-        if (half == 0 && wp == 0) p.delta[at] = delta;
     }
     delta = delta / p.keep_scale;
     float bias_lo = 0.0f, bias_hi = 0.0f;
     if (p.lut) {
         for (int i = t; i < p.side; i += 256) starts[i] = p.starts[i];
-        if (p.part)
-            for (int i = t; i < 4 * (kDiagonal + p.lut); i += 256) diagonals[i] = 0.0f;
         __syncthreads();
         fill_lut<T>(p, h, lut, starts, t, 256);
         __syncthreads();
         bias_lo = lut[0];
         bias_hi = lut[p.lut - 1];
     }
-    float far_lo = 0.0f, far_hi = 0.0f;              // distances at or past the last change
-    float *diagonal = diagonals + wave * kDiagonal + 32, *mine = near + wave * p.lut;
-
     f32x16 acc[DP / 32];
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
 
-    for (int k0 = begin, n = 0; k0 < end; k0 += STEP, ++n) {
-        const raw_t *Ks = Kt + (Geo::bufs == 2 ? (n & 1) * 2 * Geo::tile_elems : 0);
-        const raw_t *Vs = Ks + Geo::tile_elems;
-        async_wait();
-        tile_sync<FEW>();
-        const bool more = k0 + STEP < end;
-        if (Geo::bufs == 2 && more) load(Kt + ((n + 1) & 1) * 2 * Geo::tile_elems, k0 + STEP);
+    const int passes = end <= kExactKeys ? 2 : 1;
+    for (int pass = 0; pass < passes; ++pass) {
+        const bool last = pass == passes - 1;
+        float sum = 0.0f;                            // of the query's dS
+        if (pass > 0) {
+            __syncthreads();
+            if (begin < end) load(Kt, begin);
+        }
+        for (int k0 = begin, n = 0; k0 < end; k0 += STEP, ++n) {
+            const raw_t *Ks = Kt + (Geo::bufs == 2 ? (n & 1) * 2 * Geo::tile_elems : 0);
+            const raw_t *Vs = Ks + Geo::tile_elems;
+            async_wait();
+            tile_sync<FEW>();
+            const bool more = k0 + STEP < end;
+            if (Geo::bufs == 2 && more) load(Kt + ((n + 1) & 1) * 2 * Geo::tile_elems, k0 + STEP);
 #pragma unroll
-        for (int u = 0; u < KEYS / 32; ++u) {
-            const int ku = k0 + 32 * u;              // this 32-key part
-            if (q0 >= p.Lq || ku >= end || (p.causal && ku > wave_last)) continue;
-            f32x16 st, dp;
+            for (int u = 0; u < KEYS / 32; ++u) {
+                const int ku = k0 + 32 * u;              // this 32-key part
+                if (q0 >= p.Lq || ku >= end || (p.causal && ku > wave_last)) continue;
+                f32x16 st, dp;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) st[r] = dp[r] = 0.0f;
-            const int row = 32 * u + a_row(lane & 31);
-            pipelined<T, 2 * (DP / 16), T::bytes == 4 ? 1 : 4>(
-                [&](int i) { return frag_lds<T, DP>(i & 1 ? Vs : Ks, row, 8 * (i & ~1) + 8 * half); },
-                [&](int i, const Frag<T> &a) { mma<T>(i & 1 ? dp : st, a, i & 1 ? gf[i >> 1] : qf[i >> 1]); });
-            const int key0 = ku + 8 * half;
-            u32x4 rnd[2];                            // the generator runs while the products do
-            if constexpr (DROP)
+                for (int r = 0; r < 16; ++r) st[r] = dp[r] = 0.0f;
+                const int row = 32 * u + a_row(lane & 31);
+                pipelined<T, 2 * (DP / 16), T::bytes == 4 ? 1 : 4>(
+                    [&](int i) { return frag_lds<T, DP>(i & 1 ? Vs : Ks, row, 8 * (i & ~1) + 8 * half); },
+                    [&](int i, const Frag<T> &a) { mma<T>(i & 1 ? dp : st, a, i & 1 ? gf[i >> 1] : qf[i >> 1]); });
+                const int key0 = ku + 8 * half;
+                u32x4 rnd[2];                            // the generator runs while the products do
+                if constexpr (DROP)
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    rnd[x] = philox((uint32_t)(key0 + 16 * x) >> 3, (uint32_t)qi, (uint32_t)unit, p.call, p.seed_lo,
-                                    p.seed_hi);
-            const int cls = bias_class(p, ku - wave_last, ku + 31 - wave_first);
-            float e[16];
-            if (cls == 0) {
-                float bias[16];
-                read_all<16>(lut + (key0 - pos + p.border + kLutPad), bias,
-                             [](int i) { return 16 * (i >> 3) + (i & 7); });
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    e[i] = __builtin_amdgcn_exp2f(fmaf(st[i], p.scale2, bias[i]) + minus_lse);
-            } else {
-                const float c = minus_lse + (cls == 1 ? bias_lo : cls == 2 ? bias_hi : 0.0f);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(st[i], p.scale2, c));
-            }
-            float ds[16];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int i = 8 * x + j;
-                    float g = dp[i];
-                    if constexpr (DROP) g = kept(rnd[x], j, p.threshold) ? g : 0.0f;
-                    ds[i] = e[i] * (g - delta);
-                }
-            }
-            if (ku + 32 > end || (p.causal && ku + 31 > wave_first)) {
-                rare<16>(ds);
-                const int seen = (p.causal ? min(end, pos + 1) : end) - key0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (16 * (i >> 3) + (i & 7) >= seen) ds[i] = 0.0f;
-            }
-            if (p.part) {
+                    for (int x = 0; x < 2; ++x)
+                        rnd[x] = philox((uint32_t)(key0 + 16 * x) >> 3, (uint32_t)qi, (uint32_t)unit, p.call, p.seed_lo,
+                                        p.seed_hi);
+                const int cls = bias_class(p, ku - wave_last, ku + 31 - wave_first);
+                float e[16];
                 if (cls == 0) {
-                    float *row = diagonal + (lane & 31) * kDiagonalRow + 8 * half;
+                    float bias[16];
+                    read_all<16>(lut + (key0 - pos + p.border + kLutPad), bias,
+                                 [](int i) { return 16 * (i >> 3) + (i & 7); });
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        *(tokens_f32x4 *)(row + 16 * (i >> 3) + (i & 7)) =
-                            tokens_f32x4{ds[i], ds[i + 1], ds[i + 2], ds[i + 3]};
-                    tile_sync<true>();
-                    float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-                    for (int q = 0; q < 32; q += 16) {
-                        float v[16];
-                        read_all<16>(diagonal + lane - 31 + (kDiagonalRow + 1) * q, v,
-                                     [](int i) { return (kDiagonalRow + 1) * i; });
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) sum[i & 1] += v[i];
-                    }
-                    mine[ku - wave_first - 31 + lane + p.border + kLutPad] += sum[0] + sum[1];
-                    tile_sync<true>();
+                    for (int i = 0; i < 16; ++i)
+                        e[i] = __builtin_amdgcn_exp2f(fmaf(st[i], p.scale2, bias[i]) + minus_lse);
                 } else {
-                    float sum = 0.0f;
+                    const float c = minus_lse + (cls == 1 ? bias_lo : cls == 2 ? bias_hi : 0.0f);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) sum += (ds[i] + ds[i + 1]) + (ds[i + 2] + ds[i + 3]);
-                    if (cls == 1) far_lo += sum;
-                    else far_hi += sum;
+                    for (int i = 0; i < 16; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(st[i], p.scale2, c));
                 }
+                float ds[16];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int i = 8 * x + j;
+                        float g = dp[i];
+                        if constexpr (DROP) g = kept(rnd[x], j, p.threshold) ? g : 0.0f;
+                        ds[i] = e[i] * (g - delta);
+                    }
+                }
+                if (ku + 32 > end || (p.causal && ku + 31 > wave_first)) {
+                    rare<16>(ds);
+                    const int seen = (p.causal ? min(end, pos + 1) : end) - key0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (16 * (i >> 3) + (i & 7) >= seen) ds[i] = 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) sum += (ds[i] + ds[i + 1]) + (ds[i + 2] + ds[i + 3]);
+                if (!last) continue;
+                const Frag<T> df[2] = {frag_pack<T>(ds), frag_pack<T>(ds + 8)};
+                pipelined<T, 2 * (DP / 32), T::bytes == 4 ? 1 : DP / 32>(
+                    [&](int i) {
+                        return frag_lds_transposed<T, DP>(Ks, 32 * u + 16 * (i / (DP / 32)), 32 * (i % (DP / 32)), lane);
+                    },
+                    [&](int i, const Frag<T> &a) { mma<T>(acc[i % (DP / 32)], a, df[i / (DP / 32)]); });
             }
-            const Frag<T> df[2] = {frag_pack<T>(ds), frag_pack<T>(ds + 8)};
-            pipelined<T, 2 * (DP / 32), T::bytes == 4 ? 1 : DP / 32>(
-                [&](int i) {
-                    return frag_lds_transposed<T, DP>(Ks, 32 * u + 16 * (i / (DP / 32)), 32 * (i % (DP / 32)), lane);
-                },
-                [&](int i, const Frag<T> &a) { mma<T>(acc[i % (DP / 32)], a, df[i / (DP / 32)]); });
+            if (Geo::bufs == 1 && more) {
+                tile_sync<true>();
+                load(Kt, k0 + STEP);
+            }
         }
-        if (Geo::bufs == 1 && more) {
-            tile_sync<true>();
-            load(Kt, k0 + STEP);
+        sum += other_half(sum);
+        if constexpr (WS > 1) {
+            if (half == 0) row_sums[wp][rg * 32 + lane] = sum;
+            __syncthreads();
+            sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WS; ++w) sum += row_sums[w][rg * 32 + (lane & 31)];
         }
+        delta += sum;
     }
+    if (live && half == 0 && wp == 0) p.delta[(int64_t)unit * p.Lq + qi] = delta * p.keep_scale;
     const float scale = p.scale * p.keep_scale;
     if constexpr (WS == 1) {
         if (live) {
@@ -285,43 +283,6 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
             store4<T>(drow, at, p.D, vec, v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
         }
     }
-    if (!p.part) return;
-    far_lo = wave_sum(far_lo);
-    far_hi = wave_sum(far_hi);
-    if (lane == 0) {
-        far[wave * 2] = far_lo;
-        far[wave * 2 + 1] = far_hi;
-    }
-    __syncthreads();
-    for (int i = t; i < p.lut; i += 256)
-        near[i] = (near[i] + near[p.lut + i]) + (near[2 * p.lut + i] + near[3 * p.lut + i]);
-    __syncthreads();
-    // bucket n of a side holds distances starts[n] .. starts[n + 1] - 1, the
-    // last one all that follow.  Without the other side a key after the query
-    // counts as distance 0.  Eight lanes a bucket: the last ones are long.
-    float *out = p.part + (((int64_t)h * p.B + b) * p.tiles + tile) * p.buckets;
-    const float *zero = near + p.border + kLutPad;   // of distance 0
-    for (int n0 = 0; n0 < p.buckets; n0 += 32) {
-        const int n = n0 + (t >> 3), e = t & 7;
-        const bool after = n >= p.side;              // the side of keys after the query
-        const int m = after ? n - p.side : n;
-        const bool last = m == p.side - 1, in = n < p.buckets;
-        float sum = 0.0f;
-        if (in) {
-            const int lo = max((int)starts[m], after ? 1 : 0), hi = last ? p.border + kLutPad + 1 : starts[m + 1];
-            for (int d = lo + e; d < hi; d += 8) sum += zero[after ? d : -d];
-            if (!p.bidirectional && m == 0)
-                for (int d = 1 + e; d <= kLutPad; d += 8) sum += zero[d];
-        }
-#pragma unroll
-        for (int s = 1; s < 8; s <<= 1) sum += __shfl_xor(sum, s);
-        if (!in || e) continue;
-        if (last)
-            for (int w = 0; w < 4; ++w) sum += far[2 * w + (after ? 1 : 0)];
-        if (!p.bidirectional && m == 0)
-            for (int w = 0; w < 4; ++w) sum += far[2 * w + 1];
-        out[n] = sum * p.keep_scale;
-    }
 }
 
 template <typename T, int DP, bool DROP, int WS>
@@ -335,7 +296,10 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
     float *row_stats = (float *)(smem + Geo::tile_bytes);
     unsigned char *masks = (unsigned char *)(row_stats + Geo::copies * 4 * ROWS);   // [wave][4][32]
     float *lut = (float *)(masks + 512);
-    uint16_t *starts = (uint16_t *)(lut + (p.lut + 3) / 4 * 4);
+    float *diagonals = lut + (p.lut + 3) / 4 * 4;    // [wave][kDiagonal]
+    float *near = diagonals + (p.part ? 4 * kDiagonal : 0);   // [wave][lut]
+    float *far = near + (p.part ? 4 * p.lut : 0);    // [wave][2]
+    uint16_t *starts = (uint16_t *)(far + 8);
 
     int unit, tile, part;
     if (!block_place(p, false, 1, unit, tile, part)) return;
@@ -378,18 +342,30 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
     float *stats = row_stats + (FEW ? wave * Geo::bufs * 4 * ROWS : 0);
     unsigned char *mask = masks + wave * 128;
     const float keep_inv = 1.0f / p.keep_scale;
+    float *diagonal = diagonals + wave * kDiagonal + 32, *mine = near + wave * p.lut;
+    if (p.part)
+        for (int i = t; i < 4 * kDiagonal; i += 256) diagonals[i] = 0.0f;
 
     for (int g = 0; g < p.G; ++g) {
         const int64_t base = (int64_t)g * q_tiles;
         const int t0 = (int)max(p0 - base, (int64_t)0), t1 = (int)min(p1 - base, (int64_t)q_tiles);
-        if (t0 >= t1) continue;
         const int h = hk * p.G + g, bh = b * p.H + h;
+        float *sums_out =
+            p.part ? p.part + ((((int64_t)h * p.B + b) * p.tiles + tile) * p.splits + part) * p.buckets : nullptr;
+        if (t0 >= t1) {
+            if (p.part)
+                for (int n = t; n < p.buckets; n += 256) sums_out[n] = 0.0f;
+            continue;
+        }
         const raw_t *qb = (const raw_t *)p.q + (int64_t)b * p.qs[0] + (int64_t)h * p.qs[1];
         const raw_t *gb = (const raw_t *)p.d_o + (int64_t)b * p.dos[0] + (int64_t)h * p.dos[1];
         __syncthreads();
         float bias_lo = 0.0f, bias_hi = 0.0f;
+        float far_lo = 0.0f, far_hi = 0.0f;          // sums of distances past the last change
         if (p.lut) {
             fill_lut<T>(p, h, lut, starts, t, 256);
+            if (p.part)
+                for (int i = t; i < 4 * p.lut; i += 256) near[i] = 0.0f;
             __syncthreads();
             bias_lo = lut[0];
             bias_hi = lut[p.lut - 1];
@@ -460,12 +436,13 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
                 const int cls = bias_class(p, k0 - (first + qu + 31), k0 + 31 - (first + qu));
                 const bool edge = k0 + 32 > len || (p.causal && first + qu < k0 + 31);
                 Frag<T> pf[2], df[2];
+                float all[16];                       // dS
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int r0 = 32 * u + 16 * x + 8 * half;   // this lane's eight queries
                     const float *ml = rs + (cls == 1 ? ROWS : cls == 2 ? 2 * ROWS : 0) + r0;
                     const float *dl = rs + 3 * ROWS + r0;
-                    float pd[8], ds[8];
+                    float pd[8], *ds = all + 8 * x;
                     if (cls == 0) {
                         float bias[8];
                         read_all<8>(lut + (key - first - q0 - r0 + p.border + kLutPad), bias,
@@ -504,6 +481,33 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
                     pf[x] = frag_pack<T>(pd);
                     df[x] = frag_pack<T>(ds);
                 }
+                if (p.part) {
+                    if (cls == 0) {
+                        float *to = diagonal + (lane & 31) * kDiagonalRow + 8 * half;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            *(tokens_f32x4 *)(to + 16 * (i >> 3) + (i & 7)) =
+                                tokens_f32x4{all[i], all[i + 1], all[i + 2], all[i + 3]};
+                        tile_sync<true>();
+                        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                        for (int k = 0; k < 32; k += 16) {
+                            float v[16];
+                            read_all<16>(diagonal + lane - 31 + (kDiagonalRow + 1) * k, v,
+                                         [](int i) { return (kDiagonalRow + 1) * i; });
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sum[i & 1] += v[i];
+                        }
+                        mine[k0 - first - qu + 31 - lane + p.border + kLutPad] += sum[0] + sum[1];
+                        tile_sync<true>();
+                    } else {
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) sum += (all[i] + all[i + 1]) + (all[i + 2] + all[i + 3]);
+                        if (cls == 1) far_lo += sum;
+                        else far_hi += sum;
+                    }
+                }
                 // i: (16 queries, 32 columns, dV or dK)
                 pipelined<T, 4 * (DP / 32), T::bytes == 4 ? 1 : 4>(
                     [&](int i) {
@@ -521,6 +525,43 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
                     load(0, q0 + STEP * ROWS);
                 }
                 put_stats(Geo::bufs == 2 ? (it + 1) & 1 : 0);
+            }
+        }
+        if (p.part) {
+            far_lo = wave_sum(far_lo);
+            far_hi = wave_sum(far_hi);
+            if (lane == 0) {
+                far[wave * 2] = far_lo;
+                far[wave * 2 + 1] = far_hi;
+            }
+            __syncthreads();
+            for (int i = t; i < p.lut; i += 256)
+                near[i] = (near[i] + near[p.lut + i]) + (near[2 * p.lut + i] + near[3 * p.lut + i]);
+            __syncthreads();
+            // bucket n of a side holds distances starts[n] .. starts[n + 1] - 1, the
+            // last one all that follow.  Without the other side a key after the query
+            // counts as distance 0.  Eight lanes a bucket: the last ones are long.
+            const float *zero = near + p.border + kLutPad;   // of distance 0
+            for (int n0 = 0; n0 < p.buckets; n0 += 32) {
+                const int n = n0 + (t >> 3), e = t & 7;
+                const bool after = n >= p.side;              // the side of keys after the query
+                const int m = after ? n - p.side : n;
+                const bool last = m == p.side - 1, in = n < p.buckets;
+                float sum = 0.0f;
+                if (in) {
+                    const int lo = max((int)starts[m], after ? 1 : 0), hi = last ? p.border + kLutPad + 1 : starts[m + 1];
+                    for (int d = lo + e; d < hi; d += 8) sum += zero[after ? d : -d];
+                    if (!p.bidirectional && m == 0)
+                        for (int d = 1 + e; d <= kLutPad; d += 8) sum += zero[d];
+                }
+#pragma unroll
+                for (int s = 1; s < 8; s <<= 1) sum += __shfl_xor(sum, s);
+                if (!in || e) continue;
+                if (last)
+                    for (int w = 0; w < 4; ++w) sum += far[2 * w + (after ? 1 : 0)];
+                if (!p.bidirectional && m == 0)
+                    for (int w = 0; w < 4; ++w) sum += far[2 * w + 1];
+                sums_out[n] = sum * p.keep_scale;
             }
         }
     }
@@ -602,13 +643,13 @@ __global__ __launch_bounds__(256) void attention_backward_join(AttnParams p) {
     store4<T>(to, second ? at - dr : at, p.D, p.vec, v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
 }
 
-// dtable[n][h]: the sums of one head over sequences and query tiles, in
+// dtable[n][h]: the sums of one head over sequences, key tiles and parts, in
 // double, one block per head and bucket.
 template <typename T>
 __global__ __launch_bounds__(256) void attention_backward_table(AttnParams p) {
     __shared__ double red[4];
     const int n = blockIdx.x % p.buckets, h = blockIdx.x / p.buckets, t = threadIdx.x;
-    const int64_t rows = (int64_t)p.B * p.tiles;
+    const int64_t rows = (int64_t)p.B * p.tiles * p.splits;
     const float *part = p.part + (int64_t)h * rows * p.buckets + n;
     double sum = 0.0;
     for (int64_t r = t; r < rows; r += 256) sum += (double)part[r * p.buckets];
@@ -624,16 +665,15 @@ __global__ __launch_bounds__(256) void attention_backward_table(AttnParams p) {
 }
 
 template <typename T, int DP, int WS>
-int q_lds(const AttnParams &p, bool table) {
-    return BwdGeo<T, DP, WS, false>::tile_bytes + (p.lut + 3) / 4 * 16 + (table ? 4 * (kDiagonal + p.lut) * 4 : 0) + 32 +
-           p.side * 2;
+int q_lds(const AttnParams &p) {
+    return BwdGeo<T, DP, WS, false>::tile_bytes + (p.lut + 3) / 4 * 16 + p.side * 2;
 }
 
 template <typename T, int DP, int WS>
-int kv_lds(const AttnParams &p) {
+int kv_lds(const AttnParams &p, bool table) {
     typedef BwdGeo<T, DP, WS, true> Geo;
-    return Geo::tile_bytes + Geo::copies * 4 * Geo::ROWS * 4 + 512 +
-           (p.lut + 3) / 4 * 16 + p.side * 2;
+    return Geo::tile_bytes + Geo::copies * 4 * Geo::ROWS * 4 + 512 + (p.lut + 3) / 4 * 16 +
+           (table ? 4 * (kDiagonal + p.lut) * 4 : 0) + 32 + p.side * 2;
 }
 
 int launch(void (*fn)(AttnParams), const AttnParams &p, int smem, hipStream_t stream) {
@@ -655,13 +695,13 @@ void take_plan(AttnParams &p, const AttnPlan &a) {
 template <typename T, int DP, int WS>
 int launch_q(const AttnParams &p, hipStream_t stream) {
     return launch(p.threshold ? attention_backward_q<T, DP, true, WS> : attention_backward_q<T, DP, false, WS>, p,
-                  q_lds<T, DP, WS>(p, p.part != nullptr), stream);
+                  q_lds<T, DP, WS>(p), stream);
 }
 
 template <typename T, int DP, int WS>
 int launch_kv(const AttnParams &p, hipStream_t stream) {
     return launch(p.threshold ? attention_backward_kv<T, DP, true, WS> : attention_backward_kv<T, DP, false, WS>, p,
-                  kv_lds<T, DP, WS>(p), stream);
+                  kv_lds<T, DP, WS>(p, p.part != nullptr), stream);
 }
 
 template <typename T, int DP>
@@ -672,15 +712,16 @@ int launch_dp(const AttnParams &p0, int dtype, hipStream_t stream) {
     if (p.nblocks > 0) {
         if (const int e = a.ways == 4 ? launch_q<T, DP, 4>(p, stream) : launch_q<T, DP, 1>(p, stream)) return e;
     }
+    a = plan_backward_kv(p, dtype);
+    take_plan(p, a);
+    if (p.nblocks > 0) {
+        if (const int e = a.ways == 4 ? launch_kv<T, DP, 4>(p, stream) : launch_kv<T, DP, 1>(p, stream)) return e;
+    }
     if (p.dtable && p.buckets) {
         hipLaunchKernelGGL(attention_backward_table<T>, dim3(p.buckets * p.H), dim3(256), 0, stream, p);
         if (const int e = (int)hipGetLastError()) return e;
     }
-    a = plan_backward_kv(p, dtype);
-    take_plan(p, a);
-    if (p.nblocks == 0) return 0;
-    const int e = a.ways == 4 ? launch_kv<T, DP, 4>(p, stream) : launch_kv<T, DP, 1>(p, stream);
-    if (e || p.splits <= 1) return e;
+    if (p.nblocks == 0 || p.splits <= 1) return 0;
     const int64_t threads = (int64_t)p.units * p.Lk * (split_row(p.D) / 2);
     hipLaunchKernelGGL(attention_backward_join<T>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, p);
     return (int)hipGetLastError();
@@ -695,28 +736,29 @@ int launch_t(const AttnParams &p, int dtype, hipStream_t stream) {
     return launch_dp<T, 128>(p, dtype, stream);
 }
 
-// LDS of the 32-row form of the dQ kernel.
-int few_q_lds(const AttnParams &p, int dtype) {
+// LDS of the 32-row form of the dK / dV kernel.
+int few_kv_lds(const AttnParams &p, int dtype) {
     const int dp = padded_dim(p.D);
+    const bool table = p.buckets > 0;
     if (dtype == 0)
-        return dp == 32   ? q_lds<F32, 32, 4>(p, true)
-               : dp == 64 ? q_lds<F32, 64, 4>(p, true)
-               : dp == 96 ? q_lds<F32, 96, 4>(p, true)
-                          : q_lds<F32, 128, 4>(p, true);
-    return dp == 32   ? q_lds<F16, 32, 4>(p, true)
-           : dp == 64 ? q_lds<F16, 64, 4>(p, true)
-           : dp == 96 ? q_lds<F16, 96, 4>(p, true)
-                      : q_lds<F16, 128, 4>(p, true);
+        return dp == 32   ? kv_lds<F32, 32, 4>(p, table)
+               : dp == 64 ? kv_lds<F32, 64, 4>(p, table)
+               : dp == 96 ? kv_lds<F32, 96, 4>(p, table)
+                          : kv_lds<F32, 128, 4>(p, table);
+    return dp == 32   ? kv_lds<F16, 32, 4>(p, table)
+           : dp == 64 ? kv_lds<F16, 64, 4>(p, table)
+           : dp == 96 ? kv_lds<F16, 96, 4>(p, table)
+                      : kv_lds<F16, 128, 4>(p, table);
 }
 
 }  // namespace
 
-AttnPlan plan_backward_q(const AttnParams &p, int dtype) {
+AttnPlan plan_backward_q(const AttnParams &p, int) {
     AttnPlan a = {};
     a.splits = 1;
     a.units = p.B * p.H;
     const int64_t full = (int64_t)a.units * ((p.Lq + kAttnRows - 1) / kAttnRows);
-    a.ways = full < 256 && few_q_lds(p, dtype) <= kMaxLds ? 4 : 1;
+    a.ways = full < 256 ? 4 : 1;
     a.tiles = (p.Lq + kAttnRows / a.ways - 1) / (kAttnRows / a.ways);
     return a;
 }
@@ -730,7 +772,7 @@ AttnPlan plan_backward_kv(const AttnParams &p, int dtype) {
     a.splits = 1;
     a.units = p.B * p.Hkv;
     const int64_t full = (int64_t)a.units * ((p.Lk + kAttnRows - 1) / kAttnRows);
-    a.ways = full < 64 ? 4 : 1;
+    a.ways = full < 64 && few_kv_lds(p, dtype) <= kMaxLds ? 4 : 1;
     a.tiles = (p.Lk + kAttnRows / a.ways - 1) / (kAttnRows / a.ways);
     const int64_t blocks = (int64_t)a.units * a.tiles, tile = a.ways == 4 ? 32 : 64;
     const int64_t room = (padded_dim(p.D) > (dtype == 0 ? 32 : 64) ? 256 : 512);

@@ -40,8 +40,8 @@ struct AttnParams {
     void *o, *dq, *dk, *dv, *dtable;
     float *lse;
     const int32_t *lengths;
-    float *delta;             // backward: (B, H, Lq) row sums of dO * O
-    float *part;              // backward: (H, B * q_tiles, buckets) sums of dS
+    float *delta;             // backward: (B, H, Lq), sums of P dropout(dO V^T)
+    float *part;              // backward: (H, B, key tiles, parts, buckets) sums of dS
     float *split;             // sums of the parts of a split axis (see each kernel)
     int64_t qs[3], ks[3], vs[3], os[3], dos[3], dqs[3], dks[3], dvs[3];
     int B, H, Hkv, G, Lq, Lk, D;

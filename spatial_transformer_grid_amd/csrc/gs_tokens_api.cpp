@@ -150,17 +150,17 @@ int attention_setup(const gs_attention_desc *d, bool backward, gs::AttnParams &p
 // byte offset.
 bool stride_async(int64_t s) { return s <= (int64_t(1) << 22); }
 
-// Workspace of a backward call: delta, the query tiles' sums for the table, the
+// Workspace of a backward call: delta, the key tiles' sums for the table, the
 // parts' sums of dK and dV; each 256-byte aligned.
 struct BackwardSpace {
     int64_t part, split, bytes;
 };
 
 BackwardSpace backward_space(const gs::AttnParams &p, int dtype) {
-    const gs::AttnPlan q = gs::plan_backward_q(p, dtype), kv = gs::plan_backward_kv(p, dtype);
+    const gs::AttnPlan kv = gs::plan_backward_kv(p, dtype);
     BackwardSpace s;
     s.part = round_ws((int64_t)p.B * p.H * p.Lq * 4);
-    s.split = s.part + round_ws((int64_t)p.B * p.H * q.tiles * p.buckets * 4);
+    s.split = s.part + round_ws((int64_t)p.B * p.H * kv.tiles * kv.splits * p.buckets * 4);
     s.bytes = s.split + round_ws(kv.split_floats * 4);
     return s;
 }
