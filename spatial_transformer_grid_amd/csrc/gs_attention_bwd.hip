@@ -228,7 +228,8 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
                 }
                 if (ku + 32 > end || (p.causal && ku + 31 > wave_first)) {
                     rare<16>(ds);
-                    const int seen = (p.causal ? min(end, pos + 1) : end) - key0;
+                    int seen = p.causal ? min(end, pos + 1) : end;
+                    seen = (seen == 1 ? 0 : seen) - key0;    // the softmax of one key does not change
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (16 * (i >> 3) + (i & 7) >= seen) ds[i] = 0.0f;
@@ -477,6 +478,10 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             if (!live || j < hidden) pd[j] = ds[j] = 0.0f;
+                        if (key == 0)                // queries that see no other key: dS is 0
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (len == 1 || (p.causal && first + q0 + r0 + j == 0)) ds[j] = 0.0f;
                     }
                     pf[x] = frag_pack<T>(pd);
                     df[x] = frag_pack<T>(ds);

@@ -357,6 +357,42 @@ def test_attention_ignores_what_lies_past_a_length(gs, dtype, Lq):
     assert not base[3][1, :, 67:].any() and not base[4][1, :, 67:].any()
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("Lk,causal", [(1, 0), (40, 1)])
+def test_attention_of_one_key_has_no_gradient(gs, dtype, Lk, causal):
+    """A query that sees one key: its probability is 1 whatever the scores, so its dS is 0, not a rounding."""
+    g = torch.Generator().manual_seed(11)
+    t = TYPES[dtype]
+    q, do = heads(g, 2, 4, Lk, 48, t, False), heads(g, 2, 4, Lk, 48, t, False)
+    k, v = heads(g, 2, 2, Lk, 48, t, False), heads(g, 2, 2, Lk, 48, t, False)
+    how = dict(causal=causal, table=torch.randn(8, 4, generator=g).cuda(), max_distance=20, ratio=0.3, seed=2)
+    o, lse = gs.attention(q, k, v, return_lse=True, **how)
+    if causal:
+        do[:, :, 1:] = 0
+    dq, dk, dv, dt = gs.attention_backward(do, q, k, v, o, lse, **how)
+    assert not dq.any() and not dk.any() and not dt.any() and dv[:, :, 0].any() and not dv[:, :, 1:].any()
+
+
+def test_attention_bias_gradient_does_not_lose_what_o_rounds_off(gs):
+    """Buckets that hold most keys: their sums are those of the few others, negated."""
+    for dtype in ("f16", "bf16"):
+        t = TYPES[dtype]
+        g = torch.Generator().manual_seed(12)
+        q, do = heads(g, 2, 4, 3, 32, t, False), heads(g, 2, 4, 3, 32, t, False)
+        k, v = heads(g, 2, 2, 1500, 32, t, False), heads(g, 2, 2, 1500, 32, t, False)
+        table = torch.randn(4, 4, generator=g).cuda()
+        how = dict(table=table, max_distance=40)
+        o, lse = gs.attention(q, k, v, return_lse=True, **how)
+        got = gs.attention_backward(do, q, k, v, o, lse, **how)[3].cpu().double()
+        want = ref.attention(q.cpu(), k.cpu(), v.cpu(), 1 / math.sqrt(32), 0, None, table.cpu(), 40, 1, 0, 0.0, 0, 0,
+                             do.cpu(), unit(t), tiny(t))["dtable"][0]
+        # 2^-24 for each of at most 256 roundings on the way of a dS, which is of the size of p |dO . V|
+        p = torch.softmax(torch.einsum("bhid,bhjd->bhij", q.cpu().double(), k.cpu().double().repeat_interleave(2, 1)) /
+                          math.sqrt(32), -1)
+        size = (p * torch.einsum("bhid,bhjd->bhij", do.cpu().double(), v.cpu().double().repeat_interleave(2, 1)).abs()).sum()
+        assert (got - want).abs().max() <= 2.0 ** -16 * size, dtype
+
+
 def test_attention_extreme_scores(gs):
     """Scores far apart and far from zero: the softmax stays exact where one key dominates."""
     q = torch.full((1, 1, 4, 32), 30.0, device="cuda")
