@@ -202,8 +202,10 @@ int gs_attention_workspace_size(const gs_attention_desc *desc, int64_t *bytes);
  * Gradients of gs_attention from dO, its inputs, and the O and lse that it
  * wrote, under the same descriptor.  dQ, dK, dV and dtable (num_buckets,
  * q_heads; contiguous, table_dtype) are overwritten whole; keys that no query
- * sees get 0.  dtable may be NULL where it is not wanted.  The workspace
- * (256-byte aligned) is required.  Errors as gs_attention; GS_ERR_ATTR for a
+ * sees get 0, as do the scores of a query that sees one key (its probability
+ * is 1 whatever they are).  dtable may be NULL where it is not wanted.  dS is
+ * rounded to dtype before it multiplies Q and K (with GS_F32 not at all).  The
+ * workspace (256-byte aligned) is required.  Errors as gs_attention; GS_ERR_ATTR for a
  * workspace that is too small.
  */
 int gs_attention_backward(const gs_attention_desc *desc, const void *dO, const void *Q,

