@@ -23,7 +23,7 @@
 // with a bias 170 us (810 TFLOP/s, where an 8192^3 product reaches 1093);
 // 2 x 16 x 2048 x 64 causal bf16 with bias and dropout 59 us, 40 us without
 // either; 16 caches of up to 8192 keys x 8 heads x 128 bf16, one query each:
-// 80 us (4.4 TB/s, memory) and 5 us for the join.
+// 71 us (4.9 TB/s, memory) and 5 us for the join.
 #include "gs_tokens.hpp"
 
 namespace gs {
@@ -158,7 +158,9 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
                 [&](int i) {
                     return frag_lds<T, DP>(Ks, 32 * (i % U) + a_row(lane & 31), 16 * (i / U) + 8 * half);
                 },
-                [&](int i, const Frag<T> &a) { mma<T>(st[i % U], a, qf[i / U]); });
+                [&](int i, const Frag<T> &a) {
+                    if (step_counts<T>(p, i / U)) mma<T>(st[i % U], a, qf[i / U]);
+                });
             // the generator runs while the products do
             u32x4 rnd[2 * U];
             if constexpr (DROP)
@@ -401,7 +403,7 @@ int launch_t(const AttnParams &p, int ways, hipStream_t stream) {
 }  // namespace
 
 // The 32-row form where 128-row blocks would leave compute units without one,
-// or would be mostly empty.  Decode of 16 ragged caches: 86 us, with 128-row
+// or would be mostly empty.  Decode of 16 ragged caches: 77 us, with 128-row
 // blocks 216 us; 512 blocks of 2048 x 64 causal: 76 us, with 128-row blocks 59 us.
 AttnPlan plan_forward(const AttnParams &p, int, bool workspace) {
     AttnPlan a = {};
@@ -418,9 +420,11 @@ AttnPlan plan_forward(const AttnParams &p, int, bool workspace) {
         a.units = p.B * p.Hkv;
     }
     a.tiles = a.pack ? 1 : (p.Lq + 31) / 32;
+    // two blocks a compute unit; more only repeat what a block does before its
+    // first key (the ragged decode: 4 parts 71 us, 8 parts 80 us, 16 parts 91 us)
     const int64_t blocks = (int64_t)a.units * a.tiles;
-    if (!workspace || blocks >= 512 || blocks == 0) return a;
-    int64_t splits = (1024 + blocks - 1) / blocks;
+    if (!workspace || blocks >= 256 || blocks == 0) return a;
+    int64_t splits = 512 / blocks;
     if (splits > p.Lk / 256) splits = p.Lk / 256;    // two tiles a wave at least
     if (splits <= 1) return a;
     a.chunk = (int)(((p.Lk + splits - 1) / splits + 127) / 128 * 128);

@@ -199,7 +199,9 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
                 const int row = 32 * u + a_row(lane & 31);
                 pipelined<T, 2 * (DP / 16), T::bytes == 4 ? 1 : 4>(
                     [&](int i) { return frag_lds<T, DP>(i & 1 ? Vs : Ks, row, 8 * (i & ~1) + 8 * half); },
-                    [&](int i, const Frag<T> &a) { mma<T>(i & 1 ? dp : st, a, i & 1 ? gf[i >> 1] : qf[i >> 1]); });
+                    [&](int i, const Frag<T> &a) {
+                        if (step_counts<T>(p, i >> 1)) mma<T>(i & 1 ? dp : st, a, i & 1 ? gf[i >> 1] : qf[i >> 1]);
+                    });
                 const int key0 = ku + 8 * half;
                 u32x4 rnd[2];                            // the generator runs while the products do
                 if constexpr (DROP)
@@ -426,7 +428,9 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
                 const int row = 32 * u + a_row(lane & 31);
                 pipelined<T, 2 * (DP / 16), T::bytes == 4 ? 1 : 4>(
                     [&](int i) { return frag_lds<T, DP>(i & 1 ? Gs : Qs, row, 8 * (i & ~1) + 8 * half); },
-                    [&](int i, const Frag<T> &a) { mma<T>(i & 1 ? dp : st, a, i & 1 ? vf[i >> 1] : kf[i >> 1]); });
+                    [&](int i, const Frag<T> &a) {
+                        if (step_counts<T>(p, i >> 1)) mma<T>(i & 1 ? dp : st, a, i & 1 ? vf[i >> 1] : kf[i >> 1]);
+                    });
                 if constexpr (DROP) {
                     // this lane's two calls: query qu + lane % 32, keys
                     // k0 + 16 half .. + 15; one byte of kept bits each
@@ -634,13 +638,34 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
     }
 }
 
-// dK and dV from the sums of the parts, added in their order: a thread takes
-// four columns of a row.
+// What is left once the sums of all blocks are there.  The first blocks, one a
+// head and bucket, make dtable[n][h]: the sums of one head over sequences, key
+// tiles and parts, in double.  The others add the parts of dK and dV in their
+// order, a thread four columns of a row.
 template <typename T>
-__global__ __launch_bounds__(256) void attention_backward_join(AttnParams p) {
+__global__ __launch_bounds__(256) void attention_backward_finish(AttnParams p) {
     typedef typename T::raw_t raw_t;
+    const int tables = p.dtable ? p.buckets * p.H : 0;
+    if ((int)blockIdx.x < tables) {
+        __shared__ double red[4];
+        const int n = blockIdx.x % p.buckets, h = blockIdx.x / p.buckets, t = threadIdx.x;
+        const int64_t rows = (int64_t)p.B * p.tiles * p.splits;
+        const float *part = p.part + (int64_t)h * rows * p.buckets + n;
+        double sum = 0.0;
+        for (int64_t r = t; r < rows; r += 256) sum += (double)part[r * p.buckets];
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor(sum, s);
+        if ((t & 63) == 0) red[t >> 6] = sum;
+        __syncthreads();
+        if (t != 0) return;
+        const float v = (float)((red[0] + red[1]) + (red[2] + red[3]));
+        const int64_t at = (int64_t)n * p.H + h;
+        if (p.table_f32) ((float *)p.dtable)[at] = v;
+        else ((typename T::raw_t *)p.dtable)[at] = to_bits<T>(v);
+        return;
+    }
     const int dr = split_row(p.D), quads = 2 * dr / 4;
-    const int64_t rows = (int64_t)p.units * p.Lk, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t rows = (int64_t)p.units * p.Lk, i = (int64_t)(blockIdx.x - tables) * 256 + threadIdx.x;
     const int64_t row = i / quads;
     if (row >= rows) return;
     const int at = (int)(i - row * quads) * 4;
@@ -652,27 +677,6 @@ __global__ __launch_bounds__(256) void attention_backward_join(AttnParams p) {
     const int64_t *st = second ? p.dvs : p.dks;
     raw_t *to = (raw_t *)(second ? p.dv : p.dk) + b * st[0] + hk * st[1] + key * st[2];
     store4<T>(to, second ? at - dr : at, p.D, p.vec, v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
-}
-
-// dtable[n][h]: the sums of one head over sequences, key tiles and parts, in
-// double, one block per head and bucket.
-template <typename T>
-__global__ __launch_bounds__(256) void attention_backward_table(AttnParams p) {
-    __shared__ double red[4];
-    const int n = blockIdx.x % p.buckets, h = blockIdx.x / p.buckets, t = threadIdx.x;
-    const int64_t rows = (int64_t)p.B * p.tiles * p.splits;
-    const float *part = p.part + (int64_t)h * rows * p.buckets + n;
-    double sum = 0.0;
-    for (int64_t r = t; r < rows; r += 256) sum += (double)part[r * p.buckets];
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor(sum, s);
-    if ((t & 63) == 0) red[t >> 6] = sum;
-    __syncthreads();
-    if (t != 0) return;
-    const float v = (float)((red[0] + red[1]) + (red[2] + red[3]));
-    const int64_t at = (int64_t)n * p.H + h;
-    if (p.table_f32) ((float *)p.dtable)[at] = v;
-    else ((typename T::raw_t *)p.dtable)[at] = to_bits<T>(v);
 }
 
 template <typename T, int DP, int WS>
@@ -728,13 +732,11 @@ int launch_dp(const AttnParams &p0, int dtype, hipStream_t stream) {
     if (p.nblocks > 0) {
         if (const int e = a.ways == 4 ? launch_kv<T, DP, 4>(p, stream) : launch_kv<T, DP, 1>(p, stream)) return e;
     }
-    if (p.dtable && p.buckets) {
-        hipLaunchKernelGGL(attention_backward_table<T>, dim3(p.buckets * p.H), dim3(256), 0, stream, p);
-        if (const int e = (int)hipGetLastError()) return e;
-    }
-    if (p.nblocks == 0 || p.splits <= 1) return 0;
-    const int64_t threads = (int64_t)p.units * p.Lk * (split_row(p.D) / 2);
-    hipLaunchKernelGGL(attention_backward_join<T>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, p);
+    const int64_t tables = p.dtable ? (int64_t)p.buckets * p.H : 0;
+    const int64_t threads = p.nblocks > 0 && p.splits > 1 ? (int64_t)p.units * p.Lk * (split_row(p.D) / 2) : 0;
+    const int64_t blocks = tables + (threads + 255) / 256;
+    if (blocks == 0) return 0;
+    hipLaunchKernelGGL(attention_backward_finish<T>, dim3((unsigned)blocks), dim3(256), 0, stream, p);
     return (int)hipGetLastError();
 }
 

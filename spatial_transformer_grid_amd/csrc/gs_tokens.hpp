@@ -434,6 +434,13 @@ __device__ __forceinline__ void pipelined(const Read &read, const Multiply &mult
     }
 }
 
+// Whether 16 columns of the contracted axis hold any: a step past head_dim is
+// left out where it is long (fp32: eight products of 64 clocks).
+template <typename T>
+__device__ __forceinline__ bool step_counts(const AttnParams &p, int step) {
+    return T::bytes == 2 || 16 * step < p.D;
+}
+
 // Four consecutive elements of an output row.
 template <typename T>
 __device__ __forceinline__ void store4(typename T::raw_t *row, int col, int D, bool vec, float a, float b,
