@@ -504,16 +504,15 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
                             *(tokens_f32x4 *)(to + 16 * (i >> 3) + (i & 7)) =
                                 tokens_f32x4{all[i], all[i + 1], all[i + 2], all[i + 3]};
                         tile_sync<true>();
-                        float sum[2] = {0.0f, 0.0f};
+                        float v[32];
+                        read_all<32>(diagonal + lane - 31, v, [](int i) { return (kDiagonalRow + 1) * i; });
+                        float sum[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                        for (int k = 0; k < 32; k += 16) {
-                            float v[16];
-                            read_all<16>(diagonal + lane - 31 + (kDiagonalRow + 1) * k, v,
-                                         [](int i) { return (kDiagonalRow + 1) * i; });
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) sum[i & 1] += v[i];
-                        }
-                        mine[k0 - first - qu + 31 - lane + p.border + kLutPad] += sum[0] + sum[1];
+                        for (int i = 4; i < 32; ++i) sum[i & 3] += v[i];
+                        // one entry a lane; a wave's additions keep their order, and nothing waits for them
+                        __hip_atomic_fetch_add(mine + (k0 - first - qu + 31 - lane + p.border + kLutPad),
+                                               (sum[0] + sum[1]) + (sum[2] + sum[3]), __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_WORKGROUP);
                         tile_sync<true>();
                     } else {
                         float sum = 0.0f;
