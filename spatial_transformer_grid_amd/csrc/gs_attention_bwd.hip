@@ -25,7 +25,7 @@
 // delta is divided by keep_scale.
 //
 // Measured: 16 heads of 4096 x 4096 x 128 fp16 on four key heads, with a bias:
-// dQ 230 us (900 TFLOP/s over its three products), dK and dV 450 us (610 over
+// dQ 230 us (900 TFLOP/s over its three products), dK and dV 440 us (625 over
 // four; K, V and both sums fill the registers of a SIMD's one wave, whose
 // products and exponentials follow one another); 2 x 16 x 2048 x 64 causal
 // bf16 with bias and dropout: 76 and 110 us, of which the generator takes 20 each.

@@ -7,30 +7,35 @@
 // and added up by a second kernel, so that the order is fixed.
 //
 // Both are bound by memory, so each row is read once and stays in registers
-// between its passes: NT threads hold E elements each (a wave up to 2048
-// columns, a block of 256 threads up to 8192, one of 1024 up to 32768), and
+// between its passes: NT threads hold E elements each (eight lanes up to 64
+// columns, 32 up to 256, a wave up to 2048, a block of 256 threads up to 8192, one
+// of 1024 up to 32768), and
 // what belongs to a column (scale, bias, the sums of dscale and dbias) stays
 // there from row to row.  Wider rows take the loops over memory at the end.
 // Measured at 16384 x 2048 bf16 with fp32 parameters: forward 23 us (5.8 TB/s),
 // backward 39 us (5.2 TB/s), the parts' sums 4.6 us; with a block a row and the
-// row read again for each pass it was 68, 61 + 75 and 21 us.
+// row read again for each pass it was 68, 61 + 75 and 21 us.  40000 x 40 bf16:
+// 3.8 and 11 us, a wave a row 12.5 and 17 us.  4000 x 8000 bf16: 23 and 51 us,
+// with 1024 threads of eight elements 29 and 63 us.
 #include "gs_tokens.hpp"
 
 namespace gs {
 
 namespace {
 
-__device__ __forceinline__ float wave_total(float v) {
+template <int N>
+__device__ __forceinline__ float lanes_total(float v) {
 #pragma unroll
-    for (int s = 1; s < 64; s <<= 1) v += __shfl_xor(v, s);
+    for (int s = 1; s < N; s <<= 1) v += __shfl_xor(v, s);
     return v;
 }
 
-// Sums over the NT threads of a row, two at once; `red` holds 2 NT / 64 floats.
+// Sums over the NT threads of a row, two at once; `red` holds 2 NT / 64 floats
+// where they are more than a wave.
 template <int NT>
 __device__ __forceinline__ void row_totals(float &a, float &b, float *red) {
-    a = wave_total(a);
-    b = wave_total(b);
+    a = lanes_total<(NT < 64 ? NT : 64)>(a);
+    b = lanes_total<(NT < 64 ? NT : 64)>(b);
     if constexpr (NT > 64) {
         constexpr int W = NT / 64;
         __syncthreads();
@@ -125,7 +130,7 @@ template <typename T, int NT, int E, bool VEC>
 __global__ __launch_bounds__(block_threads(NT)) void layer_norm_rows(NormParams p) {
     typedef typename T::raw_t raw_t;
     constexpr int ROWS = block_threads(NT) / NT;    // rows of a block at a time
-    __shared__ float red[2 * NT / 64];
+    __shared__ float red[NT > 64 ? 2 * NT / 64 : 1];
     const int t = threadIdx.x % NT, cols = p.cols;
     const float inv_n = 1.0f / (float)cols;
     float w[E], b[E];
@@ -161,7 +166,7 @@ template <typename T, int NT, int E, bool VEC>
 __global__ __launch_bounds__(block_threads(NT)) void layer_norm_backward_rows(NormParams p) {
     typedef typename T::raw_t raw_t;
     constexpr int ROWS = block_threads(NT) / NT;
-    __shared__ float red[2 * NT / 64];
+    __shared__ float red[NT > 64 ? 2 * NT / 64 : 1];
     __shared__ float sums[ROWS > 1 ? ROWS * NT * 8 : 1];
     const int t = threadIdx.x % NT, group = threadIdx.x / NT, cols = p.cols;
     const float inv_n = 1.0f / (float)cols;
@@ -340,8 +345,11 @@ __global__ __launch_bounds__(256) void layer_norm_params_wide(NormParams p) {
 
 constexpr int kWidest = 32768;       // columns of a row that stays in registers
 
-// Rows of a block at a time.
-int block_rows(int64_t cols) { return cols <= 2048 ? 4 : 1; }
+// Rows of a block at a time, and blocks that run at once (registers allow two to
+// eight a compute unit).
+int block_rows(int64_t cols) { return cols <= 64 ? 32 : cols <= 256 ? 8 : cols <= 2048 ? 4 : 1; }
+int forward_blocks(int64_t cols) { return cols <= 512 ? 2048 : cols <= 1024 ? 1536 : 1024; }
+int backward_blocks(int64_t cols) { return cols <= 512 ? 1536 : cols <= 1024 ? 768 : 512; }
 
 template <typename T, int NT, int E>
 void rows_form(const NormParams &p, bool backward, hipStream_t stream) {
@@ -352,15 +360,17 @@ void rows_form(const NormParams &p, bool backward, hipStream_t stream) {
         else hipLaunchKernelGGL((layer_norm_backward_rows<T, NT, E, false>), grid, dim3(B), 0, stream, p);
         return;
     }
-    const int64_t blocks = (p.rows + B / NT - 1) / (B / NT);
-    const dim3 grid((unsigned)(blocks < 1024 ? blocks : 1024));    // four blocks a compute unit
+    const int64_t blocks = (p.rows + B / NT - 1) / (B / NT), most = forward_blocks(p.cols);
+    const dim3 grid((unsigned)(blocks < most ? blocks : most));
     if (p.vec) hipLaunchKernelGGL((layer_norm_rows<T, NT, E, true>), grid, dim3(B), 0, stream, p);
     else hipLaunchKernelGGL((layer_norm_rows<T, NT, E, false>), grid, dim3(B), 0, stream, p);
 }
 
 template <typename T>
 int rows_launch(const NormParams &p, bool backward, hipStream_t stream) {
-    if (p.cols <= 512) rows_form<T, 64, 8>(p, backward, stream);
+    if (p.cols <= 64) rows_form<T, 8, 8>(p, backward, stream);
+    else if (p.cols <= 256) rows_form<T, 32, 8>(p, backward, stream);
+    else if (p.cols <= 512) rows_form<T, 64, 8>(p, backward, stream);
     else if (p.cols <= 1024) rows_form<T, 64, 16>(p, backward, stream);
     else if (p.cols <= 2048) rows_form<T, 64, 32>(p, backward, stream);
     else if (p.cols <= 4096) rows_form<T, 256, 16>(p, backward, stream);
@@ -399,12 +409,12 @@ int backward(const NormParams &p, hipStream_t stream) {
 
 }  // namespace
 
-// Two blocks a compute unit, fewer where their sums would pass 32 MiB.
+// As many parts as run at once, fewer where their sums would pass 32 MiB.
 int layer_norm_parts(int64_t rows, int64_t cols) {
     if (rows == 0) return 0;
     int64_t n = (rows + block_rows(cols) - 1) / block_rows(cols);
     const int64_t most = (int64_t(1) << 22) / cols;
-    if (n > 512) n = 512;
+    if (n > backward_blocks(cols)) n = backward_blocks(cols);
     if (n > most) n = most < 1 ? 1 : most;
     return (int)n;
 }

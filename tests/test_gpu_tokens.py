@@ -102,6 +102,14 @@ def test_layer_norm(gs, rows, cols, dtype, params):
     assert all(torch.equal(p, q) for p, q in zip(again, (dx, dw, db)))
 
 
+@pytest.mark.parametrize("rows,cols", [(70, 64), (333, 63), (40, 72), (19, 256), (21, 257), (6, 4104), (5, 8193),
+                                       (3, 16385), (2, 32768), (3, 40000)])
+@pytest.mark.parametrize("dtype,params", [("f32", "f32"), ("bf16", "f32")])
+def test_layer_norm_of_every_form(gs, rows, cols, dtype, params):
+    """Eight lanes a row up to 1024 threads, and the loops past them."""
+    test_layer_norm(gs, rows, cols, dtype, params)
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_layer_norm_strides_alignment_and_shapes(gs, dtype):
     """Rows apart, rows off their 16-byte alignment, a broadcast row, more axes than two, no bias."""
