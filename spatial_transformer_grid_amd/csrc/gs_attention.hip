@@ -52,6 +52,13 @@ struct FwdGeo {
 // largest fp16 value, and O is not scaled again with each small step.
 constexpr float kSlack = 8.0f;
 
+// What a part of the keys with maximum m counts under the common maximum.  Where
+// no part has one, a row's scores are all -inf (sums 0) or all NaN (a maximum
+// leaves NaN out, a sum does not): the sums count as they are, so that NaN stays.
+__device__ __forceinline__ float part_weight(float m, float common) {
+    return common == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - common);
+}
+
 template <typename T, int DP, bool DROP, int WS>
 __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attention_forward(AttnParams p) {
     typedef typename T::raw_t raw_t;
@@ -292,8 +299,7 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
 #pragma unroll
             for (int w = 1; w < WS; ++w) big = fmaxf(big, stat[w][0][r]);
 #pragma unroll
-            for (int w = 0; w < WS; ++w)
-                if (big != -INFINITY) lr = fmaf(stat[w][1][r], __builtin_amdgcn_exp2f(stat[w][0][r] - big), lr);
+            for (int w = 0; w < WS; ++w) lr = fmaf(stat[w][1][r], part_weight(stat[w][0][r], big), lr);
             tokens_f32x4 v = *(const tokens_f32x4 *)(sums + r * Geo::SUM + at);
 #pragma unroll
             for (int w = 1; w < WS; ++w) v += *(const tokens_f32x4 *)(sums + (w * ROWS + r) * Geo::SUM + at);
@@ -336,23 +342,22 @@ __global__ __launch_bounds__(256) void attention_combine(AttnParams p) {
     for (int x = 1; x < 64; x <<= 1) big = fmaxf(big, __shfl_xor(big, x));
     float l = 0.0f, v[2] = {0.0f, 0.0f};
     const int c0 = lane < p.D ? lane : 0, c1 = lane + 64 < p.D ? lane + 64 : 0;
-    if (big != -INFINITY)
-        for (int i0 = 0; i0 < p.splits; i0 += 64) {
-            const int left = min(64, p.splits - i0);
-            float w = 0.0f, mine = 0.0f;
-            if (lane < left) {
-                const int64_t at = ((i0 + lane) * rows + r) * 2;
-                w = __builtin_amdgcn_exp2f(st[at] - big);
-                mine = st[at + 1];
-            }
-            for (int i = 0; i < left; ++i) {
-                const float wi = __shfl(w, i);
-                const float *o = p.split + ((i0 + i) * rows + r) * dr;
-                l = fmaf(__shfl(mine, i), wi, l);
-                v[0] = fmaf(o[c0], wi, v[0]);
-                v[1] = fmaf(o[c1], wi, v[1]);
-            }
+    for (int i0 = 0; i0 < p.splits; i0 += 64) {
+        const int left = min(64, p.splits - i0);
+        float w = 0.0f, mine = 0.0f;
+        if (lane < left) {
+            const int64_t at = ((i0 + lane) * rows + r) * 2;
+            w = part_weight(st[at], big);
+            mine = st[at + 1];
         }
+        for (int i = 0; i < left; ++i) {
+            const float wi = __shfl(w, i);
+            const float *o = p.split + ((i0 + i) * rows + r) * dr;
+            l = fmaf(__shfl(mine, i), wi, l);
+            v[0] = fmaf(o[c0], wi, v[0]);
+            v[1] = fmaf(o[c1], wi, v[1]);
+        }
+    }
     const float norm = l > 0.0f || l != l ? p.keep_scale / l : 0.0f;
     const int64_t bh = r / p.Lq;
     const int b = (int)(bh / p.H), h = (int)(bh - (int64_t)b * p.H), q = (int)(r - bh * p.Lq);
