@@ -325,9 +325,6 @@ int gs_attention_backward(const gs_attention_desc *desc, const void *dO, const v
     const int rc = attention_setup(desc, true, p);
     if (rc != GS_OK) return rc;
     if (workspace_bytes < 0) return GS_ERR_ATTR;
-    if (p.B == 0 || p.H == 0) {
-        if (!p.H || !dtable || !p.buckets) return GS_OK;
-    }
     const bool queries = p.units > 0 && p.tiles > 0, keys = (int64_t)p.B * p.Hkv * p.Lk > 0;
     if (queries && (!dO || !Q || !O || !lse || !dQ)) return GS_ERR_NULL;
     if (keys && (!K || !V || !dK || !dV)) return GS_ERR_NULL;

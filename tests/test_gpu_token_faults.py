@@ -65,3 +65,17 @@ def test_attention_nan_key_reaches_the_queries_that_see_it(gs, form, dtype):
     assert got[0, :G, Lq - 1].isnan().all() and got_lse[0, :G, Lq - 1].isnan().all()
     got[0, :G, Lq - 1], got_lse[0, :G, Lq - 1] = o[0, :G, Lq - 1], lse[0, :G, Lq - 1]
     assert torch.equal(got, o) and torch.equal(got_lse, lse)
+
+
+# ------------------------------------------------- keys without query heads
+
+@pytest.mark.parametrize("Lk", [7, 300])
+@pytest.mark.parametrize("table", [False, True])
+def test_attention_gradients_without_query_heads_are_zero(gs, Lk, table):
+    q, k = torch.empty(2, 0, 5, 24, device="cuda"), torch.randn(2, 4, Lk, 24, device="cuda")
+    used = [torch.full_like(k, 7.0) for _ in range(6)]
+    del used                                         # what a new tensor is likely to hold
+    how = dict(table=torch.empty(8, 0, device="cuda")) if table else {}
+    o, lse = gs.attention(q, k, k, return_lse=True, **how)
+    dq, dk, dv, _ = gs.attention_backward(q, q, k, k, o, lse, **how)
+    assert dq.shape == q.shape and dk.shape == dv.shape == k.shape and not dk.any() and not dv.any()
