@@ -145,10 +145,38 @@ def _device_tensor(t, name):
 
 
 def _stream(stream, device):
+    """The hipStream_t of the device's current stream (of `stream`, where one is given)."""
     torch = _torch()
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _on_stream(stream, call, *args, **kwargs):
+    """call(*args, **kwargs) with `stream` (a stream object or a hipStream_t) as the current one.
+
+    It starts after what the caller's current stream holds so far, the copies and
+    scratch that the call makes belong to `stream`, and the memory of inputs and
+    outputs is not given out again while either stream may still use it."""
+    torch = _torch()
+    tensors = [a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor) and a.is_cuda]
+    if not tensors:
+        return call(*args, **kwargs)  # which refuses its inputs
+    current = torch.cuda.current_stream(tensors[0].device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, tensors[0].device)
+    if stream.cuda_stream == current.cuda_stream:
+        return call(*args, **kwargs)
+    stream.wait_stream(current)
+    for t in tensors:
+        t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        result = call(*args, **kwargs)
+    for t in result if isinstance(result, tuple) else (result,):
+        if t is not None:
+            t.record_stream(current)
+    return result
 
 
 def _check(status: int, where: str):
@@ -159,6 +187,8 @@ def _check(status: int, where: str):
 def affine_grid(theta, size, align_corners: int = 0, out=None, stream=None):
     """AffineGrid(theta, size) -> grid on the GPU (gs_affine_grid); the grid
     has theta's element type."""
+    if stream is not None:
+        return _on_stream(stream, affine_grid, theta, size, align_corners, out)
     torch = _torch()
     theta = _device_tensor(theta, "theta")
     size = [int(s) for s in size]
@@ -204,6 +234,9 @@ def grid_sample(X, grid, mode: str = "linear", padding_mode: str = "zeros",
     one of the size the library asks for from torch's allocator; with it the
     call is gs_grid_sample_2d_ws, which gathers from a channels-last copy of X
     when the grid scatters its locations (a random flow)."""
+    if stream is not None:
+        return _on_stream(stream, grid_sample, X, grid, mode, padding_mode, align_corners, out,
+                          workspace=workspace)
     X = _device_tensor(X, "X")
     grid = _device_tensor(grid, "grid")
     r = X.dim() - 2
@@ -241,6 +274,9 @@ def affine_grid_sample_fused(theta, X, out_spatial, mode: str = "linear",
                              padding_mode: str = "zeros", align_corners: int = 0, out=None,
                              stream=None):
     """AffineGrid + GridSample in one pass, the grid never materialised."""
+    if stream is not None:
+        return _on_stream(stream, affine_grid_sample_fused, theta, X, out_spatial, mode,
+                          padding_mode, align_corners, out)
     theta = _device_tensor(theta, "theta")
     X = _device_tensor(X, "X")
     r = X.dim() - 2
@@ -287,6 +323,10 @@ def resize(X, scales=None, sizes=None, axes=None, mode: str = "nearest",
 
     Attribute names and defaults follow the Resize page (version 18); scales
     or sizes refer to `axes` (all axes when None)."""
+    if stream is not None:
+        return _on_stream(stream, resize, X, scales, sizes, axes, mode, coordinate_transformation_mode,
+                          nearest_mode, cubic_coeff_a, exclude_outside, keep_aspect_ratio_policy,
+                          out)
     X = _device_tensor(X, "X")
     rank = X.dim()
     shape = resize_output_shape(X.shape, scales, sizes, axes, keep_aspect_ratio_policy)
@@ -312,6 +352,9 @@ def resize_to(X, y_shape, scales=None, mode: str = "nearest",
               nearest_mode: str = "round_prefer_floor", cubic_coeff_a: float = -0.75,
               exclude_outside: int = 0, out=None, stream=None):
     """gs_resize with explicit output extents and per-axis scales (or None)."""
+    if stream is not None:
+        return _on_stream(stream, resize_to, X, y_shape, scales, mode, coordinate_transformation_mode,
+                          nearest_mode, cubic_coeff_a, exclude_outside, out)
     X = _device_tensor(X, "X")
     rank = X.dim()
     y_shape = [int(v) for v in y_shape]
@@ -381,6 +424,9 @@ def deform_conv(X, W, offset, B=None, mask=None, strides=None, pads=None, dilati
     then ends, dilations, group, offset_group).  `workspace`: a device tensor
     of scratch bytes; None takes one of the size the library asks for from
     torch's allocator, and an empty tensor runs without one."""
+    if stream is not None:
+        return _on_stream(stream, deform_conv, X, W, offset, B, mask, strides, pads, dilations, group,
+                          offset_group, out, workspace=workspace)
     X, W, offset, B, mask, Y = _deform_tensors(X, W, offset, B, mask, strides, pads, dilations,
                                                offset_group, out)
     ptr, arr = _ptr, _arr
@@ -408,6 +454,9 @@ def deform_conv_noalloc(X, W, offset, B=None, mask=None, strides=None, pads=None
     scratch array per GPU instead of a workspace (for callers that cannot
     allocate; pass `out` to allocate nothing here either).  Calls that may
     overlap on one GPU race on that array."""
+    if stream is not None:
+        return _on_stream(stream, deform_conv_noalloc, X, W, offset, B, mask, strides, pads, dilations,
+                          group, offset_group, out)
     X, W, offset, B, mask, Y = _deform_tensors(X, W, offset, B, mask, strides, pads, dilations,
                                                offset_group, out)
     st = lib().gs_deform_conv_noalloc(_ptr(X), dtype_code(X), int64_array(X.shape), X.dim(),

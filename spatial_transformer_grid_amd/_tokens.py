@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 
-from ._binding import GS_F32, GS_OK, _check, _device_tensor, _I, _P, _ptr, _stream, _torch, dtype_code
+from ._binding import GS_F32, GS_OK, _check, _device_tensor, _I, _on_stream, _P, _ptr, _stream, _torch, dtype_code
 from ._binding import lib as _library
 
 _I64 = ctypes.c_int64
@@ -114,16 +114,15 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_handle(stream, device):
-    """The hipStream_t of `stream`, or of the device's current stream.  A call of a few microseconds is
-    made of such steps, so the handle is read without a stream object around it."""
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(device.index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _stream_handle(device):
+    """The hipStream_t of the device's current stream.  A call of a few microseconds is made of such
+    steps, so the handle is read without a stream object around it."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _workspace(workspace, need, device):
-    """The scratch tensor (kept alive by the caller until the launch), its address and its bytes."""
+    """The scratch tensor (of the current stream, kept alive by the caller until the launch), its address
+    and its bytes."""
     if workspace is None:
         if not need:
             return None, None, 0
@@ -156,6 +155,8 @@ def layer_norm(X, scale, bias=None, epsilon: float = 1e-5, return_stats: bool = 
     scale and bias have X's element type or float32.  With `return_stats` the
     mean and inverse standard deviation of each row are returned too (float32,
     X's shape without its last axis): layer_norm_backward takes them."""
+    if stream is not None:
+        return _on_stream(stream, layer_norm, X, scale, bias, epsilon, return_stats, out)
     torch = _torch()
     X = _tensor(X, "X")
     if X.dim() < 1:
@@ -171,7 +172,7 @@ def layer_norm(X, scale, bias=None, epsilon: float = 1e-5, return_stats: bool = 
         inv_std = torch.empty_like(mean)
     st = token_lib().gs_layer_norm(
         x.data_ptr(), dtype_code(X), rows, cols, xs, scale.data_ptr(), _address(bias), dtype_code(scale),
-        epsilon, Y.data_ptr(), cols, _address(mean), _address(inv_std), _stream_handle(stream, X.device))
+        epsilon, Y.data_ptr(), cols, _address(mean), _address(inv_std), _stream_handle(X.device))
     if st != GS_OK:
         _check(st, "gs_layer_norm")
     return (Y, mean, inv_std) if return_stats else Y
@@ -180,6 +181,8 @@ def layer_norm(X, scale, bias=None, epsilon: float = 1e-5, return_stats: bool = 
 def layer_norm_backward(dY, X, scale, mean, inv_std, stream=None, workspace=None):
     """Gradients (dX, dscale, dbias) of layer_norm (gs_layer_norm_backward).
     `workspace`: device scratch; None takes it from torch's allocator."""
+    if stream is not None:
+        return _on_stream(stream, layer_norm_backward, dY, X, scale, mean, inv_std, workspace=workspace)
     torch = _torch()
     X = _tensor(X, "X")
     dY = _tensor(dY, "dY", X.dtype, X.shape)
@@ -201,7 +204,7 @@ def layer_norm_backward(dY, X, scale, mean, inv_std, stream=None, workspace=None
     st = token_lib().gs_layer_norm_backward(
         dy.data_ptr(), x.data_ptr(), dtype_code(X), rows, cols, dys, xs, scale.data_ptr(), dtype_code(scale),
         mean.data_ptr(), inv_std.data_ptr(), dX.data_ptr(), cols, dscale.data_ptr(), dbias.data_ptr(), ws,
-        ws_bytes, _stream_handle(stream, X.device))
+        ws_bytes, _stream_handle(X.device))
     _check(st, "gs_layer_norm_backward")
     return dX, dscale, dbias
 
@@ -210,6 +213,8 @@ def dropout(X, ratio: float, seed: int, call: int = 0, residual=None, out=None, 
     """residual + dropout(X) (gs_dropout); the mask follows from seed, call and
     an element's place in X.  The gradient with respect to X is
     dropout(dY, ratio, seed, call); with respect to the residual it is dY."""
+    if stream is not None:
+        return _on_stream(stream, dropout, X, ratio, seed, call, residual, out)
     X = _device_tensor(X, "X")
     if residual is not None:
         residual = _device_tensor(residual, "residual")
@@ -218,7 +223,7 @@ def dropout(X, ratio: float, seed: int, call: int = 0, residual=None, out=None, 
     Y = _output(out, X, True)
     st = token_lib().gs_dropout(X.data_ptr(), dtype_code(X), X.numel(), _address(residual), ratio,
                                 int(seed) & _MASK64, int(call) & _MASK32, Y.data_ptr(),
-                                _stream_handle(stream, X.device))
+                                _stream_handle(X.device))
     if st != GS_OK:
         _check(st, "gs_dropout")
     return Y
@@ -296,6 +301,9 @@ def attention(Q, K, V, scale=None, causal: int = 0, kv_lengths=None, table=None,
     sequence (a cache is read).  O is laid out like Q.  With `return_lse` the
     log-sum-exp of the scores (float32, batch x heads x length) is returned
     too: attention_backward takes it."""
+    if stream is not None:
+        return _on_stream(stream, attention, Q, K, V, scale, causal, kv_lengths, table, max_distance,
+                          bidirectional, q_position, ratio, seed, call, return_lse, out, workspace=workspace)
     torch = _torch()
     Q, K, V, kv_lengths, table, d = _attention_inputs(
         Q, K, V, scale, causal, kv_lengths, table, max_distance, bidirectional, q_position, ratio,
@@ -312,7 +320,7 @@ def attention(Q, K, V, scale=None, causal: int = 0, kv_lengths=None, table=None,
         workspace, ws, ws_bytes = _workspace(workspace, 0, Q.device)
     st = token_lib().gs_attention(ctypes.byref(d), Q.data_ptr(), K.data_ptr(), V.data_ptr(),
                                   _address(kv_lengths), _address(table), O.data_ptr(), _address(lse), ws,
-                                  ws_bytes, _stream_handle(stream, Q.device))
+                                  ws_bytes, _stream_handle(Q.device))
     if st != GS_OK:
         _check(st, "gs_attention")
     return (O, lse) if return_lse else O
@@ -324,6 +332,9 @@ def attention_backward(dO, Q, K, V, O, lse, scale=None, causal: int = 0, kv_leng
                        workspace=None):
     """Gradients (dQ, dK, dV, dtable) of attention (gs_attention_backward) from
     its inputs, its O and its lse; dtable is None without a table."""
+    if stream is not None:
+        return _on_stream(stream, attention_backward, dO, Q, K, V, O, lse, scale, causal, kv_lengths, table,
+                          max_distance, bidirectional, q_position, ratio, seed, call, workspace=workspace)
     torch = _torch()
     Q, K, V, kv_lengths, table, d = _attention_inputs(
         Q, K, V, scale, causal, kv_lengths, table, max_distance, bidirectional, q_position, ratio,
@@ -342,6 +353,6 @@ def attention_backward(dO, Q, K, V, O, lse, scale=None, causal: int = 0, kv_leng
     st = token_lib().gs_attention_backward(
         ctypes.byref(d), dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
         lse.data_ptr(), _address(kv_lengths), _address(table), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(),
-        _address(dtable), ws, ws_bytes, _stream_handle(stream, Q.device))
+        _address(dtable), ws, ws_bytes, _stream_handle(Q.device))
     _check(st, "gs_attention_backward")
     return dQ, dK, dV, dtable

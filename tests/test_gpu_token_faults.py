@@ -79,3 +79,96 @@ def test_attention_gradients_without_query_heads_are_zero(gs, Lk, table):
     o, lse = gs.attention(q, k, k, return_lse=True, **how)
     dq, dk, dv, _ = gs.attention_backward(q, q, k, k, o, lse, **how)
     assert dq.shape == q.shape and dk.shape == dv.shape == k.shape and not dk.any() and not dv.any()
+
+
+# ---------------------------------------------------------------- streams
+
+def test_calls_on_a_stream_given_by_name(gs):
+    """stream=s with strided inputs that the current stream has only just been asked to write, s busy, and the current
+    stream's allocations filled right after each call: the bits are those of plain calls."""
+    g = torch.Generator().manual_seed(21)
+    t = torch.bfloat16
+    wide = torch.randn(2, 300, 4, 128, generator=g).to(t).cuda()
+    rows = torch.randn(600, 2 * 264, generator=g).to(t).cuda()
+    q1 = torch.randn(2, 1, 4, 128, generator=g).to(t).cuda()
+    table = torch.randn(4, 32, generator=g).to(t).cuda()
+    square = torch.randn(4096, 4096, device="cuda")
+    s = torch.cuda.Stream()
+
+    def busy(n):
+        for _ in range(n):
+            torch.mm(square, square)
+
+    def calls(stream):
+        """Every call's outputs; the inputs are made anew and die at once."""
+        def every_other(x):
+            return (x * 1.0)[..., ::2]               # its last axis is copied by the call
+        def heads_of(x):
+            return every_other(x).transpose(1, 2)
+        def after():
+            if stream is not None:
+                for n in (1 << 10, 1 << 16, 1 << 20, 1 << 24):
+                    for _ in range(4):
+                        torch.full((n,), float("nan"), device="cuda")
+        out = []
+        x, w = every_other(rows), torch.ones(264, device="cuda", dtype=t)
+        y, mean, inv = gs.layer_norm(x, w, w, return_stats=True, stream=stream)
+        after()
+        out += [y, mean, inv, *gs.layer_norm_backward(every_other(rows) + 1, x, w, mean, inv, stream=stream)]
+        after()
+        out.append(gs.dropout(every_other(rows), 0.2, 7, residual=x, stream=stream))
+        after()
+        how = dict(table=table.t() * 1.0, ratio=0.1, seed=5, stream=stream)
+        o, lse = gs.attention(heads_of(wide), heads_of(wide) + 1, heads_of(wide) * 2, return_lse=True, **how)
+        after()
+        out += [o, lse, *gs.attention_backward(heads_of(wide) - 1, heads_of(wide), heads_of(wide) + 1, heads_of(wide) * 2,
+                                               o, lse, **how)]
+        after()
+        out.append(gs.attention(heads_of(q1), heads_of(wide), heads_of(wide), stream=stream))
+        after()
+        return out
+
+    want = calls(None)
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream, torch.cuda.current_stream(), 0):
+        busy(3)
+        with torch.cuda.stream(s):
+            busy(6)
+        got = calls(stream)
+        torch.cuda.current_stream().wait_stream(s)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    torch.cuda.synchronize()
+
+
+def test_older_calls_on_a_stream_given_by_name(gs):
+    """The sampler, Resize and DeformConv with its scratch, the same way."""
+    g = torch.Generator().manual_seed(22)
+    X = torch.randn(2, 16, 24, 2 * 24, generator=g).cuda()
+    W = torch.randn(16, 16, 3, 3, generator=g).cuda()
+    offset = torch.randn(2, 18, 24, 24, generator=g).cuda()
+    theta = torch.eye(2, 3).repeat(2, 1, 1).cuda() * 0.9
+    square = torch.randn(4096, 4096, device="cuda")
+    s = torch.cuda.Stream()
+
+    def calls(stream):
+        x = lambda: (X * 1.0)[..., ::2]
+        out = [gs.affine_grid(theta * 1.0, (2, 16, 24, 24), stream=stream)]
+        out.append(gs.grid_sample(x(), out[0] * 1.0 if stream is None else out[0], workspace="auto", stream=stream))
+        out.append(gs.affine_grid_sample_fused(theta * 1.0, x(), (24, 24), stream=stream))
+        out.append(gs.resize(x(), sizes=(2, 16, 48, 40), mode="linear", stream=stream))
+        out.append(gs.resize_to(x(), (2, 16, 48, 40), mode="linear", stream=stream))
+        out.append(gs.deform_conv(x(), W * 1.0, offset * 1.0, pads=[1, 1, 1, 1], stream=stream))
+        if stream is not None:
+            for n in (1 << 12, 1 << 20, 1 << 22):
+                torch.full((n,), float("nan"), device="cuda")
+        return out
+
+    want = calls(None)
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        for _ in range(3):
+            torch.mm(square, square)
+        got = calls(stream)
+        torch.cuda.current_stream().wait_stream(s)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    torch.cuda.synchronize()
