@@ -144,6 +144,13 @@ def _device_tensor(t, name):
     return t.contiguous()
 
 
+def _scratch(workspace, device):
+    """Checks a caller's scratch tensor: its bytes are used from its address on (an empty one is none)."""
+    if workspace.numel() and (not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the inputs' GPU")
+    return workspace
+
+
 def _stream(stream, device):
     """The hipStream_t of the device's current stream (of `stream`, where one is given)."""
     torch = _torch()
@@ -255,6 +262,7 @@ def grid_sample(X, grid, mode: str = "linear", padding_mode: str = "zeros",
             need = grid_sample_2d_workspace_size(tuple(X.shape), tuple(grid.shape),
                                                  dtype_code(X))
             workspace = _torch().empty(need, dtype=_torch().uint8, device=X.device)
+        _scratch(workspace, X.device)
         ws_ptr = ctypes.c_void_p(workspace.data_ptr()) if workspace.numel() else None
         st = lib().gs_grid_sample_2d_ws(*args, *rest[:-1], ws_ptr,
                                         workspace.numel() * workspace.element_size(), rest[-1])
@@ -437,7 +445,7 @@ def deform_conv(X, W, offset, B=None, mask=None, strides=None, pads=None, dilati
         "gs_deform_conv_workspace_size")
     if workspace is None and need.value > 0:
         workspace = _torch().empty(need.value, dtype=_torch().uint8, device=X.device)
-    ws_ptr = ptr(workspace) if workspace is not None else None
+    ws_ptr = ptr(_scratch(workspace, X.device)) if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = lib().gs_deform_conv(ptr(X), dtype_code(X), int64_array(X.shape), X.dim(), ptr(W),
                               int64_array(W.shape), ptr(offset), ptr(B), ptr(mask), arr(strides),

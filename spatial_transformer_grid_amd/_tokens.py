@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 
-from ._binding import GS_F32, GS_OK, _check, _device_tensor, _I, _on_stream, _P, _ptr, _stream, _torch, dtype_code
+from ._binding import GS_F32, GS_OK, _check, _device_tensor, _I, _on_stream, _P, _ptr, _scratch, _stream, _torch, dtype_code
 from ._binding import lib as _library
 
 _I64 = ctypes.c_int64
@@ -128,7 +128,7 @@ def _workspace(workspace, need, device):
             return None, None, 0
         workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
         return workspace, workspace.data_ptr(), need
-    if workspace.numel() == 0:
+    if _scratch(workspace, device).numel() == 0:
         return None, None, 0
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 

@@ -172,3 +172,22 @@ def test_older_calls_on_a_stream_given_by_name(gs):
         torch.cuda.current_stream().wait_stream(s)
         assert all(torch.equal(a, b) for a, b in zip(want, got))
     torch.cuda.synchronize()
+
+
+# --------------------------------------------------------------- refusals
+
+def test_scratch_in_host_memory_is_refused(gs):
+    x, w = torch.randn(4, 16, device="cuda"), torch.ones(16, device="cuda")
+    q = torch.randn(1, 2, 40, 16, device="cuda")
+    y, mean, inv = gs.layer_norm(x, w, return_stats=True)
+    o, lse = gs.attention(q, q, q, return_lse=True)
+    image, kernel = torch.randn(1, 4, 8, 8, device="cuda"), torch.randn(4, 4, 3, 3, device="cuda")
+    offset, grid = torch.zeros(1, 18, 6, 6, device="cuda"), torch.zeros(1, 6, 6, 2, device="cuda")
+    for bad in (torch.empty(1 << 16, dtype=torch.uint8), torch.empty(1 << 17, dtype=torch.uint8, device="cuda")[::2]):
+        for call in (lambda: gs.layer_norm_backward(x, x, w, mean, inv, workspace=bad),
+                     lambda: gs.attention(q, q, q, workspace=bad),
+                     lambda: gs.attention_backward(q, q, q, q, o, lse, workspace=bad),
+                     lambda: gs.deform_conv(image, kernel, offset, workspace=bad),
+                     lambda: gs.grid_sample(image, grid, workspace=bad)):
+            with pytest.raises(ValueError):
+                call()

@@ -118,3 +118,27 @@ def test_every_call_with_a_stream_hands_over(monkeypatch):
         # every argument is handed on under its own name
         bound = inspect.signature(c).bind(*a[2:], **kw).arguments
         assert dict(bound) == given
+
+
+# ---------------------------------------------------------------- scratch
+
+def test_scratch_must_be_contiguous_gpu_memory(tk):  # noqa: F811
+    """Scratch in host memory, on another GPU or with gaps is refused, by the token calls and the older ones."""
+    class Scratch(torch.Tensor):
+        @staticmethod
+        def of(t, device):
+            t = t.as_subclass(Scratch)
+            t.place = torch.device(device)
+            return t
+
+        is_cuda = property(lambda self: self.place.type == "cuda")
+        device = property(lambda self: self.place)
+
+    here = torch.device("cuda:0")
+    flat = torch.zeros(512, dtype=torch.uint8)
+    for bad in (flat, Scratch.of(flat, "cuda:1"), Scratch.of(flat[::2], "cuda:0")):
+        with pytest.raises(ValueError):
+            tk._workspace(bad, 256, here)
+    good = Scratch.of(flat, "cuda:0")
+    assert tk._workspace(good, 256, here)[1:] == (flat.data_ptr(), 512)
+    assert tk._workspace(flat[:0], 256, here) == (None, None, 0)
