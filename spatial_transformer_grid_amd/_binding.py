@@ -138,9 +138,12 @@ def dtype_code(t) -> int:
     return code
 
 
-def _device_tensor(t, name):
+def _device_tensor(t, name, like=None):
+    """`t`, contiguous, on a GPU (that of `like`)."""
     if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % name)
+    if like is not None and t.get_device() != like.get_device():
+        raise ValueError("%s must be on the same GPU as the first input" % name)
     return t.contiguous()
 
 
@@ -205,8 +208,10 @@ def affine_grid(theta, size, align_corners: int = 0, out=None, stream=None):
     shape = (size[0], *size[2:], r)
     if out is None:
         out = torch.empty(shape, dtype=theta.dtype, device=theta.device)
-    elif tuple(out.shape) != shape or not out.is_contiguous() or out.dtype != theta.dtype:
-        raise ValueError("out must be a contiguous %s tensor of shape %s" % (theta.dtype, shape))
+    elif (tuple(out.shape) != shape or not out.is_contiguous() or out.dtype != theta.dtype
+          or out.get_device() != theta.get_device()):
+        raise ValueError("out must be a contiguous %s tensor of shape %s on theta's GPU"
+                         % (theta.dtype, shape))
     st = lib().gs_affine_grid(ctypes.c_void_p(theta.data_ptr()), dtype_code(theta), int64_array(size),
                               len(size), int(align_corners), ctypes.c_void_p(out.data_ptr()),
                               _stream(stream, theta.device))
@@ -218,8 +223,10 @@ def _out_tensor(out, shape, like):
     torch = _torch()
     if out is None:
         return torch.empty(shape, dtype=like.dtype, device=like.device)
-    if tuple(out.shape) != tuple(shape) or out.dtype != like.dtype or not out.is_contiguous():
-        raise ValueError("out must be a contiguous %s tensor of shape %s" % (like.dtype, shape))
+    if (tuple(out.shape) != tuple(shape) or out.dtype != like.dtype or not out.is_contiguous()
+            or out.get_device() != like.get_device()):
+        raise ValueError("out must be a contiguous %s tensor of shape %s on the inputs' GPU"
+                         % (like.dtype, shape))
     return out
 
 
@@ -245,7 +252,7 @@ def grid_sample(X, grid, mode: str = "linear", padding_mode: str = "zeros",
         return _on_stream(stream, grid_sample, X, grid, mode, padding_mode, align_corners, out,
                           workspace=workspace)
     X = _device_tensor(X, "X")
-    grid = _device_tensor(grid, "grid")
+    grid = _device_tensor(grid, "grid", X)
     r = X.dim() - 2
     if grid.dim() != r + 2:
         raise ValueError("grid must have rank %d" % (r + 2))
@@ -286,7 +293,7 @@ def affine_grid_sample_fused(theta, X, out_spatial, mode: str = "linear",
         return _on_stream(stream, affine_grid_sample_fused, theta, X, out_spatial, mode,
                           padding_mode, align_corners, out)
     theta = _device_tensor(theta, "theta")
-    X = _device_tensor(X, "X")
+    X = _device_tensor(X, "X", theta)
     r = X.dim() - 2
     out_spatial = [int(s) for s in out_spatial]
     if len(out_spatial) != r:
@@ -390,10 +397,10 @@ def deform_conv_output_shape(x_shape, w_shape, strides=None, pads=None, dilation
 def _deform_tensors(X, W, offset, B, mask, strides, pads, dilations, offset_group, out):
     """Checked device tensors of a DeformConv call and its output."""
     X = _device_tensor(X, "X")
-    W = _device_tensor(W, "W")
-    offset = _device_tensor(offset, "offset")
-    B = _device_tensor(B, "B") if B is not None else None
-    mask = _device_tensor(mask, "mask") if mask is not None else None
+    W = _device_tensor(W, "W", X)
+    offset = _device_tensor(offset, "offset", X)
+    B = _device_tensor(B, "B", X) if B is not None else None
+    mask = _device_tensor(mask, "mask", X) if mask is not None else None
     for name, t in (("W", W), ("offset", offset), ("B", B), ("mask", mask)):
         if t is not None and t.dtype != X.dtype:
             raise TypeError("%s must have X's element type" % name)

@@ -65,10 +65,12 @@ def token_lib():
     return _typed
 
 
-def _tensor(t, name, dtype=None, shape=None):
-    """`t` on the GPU with a contiguous last axis, its type and shape checked."""
+def _tensor(t, name, like=None, dtype=None, shape=None):
+    """`t` on the GPU (that of `like`) with a contiguous last axis, its type and shape checked."""
     if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % name)
+    if like is not None and t.get_device() != like.get_device():
+        raise ValueError("%s must be on the same GPU as the first input" % name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must have element type %s" % (name, dtype))
     if shape is not None and tuple(t.shape) != tuple(shape):
@@ -94,9 +96,9 @@ def _output(out, like, dense):
         torch = _torch()
         return torch.empty_like(like) if like.is_contiguous() else torch.empty(
             like.shape, dtype=like.dtype, device=like.device)
-    if not out.is_cuda or out.shape != like.shape or out.dtype != like.dtype or (
+    if out.get_device() != like.get_device() or out.shape != like.shape or out.dtype != like.dtype or (
             not out.is_contiguous() if dense else out.shape[-1] > 1 and out.stride(-1) != 1):
-        raise ValueError("out must be a %s GPU tensor of shape %s and type %s"
+        raise ValueError("out must be a %s tensor of shape %s and type %s on the inputs' GPU"
                          % ("contiguous" if dense else "(last axis contiguous)", tuple(like.shape), like.dtype))
     return out
 
@@ -135,14 +137,14 @@ def _workspace(workspace, need, device):
 
 def _norm_params(X, scale, bias):
     cols = X.shape[-1]
-    scale = _device_tensor(scale, "scale")
+    scale = _device_tensor(scale, "scale", X)
     for name, t in (("scale", scale), ("bias", bias)):
         if t is not None and tuple(t.shape) != (cols,):
             raise ValueError("%s must have shape (%d,)" % (name, cols))
     if scale.dtype != X.dtype and scale.dtype != _torch().float32:
         raise TypeError("scale must have X's element type or float32")
     if bias is not None:
-        bias = _device_tensor(bias, "bias")
+        bias = _device_tensor(bias, "bias", X)
         if bias.dtype != scale.dtype:
             raise TypeError("bias must have scale's element type")
     return scale, bias
@@ -185,13 +187,13 @@ def layer_norm_backward(dY, X, scale, mean, inv_std, stream=None, workspace=None
         return _on_stream(stream, layer_norm_backward, dY, X, scale, mean, inv_std, workspace=workspace)
     torch = _torch()
     X = _tensor(X, "X")
-    dY = _tensor(dY, "dY", X.dtype, X.shape)
+    dY = _tensor(dY, "dY", X, X.dtype, X.shape)
     scale, _ = _norm_params(X, scale, None)
     cols = X.shape[-1]
     rows = math.prod(X.shape[:-1])
     for name, t in (("mean", mean), ("inv_std", inv_std)):
-        if t.dtype != torch.float32 or t.numel() != rows or not t.is_cuda:
-            raise ValueError("%s must be a float32 GPU tensor with an element per row" % name)
+        if t.dtype != torch.float32 or t.numel() != rows or t.get_device() != X.get_device():
+            raise ValueError("%s must be a float32 tensor on X's GPU with an element per row" % name)
     mean, inv_std = mean.contiguous(), inv_std.contiguous()
     x, xs = _rows(X)
     dy, dys = _rows(dY)
@@ -217,7 +219,7 @@ def dropout(X, ratio: float, seed: int, call: int = 0, residual=None, out=None, 
         return _on_stream(stream, dropout, X, ratio, seed, call, residual, out)
     X = _device_tensor(X, "X")
     if residual is not None:
-        residual = _device_tensor(residual, "residual")
+        residual = _device_tensor(residual, "residual", X)
         if residual.dtype != X.dtype or residual.shape != X.shape:
             raise ValueError("residual must have X's shape and element type")
     Y = _output(out, X, True)
@@ -250,13 +252,13 @@ def _attention_inputs(Q, K, V, scale, causal, kv_lengths, table, max_distance, b
     if Q.dim() != 4 or K.dim() != 4:
         raise ValueError("Q and K must have shape (batch, heads, length, head_dim)")
     Q = _tensor(Q, "Q")
-    K = _tensor(K, "K", Q.dtype)
+    K = _tensor(K, "K", Q, Q.dtype)
     if K.shape[0] != Q.shape[0] or K.shape[3] != Q.shape[3]:
         raise ValueError("K must share Q's batch and head_dim")
-    V = _tensor(V, "V", Q.dtype, K.shape)
+    V = _tensor(V, "V", Q, Q.dtype, K.shape)
     B, H, Lq, D = Q.shape
     if kv_lengths is not None:
-        kv_lengths = _tensor(kv_lengths, "kv_lengths", torch.int32, (B,)).contiguous()
+        kv_lengths = _tensor(kv_lengths, "kv_lengths", Q, torch.int32, (B,)).contiguous()
     d = AttentionDesc()
     d.dtype = dtype_code(Q)
     d.batch, d.q_heads, d.q_len, d.head_dim = B, H, Lq, D
@@ -271,7 +273,7 @@ def _attention_inputs(Q, K, V, scale, causal, kv_lengths, table, max_distance, b
     else:
         d.q_position = int(q_position)
     if table is not None:
-        table = _device_tensor(table, "table")
+        table = _device_tensor(table, "table", Q)
         if table.dim() != 2 or table.shape[1] != H:
             raise ValueError("table must have shape (buckets, %d)" % H)
         if table.dtype != Q.dtype and table.dtype != torch.float32:
@@ -339,9 +341,9 @@ def attention_backward(dO, Q, K, V, O, lse, scale=None, causal: int = 0, kv_leng
     Q, K, V, kv_lengths, table, d = _attention_inputs(
         Q, K, V, scale, causal, kv_lengths, table, max_distance, bidirectional, q_position, ratio,
         seed, call)
-    O = _tensor(O, "O", Q.dtype, Q.shape)
-    dO = _tensor(dO, "dO", Q.dtype, Q.shape)
-    lse = _tensor(lse, "lse", torch.float32, Q.shape[:3]).contiguous()
+    O = _tensor(O, "O", Q, Q.dtype, Q.shape)
+    dO = _tensor(dO, "dO", Q, Q.dtype, Q.shape)
+    lse = _tensor(lse, "lse", Q, torch.float32, Q.shape[:3]).contiguous()
     dQ, dK, dV = _like(Q), _like(K), _like(V)
     dtable = torch.empty_like(table) if table is not None else None
     d.o_stride, d.do_stride = _strides(O), _strides(dO)

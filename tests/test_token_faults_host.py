@@ -120,25 +120,60 @@ def test_every_call_with_a_stream_hands_over(monkeypatch):
         assert dict(bound) == given
 
 
-# ---------------------------------------------------------------- scratch
+# ------------------------------------------------------ scratch and devices
+
+class Placed(torch.Tensor):
+    """A host tensor that says it lies on a device."""
+
+    @staticmethod
+    def of(t, device):
+        t = t.as_subclass(Placed)
+        t.place = torch.device(device)
+        return t
+
+    is_cuda = property(lambda self: self.place.type == "cuda")
+    device = property(lambda self: self.place)
+
+    def get_device(self):
+        return self.place.index if self.is_cuda else -1
+
 
 def test_scratch_must_be_contiguous_gpu_memory(tk):  # noqa: F811
     """Scratch in host memory, on another GPU or with gaps is refused, by the token calls and the older ones."""
-    class Scratch(torch.Tensor):
-        @staticmethod
-        def of(t, device):
-            t = t.as_subclass(Scratch)
-            t.place = torch.device(device)
-            return t
-
-        is_cuda = property(lambda self: self.place.type == "cuda")
-        device = property(lambda self: self.place)
-
     here = torch.device("cuda:0")
     flat = torch.zeros(512, dtype=torch.uint8)
-    for bad in (flat, Scratch.of(flat, "cuda:1"), Scratch.of(flat[::2], "cuda:0")):
+    for bad in (flat, Placed.of(flat, "cuda:1"), Placed.of(flat[::2], "cuda:0")):
         with pytest.raises(ValueError):
             tk._workspace(bad, 256, here)
-    good = Scratch.of(flat, "cuda:0")
+    good = Placed.of(flat, "cuda:0")
     assert tk._workspace(good, 256, here)[1:] == (flat.data_ptr(), 512)
     assert tk._workspace(flat[:0], 256, here) == (None, None, 0)
+
+
+def test_tensors_of_two_gpus_are_refused(tk):  # noqa: F811
+    import spatial_transformer_grid_amd as gsa
+
+    def on(i, *shape, dtype=torch.float32):
+        return Placed.of(torch.zeros(*shape, dtype=dtype), "cuda:%d" % i)
+
+    q, far, lse = on(0, 1, 2, 3, 8), on(1, 1, 2, 3, 8), on(0, 1, 2, 3)
+    x, w, row = on(0, 4, 8), on(0, 8), on(0, 4)
+    for call in (lambda: gsa.attention(q, far, q), lambda: gsa.attention(q, q, far),
+                 lambda: gsa.attention(q, q, q, kv_lengths=on(1, 1, dtype=torch.int32)),
+                 lambda: gsa.attention(q, q, q, table=on(1, 8, 2)), lambda: gsa.attention(q, q, q, out=far),
+                 lambda: gsa.attention_backward(far, q, q, q, q, lse),
+                 lambda: gsa.attention_backward(q, q, q, q, far, lse),
+                 lambda: gsa.attention_backward(q, q, q, q, q, on(1, 1, 2, 3)),
+                 lambda: gsa.layer_norm(x, on(1, 8)), lambda: gsa.layer_norm(x, w, on(1, 8)),
+                 lambda: gsa.layer_norm(x, w, out=on(1, 4, 8)),
+                 lambda: gsa.layer_norm_backward(on(1, 4, 8), x, w, row, row),
+                 lambda: gsa.layer_norm_backward(x, x, w, on(1, 4), row),
+                 lambda: gsa.layer_norm_backward(x, x, w, row, on(1, 4)),
+                 lambda: gsa.dropout(x, 0.1, 1, residual=on(1, 4, 8)), lambda: gsa.dropout(x, 0.1, 1, out=on(1, 4, 8)),
+                 lambda: gsa.affine_grid(on(0, 1, 2, 3), (1, 1, 2, 2), out=on(1, 1, 2, 2, 2)),
+                 lambda: gsa.grid_sample(q, on(1, 1, 3, 3, 2)), lambda: gsa.resize(q, sizes=(1, 2, 3, 8), out=far),
+                 lambda: gsa.affine_grid_sample_fused(on(1, 1, 2, 3), q, (3, 8)),
+                 lambda: gsa.deform_conv(q, on(1, 2, 2, 1, 1), on(0, 1, 2, 3, 8)),
+                 lambda: gsa.deform_conv(q, on(0, 2, 2, 1, 1), on(1, 1, 2, 3, 8))):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
