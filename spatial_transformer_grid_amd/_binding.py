@@ -175,7 +175,8 @@ def _on_stream(stream, call, *args, **kwargs):
     current = torch.cuda.current_stream(tensors[0].device)
     if not isinstance(stream, torch.cuda.Stream):
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        stream = torch.cuda.ExternalStream(handle, tensors[0].device)
+        stream = (torch.cuda.ExternalStream(handle, tensors[0].device) if handle
+                  else torch.cuda.default_stream(tensors[0].device))  # (0 would make a new stream)
     if stream.cuda_stream == current.cuda_stream:
         return call(*args, **kwargs)
     stream.wait_stream(current)

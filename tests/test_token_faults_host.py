@@ -55,7 +55,12 @@ class FakeTorch:
                 return torch_.now
 
             @staticmethod
+            def default_stream(device):
+                return FakeStream(0, log)
+
+            @staticmethod
             def ExternalStream(handle, device):
+                assert handle
                 return FakeStream(handle, log)
 
             @staticmethod
@@ -71,7 +76,7 @@ class FakeTorch:
         self.cuda, self.now = cuda, FakeStream(1, log)
 
 
-@pytest.mark.parametrize("given", ["stream", "handle", "current", None])
+@pytest.mark.parametrize("given", ["stream", "handle", "null", "current", None])
 def test_stream_argument_hands_memory_over(monkeypatch, given):
     """A call on a named stream starts after the current one, runs with it current (so copies and scratch are its
     own), and inputs and outputs are kept for both."""
@@ -87,12 +92,13 @@ def test_stream_argument_hands_memory_over(monkeypatch, given):
         log.append(("call", fake.now.cuda_stream))
         return y, None, z
 
-    stream = {"stream": FakeStream(2, log), "handle": 2, "current": fake.now, None: 1}[given]
+    stream = {"stream": FakeStream(2, log), "handle": 2, "null": 0, "current": fake.now, None: 1}[given]
     assert _binding._on_stream(stream, call, x, 3, workspace=ws) == (y, None, z)
     if given in ("current", None):
         assert log == [("call", 1)]
     else:
-        assert log == [("wait", 2, 1), ("record", "x", 2), ("record", "ws", 2), ("call", 2), ("record", "y", 1),
+        to = 0 if given == "null" else 2
+        assert log == [("wait", to, 1), ("record", "x", to), ("record", "ws", to), ("call", to), ("record", "y", 1),
                        ("record", "z", 1)]
     assert fake.now.cuda_stream == 1
 
