@@ -183,7 +183,8 @@ typedef struct {
  * GS_F32 not at all).  A NaN or infinity in V reaches every query of the
  * call whose mask leaves its key, and may reach the other queries of its head.
  * Errors: GS_ERR_NULL, GS_ERR_SHAPE (an extent negative, q_heads no multiple
- * of kv_heads, head_dim 0, a negative stride), GS_ERR_DTYPE, GS_ERR_ATTR
+ * of kv_heads, head_dim 0, a negative stride, one below head_dim along an axis
+ * of more than one element of an output: rows must not overlap), GS_ERR_DTYPE, GS_ERR_ATTR
  * (scale not finite, a flag not 0 or 1, ratio, buckets as in
  * gs_relative_bucket, a workspace that is misaligned), GS_ERR_TOO_LARGE
  * (head_dim above 128, q_len, kv_len or |q_position| above 2^29, heads above

@@ -76,6 +76,16 @@ bool strides_vec(const int64_t *s, int epc) {
     return true;
 }
 
+// Whether rows of an output of these extents lie apart: along an axis of more
+// than one element by at least a row.
+bool rows_apart(const int64_t *s, int64_t batch, int64_t heads, int64_t len, int64_t dim) {
+    const int64_t n[3] = {batch, heads, len};
+    if (batch * heads * len == 0) return true;
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && s[i] < dim) return false;
+    return true;
+}
+
 // Validation shared by the forward and backward calls; fills all of p but
 // the pointers.
 int attention_setup(const gs_attention_desc *d, bool backward, gs::AttnParams &p) {
@@ -110,6 +120,12 @@ int attention_setup(const gs_attention_desc *d, bool backward, gs::AttnParams &p
     const int64_t pairs = d->batch * d->q_heads, kv_pairs = d->batch * d->kv_heads;
     if (pairs > kMaxBlocks || pairs * tiles > kMaxBlocks || kv_pairs > kMaxBlocks || kv_pairs * ktiles > kMaxBlocks)
         return GS_ERR_TOO_LARGE;
+    const int64_t B = d->batch, D = d->head_dim;
+    if (backward ? !rows_apart(d->dq_stride, B, d->q_heads, d->q_len, D) ||
+                       !rows_apart(d->dk_stride, B, d->kv_heads, d->kv_len, D) ||
+                       !rows_apart(d->dv_stride, B, d->kv_heads, d->kv_len, D)
+                 : !rows_apart(d->o_stride, B, d->q_heads, d->q_len, D))
+        return GS_ERR_SHAPE;
     for (int i = 0; i < 3; ++i) {
         p.qs[i] = d->q_stride[i];
         p.ks[i] = d->k_stride[i];

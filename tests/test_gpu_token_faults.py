@@ -191,3 +191,13 @@ def test_scratch_in_host_memory_is_refused(gs):
                      lambda: gs.grid_sample(image, grid, workspace=bad)):
             with pytest.raises(ValueError):
                 call()
+
+
+def test_attention_refuses_an_expanded_output(gs):
+    q = torch.randn(2, 3, 5, 16, device="cuda")
+    for out in (torch.empty(2, 3, 1, 16, device="cuda").expand(2, 3, 5, 16),
+                torch.empty(1, 3, 5, 16, device="cuda").expand(2, 3, 5, 16),
+                torch.empty(2, 3, 200, device="cuda").as_strided((2, 3, 5, 16), (600, 200, 8, 1))):
+        with pytest.raises(gs.GSError) as e:
+            gs.attention(q, q, q, out=out)
+        assert e.value.status == 2

@@ -183,3 +183,34 @@ def test_tensors_of_two_gpus_are_refused(tk):  # noqa: F811
                  lambda: gsa.deform_conv(q, on(0, 2, 2, 1, 1), on(1, 1, 2, 3, 8))):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+# ---------------------------------------------------------------- outputs
+
+@pytest.mark.parametrize("axis", [0, 1, 2])
+@pytest.mark.parametrize("name", ["o", "dq", "dk", "dv"])
+def test_outputs_with_overlapping_rows_are_refused(tk, name, axis):  # noqa: F811
+    """A broadcast output, or one whose rows begin inside the row before, along any axis; an axis of one element
+    takes any stride, and so does every axis of a tensor without elements."""
+    lib, need = tk.token_lib(), ctypes.c_int64(0)
+    def strides(value):
+        s = [280, 56, 8]
+        s[axis] = value
+        return {name + "_stride": (ctypes.c_int64 * 3)(*s)}
+    def statuses(**over):
+        d = ctypes.byref(desc(tk, **over))
+        return (lib.gs_attention_workspace_size(d, ctypes.byref(need)),
+                lib.gs_attention_backward_workspace_size(d, ctypes.byref(need)))
+    forward = name == "o"
+    for bad in (0, 1, 7):
+        got = statuses(**strides(bad))
+        assert got == ((2, 0) if forward else (0, 2)), bad
+        d = ctypes.byref(desc(tk, **strides(bad)))
+        if forward:
+            assert lib.gs_attention(d, FAKE, FAKE, FAKE, None, FAKE, FAKE, None, None, 0, None) == 2
+        else:
+            assert lib.gs_attention_backward(d, *[FAKE] * 6, None, *[FAKE] * 5, FAKE, 1 << 20, None) == 2
+    one = [dict(batch=1), dict(q_heads=1, kv_heads=1), dict(q_len=1, kv_len=1)][axis]
+    assert statuses(**strides(0), **one) == (0, 0)
+    assert statuses(**strides(0), batch=0) == (0, 0)
+    assert statuses(**strides(8)) == (0, 0)
