@@ -214,3 +214,18 @@ def test_outputs_with_overlapping_rows_are_refused(tk, name, axis):  # noqa: F81
     assert statuses(**strides(0), **one) == (0, 0)
     assert statuses(**strides(0), batch=0) == (0, 0)
     assert statuses(**strides(8)) == (0, 0)
+
+
+# ---------------------------------------------------------------- buckets
+
+@pytest.mark.parametrize("num,distance,both", [
+    (21, 1006, 0), (42, 1006, 1),                    # the border whose two sides are closest to each other
+    (32, 128, 1), (16, 512, 0), (6, 24, 1), (64, 1000, 0), (511, 1000, 0), (512, 1024, 1), (24, 96, 0), (5, 32, 0),
+    (3, 1 << 20, 0), (2, 2 ** 31 - 1, 0), (4, 2 ** 31 - 1, 1), (7, 4000, 0), (20, 640, 1), (100, 800, 0)])
+def test_bucket_borders_where_both_sides_are_close_or_equal(tk, num, distance, both):  # noqa: F811
+    import numpy as np
+
+    import token_reference as ref
+
+    d = np.arange(-1100, 1101)
+    assert [tk.relative_bucket(int(r), num, distance, both) for r in d] == ref.bucket(d, num, distance, both).tolist()
