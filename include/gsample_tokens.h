@@ -188,8 +188,8 @@ typedef struct {
  * (scale not finite, a flag not 0 or 1, ratio, buckets as in
  * gs_relative_bucket, a workspace that is misaligned), GS_ERR_TOO_LARGE
  * (head_dim above 128, q_len, kv_len or |q_position| above 2^29, heads above
- * 2^20, the last border as in gs_relative_bucket, more than 2^24 thread
- * blocks), GS_ERR_HIP.
+ * 2^20, the last border as in gs_relative_bucket, 2^24 thread blocks or
+ * more: a block has at least 32 queries or keys of a head), GS_ERR_HIP.
  */
 int gs_attention(const gs_attention_desc *desc, const void *Q, const void *K, const void *V,
                  const int32_t *lengths, const void *table, void *O, float *lse, void *workspace,
@@ -207,7 +207,8 @@ int gs_attention_workspace_size(const gs_attention_desc *desc, int64_t *bytes);
  * is 1 whatever they are).  dtable may be NULL where it is not wanted.  dS is
  * rounded to dtype before it multiplies Q and K (with GS_F32 not at all).  The
  * workspace (256-byte aligned) is required.  Errors as gs_attention; GS_ERR_ATTR for a
- * workspace that is too small.
+ * workspace that is too small, GS_ERR_TOO_LARGE for a dtable of 2^24 - 8200
+ * elements or more.
  */
 int gs_attention_backward(const gs_attention_desc *desc, const void *dO, const void *Q,
                           const void *K, const void *V, const void *O, const float *lse,

@@ -10,7 +10,11 @@
 namespace {
 
 constexpr int64_t kInt32Max = 0x7fffffff;
-constexpr int64_t kMaxBlocks = int64_t(1) << 24;
+// Blocks of a launch: of 256 threads, whose number has to stay below 2^32, in
+// whole eighths (one an XCD).  Beside the table's sums there are at most 8192
+// blocks that add up parts (of 256 blocks of 128 rows of 128 columns, dK and dV).
+constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 8;
+constexpr int64_t kMaxTableSums = kMaxBlocks - 8192;
 constexpr int64_t kMaxPosition = int64_t(1) << 29;  // positions and their differences fit 32 bits
 constexpr int64_t kMaxHeads = int64_t(1) << 20;
 constexpr uintptr_t kWsAlign = 256;
@@ -343,6 +347,7 @@ int gs_attention_backward(const gs_attention_desc *desc, const void *dO, const v
     const int rc = attention_setup(desc, true, p);
     if (rc != GS_OK) return rc;
     if (workspace_bytes < 0) return GS_ERR_ATTR;
+    if (dtable && p.buckets * (int64_t)p.H > kMaxTableSums) return GS_ERR_TOO_LARGE;
     const bool queries = p.units > 0 && p.tiles > 0, keys = (int64_t)p.B * p.Hkv * p.Lk > 0;
     if (queries && (!dO || !Q || !O || !lse || !dQ)) return GS_ERR_NULL;
     if (keys && (!K || !V || !dK || !dV)) return GS_ERR_NULL;

@@ -201,3 +201,22 @@ def test_attention_refuses_an_expanded_output(gs):
         with pytest.raises(gs.GSError) as e:
             gs.attention(q, q, q, out=out)
         assert e.value.status == 2
+
+
+# ---------------------------------------------------------- launch limits
+
+def test_attention_of_as_many_blocks_as_a_launch_takes(gs):
+    for heads_, ok in ((2 ** 20 - 1, True), (2 ** 20, False)):
+        q = torch.ones(16, heads_, 1, 1, device="cuda", dtype=torch.float16)
+        if ok:
+            o, lse = gs.attention(q, q, q, return_lse=True)
+            assert (o == 1).all() and (lse == 1).all()
+        else:
+            with pytest.raises(gs.GSError) as e:
+                gs.attention(q, q, q)
+            assert e.value.status == 6
+    q = torch.ones(1, 2 ** 14, 1, 1, device="cuda", dtype=torch.float16)
+    table = torch.zeros(512, 2 ** 14, device="cuda", dtype=torch.float16)
+    how = dict(table=table, max_distance=1000)
+    o, lse = gs.attention(q, q, q, return_lse=True, **how)
+    assert not gs.attention_backward(q, q, q, q, o, lse, **how)[3].any()

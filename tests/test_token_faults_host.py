@@ -229,3 +229,25 @@ def test_bucket_borders_where_both_sides_are_close_or_equal(tk, num, distance, b
 
     d = np.arange(-1100, 1101)
     assert [tk.relative_bucket(int(r), num, distance, both) for r in d] == ref.bucket(d, num, distance, both).tolist()
+
+
+# ---------------------------------------------------------- launch limits
+
+def test_grids_that_no_launch_takes_are_refused(tk):  # noqa: F811
+    """2^24 blocks of 256 threads are 2^32 threads: the first size that a launch refuses."""
+    lib, need = tk.token_lib(), ctypes.c_int64(0)
+    strides = {n + "_stride": (ctypes.c_int64 * 3)(1 << 24, 8, 8) for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")}
+    heads = 1 << 20
+    for over, status in [(dict(batch=16, q_heads=heads, kv_heads=heads), 6),
+                         (dict(batch=16, q_heads=heads - 1, kv_heads=heads - 1), 0),
+                         (dict(batch=1, q_heads=heads, kv_heads=heads, q_len=512, kv_len=1), 6),
+                         (dict(batch=1, q_heads=heads, kv_heads=heads, q_len=1, kv_len=481), 6),
+                         (dict(batch=1, q_heads=heads, kv_heads=heads, q_len=480, kv_len=480), 0)]:
+        d = ctypes.byref(desc(tk, **{**dict(q_len=1, kv_len=1, **strides), **over}))
+        assert lib.gs_attention_workspace_size(d, ctypes.byref(need)) == status, over
+        assert lib.gs_attention_backward_workspace_size(d, ctypes.byref(need)) == status, over
+    d = ctypes.byref(desc(tk, batch=1, q_heads=1 << 15, kv_heads=1 << 15, q_len=1, kv_len=1, num_buckets=512,
+                          max_distance=1000, **strides))
+    assert lib.gs_attention_backward(d, *[FAKE] * 6, None, *[FAKE] * 5, None, 0, None) == 6
+    # without dtable nothing is summed for it
+    assert lib.gs_attention_backward(d, *[FAKE] * 6, None, FAKE, FAKE, FAKE, FAKE, None, None, 0, None) == 1
