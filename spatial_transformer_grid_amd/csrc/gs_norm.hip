@@ -183,7 +183,8 @@ __global__ __launch_bounds__(block_threads(NT)) void layer_norm_backward_rows(No
         float a = 0.0f, c = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            x[e] = (x[e] - mean) * inv;
+            // (past the row's end x is 0, and mean inv_std may be infinite)
+            x[e] = column<NT, VEC>(t, e) < cols ? (x[e] - mean) * inv : 0.0f;
             ds[e] = fmaf(g[e], x[e], ds[e]);
             db[e] += g[e];
             g[e] *= w[e];                            // 0 past the row's end, with w

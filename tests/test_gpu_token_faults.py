@@ -220,3 +220,32 @@ def test_attention_of_as_many_blocks_as_a_launch_takes(gs):
     how = dict(table=table, max_distance=1000)
     o, lse = gs.attention(q, q, q, return_lse=True, **how)
     assert not gs.attention_backward(q, q, q, q, o, lse, **how)[3].any()
+
+
+# ------------------------------------------------------------------- norm
+
+@pytest.mark.parametrize("cols", [1, 3, 8, 10, 40, 72, 100, 264, 300])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_layer_norm_backward_of_large_constant_rows(gs, cols, dtype):
+    """A row of one large value (without variance; mean * inv_std passes the largest fp32) has xh = 0, so that
+    dx = inv_std (g - mean(g)) and dscale = 0; other rows are as without it."""
+    t = TYPES[dtype]
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randn(5, cols, generator=g).to(t)
+    x[2] = 2.0 ** 118                                # its sum of up to 300 columns stays finite
+    dy = torch.randn(5, cols, generator=g).to(t)
+    w = (torch.randn(cols, generator=g) + 1).to(t)
+    X, dY, W = x.cuda(), dy.cuda(), w.cuda()
+    y, mean, inv = gs.layer_norm(X, W, return_stats=True)
+    assert not y[2].any() and mean[2] == 2.0 ** 118
+    dx, dw, db = gs.layer_norm_backward(dY, X, W, mean, inv)
+    gw = dy[2].double() * w.double()
+    want = (gw - gw.mean()) / math.sqrt(1e-5)
+    # g, its mean (a sum of `cols` terms), the difference and inv_std round once or twice each
+    bound = unit(t) * want.abs() + 1.01 * ((cols + 8) * E32 * (gw.abs() + gw.abs().mean()) / math.sqrt(1e-5))
+    close(dx[2], want, bound, "dx")
+    rest = [0, 1, 3, 4]
+    alone = gs.layer_norm_backward(dY[rest], X[rest], W, mean[rest], inv[rest])
+    assert torch.equal(dx[rest], alone[0])
+    ref_w = ref.layer_norm_backward(dy[rest], x[rest], w, 1e-5)[1]
+    close(dw, ref_w, unit(t) * ref_w.abs() + 1e-3 * dy.double().abs().sum(0), "dscale")
