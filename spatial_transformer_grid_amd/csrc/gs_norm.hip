@@ -1,7 +1,10 @@
 // gs_norm.hip -- layer normalisation, forward and backward.
 //
 // Forward: mean, then the sum of (x - mean)^2 (two passes over the row, so
-// that a large mean does not cancel).  Backward, with xh = (x - mean) inv_std
+// that a large mean does not cancel).  The mean is a division: times a rounded
+// 1 / cols a constant row of 1e4 in 41 columns keeps a deviation of 1e-3, which
+// epsilon = 1e-5 makes y = 0.3 (400000 x 40 bf16: 14.8 us, with a product 14.3;
+// wider rows the same).  Backward, with xh = (x - mean) inv_std
 // and g = dy scale: dx = inv_std (g - mean(g) - xh mean(g xh)); dscale and
 // dbias are sums over rows, made in parts (one per block, its rows in order)
 // and added up by a second kernel, so that the order is fixed.
@@ -142,7 +145,7 @@ __global__ __launch_bounds__(block_threads(NT)) void layer_norm_rows(NormParams 
         float s = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) s += x[e];
-        const float mean = row_total<NT>(s, red) * inv_n;
+        const float mean = row_total<NT>(s, red) / (float)cols;
         s = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -276,7 +279,7 @@ __global__ __launch_bounds__(1024) void layer_norm_wide(NormParams p) {
         raw_t *y = (raw_t *)p.Y + r * p.y_stride;
         float s = 0.0f;
         for (int c = t; c < p.cols; c += 1024) s += T::from_raw(x[c]);
-        const float mean = row_total<1024>(s, red) * inv_n;
+        const float mean = row_total<1024>(s, red) / (float)p.cols;
         s = 0.0f;
         for (int c = t; c < p.cols; c += 1024) {
             const float d = T::from_raw(x[c]) - mean;

@@ -249,3 +249,13 @@ def test_layer_norm_backward_of_large_constant_rows(gs, cols, dtype):
     assert torch.equal(dx[rest], alone[0])
     ref_w = ref.layer_norm_backward(dy[rest], x[rest], w, 1e-5)[1]
     close(dw, ref_w, unit(t) * ref_w.abs() + 1e-3 * dy.double().abs().sum(0), "dscale")
+
+
+@pytest.mark.parametrize("cols", [41, 47, 82, 328, 656, 1128, 2256, 4512, 8437, 9024, 17704, 33255])
+@pytest.mark.parametrize("value", [1.0, 2.5, -1e4])
+def test_layer_norm_of_constant_rows_is_the_bias(gs, cols, value):
+    """Widths whose rounded reciprocal is not good enough for a mean: a sum that is exact has an exact mean."""
+    x, w = torch.full((3, cols), value, device="cuda"), torch.ones(cols, device="cuda")
+    b = torch.arange(float(cols), device="cuda")
+    y, mean, inv = gs.layer_norm(x, w, b, return_stats=True)
+    assert (mean == value).all() and torch.equal(y, b.expand(3, cols))
