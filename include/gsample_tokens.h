@@ -176,8 +176,9 @@ typedef struct {
  *   lse          device fp32 (batch, q_heads, q_len), contiguous: log of the
  *                sum of exp(s), -inf for a query that sees no key; or NULL.
  *   workspace    device, 256-byte aligned, of gs_attention_workspace_size()
- *                bytes; without it (NULL, 0) a long key axis of few queries
- *                is not split over thread blocks.
+ *                bytes; without it (NULL, 0), or with less, a long key axis of
+ *                few queries is not split over thread blocks: slower, and the
+ *                sums in another order.
  *
  * The probabilities are rounded to dtype before they multiply V (with
  * GS_F32 not at all).  A NaN or infinity in V reaches every query of the

@@ -259,3 +259,86 @@ def test_layer_norm_of_constant_rows_is_the_bias(gs, cols, value):
     b = torch.arange(float(cols), device="cuda")
     y, mean, inv = gs.layer_norm(x, w, b, return_stats=True)
     assert (mean == value).all() and torch.equal(y, b.expand(3, cols))
+
+
+# --------------------------------------------- forms of large grids alone
+
+@pytest.mark.parametrize("shape", [(4, 64, 16, 520, 33, 64), (4, 32, 8, 520, 201, 128), (2, 64, 32, 1100, 77, 48),
+                                   (8, 8, 8, 1030, 65, 128)])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("over", [dict(buckets=8, distance=24, ratio=0.2),
+                                  dict(causal=1, position="end", ragged=True, by_position=True),
+                                  dict(causal=1, position=-3, buckets=32, both=0, ratio=0.1, ragged=True)])
+def test_attention_backward_of_split_128_key_blocks(gs, shape, dtype, over):
+    """dK / dV blocks of 128 keys whose queries are split over parts, a part from the middle of a head on."""
+    over = dict(over)
+    if over.pop("ragged", False):
+        B, Lk = shape[0], shape[4]
+        over["lengths"] = [Lk - b * Lk // B for b in range(B - 1)] + [0]
+    check_attention(gs, *shape, dtype, **over)
+
+
+# ------------------------------------------------------------ small scratch
+
+def test_attention_with_less_scratch_than_it_asks_for(gs):
+    """Scratch that is too small for a split of the keys is left alone, and the call is as without any."""
+    g = torch.Generator().manual_seed(31)
+    q, k, v = (heads(g, 1, 8, n, 64, torch.bfloat16, False) for n in (1, 3000, 3000))
+    none = gs.attention(q, k, v, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    small = torch.full((256,), 7, dtype=torch.uint8, device="cuda")
+    assert torch.equal(gs.attention(q, k, v, workspace=small), none) and (small == 7).all()
+
+
+# ----------------------------------------------- past 2^31 elements or bytes
+
+@pytest.mark.parametrize("step", [1 << 22, (1 << 22) + 8, (1 << 22) + 1])
+def test_attention_of_rows_far_apart(gs, step):
+    """A cache whose rows lie up to 2^31.5 elements from its first, queries as far: the bits of dense tensors."""
+    g = torch.Generator().manual_seed(32)
+    t = torch.bfloat16
+    n = 700
+    cache = torch.empty(n * step + 512, dtype=t, device="cuda")
+    far = lambda at, heads_, length, s: cache.as_strided((1, heads_, length, 64), (n * step, 64, s, 1), at)
+    dense = [heads(g, 1, h, length, 64, t, False) for h, length in ((4, 65), (2, n), (2, n), (4, 65))]
+    views = [far(256, 4, 65, 10 * step), far(0, 2, n, step), far(128, 2, n, step)]
+    for view, x in zip(views, dense):
+        view.copy_(x)
+    how = dict(table=torch.randn(8, 4, generator=g).to(t).cuda(), max_distance=20, causal=1, q_position=n - 65)
+    o, lse = gs.attention(*views, out=torch.empty_like(dense[0]), return_lse=True, **how)
+    want, want_lse = gs.attention(*dense[:3], return_lse=True, **how)
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    assert torch.equal(gs.attention(views[0][:, :, -1:], *views[1:], **{**how, "q_position": n - 1}),
+                       gs.attention(dense[0][:, :, -1:], *dense[1:3], **{**how, "q_position": n - 1}))
+    got = gs.attention_backward(dense[3], *views, o, lse, **how)
+    for a, b in zip(got, gs.attention_backward(dense[3], *dense[:3], o, lse, **how)):
+        assert torch.equal(a, b)
+
+
+def test_layer_norm_past_2_31_elements(gs):
+    t = torch.bfloat16
+    w = torch.ones(1032, device="cuda", dtype=t)
+    rows = (1 << 21) + 3
+    x = torch.empty(rows, 1032, device="cuda", dtype=t)
+    x[:-4096].fill_(1.0)
+    x[-4096:] = torch.randn(4096, 1032, device="cuda", dtype=t)
+    y, mean, inv = gs.layer_norm(x, w, return_stats=True)
+    tail = gs.layer_norm(x[-4096:], w, return_stats=True)
+    assert torch.equal(y[-4096:], tail[0]) and torch.equal(mean[-4096:], tail[1]) and torch.equal(inv[-4096:], tail[2])
+    assert not y[:64].any()
+    del tail
+    dx = gs.layer_norm_backward(y, x, w, mean, inv)[0]
+    assert torch.equal(dx[-4096:], gs.layer_norm_backward(y[-4096:], x[-4096:], w, mean[-4096:], inv[-4096:])[0])
+    del y, dx
+    apart = x.flatten().as_strided((3, 1032), (1 << 30, 1))
+    assert torch.equal(gs.layer_norm(apart, w), gs.layer_norm(apart.clone(), w))
+
+
+def test_dropout_past_2_31_elements(gs):
+    import numpy as np
+
+    n, first = (1 << 31) + 100003, (1 << 31) - 4096
+    x = torch.ones(n, device="cuda", dtype=torch.bfloat16)
+    y = gs.dropout(x, 0.3, 11, 2)[first:].cpu()
+    at = np.arange(first // 8, (n + 7) // 8, dtype=np.uint64)
+    want = ref.factors(ref.numbers((at, 0, 0, 2), 11).reshape(-1)[:n - first], 0.3)
+    close(y, want, unit(torch.bfloat16) * want + 4 * E32 * want, "y")

@@ -251,3 +251,28 @@ def test_grids_that_no_launch_takes_are_refused(tk):  # noqa: F811
     assert lib.gs_attention_backward(d, *[FAKE] * 6, None, *[FAKE] * 5, None, 0, None) == 6
     # without dtable nothing is summed for it
     assert lib.gs_attention_backward(d, *[FAKE] * 6, None, FAKE, FAKE, FAKE, FAKE, None, None, 0, None) == 1
+
+
+# ------------------------------------------------------------------ plans
+
+# B, H, Hkv, Lq, Lk, D: 64 blocks of 128 keys whose (head, query tile) pairs are split over parts
+SPLIT_128 = [(4, 64, 16, 520, 33, 64), (4, 32, 8, 520, 201, 128), (2, 64, 32, 1100, 77, 48), (8, 8, 8, 1030, 65, 128)]
+
+
+@pytest.mark.parametrize("shape", SPLIT_128)
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+def test_split_of_128_key_blocks_is_planned(tk, shape, dtype):  # noqa: F811
+    """The workspace holds delta, the table's sums of (blocks of 128 keys) x parts, and the parts of dK and dV."""
+    B, H, Hkv, Lq, Lk, D = shape
+    lib, need = tk.token_lib(), ctypes.c_int64(0)
+    def size(buckets):
+        d = ctypes.byref(desc(tk, dtype=dtype, table_dtype=0, batch=B, q_heads=H, kv_heads=Hkv, q_len=Lq, kv_len=Lk,
+                              head_dim=D, num_buckets=buckets, **{n + "_stride": (ctypes.c_int64 * 3)(1 << 30, 1 << 20, 128)
+                                                                  for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")}))
+        assert lib.gs_attention_backward_workspace_size(d, ctypes.byref(need)) == 0
+        return need.value
+    rounded = lambda n: (n + 255) // 256 * 256
+    sums = size(0) - rounded(B * H * Lq * 4)
+    parts, rest = divmod(sums, rounded(B * Hkv * Lk * 2 * D * 4))
+    assert rest == 0 and parts >= 2
+    assert size(8) - size(0) == rounded(B * H * ((Lk + 127) // 128) * parts * 8 * 4)
