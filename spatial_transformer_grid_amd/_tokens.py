@@ -234,9 +234,19 @@ def dropout(X, ratio: float, seed: int, call: int = 0, residual=None, out=None, 
 def relative_bucket(r: int, num_buckets: int, max_distance: int = 128, bidirectional: int = 1) -> int:
     """Bucket of key position minus query position (gs_relative_bucket)."""
     got = _I(0)
-    _check(token_lib().gs_relative_bucket(int(r), int(num_buckets), int(max_distance),
-                                          int(bidirectional), ctypes.byref(got)), "gs_relative_bucket")
+    _check(token_lib().gs_relative_bucket(_whole(r, "r", 64), _whole(num_buckets, "num_buckets"),
+                                          _whole(max_distance, "max_distance"),
+                                          _whole(bidirectional, "bidirectional"), ctypes.byref(got)),
+           "gs_relative_bucket")
     return got.value
+
+
+def _whole(value, name, bits=32):
+    """`value` as a whole number that a field of the C interface holds (ctypes would cut it)."""
+    value = int(value)
+    if not -(1 << (bits - 1)) <= value < 1 << (bits - 1):
+        raise ValueError("%s must fit %d bits" % (name, bits))
+    return value
 
 
 def _strides(t):
@@ -265,13 +275,13 @@ def _attention_inputs(Q, K, V, scale, causal, kv_lengths, table, max_distance, b
     d.kv_heads, d.kv_len = K.shape[1], K.shape[2]
     d.q_stride, d.k_stride, d.v_stride = _strides(Q), _strides(K), _strides(V)
     d.scale = 1.0 / math.sqrt(D) if scale is None and D else float(scale or 0.0)
-    d.causal = int(causal)
+    d.causal = _whole(causal, "causal")
     if isinstance(q_position, str):
         if q_position != "end":
             raise ValueError('q_position must be a number or "end"')
         d.q_from_end = 1
     else:
-        d.q_position = int(q_position)
+        d.q_position = _whole(q_position, "q_position", 64)
     if table is not None:
         table = _device_tensor(table, "table", Q)
         if table.dim() != 2 or table.shape[1] != H:
@@ -281,7 +291,8 @@ def _attention_inputs(Q, K, V, scale, causal, kv_lengths, table, max_distance, b
         if table.shape[0] < 2:
             raise ValueError("table needs two buckets or more")
         d.table_dtype = dtype_code(table)
-        d.num_buckets, d.max_distance, d.bidirectional = table.shape[0], int(max_distance), int(bidirectional)
+        d.num_buckets, d.max_distance = _whole(table.shape[0], "buckets"), _whole(max_distance, "max_distance")
+        d.bidirectional = _whole(bidirectional, "bidirectional")
     else:
         d.table_dtype = GS_F32
     d.ratio, d.seed, d.call = ratio, int(seed) & _MASK64, int(call) & _MASK32

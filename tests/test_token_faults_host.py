@@ -253,6 +253,23 @@ def test_grids_that_no_launch_takes_are_refused(tk):  # noqa: F811
     assert lib.gs_attention_backward(d, *[FAKE] * 6, None, FAKE, FAKE, FAKE, FAKE, None, None, 0, None) == 1
 
 
+@pytest.mark.parametrize("over", [dict(r=1 << 63), dict(num_buckets=(1 << 32) + 32), dict(max_distance=(1 << 32) + 128),
+                                  dict(bidirectional=1 << 32)])
+def test_numbers_that_a_field_cuts_are_refused(tk, over):  # noqa: F811
+    good = dict(r=-20, num_buckets=32, max_distance=128, bidirectional=1)
+    assert tk.relative_bucket(**good) == 10
+    with pytest.raises(ValueError):
+        tk.relative_bucket(**{**good, **over})
+    if "max_distance" in over or "bidirectional" in over:
+        q = Placed.of(torch.zeros(1, 2, 3, 8), "cuda:0")
+        table = Placed.of(torch.zeros(32, 2), "cuda:0")
+        for wrong in (over, dict(causal=1 << 32), dict(q_position=1 << 64)):
+            with pytest.raises(ValueError, match="bits"):
+                tk._attention_inputs(q, q, q, **{**dict(
+                    scale=None, causal=0, kv_lengths=None, table=table, max_distance=128, bidirectional=1, q_position=0,
+                    ratio=0.0, seed=0, call=0), **wrong})
+
+
 # ------------------------------------------------------------------ plans
 
 # B, H, Hkv, Lq, Lk, D: 64 blocks of 128 keys whose (head, query tile) pairs are split over parts
