@@ -165,6 +165,9 @@ typedef struct {
  *   p_j = exp(s_j) / sum of exp(s),  o_i = sum of dropout(p_j) * v_j.
  * Key j of query i uses number j % 8 of the counter
  * (j / 8, i, b * q_heads + h, call).  A query that sees no key gives 0.
+ * A bias of any finite size may serve as a mask: a query whose every key has
+ * one keeps the softmax of its products, which a constant does not change.
+ * (Values beyond 2.35e38 count as that; -inf hides a key as a mask does.)
  *
  *   Q            device (batch, q_heads, q_len, head_dim)
  *   K, V         device (batch, kv_heads, kv_len, head_dim)
@@ -205,7 +208,8 @@ int gs_attention_workspace_size(const gs_attention_desc *desc, int64_t *bytes);
  * wrote, under the same descriptor.  dQ, dK, dV and dtable (num_buckets,
  * q_heads; contiguous, table_dtype) are overwritten whole; keys that no query
  * sees get 0, as do the scores of a query that sees one key (its probability
- * is 1 whatever they are).  dtable may be NULL where it is not wanted.  dS is
+ * is 1 whatever they are).  Probabilities are made again from lse: its fp32
+ * rounding is a relative error of up to |lse| 2^-23 of theirs.  dtable may be NULL where it is not wanted.  dS is
  * rounded to dtype before it multiplies Q and K (with GS_F32 not at all).  The
  * workspace (256-byte aligned) is required.  Errors as gs_attention; GS_ERR_ATTR for a
  * workspace that is too small, GS_ERR_TOO_LARGE for a dtable of 2^24 - 8200

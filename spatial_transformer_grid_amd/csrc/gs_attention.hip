@@ -68,6 +68,8 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
     extern __shared__ __align__(16) unsigned char smem[];
     float *luts = (float *)(smem + Geo::fixed_bytes);
     __shared__ float stat[WS][2][ROWS];              // maximum and sum of each part
+    __shared__ float shifts[ROWS];                   // row_shift of each row, where `shifted`
+    __shared__ int large;                            // the table holds a bias that row_shift is for
 
     int unit, tile, part;
     if (!block_place(p, !FEW, FEW && p.pack ? 1 : p.G, unit, tile, part)) return;
@@ -126,17 +128,28 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
     }
     const float *lut = luts;
     float bias_lo = 0.0f, bias_hi = 0.0f;
+    bool shifted = false;
+    const int col = rg * 32 + (lane & 31);           // the lane's row in the block
     if (p.lut) {
+        if (t == 0) large = 0;
         const int heads = FEW && p.pack ? p.G : 1;
         uint16_t *starts = (uint16_t *)(luts + heads * p.lut);
         for (int i = t; i < p.side; i += 256) starts[i] = p.starts[i];
         __syncthreads();
         for (int i = 0; i < heads; ++i)
-            fill_lut<T>(p, FEW && p.pack ? hk * p.G + i : h, luts + i * p.lut, starts, t, 256);
+            if (fill_lut<T>(p, FEW && p.pack ? hk * p.G + i : h, luts + i * p.lut, starts, t, 256)) large = 1;
         __syncthreads();
         lut = luts + (FEW ? g * p.lut : 0);
+        shifted = __builtin_amdgcn_readfirstlane(large);
         bias_lo = lut[0];
         bias_hi = lut[p.lut - 1];
+        if (shifted) {
+            const float shift = row_shift(p, lut, pos, p.causal ? min(len, pos + 1) : len);
+            bias_lo -= shift;
+            bias_hi -= shift;
+            shifts[col] = shift;                     // (kept there: no register of the loop's)
+            tile_sync<true>();
+        }
     }
 
     f32x16 acc[DP / 32];
@@ -188,17 +201,24 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
             const int key0 = k0 + 8 * half;
             float mul = scale2, c = 0.0f;
             const int cls = bias_class(p, k0 - wave_last, k0 + KEYS - 1 - wave_first);
-            const bool edge = k0 + KEYS > end || (p.causal && k0 + KEYS - 1 > wave_first);
+            const bool edge = shifted || k0 + KEYS > end || (p.causal && k0 + KEYS - 1 > wave_first);
             if (cls == 1) c = bias_lo;
             if (cls == 2) c = bias_hi;
             // fp32 rounds every score before the maximum leaves it, so that the
             // largest one's probability is 1 exactly; elsewhere the probability's
-            // own rounding hides the difference
+            // own rounding hides the difference, but for a bias so large that the
+            // maximum loses the products (`shifted`: keys masked by -1e9 before others)
             if (cls == 0 || edge || T::bytes == 4) {
                 if (cls == 0) {
                     float bias[16 * U];
                     read_all<16 * U>(lut + (key0 - pos + p.border + kLutPad), bias,
                                      [](int i) { return 16 * (i >> 3) + (i & 7); });
+                    if (shifted) {
+                        rare<16 * U>(bias);
+                        const float shift = *(volatile float *)(shifts + col);
+#pragma unroll
+                        for (int i = 0; i < 16 * U; ++i) bias[i] -= shift;
+                    }
 #pragma unroll
                     for (int i = 0; i < 16 * U; ++i) s[i] = fmaf(s[i], mul, bias[i]);
                 } else {
@@ -269,10 +289,10 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
                 store4<T>(orow, 32 * d + 2 * r + 4 * half, p.D, vec, acc[d][r] * norm, acc[d][r + 1] * norm,
                           acc[d][r + 2] * norm, acc[d][r + 3] * norm);
         if (p.lse && half == 0)
-            p.lse[(int64_t)unit * p.Lq + qi] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+            p.lse[(int64_t)unit * p.Lq + qi] =
+                l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2 + (shifted ? natural(shifts[col]) : 0.0f);
     } else {
         // the parts' O and l under a common maximum, added in the order of the parts
-        const int col = rg * 32 + (lane & 31);
         if (half == 0) {
             stat[wp][0][col] = m;
             stat[wp][1][col] = l;
@@ -312,6 +332,8 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
                     float *st = p.split + (int64_t)p.splits * all_rows * dr + ((int64_t)part * all_rows + flat) * 2;
                     st[0] = big;
                     st[1] = lr;
+                    if (p.lse && part == 0)                  // attention_combine adds the rest
+                        p.lse[flat] = shifted ? natural(shifts[r]) : 0.0f;
                 }
                 continue;
             }
@@ -320,7 +342,9 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
             const int bb = (int)(bh / p.H), hh = (int)(bh - (int64_t)bb * p.H), q = (int)(flat - bh * p.Lq);
             raw_t *orow = (raw_t *)p.o + (int64_t)bb * p.os[0] + (int64_t)hh * p.os[1] + (int64_t)q * p.os[2];
             store4<T>(orow, at, p.D, vec, v[0] * norm, v[1] * norm, v[2] * norm, v[3] * norm);
-            if (p.lse && at == 0) p.lse[flat] = lr == 0.0f ? -INFINITY : (big + __builtin_amdgcn_logf(lr)) * kLn2;
+            if (p.lse && at == 0)
+                p.lse[flat] = lr == 0.0f ? -INFINITY
+                                         : (big + __builtin_amdgcn_logf(lr)) * kLn2 + (shifted ? natural(shifts[r]) : 0.0f);
         }
     }
 }
@@ -364,7 +388,7 @@ __global__ __launch_bounds__(256) void attention_combine(AttnParams p) {
     raw_t *orow = (raw_t *)p.o + (int64_t)b * p.os[0] + (int64_t)h * p.os[1] + (int64_t)q * p.os[2];
     if (lane < p.D) orow[lane] = to_bits<T>(v[0] * norm);
     if (lane + 64 < p.D) orow[lane + 64] = to_bits<T>(v[1] * norm);
-    if (p.lse && lane == 0) p.lse[r] = l == 0.0f ? -INFINITY : (big + __builtin_amdgcn_logf(l)) * kLn2;
+    if (p.lse && lane == 0) p.lse[r] = l == 0.0f ? -INFINITY : (big + __builtin_amdgcn_logf(l)) * kLn2 + p.lse[r];
 }
 
 template <typename T, int DP, bool DROP, int WS>

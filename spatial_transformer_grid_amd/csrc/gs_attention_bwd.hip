@@ -47,6 +47,38 @@ constexpr int kExactKeys = 256;
 constexpr int kDiagonalRow = 68;
 constexpr int kDiagonal = 32 + 32 * kDiagonalRow;    // floats of a wave
 
+// What the dK / dV kernel takes of 64 queries from the dQ kernel: -lse (base 2,
+// relative to the row's shift) without and with the biases of the two ends of the
+// table, and delta / keep_scale; 64 of each, so that one asynchronous load of a wave
+// brings them.  Queries past the last have -inf: their probabilities are 0.  The
+// shifts themselves, read where a table has any, follow the stats of all rows.
+constexpr int kRowStats = 4 * 64;
+
+__device__ __forceinline__ float *row_stats(const AttnParams &p, int64_t bh, int tile) {
+    return p.rows + (bh * ((p.Lq + 63) >> 6) + tile) * kRowStats;
+}
+
+__device__ __forceinline__ float *row_shifts(const AttnParams &p, int64_t bh) {
+    const int64_t tiles = (p.Lq + 63) >> 6;
+    return p.rows + (int64_t)p.B * p.H * tiles * kRowStats + bh * tiles * 64;
+}
+
+__device__ __forceinline__ void put_row(const AttnParams &p, int64_t bh, int q, float minus_lse, float lo, float hi,
+                                        float delta, float shift) {
+    float *s = row_stats(p, bh, q >> 6) + (q & 63);
+    s[0] = minus_lse;
+    s[64] = lo;
+    s[128] = hi;
+    s[192] = delta;
+    if (p.lut) row_shifts(p, bh)[q] = shift;
+}
+
+// The stats of 64 rows into LDS, by one wave.
+__device__ __forceinline__ void copy_rows(float *lds, const float *from, int lane) {
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)from, 0, kRowStats * 4, 0x00027000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void *)lds, 16, lane * 16, 0, 0, 0);
+}
+
 // Geometry of both kernels.  WS: into how many parts (1 or 4) the waves of a block
 // split the axis that is walked; a block has BLOCK = 128 / WS rows of the other.  ROWS
 // rows of the walked axis in an LDS tile, two buffers of two tensors, a block's
@@ -103,7 +135,9 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
     extern __shared__ __align__(16) unsigned char smem[];
     float *lut = (float *)(smem + Geo::tile_bytes);
     uint16_t *starts = (uint16_t *)(lut + (p.lut + 3) / 4 * 4);
-    __shared__ float row_sums[WS][BLOCK];
+    __shared__ float row_sums[WS][BLOCK], row_tops[WS][BLOCK];
+    __shared__ float shifts[BLOCK];                  // row_shift of each row, where `shifted`
+    __shared__ int large;                            // the table holds a bias that row_shift is for
 
     int unit, tile, part;
     if (!block_place(p, !FEW, p.G, unit, tile, part)) return;
@@ -160,13 +194,87 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
     }
     delta = delta / p.keep_scale;
     float bias_lo = 0.0f, bias_hi = 0.0f;
+    bool shifted = false;
+    const int col = rg * 32 + (lane & 31);           // the lane's row in the block
     if (p.lut) {
+        if (t == 0) large = 0;
         for (int i = t; i < p.side; i += 256) starts[i] = p.starts[i];
         __syncthreads();
-        fill_lut<T>(p, h, lut, starts, t, 256);
+        if (fill_lut<T>(p, h, lut, starts, t, 256)) large = 1;
         __syncthreads();
         bias_lo = lut[0];
         bias_hi = lut[p.lut - 1];
+        shifted = __builtin_amdgcn_readfirstlane(large);
+    }
+    if (shifted) {
+        const float shift = row_shift(p, lut, pos, p.causal ? min(len, pos + 1) : len);
+        bias_lo -= shift;
+        bias_hi -= shift;
+        shifts[col] = shift;                         // (kept there: no register of the loop's)
+        if (__syncthreads_or(shift != 0.0f)) {
+            // the lse of a row with a shift has lost the sum beside it: maximum and
+            // sum of the exponentials once more, relative to the shift
+            float top = -INFINITY, sum = 0.0f;
+            for (int k0 = begin, n = 0; k0 < end; k0 += STEP, ++n) {
+                const raw_t *Ks = Kt + (Geo::bufs == 2 ? (n & 1) * 2 * Geo::tile_elems : 0);
+                async_wait();
+                tile_sync<FEW>();
+                const bool more = k0 + STEP < end;
+                if (Geo::bufs == 2 && more) load(Kt + ((n + 1) & 1) * 2 * Geo::tile_elems, k0 + STEP);
+#pragma unroll 1
+                for (int u = 0; u < KEYS / 32; ++u) {
+                    const int ku = k0 + 32 * u, key0 = ku + 8 * half;
+                    if (q0 >= p.Lq || ku >= end || (p.causal && ku > wave_last)) continue;
+                    f32x16 st;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) st[r] = 0.0f;
+                    const int row = 32 * u + a_row(lane & 31);
+                    pipelined<T, DP / 16, 1>([&](int i) { return frag_lds<T, DP>(Ks, row, 16 * i + 8 * half); },
+                                             [&](int i, const Frag<T> &a) {
+                                                 if (step_counts<T>(p, i)) mma<T>(st, a, qf[i]);
+                                             });
+                    const int cls = bias_class(p, ku - wave_last, ku + 31 - wave_first);
+                    const int seen = (p.causal ? min(end, pos + 1) : end) - key0;
+                    float high = top;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int j = 16 * (i >> 3) + (i & 7);
+                        const float c = cls == 0 ? lut[key0 - pos + p.border + kLutPad + j] - shift
+                                                 : cls == 1 ? bias_lo : bias_hi;
+                        st[i] = j < seen ? fmaf(st[i], p.scale2, c) : -INFINITY;
+                        high = fmaxf(high, st[i]);
+                    }
+                    const float from = high == -INFINITY ? 0.0f : high;
+                    sum *= __builtin_amdgcn_exp2f(top - from);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum += __builtin_amdgcn_exp2f(st[i] - from);
+                    top = high;
+                }
+                if (Geo::bufs == 1 && more) {
+                    tile_sync<true>();
+                    load(Kt, k0 + STEP);
+                }
+            }
+            float all = fmaxf(top, other_half(top));
+            if constexpr (WS > 1) {
+                if (half == 0) row_tops[wp][col] = all;
+                __syncthreads();
+#pragma unroll
+                for (int w = 0; w < WS; ++w) all = fmaxf(all, row_tops[w][col]);
+            }
+            sum *= __builtin_amdgcn_exp2f(top - (all == -INFINITY ? 0.0f : all));
+            sum += other_half(sum);
+            if constexpr (WS > 1) {
+                if (half == 0) row_sums[wp][col] = sum;
+                __syncthreads();
+                sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < WS; ++w) sum += row_sums[w][col];
+            }
+            if (shift != 0.0f) minus_lse = -(all + __builtin_amdgcn_logf(sum));
+            __syncthreads();
+            if (begin < end) load(Kt, begin);
+        }
     }
     f32x16 acc[DP / 32];
 #pragma unroll
@@ -215,6 +323,12 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
                     float bias[16];
                     read_all<16>(lut + (key0 - pos + p.border + kLutPad), bias,
                                  [](int i) { return 16 * (i >> 3) + (i & 7); });
+                    if (shifted) {
+                        rare<16>(bias);
+                        const float shift = *(volatile float *)(shifts + col);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) bias[i] -= shift;
+                    }
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         e[i] = __builtin_amdgcn_exp2f(fmaf(st[i], p.scale2, bias[i]) + minus_lse);
@@ -259,15 +373,19 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
         }
         sum += other_half(sum);
         if constexpr (WS > 1) {
-            if (half == 0) row_sums[wp][rg * 32 + lane] = sum;
+            if (half == 0) row_sums[wp][col] = sum;
             __syncthreads();
             sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < WS; ++w) sum += row_sums[w][rg * 32 + (lane & 31)];
+            for (int w = 0; w < WS; ++w) sum += row_sums[w][col];
         }
         delta += sum;
     }
-    if (live && half == 0 && wp == 0) p.delta[(int64_t)unit * p.Lq + qi] = delta * p.keep_scale;
+    if (live && half == 0 && wp == 0)
+        put_row(p, unit, qi, minus_lse, minus_lse + bias_lo, minus_lse + bias_hi, delta, shifted ? shifts[col] : 0.0f);
+    if (tile == p.tiles - 1)
+        for (int q = p.Lq + t; q < (p.Lq + 63) / 64 * 64; q += 256)
+            put_row(p, unit, q, -INFINITY, -INFINITY, -INFINITY, 0.0f, 0.0f);
     const float scale = p.scale * p.keep_scale;
     if constexpr (WS == 1) {
         if (live) {
@@ -301,14 +419,14 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
     constexpr bool FEW = Geo::FEW;
     constexpr int ROWS = Geo::ROWS, BLOCK = Geo::BLOCK, NT = FEW ? 64 : 256;
     extern __shared__ __align__(16) unsigned char smem[];
-    // per copy of a tile: minus lse without and with the biases of the two ends, delta
-    float *row_stats = (float *)(smem + Geo::tile_bytes);
-    unsigned char *masks = (unsigned char *)(row_stats + Geo::copies * 4 * ROWS);   // [wave][4][32]
+    float *stats = (float *)(smem + Geo::tile_bytes);          // row_stats of each copy of a tile
+    unsigned char *masks = (unsigned char *)(stats + Geo::copies * kRowStats);   // [wave][4][32]
     float *lut = (float *)(masks + 512);
     float *diagonals = lut + (p.lut + 3) / 4 * 4;    // [wave][kDiagonal]
     float *near = diagonals + (p.part ? 4 * kDiagonal : 0);   // [wave][lut]
     float *far = near + (p.part ? 4 * p.lut : 0);    // [wave][2]
     uint16_t *starts = (uint16_t *)(far + 8);
+    __shared__ int large;                            // a head's table holds a bias that row_shift is for
 
     int unit, tile, part;
     if (!block_place(p, false, 1, unit, tile, part)) return;
@@ -348,10 +466,10 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
     const int64_t p0 = pairs * part / p.splits, p1 = pairs * (part + 1) / p.splits;
     const int tt = FEW ? lane : t;
     raw_t *Qt = (raw_t *)smem + (FEW ? wave * Geo::bufs * 2 * Geo::tile_elems : 0);
-    float *stats = row_stats + (FEW ? wave * Geo::bufs * 4 * ROWS : 0);
+    if (FEW) stats += wave * Geo::bufs * kRowStats;
     unsigned char *mask = masks + wave * 128;
-    const float keep_inv = 1.0f / p.keep_scale;
     float *diagonal = diagonals + wave * kDiagonal + 32, *mine = near + wave * p.lut;
+    if (t == 0) large = 0;
     if (p.part)
         for (int i = t; i < 4 * kDiagonal; i += 256) diagonals[i] = 0.0f;
 
@@ -369,51 +487,28 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
         const raw_t *qb = (const raw_t *)p.q + (int64_t)b * p.qs[0] + (int64_t)h * p.qs[1];
         const raw_t *gb = (const raw_t *)p.d_o + (int64_t)b * p.dos[0] + (int64_t)h * p.dos[1];
         __syncthreads();
-        float bias_lo = 0.0f, bias_hi = 0.0f;
         float far_lo = 0.0f, far_hi = 0.0f;          // sums of distances past the last change
+        bool shifted = false;
         if (p.lut) {
-            fill_lut<T>(p, h, lut, starts, t, 256);
+            if (fill_lut<T>(p, h, lut, starts, t, 256)) large = 1;
             if (p.part)
                 for (int i = t; i < 4 * p.lut; i += 256) near[i] = 0.0f;
             __syncthreads();
-            bias_lo = lut[0];
-            bias_hi = lut[p.lut - 1];
+            shifted = __builtin_amdgcn_readfirstlane(large);
         }
-        float lse = 0.0f, delta = 0.0f;              // of row tt of the tile in flight
-        const auto fetch_stats = [&](int q0) {
-            if (tt < ROWS) {
-                const bool in = q0 + tt < p.Lq;
-                const int64_t at = (int64_t)bh * p.Lq + q0 + tt;
-                lse = in ? p.lse[at] : -INFINITY;
-                delta = in ? p.delta[at] : 0.0f;
-            }
-        };
-        const auto put_stats = [&](int copy) {
-            if (tt < ROWS) {
-                float *s = stats + copy * 4 * ROWS;
-                const float e = lse == -INFINITY ? -INFINITY : -lse * kLog2e;   // 2^(s - inf) = 0: no key seen
-                s[tt] = e;
-                s[ROWS + tt] = e + bias_lo;
-                s[2 * ROWS + tt] = e + bias_hi;
-                s[3 * ROWS + tt] = delta * keep_inv;
-            }
-        };
         const auto load = [&](int copy, int q0) {
             raw_t *to = Qt + copy * 2 * Geo::tile_elems;
-            fetch_stats(q0);
+            if (tt < 64) copy_rows(stats + copy * kRowStats, row_stats(p, bh, q0 >> 6), tt);
             copy_tile<T, DP, ROWS, NT>(to, qb, p.qs[2], q0, p.Lq, p.D, p.async, vec, tt);
             copy_tile<T, DP, ROWS, NT>(to + Geo::tile_elems, gb, p.dos[2], q0, p.Lq, p.D, p.async, vec, tt);
         };
         constexpr int STEP = FEW ? 4 : 1;
         const int begin = FEW ? t0 + wave : t0;
-        if (begin < t1) {
-            load(0, q_begin + begin * ROWS);
-            put_stats(0);
-        }
+        if (begin < t1) load(0, q_begin + begin * ROWS);
         for (int n = begin, it = 0; n < t1; n += STEP, ++it) {
             const int q0 = q_begin + n * ROWS, copy = Geo::bufs == 2 ? it & 1 : 0;
             const raw_t *Qs = Qt + copy * 2 * Geo::tile_elems, *Gs = Qs + Geo::tile_elems;
-            const float *rs = stats + copy * 4 * ROWS;
+            const float *rs = stats + copy * kRowStats + (q0 & 63);
             async_wait();
             tile_sync<FEW>();
             const bool more = n + STEP < t1;
@@ -451,13 +546,19 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int r0 = 32 * u + 16 * x + 8 * half;   // this lane's eight queries
-                    const float *ml = rs + (cls == 1 ? ROWS : cls == 2 ? 2 * ROWS : 0) + r0;
-                    const float *dl = rs + 3 * ROWS + r0;
+                    const float *ml = rs + (cls == 1 ? 64 : cls == 2 ? 128 : 0) + r0;
+                    const float *dl = rs + 192 + r0;
                     float pd[8], *ds = all + 8 * x;
                     if (cls == 0) {
                         float bias[8];
                         read_all<8>(lut + (key - first - q0 - r0 + p.border + kLutPad), bias,
                                     [](int j) { return -j; });
+                        if (shifted) {
+                            rare<8>(bias);
+                            const float *shift = row_shifts(p, bh) + q0 + r0;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) bias[j] -= shift[j];
+                        }
 #pragma unroll
                         for (int j = 0; j < 8; ++j) pd[j] = fmaf(st[8 * x + j], p.scale2, bias[j]) + ml[j];
                     } else {
@@ -533,12 +634,9 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
                                i & 1 ? df[i / (DP / 16)] : pf[i / (DP / 16)]);
                     });
             }
-            if (more) {
-                if (Geo::bufs == 1) {
-                    tile_sync<true>();
-                    load(0, q0 + STEP * ROWS);
-                }
-                put_stats(Geo::bufs == 2 ? (it + 1) & 1 : 0);
+            if (Geo::bufs == 1 && more) {
+                tile_sync<true>();
+                load(0, q0 + STEP * ROWS);
             }
         }
         if (p.part) {
@@ -686,7 +784,7 @@ int q_lds(const AttnParams &p) {
 template <typename T, int DP, int WS>
 int kv_lds(const AttnParams &p, bool table) {
     typedef BwdGeo<T, DP, WS, true> Geo;
-    return Geo::tile_bytes + Geo::copies * 4 * Geo::ROWS * 4 + 512 + (p.lut + 3) / 4 * 16 +
+    return Geo::tile_bytes + Geo::copies * kRowStats * 4 + 512 + (p.lut + 3) / 4 * 16 +
            (table ? 4 * (kDiagonal + p.lut) * 4 : 0) + 32 + p.side * 2;
 }
 

@@ -40,7 +40,7 @@ struct AttnParams {
     void *o, *dq, *dk, *dv, *dtable;
     float *lse;
     const int32_t *lengths;
-    float *delta;             // backward: (B, H, Lq), sums of P dropout(dO V^T)
+    float *rows;              // backward: what the dK / dV kernel takes of the queries (row_stats)
     float *part;              // backward: (H, B, key tiles, parts, buckets) sums of dS
     float *split;             // sums of the parts of a split axis (see each kernel)
     int64_t qs[3], ks[3], vs[3], os[3], dos[3], dqs[3], dks[3], dvs[3];
@@ -109,6 +109,10 @@ typedef short s16v4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMaxFloat = 3.402823466e38f;
+// Largest bias (base 2) that fp32 scores carry as it is: there a product beside it
+// is still held to 2^-12.
+constexpr float kBiasKept = 4096.0f;
 
 // fp32 -> the raw bits of T, to nearest even
 template <typename T>
@@ -482,10 +486,13 @@ __device__ __forceinline__ int bucket_of(const uint16_t *starts, int side, int d
 // 2), from kLutPad positions before the first distance of the last bucket to
 // as many past the last change.  A tile that touches a change of bucket reads
 // it without limits on the index; any other tile has one bias, that of its end
-// of the table.
+// of the table.  A finite bias stays finite (the lowest value of fp32 and bf16,
+// a usual mask, would pass the range in base 2).  Returns whether the thread's
+// entries hold one that row_shift is for.
 template <typename T>
-__device__ __forceinline__ void fill_lut(const AttnParams &p, int h, float *lut, const uint16_t *starts, int t,
+__device__ __forceinline__ bool fill_lut(const AttnParams &p, int h, float *lut, const uint16_t *starts, int t,
                                          int nt) {
+    bool large = false;
     for (int i = t; i < p.lut; i += nt) {
         const int rel = i - p.border - kLutPad;
         int b = bucket_of(starts, p.side, rel < 0 ? -rel : (p.bidirectional ? rel : 0));
@@ -494,8 +501,33 @@ __device__ __forceinline__ void fill_lut(const AttnParams &p, int h, float *lut,
         float v;
         if (p.table_f32) v = ((const float *)p.table)[at];
         else v = T::from_raw(((const typename T::raw_t *)p.table)[at]);
-        lut[i] = v * kLog2e;
+        const float w = v * kLog2e, held = __builtin_amdgcn_fmed3f(w, -kMaxFloat, kMaxFloat);
+        const bool finite = fabsf(v) <= kMaxFloat;
+        lut[i] = finite ? held : w;
+        large |= finite & (fabsf(w) > kBiasKept);
     }
+    return large;
+}
+
+// What the biases of a query's scores are taken relative to: the largest one
+// among the keys that it sees (0 .. seen - 1), where that passes kBiasKept, else
+// 0.  A query whose every key has a mask's bias of, say, -1e9 would otherwise
+// lose the products beside it, and the sum of the exponentials in its lse: the
+// softmax does not change when a constant leaves every score.  Few queries are
+// such, so it costs the others nothing but a test where a tile reads the table.
+__device__ __forceinline__ float row_shift(const AttnParams &p, const float *lut, int pos, int seen) {
+    if (seen <= 0) return 0.0f;
+    const int zero = p.border + kLutPad - pos;       // entry of key 0
+    const int lo = min(max(zero, 0), p.lut - 1), hi = min(max(zero + seen - 1, 0), p.lut - 1);
+    float top = -INFINITY;
+    for (int i = lo; i <= hi; ++i) top = fmaxf(top, lut[i]);
+    return fabsf(top) > kBiasKept && fabsf(top) <= kMaxFloat ? top : 0.0f;
+}
+
+// A shift in the base of the scores as they are given (a mask's lowest value,
+// held to the range in base 2, as that).
+__device__ __forceinline__ float natural(float shift) {
+    return fabsf(shift) < kMaxFloat ? shift * kLn2 : shift;
 }
 
 // N entries of an LDS table, all on their way before the first is used.

@@ -172,8 +172,9 @@ int attention_setup(const gs_attention_desc *d, bool backward, gs::AttnParams &p
 // byte offset.
 bool stride_async(int64_t s) { return s <= (int64_t(1) << 22); }
 
-// Workspace of a backward call: delta, the key tiles' sums for the table, the
-// parts' sums of dK and dV; each 256-byte aligned.
+// Workspace of a backward call: four numbers a query, in whole tiles of 64, and with
+// a table its shift; the key tiles' sums for the table; the parts' sums of dK and
+// dV.  Each 256-byte aligned.
 struct BackwardSpace {
     int64_t part, split, bytes;
 };
@@ -181,7 +182,7 @@ struct BackwardSpace {
 BackwardSpace backward_space(const gs::AttnParams &p, int dtype) {
     const gs::AttnPlan kv = gs::plan_backward_kv(p, dtype);
     BackwardSpace s;
-    s.part = round_ws((int64_t)p.B * p.H * p.Lq * 4);
+    s.part = round_ws((int64_t)p.B * p.H * ((p.Lq + 63) / 64) * 64 * (p.buckets ? 20 : 16));
     s.split = s.part + round_ws((int64_t)p.B * p.H * kv.tiles * kv.splits * p.buckets * 4);
     s.bytes = s.split + round_ws(kv.split_floats * 4);
     return s;
@@ -370,7 +371,7 @@ int gs_attention_backward(const gs_attention_desc *desc, const void *dO, const v
     p.dk = dK;
     p.dv = dV;
     p.dtable = p.buckets ? dtable : nullptr;
-    p.delta = (float *)workspace;
+    p.rows = (float *)workspace;
     p.part = p.dtable && workspace ? (float *)((char *)workspace + space.part) : nullptr;
     p.split = (float *)((char *)workspace + space.split);
     p.vec = p.vec && aligned16(Q) && aligned16(K) && aligned16(V) && aligned16(O) && aligned16(dO) && aligned16(dQ) &&

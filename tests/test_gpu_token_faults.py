@@ -342,3 +342,85 @@ def test_dropout_past_2_31_elements(gs):
     at = np.arange(first // 8, (n + 7) // 8, dtype=np.uint64)
     want = ref.factors(ref.numbers((at, 0, 0, 2), 11).reshape(-1)[:n - first], 0.3)
     close(y, want, unit(torch.bfloat16) * want + 4 * E32 * want, "y")
+
+
+# ------------------------------------------- tables that mask by large values
+
+MASKS = {"-1e4": -1e4, "f16 lowest": -65504.0, "-1e6": -1e6, "-1e9": -1e9, "lowest": None, "1e9": 1e9}
+MASKED = {  # which buckets of 8 (both sides) hold the mask, and a shape with lengths: queries that see no other key
+    "far before": ([2, 3], (2, 4, 2, 150, 150, 32), [20, 150]), "everywhere": (list(range(8)), (1, 2, 2, 40, 300, 64), None),
+    "after": ([4, 5, 6, 7], (2, 2, 1, 70, 33, 48), [33, 5]), "many": ([2, 3], (9, 30, 15, 130, 97, 64), None),
+    "few queries": ([2, 3, 7], (1, 8, 2, 3, 1500, 64), None)}
+
+
+@pytest.mark.parametrize("mask", list(MASKS))
+@pytest.mark.parametrize("where", list(MASKED))
+@pytest.mark.parametrize("dtype,table_type", [("f32", "f32"), ("f16", "f16"), ("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("ratio", [0.0, 0.2])
+def test_attention_of_tables_that_mask(gs, mask, where, dtype, table_type, ratio):
+    """A constant leaves the softmax as it is, so a query that sees masked keys alone has the one of the products, and
+    the others have none of a masked key.  The oracle's mask is -300 (for 1e9: 300), whose e^-300 stands for 0."""
+    buckets, (B, H, Hkv, Lq, Lk, D), lengths = MASKED[where]
+    t, tt = TYPES[dtype], TYPES[table_type]
+    value = torch.finfo(tt).min if MASKS[mask] is None else MASKS[mask]
+    if tt == torch.float16 and not -65504 <= value <= 65504:
+        pytest.skip("no such fp16 value")
+    g = torch.Generator().manual_seed(41)
+    q, do = heads(g, B, H, Lq, D, t, True), heads(g, B, H, Lq, D, t, True)
+    k, v = heads(g, B, Hkv, Lk, D, t, True), heads(g, B, Hkv, Lk, D, t, True)
+    q *= 3                                           # products of up to about 40 in base 2
+    table = torch.randn(8, H, generator=g).to(tt)
+    like = table.clone()
+    table[buckets], like[buckets] = value, math.copysign(300.0, value)
+    lens = None if lengths is None else torch.tensor(lengths, dtype=torch.int32)
+    how = dict(table=table.cuda(), max_distance=20, kv_lengths=None if lens is None else lens.cuda(), ratio=ratio, seed=3)
+    first = -Lq if where == "after" else 0           # there all keys are after the queries
+    want = ref.attention(q.cpu(), k.cpu(), v.cpu(), 1 / math.sqrt(D), 0, lens, like, 20, 1, first, ratio, 3, 0,
+                         do.cpu(), unit(t) if t != torch.float32 else E32, tiny(t))
+    want = {n: (torch.where(x.abs() < 1e-100, 0.0, x), e) for n, (x, e) in want.items()}
+    o, lse = gs.attention(q, k, v, return_lse=True, q_position=first, **how)
+    close(o, *want["o"], "o")
+    natural = want["lse"][0]
+    alone = natural < -150 if value < 0 else natural > 150
+    assert alone.any() or where == "few queries"
+    kept = ~alone & (natural > -math.inf)
+    close(lse.cpu()[kept], natural[kept], want["lse"][1][kept], "lse")
+    assert ((lse.cpu()[alone] - value).abs() <= 1e-2 * abs(value)).all()
+    assert torch.equal(lse.cpu() == -math.inf, natural == -math.inf)
+    got = gs.attention_backward(do, q, k, v, o, lse, q_position=first, **how)
+    for name, x in zip(("dq", "dk", "dv", "dtable"), got):
+        close(x, *want[name], name)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_attention_of_an_infinite_mask_hides_its_keys(gs, dtype):
+    """-inf in the table: a query left without keys gives 0 and lse -inf, and no gradient."""
+    t = TYPES[dtype]
+    g = torch.Generator().manual_seed(42)
+    q, k, v, do = (heads(g, 2, 2, 150, 32, t, False) for _ in range(4))
+    table = torch.randn(8, 2, generator=g).to(t)
+    table[2:4] = -math.inf                           # of keys 10 and more before the query, and no others
+    lens = torch.tensor([20, 150], dtype=torch.int32)
+    how = dict(table=table.cuda(), max_distance=20, kv_lengths=lens.cuda())
+    like = table.clone()
+    like[2:4] = -300.0
+    none = ref.bucket(torch.arange(150).numpy()[None] - torch.arange(150).numpy()[:, None], 8, 20, 1)
+    none = torch.from_numpy(((none == 2) | (none == 3))[:, :20].all(1))
+    assert none.any()
+    do[0, :, none.cuda()] = 0
+    want = ref.attention(q.cpu(), k.cpu(), v.cpu(), 1 / math.sqrt(32), 0, lens, like, 20, 1, 0, 0.0, 0, 0, do.cpu(),
+                         unit(t) if t != torch.float32 else E32, tiny(t))
+    want = {n: (torch.where(x.abs() < 1e-100, 0.0, x), e) for n, (x, e) in want.items()}
+    o, lse = gs.attention(q, k, v, return_lse=True, **how)
+    assert not o[0, :, none.cuda()].any() and (lse[0, :, none.cuda()] == -math.inf).all()
+    got = gs.attention_backward(do, q, k, v, o, lse, **how)
+    assert not got[0][0, :, none.cuda()].any()
+    for x in (o, got[0]):
+        x[0, :, none.cuda()] = 0
+    for name, x in zip(("o", "dq", "dk", "dv", "dtable"), (o, *got)):
+        value, bound = want[name]
+        if name == "o":
+            value[0, :, none] = 0
+        if name == "dq":
+            value[0, :, none] = 0
+        close(x, value, bound, name)

@@ -279,7 +279,8 @@ SPLIT_128 = [(4, 64, 16, 520, 33, 64), (4, 32, 8, 520, 201, 128), (2, 64, 32, 11
 @pytest.mark.parametrize("shape", SPLIT_128)
 @pytest.mark.parametrize("dtype", [0, 1, 2])
 def test_split_of_128_key_blocks_is_planned(tk, shape, dtype):  # noqa: F811
-    """The workspace holds delta, the table's sums of (blocks of 128 keys) x parts, and the parts of dK and dV."""
+    """The workspace holds four numbers a query (five with a table), the table's sums of (blocks of 128 keys) x parts,
+    and the parts of dK and dV."""
     B, H, Hkv, Lq, Lk, D = shape
     lib, need = tk.token_lib(), ctypes.c_int64(0)
     def size(buckets):
@@ -289,7 +290,8 @@ def test_split_of_128_key_blocks_is_planned(tk, shape, dtype):  # noqa: F811
         assert lib.gs_attention_backward_workspace_size(d, ctypes.byref(need)) == 0
         return need.value
     rounded = lambda n: (n + 255) // 256 * 256
-    sums = size(0) - rounded(B * H * Lq * 4)
+    queries = B * H * ((Lq + 63) // 64) * 64
+    sums = size(0) - queries * 16
     parts, rest = divmod(sums, rounded(B * Hkv * Lk * 2 * D * 4))
     assert rest == 0 and parts >= 2
-    assert size(8) - size(0) == rounded(B * H * ((Lk + 127) // 128) * parts * 8 * 4)
+    assert size(8) - size(0) == rounded(B * H * ((Lk + 127) // 128) * parts * 8 * 4) + queries * 4
