@@ -186,6 +186,8 @@ typedef struct {
  * The probabilities are rounded to dtype before they multiply V (with
  * GS_F32 not at all).  A NaN or infinity in V reaches every query of the
  * call whose mask leaves its key, and may reach the other queries of its head.
+ * (In gs_attention_backward so may one in Q, K, V or dO.  Keys past a length and,
+ * with causal, queries before position 0 reach nothing, whatever they hold.)
  * Errors: GS_ERR_NULL, GS_ERR_SHAPE (an extent negative, q_heads no multiple
  * of kv_heads, head_dim 0, a negative stride, one below head_dim along an axis
  * of more than one element of an output: rows must not overlap), GS_ERR_DTYPE, GS_ERR_ATTR

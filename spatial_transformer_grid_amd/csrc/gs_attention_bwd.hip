@@ -458,9 +458,10 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
     if (p.lut)
         for (int i = t; i < p.side; i += 256) starts[i] = p.starts[i];
 
-    // queries before q_begin see no key of this block; the block's part is a
-    // range of the (head, query tile) pairs that are left
-    const int q_begin = p.causal ? max(0, block0 - first) / ROWS * ROWS : 0;
+    // queries before q_first see no key of this block, and stay out of its products
+    // (they may hold NaN: queries before a sequence's first token); the block's part
+    // is a range of the (head, query tile) pairs that are left
+    const int q_first = p.causal ? max(0, block0 - first) : 0, q_begin = q_first / ROWS * ROWS;
     const int q_tiles = block0 < len && q_begin < p.Lq ? (p.Lq - q_begin + ROWS - 1) / ROWS : 0;
     const int64_t pairs = (int64_t)p.G * q_tiles;
     const int64_t p0 = pairs * part / p.splits, p1 = pairs * (part + 1) / p.splits;
@@ -499,8 +500,8 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
         const auto load = [&](int copy, int q0) {
             raw_t *to = Qt + copy * 2 * Geo::tile_elems;
             if (tt < 64) copy_rows(stats + copy * kRowStats, row_stats(p, bh, q0 >> 6), tt);
-            copy_tile<T, DP, ROWS, NT>(to, qb, p.qs[2], q0, p.Lq, p.D, p.async, vec, tt);
-            copy_tile<T, DP, ROWS, NT>(to + Geo::tile_elems, gb, p.dos[2], q0, p.Lq, p.D, p.async, vec, tt);
+            copy_tile<T, DP, ROWS, NT, true>(to, qb, p.qs[2], q0, p.Lq, p.D, p.async, vec, tt, q_first);
+            copy_tile<T, DP, ROWS, NT, true>(to + Geo::tile_elems, gb, p.dos[2], q0, p.Lq, p.D, p.async, vec, tt, q_first);
         };
         constexpr int STEP = FEW ? 4 : 1;
         const int begin = FEW ? t0 + wave : t0;

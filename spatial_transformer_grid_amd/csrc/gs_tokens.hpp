@@ -297,15 +297,15 @@ struct Tile {
 __device__ __forceinline__ void async_wait() { __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Rows row0 .. row0 + ROWS - 1 of a strided tensor into an LDS tile, in 16-byte
-// chunks over the NT threads that share it, zeros outside rows < limit and
-// columns < D.  `async`: by loads that write LDS by themselves (async_wait,
+// chunks over the NT threads that share it, zeros outside rows < limit (FROM:
+// and from <= row) and columns < D.  `async`: by loads that write LDS by themselves (async_wait,
 // then tile_sync, before the tile is read), which leaves the registers to the
 // products.  A lane's chunk lands at its own place of the tile, so it is the
 // source column that changes place; reads outside the range of the descriptor
 // give zeros, and ROWS rows span less than 2 GiB.  Otherwise through registers.
-template <typename T, int DP, int ROWS, int NT>
+template <typename T, int DP, int ROWS, int NT, bool FROM = false>
 __device__ __forceinline__ void copy_tile(typename T::raw_t *lds, const typename T::raw_t *base, int64_t stride,
-                                          int row0, int limit, int D, bool async, bool vec, int t) {
+                                          int row0, int limit, int D, bool async, bool vec, int t, int from = 0) {
     typedef typename T::raw_t raw_t;
     typedef Tile<T, DP> L;
     constexpr int EPC = L::EPC, CPR = L::CPR, N = (ROWS * CPR + NT - 1) / NT;
@@ -313,11 +313,12 @@ __device__ __forceinline__ void copy_tile(typename T::raw_t *lds, const typename
     if (async) {
         const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
             (void *)(base + (int64_t)row0 * stride), 0, 0x7fffffff, 0x00027000);
+        const uint32_t rows = max(limit - from, 0);  // in one comparison, by wrapping
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int c = t + n * NT, r = c / CPR, col = ((c - r * CPR) ^ L::turn(r)) * EPC;
-            const uint32_t at =
-                row0 + r < limit && col < D ? (uint32_t)(r * (int)stride + col) * T::bytes : 0x80000000u;
+            const bool in = FROM ? (uint32_t)(r + (row0 - from)) < rows : row0 + r < limit;
+            const uint32_t at = in && col < D ? (uint32_t)(r * (int)stride + col) * T::bytes : 0x80000000u;
             if (ROWS * CPR % NT == 0 || c < ROWS * CPR)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
                     rsrc, (__attribute__((address_space(3))) void *)(lds + ((t & ~63) + n * NT) * EPC), 16, (int)at, 0,
@@ -329,7 +330,7 @@ __device__ __forceinline__ void copy_tile(typename T::raw_t *lds, const typename
     for (int c = t; c < ROWS * CPR; c += NT) {
         const int r = c / CPR, col = (c - r * CPR) * EPC;
         u32x4 v = {0, 0, 0, 0};
-        if (row0 + r < limit && col < D) {
+        if ((!FROM || row0 + r >= from) && row0 + r < limit && col < D) {
             const raw_t *src = base + (int64_t)(row0 + r) * stride + col;
             if (vec) {
                 v = *(const u32x4 *)src;

@@ -424,3 +424,31 @@ def test_attention_of_an_infinite_mask_hides_its_keys(gs, dtype):
         if name == "dq":
             value[0, :, none] = 0
         close(x, value, bound, name)
+
+
+# ------------------------------------------------- queries that see no key
+
+@pytest.mark.parametrize("shape", [(2, 4, 2, 64, 150, 64), (16, 16, 16, 200, 70, 64), (1, 2, 1, 300, 40, 48),
+                                   (64, 8, 8, 170, 130, 128), (4, 64, 16, 520, 33, 63)])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_queries_before_the_first_token_may_hold_nan(gs, shape, dtype):
+    """More queries than a sequence has tokens (padding before them): what Q and dO hold there reaches no gradient."""
+    B, H, Hkv, Lq, Lk, D = shape
+    t = TYPES[dtype]
+    g = torch.Generator().manual_seed(51)
+    q, do = heads(g, B, H, Lq, D, t, True), heads(g, B, H, Lq, D, t, True)
+    k, v = heads(g, B, Hkv, Lk, D, t, True), heads(g, B, Hkv, Lk, D, t, True)
+    lens = torch.tensor([max(0, min(Lk, Lq) - 1 - 9 * b) for b in range(B)], dtype=torch.int32)
+    how = dict(causal=1, q_position="end", kv_lengths=lens.cuda(), table=torch.randn(8, H, generator=g).to(t).cuda(),
+               max_distance=20, bidirectional=0, ratio=0.1, seed=2)
+    def run(fill):
+        a, d = q.clone(), do.clone()
+        for b, n in enumerate(lens.tolist()):
+            a[b, :, :Lq - n], d[b, :, :Lq - n] = fill, fill
+        o, lse = gs.attention(a, k, v, return_lse=True, **how)
+        return (o, lse) + gs.attention_backward(d, a, k, v, o, lse, **how)
+    base = run(0.0)
+    assert all(x.isfinite().all() for x in base[2:]) and not base[0][0, :, :Lq - lens[0]].any()
+    assert not base[2][0, :, :Lq - lens[0]].any()
+    for fill in (math.nan, math.inf):
+        assert all(torch.equal(a, b) for a, b in zip(base, run(fill))), fill
