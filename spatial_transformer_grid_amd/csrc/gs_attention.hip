@@ -143,7 +143,7 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
         shifted = __builtin_amdgcn_readfirstlane(large);
         bias_lo = lut[0];
         bias_hi = lut[p.lut - 1];
-        if (shifted) {
+        if (__builtin_expect(shifted, 0)) {
             const float shift = row_shift(p, lut, pos, p.causal ? min(len, pos + 1) : len);
             bias_lo -= shift;
             bias_hi -= shift;
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
                     float bias[16 * U];
                     read_all<16 * U>(lut + (key0 - pos + p.border + kLutPad), bias,
                                      [](int i) { return 16 * (i >> 3) + (i & 7); });
-                    if (shifted) {
+                    if (__builtin_expect(shifted, 0)) {
                         rare<16 * U>(bias);
                         const float shift = *(volatile float *)(shifts + col);
 #pragma unroll

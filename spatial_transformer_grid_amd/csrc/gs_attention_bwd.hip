@@ -206,7 +206,7 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
         bias_hi = lut[p.lut - 1];
         shifted = __builtin_amdgcn_readfirstlane(large);
     }
-    if (shifted) {
+    if (__builtin_expect(shifted, 0)) {
         const float shift = row_shift(p, lut, pos, p.causal ? min(len, pos + 1) : len);
         bias_lo -= shift;
         bias_hi -= shift;
@@ -323,7 +323,7 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
                     float bias[16];
                     read_all<16>(lut + (key0 - pos + p.border + kLutPad), bias,
                                  [](int i) { return 16 * (i >> 3) + (i & 7); });
-                    if (shifted) {
+                    if (__builtin_expect(shifted, 0)) {
                         rare<16>(bias);
                         const float shift = *(volatile float *)(shifts + col);
 #pragma unroll
@@ -554,7 +554,7 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
                         float bias[8];
                         read_all<8>(lut + (key - first - q0 - r0 + p.border + kLutPad), bias,
                                     [](int j) { return -j; });
-                        if (shifted) {
+                        if (__builtin_expect(shifted, 0)) {
                             rare<8>(bias);
                             const float *shift = row_shifts(p, bh) + q0 + r0;
 #pragma unroll
