@@ -72,7 +72,7 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
     __shared__ int large;                            // the table holds a bias that row_shift is for
 
     int unit, tile, part;
-    if (!block_place(p, !FEW, FEW && p.pack ? 1 : p.G, unit, tile, part)) return;
+    if (!block_place(p, true, FEW && p.pack ? 1 : p.G, unit, tile, part)) return;
     const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int rg = wave % (4 / WS), wp = wave / (4 / WS);   // the wave's 32 rows, its part of the keys

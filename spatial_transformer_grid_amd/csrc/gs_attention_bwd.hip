@@ -140,7 +140,7 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
     __shared__ int large;                            // the table holds a bias that row_shift is for
 
     int unit, tile, part;
-    if (!block_place(p, !FEW, p.G, unit, tile, part)) return;
+    if (!block_place(p, true, p.G, unit, tile, part)) return;
     const int b = unit / p.H, h = unit - b * p.H, hk = h / p.G;
     const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
