@@ -3,6 +3,8 @@
 Argument marshalling only, as in _binding: layer normalisation, dropout and
 attention with a relative position bias, forward and backward.  Tensors may be
 strided where the library takes strides; the last axis is made contiguous.
+The functions take part in no autograd graph: results are detached, and a
+training step calls the _backward functions itself.
 """
 
 from __future__ import annotations

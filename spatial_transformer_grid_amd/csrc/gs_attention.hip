@@ -20,10 +20,10 @@
 // Bound by vector arithmetic beside the products (an exponential, two products
 // and two sums a score, and with dropout a twelfth of a generator call), at 128
 // columns by the products themselves.  Measured: 16 x 4096 x 4096 x 128 fp16
-// with a bias 170 us (810 TFLOP/s, where an 8192^3 product reaches 1093);
-// 2 x 16 x 2048 x 64 causal bf16 with bias and dropout 59 us, 40 us without
-// either; 16 caches of up to 8192 keys x 8 heads x 128 bf16, one query each:
-// 71 us (4.9 TB/s, memory) and 5 us for the join.
+// with a bias 172 us (800 TFLOP/s, where an 8192^3 product reaches 1093);
+// 2 x 16 x 2048 x 64 causal bf16 with bias and dropout 57 to 61 us, 45 us without
+// dropout, 40 us without either; 16 caches of up to 8192 keys x 8 heads x 128
+// bf16, one query each: 72 us (4.8 TB/s, memory) and 5 us for the join.
 #include "gs_tokens.hpp"
 
 namespace gs {
@@ -258,6 +258,9 @@ __global__ __launch_bounds__(256, T::bytes == 4 && DP > 64 ? 1 : 2) void attenti
                 sum[i & 1] += s[i];
             }
             l += sum[0] + sum[1];
+            // P in V's type: the matrix cores multiply two operands of one type.  Its sum
+            // is of the unrounded P, whose roundings average out over the keys; lse keeps
+            // fp32.  O's error is 1.4 times that of rounding O alone.
             Frag<T> pf[2 * U];
 #pragma unroll
             for (int x = 0; x < 2 * U; ++x) {
@@ -432,8 +435,8 @@ int launch_t(const AttnParams &p, int ways, hipStream_t stream) {
 }  // namespace
 
 // The 32-row form where 128-row blocks would leave compute units without one,
-// or would be mostly empty.  Decode of 16 ragged caches: 77 us, with 128-row
-// blocks 216 us; 512 blocks of 2048 x 64 causal: 76 us, with 128-row blocks 59 us.
+// or would be mostly empty.  Decode of 16 ragged caches: 76 us, with 128-row
+// blocks 189 us; 512 blocks of 2048 x 64 causal: 77 us, with 128-row blocks 60 us.
 AttnPlan plan_forward(const AttnParams &p, int, bool workspace) {
     AttnPlan a = {};
     a.splits = 1;

@@ -18,17 +18,17 @@
 // exact dS of a query add up to 0, so the sum of those computed with dO . O
 // tells delta exactly: the dQ kernel corrects it for the dK / dV kernel, which
 // therefore makes the table's sums, and where a block sees at most kExactKeys
-// keys, where the rounding of O counts most, it goes over the keys once more
-// with the corrected delta for its own dQ.
+// keys it goes over them once more with the corrected delta for its own dQ.
 //
 // keep_scale is left out of dS until the last scaling: M is then 0 or 1 and
 // delta is divided by keep_scale.
 //
 // Measured: 16 heads of 4096 x 4096 x 128 fp16 on four key heads, with a bias:
-// dQ 230 us (900 TFLOP/s over its three products), dK and dV 440 us (625 over
-// four; K, V and both sums fill the registers of a SIMD's one wave, whose
+// dQ 230 us (900 TFLOP/s over its three products), dK and dV 445 to 460 us (600
+// over four; K, V and both sums fill the registers of a SIMD's one wave, whose
 // products and exponentials follow one another); 2 x 16 x 2048 x 64 causal
-// bf16 with bias and dropout: 76 and 110 us, of which the generator takes 20 each.
+// bf16 with bias and dropout: 74 to 80 and 108 to 116 us, of which the generator
+// takes 13 and 20, the bias 7 and 18.
 #include "gs_tokens.hpp"
 
 namespace gs {
@@ -367,6 +367,7 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) sum += (ds[i] + ds[i + 1]) + (ds[i + 2] + ds[i + 3]);
                 if (!last) continue;
+                // dS in K's type, as P in the forward pass (with V's)
                 const Frag<T> df[2] = {frag_pack<T>(ds), frag_pack<T>(ds + 8)};
                 pipelined<T, 2 * (DP / 32), T::bytes == 4 ? 1 : DP / 32>(
                     [&](int i) {
@@ -550,7 +551,7 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
                 }
                 const int cls = bias_class(p, k0 - (first + qu + 31), k0 + 31 - (first + qu));
                 const bool edge = k0 + 32 > len || (p.causal && first + qu < k0 + 31);
-                Frag<T> pf[2], df[2];
+                Frag<T> pf[2], df[2];                // P and dS in the type of dO and Q
                 float all[16];                       // dS
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -873,7 +874,7 @@ int few_kv_lds(const AttnParams &p, int dtype) {
 }  // namespace
 
 // 32-row blocks where 128-row blocks would leave compute units without one: 512
-// blocks of 2048 x 64 causal take 76 us, as 32-row blocks 218 us.
+// blocks of 2048 x 64 causal take 78 us, as 32-row blocks 90 us.
 AttnPlan plan_backward_q(const AttnParams &p, int) {
     AttnPlan a = {};
     a.splits = 1;
