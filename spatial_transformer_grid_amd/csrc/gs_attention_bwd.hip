@@ -20,8 +20,10 @@
 // therefore makes the table's sums, and where a block sees at most kExactKeys
 // keys it goes over them once more with the corrected delta for its own dQ.
 //
-// keep_scale is left out of dS until the last scaling: M is then 0 or 1 and
-// delta is divided by keep_scale.
+// M's factor is 0 or 1 beside dO . V, delta is divided by keep_scale, and P carries
+// keep_scale in its exponent: dS and P M are then rounded to the element type as
+// they are (an fp16 dS without the factor of 10 of a ratio of 0.9 loses three bits
+// below the smallest normal value).
 //
 // Measured: 16 heads of 4096 x 4096 x 128 fp16 on four key heads, with a bias:
 // dQ 230 us (900 TFLOP/s over its three products), dK and dV 445 to 460 us (600
@@ -55,8 +57,8 @@ constexpr int kExactKeys = 256;
 constexpr int kDiagonalRow = 68;
 constexpr int kDiagonal = 32 + 32 * kDiagonalRow;    // floats of a wave
 
-// What the dK / dV kernel takes of 64 queries from the dQ kernel: -lse (base 2,
-// relative to the row's shift) without and with the biases of the two ends of the
+// What the dK / dV kernel takes of 64 queries from the dQ kernel: log2(fold) - lse
+// (base 2, relative to the row's shift) without and with the biases of the two ends of the
 // table, and delta / keep_scale; 64 of each, so that one asynchronous load of a wave
 // brings them.  Queries past the last have -inf: their probabilities are 0.  The
 // shifts themselves, read where a table has any, follow the stats of all rows.
@@ -198,7 +200,7 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
     if (live) {
         const int64_t at = (int64_t)unit * p.Lq + qi;
         const float v = p.lse[at];
-        if (v != -INFINITY) minus_lse = -v * kLog2e;
+        if (v != -INFINITY) minus_lse = p.fold_log2 - v * kLog2e;
     }
     delta = delta / p.keep_scale;
     float bias_lo = 0.0f, bias_hi = 0.0f;
@@ -279,7 +281,7 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
 #pragma unroll
                 for (int w = 0; w < WS; ++w) sum += row_sums[w][col];
             }
-            if (shift != 0.0f) minus_lse = -(all + __builtin_amdgcn_logf(sum));
+            if (shift != 0.0f) minus_lse = p.fold_log2 - (all + __builtin_amdgcn_logf(sum));
             __syncthreads();
             if (begin < end) load(Kt, begin);
         }
@@ -388,14 +390,14 @@ __global__ __launch_bounds__(256, (WS == 4 || T::bytes == 4) && DP > 64 ? 1 : 2)
 #pragma unroll
             for (int w = 0; w < WS; ++w) sum += row_sums[w][col];
         }
-        delta += sum;
+        delta += sum / p.fold;
     }
     if (live && half == 0 && wp == 0)
         put_row(p, unit, qi, minus_lse, minus_lse + bias_lo, minus_lse + bias_hi, delta, shifted ? shifts[col] : 0.0f);
     if (tile == p.tiles - 1)
         for (int q = p.Lq + t; q < (p.Lq + 63) / 64 * 64; q += 256)
             put_row(p, unit, q, -INFINITY, -INFINITY, -INFINITY, 0.0f, 0.0f);
-    const float scale = p.scale * p.keep_scale;
+    const float scale = p.scale * p.rest;
     if constexpr (WS == 1) {
         if (live) {
             raw_t *drow = (raw_t *)p.dq + (int64_t)b * p.dqs[0] + (int64_t)h * p.dqs[1] + (int64_t)qi * p.dqs[2];
@@ -683,11 +685,11 @@ __global__ __launch_bounds__(256, DP > (T::bytes == 4 ? 32 : 64) ? 1 : 2) void a
                     for (int w = 0; w < 4; ++w) sum += far[2 * w + (after ? 1 : 0)];
                 if (!p.bidirectional && m == 0)
                     for (int w = 0; w < 4; ++w) sum += far[2 * w + 1];
-                sums_out[n] = sum * p.keep_scale;
+                sums_out[n] = sum * p.rest;
             }
         }
     }
-    const float sk = p.scale * p.keep_scale, sv = p.keep_scale;
+    const float sk = p.scale * p.rest, sv = p.rest;
     if constexpr (WS > 1) {
         float *sums = (float *)smem;
 #pragma unroll
@@ -779,7 +781,7 @@ __global__ __launch_bounds__(256) void attention_backward_finish(AttnParams p) {
     tokens_f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int s = 0; s < p.splits; ++s) v += *(const tokens_f32x4 *)(p.split + (s * rows + row) * 2 * dr + at);
     const bool second = at >= dr;
-    const float scale = second ? p.keep_scale : p.scale * p.keep_scale;
+    const float scale = second ? p.rest : p.scale * p.rest;
     const int64_t unit = row / p.Lk, key = row - unit * p.Lk, b = unit / p.Hkv, hk = unit - b * p.Hkv;
     const int64_t *st = second ? p.dvs : p.dks;
     raw_t *to = (raw_t *)(second ? p.dv : p.dk) + b * st[0] + hk * st[1] + key * st[2];

@@ -10,6 +10,7 @@ namespace gs {
 
 constexpr int kMaxBuckets = 512;     // buckets of a bias table
 constexpr int kMaxBorder = 1024;     // largest first distance of a last bucket
+constexpr float kMaxFold = 32768.0f; // largest factor of a probability (fp16 ends at 65504)
 
 struct NormParams {
     const void *X, *dY, *scale, *bias;
@@ -51,6 +52,8 @@ struct AttnParams {
     int lut;                  // entries of the distance table (0: no bias)
     uint32_t threshold, seed_lo, seed_hi, call;
     float keep_scale;
+    float fold, fold_log2;    // backward: the factor of keep_scale that P carries
+    float rest;               // keep_scale / fold
     int vec;                  // rows of every tensor allow 16-byte accesses
     int async;                // and their tiles asynchronous loads
     int tiles;                // row tiles of a unit (a head of a sequence)

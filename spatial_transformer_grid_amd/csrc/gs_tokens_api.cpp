@@ -157,6 +157,9 @@ int attention_setup(const gs_attention_desc *d, bool backward, gs::AttnParams &p
     p.seed_lo = (uint32_t)d->seed;
     p.seed_hi = (uint32_t)(d->seed >> 32);
     p.call = d->call;
+    p.fold = p.keep_scale < gs::kMaxFold ? p.keep_scale : gs::kMaxFold;
+    p.fold_log2 = (float)log2((double)p.fold);
+    p.rest = p.keep_scale / p.fold;
     p.units = (int)pairs;
     p.tiles = (int)tiles;
     const int epc = 16 / dtype_bytes(d->dtype);
