@@ -174,6 +174,40 @@ def test_older_calls_on_a_stream_given_by_name(gs):
     torch.cuda.synchronize()
 
 
+def test_calls_on_a_named_stream_captured(gs):
+    """A branch of a captured graph: calls with stream=s between the fork that they make and the caller's join."""
+    g = torch.Generator().manual_seed(23)
+    t = torch.float16
+    q, k, v, do = (heads(g, 2, 4, 150, 64, t, True) for _ in range(4))
+    q1, table = heads(g, 2, 4, 1, 64, t, True), torch.randn(32, 4, generator=g).to(t).cuda()
+    x, w = torch.randn(130, 2 * 264, generator=g).to(t).cuda(), torch.ones(264, device="cuda", dtype=t)
+    s = torch.cuda.Stream()
+
+    def step(stream):
+        rows = x[:, ::2]
+        y, mean, inv = gs.layer_norm(rows, w, w, return_stats=True, stream=stream)
+        grads = gs.layer_norm_backward(y, rows, w, mean, inv, stream=stream)
+        how = dict(table=table, ratio=0.1, seed=4, stream=stream)
+        o, lse = gs.attention(q, k, v, return_lse=True, **how)
+        one = gs.attention(q1, k, v, stream=stream)
+        return [y, o, lse, one, *grads, *gs.attention_backward(do, q, k, v, o, lse, **how)]
+
+    eager = [a.clone() for a in step(None)]
+    step(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(s)
+        torch.cuda.current_stream().wait_stream(s)
+    for _ in range(3):
+        for a in held:
+            a.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(eager, held))
+        assert all(torch.equal(a, b) for a, b in zip(eager, step(None)))
+
+
 # --------------------------------------------------------------- refusals
 
 def test_scratch_in_host_memory_is_refused(gs):
