@@ -138,12 +138,19 @@ def dtype_code(t) -> int:
     return code
 
 
-def _device_tensor(t, name, like=None):
-    """`t`, contiguous, on a GPU (that of `like`)."""
-    if not t.is_cuda:
+def _on_gpu(t, name, device=None):
+    """The GPU that `t` lies on, which has to be `device` where that is given."""
+    at = t.get_device()
+    if at < 0:
         raise ValueError("%s must be a GPU tensor" % name)
-    if like is not None and t.get_device() != like.get_device():
+    if device is not None and at != device:
         raise ValueError("%s must be on the same GPU as the first input" % name)
+    return at
+
+
+def _device_tensor(t, name, device=None):
+    """`t`, contiguous, on a GPU (number `device`)."""
+    _on_gpu(t, name, device)
     return t.contiguous()
 
 
@@ -253,7 +260,7 @@ def grid_sample(X, grid, mode: str = "linear", padding_mode: str = "zeros",
         return _on_stream(stream, grid_sample, X, grid, mode, padding_mode, align_corners, out,
                           workspace=workspace)
     X = _device_tensor(X, "X")
-    grid = _device_tensor(grid, "grid", X)
+    grid = _device_tensor(grid, "grid", X.get_device())
     r = X.dim() - 2
     if grid.dim() != r + 2:
         raise ValueError("grid must have rank %d" % (r + 2))
@@ -294,7 +301,7 @@ def affine_grid_sample_fused(theta, X, out_spatial, mode: str = "linear",
         return _on_stream(stream, affine_grid_sample_fused, theta, X, out_spatial, mode,
                           padding_mode, align_corners, out)
     theta = _device_tensor(theta, "theta")
-    X = _device_tensor(X, "X", theta)
+    X = _device_tensor(X, "X", theta.get_device())
     r = X.dim() - 2
     out_spatial = [int(s) for s in out_spatial]
     if len(out_spatial) != r:
@@ -398,10 +405,10 @@ def deform_conv_output_shape(x_shape, w_shape, strides=None, pads=None, dilation
 def _deform_tensors(X, W, offset, B, mask, strides, pads, dilations, offset_group, out):
     """Checked device tensors of a DeformConv call and its output."""
     X = _device_tensor(X, "X")
-    W = _device_tensor(W, "W", X)
-    offset = _device_tensor(offset, "offset", X)
-    B = _device_tensor(B, "B", X) if B is not None else None
-    mask = _device_tensor(mask, "mask", X) if mask is not None else None
+    W = _device_tensor(W, "W", X.get_device())
+    offset = _device_tensor(offset, "offset", X.get_device())
+    B = _device_tensor(B, "B", X.get_device()) if B is not None else None
+    mask = _device_tensor(mask, "mask", X.get_device()) if mask is not None else None
     for name, t in (("W", W), ("offset", offset), ("B", B), ("mask", mask)):
         if t is not None and t.dtype != X.dtype:
             raise TypeError("%s must have X's element type" % name)

@@ -12,7 +12,8 @@ from __future__ import annotations
 import ctypes
 import math
 
-from ._binding import GS_F32, GS_OK, _check, _device_tensor, _I, _on_stream, _P, _ptr, _scratch, _stream, _torch, dtype_code
+from ._binding import (GS_F32, GS_OK, _check, _device_tensor, _I, _on_gpu, _on_stream, _P, _ptr, _scratch, _stream,
+                       _torch, dtype_code)
 from ._binding import lib as _library
 
 _I64 = ctypes.c_int64
@@ -67,12 +68,9 @@ def token_lib():
     return _typed
 
 
-def _tensor(t, name, like=None, dtype=None, shape=None):
-    """`t` on the GPU (that of `like`) with a contiguous last axis, its type and shape checked."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a GPU tensor" % name)
-    if like is not None and t.get_device() != like.get_device():
-        raise ValueError("%s must be on the same GPU as the first input" % name)
+def _tensor(t, name, device=None, dtype=None, shape=None):
+    """`t` on the GPU (number `device`) with a contiguous last axis, its type and shape checked."""
+    _on_gpu(t, name, device)
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must have element type %s" % (name, dtype))
     if shape is not None and tuple(t.shape) != tuple(shape):
@@ -138,15 +136,15 @@ def _workspace(workspace, need, device):
 
 
 def _norm_params(X, scale, bias):
-    cols = X.shape[-1]
-    scale = _device_tensor(scale, "scale", X)
+    cols, device = X.shape[-1], X.get_device()
+    scale = _device_tensor(scale, "scale", device)
     for name, t in (("scale", scale), ("bias", bias)):
         if t is not None and tuple(t.shape) != (cols,):
             raise ValueError("%s must have shape (%d,)" % (name, cols))
     if scale.dtype != X.dtype and scale.dtype != _torch().float32:
         raise TypeError("scale must have X's element type or float32")
     if bias is not None:
-        bias = _device_tensor(bias, "bias", X)
+        bias = _device_tensor(bias, "bias", device)
         if bias.dtype != scale.dtype:
             raise TypeError("bias must have scale's element type")
     return scale, bias
@@ -189,7 +187,7 @@ def layer_norm_backward(dY, X, scale, mean, inv_std, stream=None, workspace=None
         return _on_stream(stream, layer_norm_backward, dY, X, scale, mean, inv_std, workspace=workspace)
     torch = _torch()
     X = _tensor(X, "X")
-    dY = _tensor(dY, "dY", X, X.dtype, X.shape)
+    dY = _tensor(dY, "dY", X.get_device(), X.dtype, X.shape)
     scale, _ = _norm_params(X, scale, None)
     cols = X.shape[-1]
     rows = math.prod(X.shape[:-1])
@@ -221,7 +219,7 @@ def dropout(X, ratio: float, seed: int, call: int = 0, residual=None, out=None, 
         return _on_stream(stream, dropout, X, ratio, seed, call, residual, out)
     X = _device_tensor(X, "X")
     if residual is not None:
-        residual = _device_tensor(residual, "residual", X)
+        residual = _device_tensor(residual, "residual", X.get_device())
         if residual.dtype != X.dtype or residual.shape != X.shape:
             raise ValueError("residual must have X's shape and element type")
     Y = _output(out, X, True)
@@ -236,19 +234,22 @@ def dropout(X, ratio: float, seed: int, call: int = 0, residual=None, out=None, 
 def relative_bucket(r: int, num_buckets: int, max_distance: int = 128, bidirectional: int = 1) -> int:
     """Bucket of key position minus query position (gs_relative_bucket)."""
     got = _I(0)
-    _check(token_lib().gs_relative_bucket(_whole(r, "r", 64), _whole(num_buckets, "num_buckets"),
+    _check(token_lib().gs_relative_bucket(_whole(r, "r", *_INT64), _whole(num_buckets, "num_buckets"),
                                           _whole(max_distance, "max_distance"),
                                           _whole(bidirectional, "bidirectional"), ctypes.byref(got)),
            "gs_relative_bucket")
     return got.value
 
 
-def _whole(value, name, bits=32):
+_INT64 = (-(2 ** 63), 2 ** 63 - 1)
+
+
+def _whole(value, name, low=-(2 ** 31), high=2 ** 31 - 1):
     """`value` as a whole number that a field of the C interface holds (ctypes would cut it)."""
     value = int(value)
-    if not -(1 << (bits - 1)) <= value < 1 << (bits - 1):
-        raise ValueError("%s must fit %d bits" % (name, bits))
-    return value
+    if low <= value <= high:
+        return value
+    raise ValueError("%s must fit %d bits" % (name, high.bit_length() + 1))
 
 
 def _strides(t):
@@ -264,13 +265,14 @@ def _attention_inputs(Q, K, V, scale, causal, kv_lengths, table, max_distance, b
     if Q.dim() != 4 or K.dim() != 4:
         raise ValueError("Q and K must have shape (batch, heads, length, head_dim)")
     Q = _tensor(Q, "Q")
-    K = _tensor(K, "K", Q, Q.dtype)
+    device = Q.get_device()
+    K = _tensor(K, "K", device, Q.dtype)
     if K.shape[0] != Q.shape[0] or K.shape[3] != Q.shape[3]:
         raise ValueError("K must share Q's batch and head_dim")
-    V = _tensor(V, "V", Q, Q.dtype, K.shape)
+    V = _tensor(V, "V", device, Q.dtype, K.shape)
     B, H, Lq, D = Q.shape
     if kv_lengths is not None:
-        kv_lengths = _tensor(kv_lengths, "kv_lengths", Q, torch.int32, (B,)).contiguous()
+        kv_lengths = _tensor(kv_lengths, "kv_lengths", device, torch.int32, (B,)).contiguous()
     d = AttentionDesc()
     d.dtype = dtype_code(Q)
     d.batch, d.q_heads, d.q_len, d.head_dim = B, H, Lq, D
@@ -283,9 +285,9 @@ def _attention_inputs(Q, K, V, scale, causal, kv_lengths, table, max_distance, b
             raise ValueError('q_position must be a number or "end"')
         d.q_from_end = 1
     else:
-        d.q_position = _whole(q_position, "q_position", 64)
+        d.q_position = _whole(q_position, "q_position", *_INT64)
     if table is not None:
-        table = _device_tensor(table, "table", Q)
+        table = _device_tensor(table, "table", device)
         if table.dim() != 2 or table.shape[1] != H:
             raise ValueError("table must have shape (buckets, %d)" % H)
         if table.dtype != Q.dtype and table.dtype != torch.float32:
@@ -354,9 +356,10 @@ def attention_backward(dO, Q, K, V, O, lse, scale=None, causal: int = 0, kv_leng
     Q, K, V, kv_lengths, table, d = _attention_inputs(
         Q, K, V, scale, causal, kv_lengths, table, max_distance, bidirectional, q_position, ratio,
         seed, call)
-    O = _tensor(O, "O", Q, Q.dtype, Q.shape)
-    dO = _tensor(dO, "dO", Q, Q.dtype, Q.shape)
-    lse = _tensor(lse, "lse", Q, torch.float32, Q.shape[:3]).contiguous()
+    device = Q.get_device()
+    O = _tensor(O, "O", device, Q.dtype, Q.shape)
+    dO = _tensor(dO, "dO", device, Q.dtype, Q.shape)
+    lse = _tensor(lse, "lse", device, torch.float32, Q.shape[:3]).contiguous()
     dQ, dK, dV = _like(Q), _like(K), _like(V)
     dtable = torch.empty_like(table) if table is not None else None
     d.o_stride, d.do_stride = _strides(O), _strides(dO)
