@@ -1,7 +1,9 @@
 /*
  * gsample_tokens.h -- C ABI of libgsample's operators on sequences of tokens:
- * layer normalisation, dropout, and attention with a learned relative
- * position bias by buckets, forward and backward.
+ * layer normalisation, dropout, attention with a learned relative position
+ * bias by buckets, gated feed-forward projections, the norms before and after
+ * a block joined with its gate and residual, and a gated linear recurrence,
+ * forward and backward.
  *
  * They are what a model computes on the feature maps that gsample.h's
  * operators sample, once their positions are read as a sequence of tokens.
@@ -225,6 +227,243 @@ int gs_attention_backward(const gs_attention_desc *desc, const void *dO, const v
 /* Bytes of workspace that gs_attention_backward needs for this descriptor,
  * written to *bytes (host). */
 int gs_attention_backward_workspace_size(const gs_attention_desc *desc, int64_t *bytes);
+
+/* ------------------------------------------------------------------------
+ * Gated feed-forward projections
+ * --------------------------------------------------------------------- */
+
+/* What the gate's projection goes through: a / (1 + exp(-a)); a Phi(a), with
+ * Phi the normal distribution (by erf); its usual form by tanh,
+ * a (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))) / 2; max(a, 0), whose slope at
+ * 0 is 0. */
+typedef enum {
+    GS_ACT_SILU = 0,
+    GS_ACT_GELU = 1,
+    GS_ACT_GELU_TANH = 2,
+    GS_ACT_RELU = 3
+} gs_activation;
+
+/*
+ * a = X Wg^T, b = X Wu^T, Y = act(a) * b: both projections, the activation
+ * and the product.  The sums are fp32, Y is rounded once.
+ *
+ *   X, dtype     device, rows x width, element type dtype (GS_F32, GS_F16,
+ *                GS_BF16), row r at r * x_stride.
+ *   Wg, Wu       device, hidden x width, contiguous, dtype.
+ *   Y            device, rows x hidden, dtype, row r at r * y_stride.
+ *   saved        device fp32, 2 x rows x hidden, contiguous: a and b, which
+ *                the backward pass takes; or NULL.
+ *   workspace    device, 256-byte aligned, of gs_gated_linear_workspace_size()
+ *                bytes; without it (NULL, 0), or with less, a long width of
+ *                few rows is not split over thread blocks: slower, and the
+ *                sums in another order.
+ *
+ * Errors: GS_ERR_NULL, GS_ERR_SHAPE (an extent negative, width 0 with rows
+ * and hidden, x_stride negative, rows of Y that overlap), GS_ERR_DTYPE,
+ * GS_ERR_ATTR (activation, a workspace that is misaligned or of negative
+ * size), GS_ERR_TOO_LARGE (rows, width or hidden above 2^22, rows * hidden
+ * above 2^36, 2^22 thread blocks or more of the call or of its gradients: a
+ * block has 128 rows of the output or more), GS_ERR_HIP.
+ */
+int gs_gated_linear(const void *X, int dtype, int64_t rows, int64_t width, int64_t hidden, int64_t x_stride,
+                    const void *Wg, const void *Wu, int activation, void *Y, int64_t y_stride, float *saved,
+                    void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that gs_gated_linear uses for these extents (0: none),
+ * written to *bytes (host). */
+int gs_gated_linear_workspace_size(int dtype, int64_t rows, int64_t width, int64_t hidden, int64_t *bytes);
+
+/*
+ * Gradients of gs_gated_linear, from dY and the a and b that it saved:
+ *   da = dY * b * act'(a),  db = dY * act(a),
+ *   dX = da Wg + db Wu,  dWg = da^T X,  dWu = db^T X.
+ * da and db are rounded to dtype before they are multiplied (with GS_F32 not
+ * at all); sums are fp32.
+ *
+ *   dY           device, rows x hidden, dtype, rows dy_stride apart.
+ *   dX           device, rows x width, dtype, rows dx_stride apart.
+ *   dWg, dWu     device, hidden x width, contiguous, dtype.  Both, or both
+ *                NULL where they are not wanted; dX may be NULL too.  What is
+ *                given is overwritten whole (rows = 0 gives zero weights'
+ *                gradients, hidden = 0 zero dX).
+ *   workspace    device, 256-byte aligned, at least
+ *                gs_gated_linear_backward_workspace_size() bytes: required.
+ *
+ * Errors: as gs_gated_linear; GS_ERR_NULL for a missing workspace, GS_ERR_ATTR
+ * for one that is too small.
+ */
+int gs_gated_linear_backward(const void *dY, const void *X, int dtype, int64_t rows, int64_t width, int64_t hidden,
+                             int64_t dy_stride, int64_t x_stride, const void *Wg, const void *Wu, int activation,
+                             const float *saved, void *dX, int64_t dx_stride, void *dWg, void *dWu, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that gs_gated_linear_backward needs for these extents,
+ * written to *bytes (host). */
+int gs_gated_linear_backward_workspace_size(int dtype, int64_t rows, int64_t width, int64_t hidden, int64_t *bytes);
+
+/* ------------------------------------------------------------------------
+ * Norms around a block, with its gate and the residual
+ * --------------------------------------------------------------------- */
+
+/*
+ * One call.  Rows of X, branch and so on lie their stride apart.
+ */
+typedef struct {
+    int dtype;             /* of X, branch, H, Y and their gradients: GS_F32, GS_F16, GS_BF16 */
+    int param_dtype;       /* of the scales and biases: dtype or GS_F32 */
+    int gate_dtype;        /* of the gate: dtype or GS_F32 */
+    int layer;             /* 0: root mean square; 1: layer norm (the mean is taken off) */
+    int64_t rows, cols;
+    int64_t gate_rows;     /* rows of the gate: 0 (none), or a divisor of rows */
+    int64_t x_stride, branch_stride, h_stride, y_stride;
+    int64_t dh_stride, dy_stride, dx_stride, dbranch_stride; /* backward only */
+    float epsilon;
+    float residual_scale;
+} gs_residual_norm_desc;
+
+/*
+ * What joins a block to the stream of residuals and feeds the next one:
+ *   H = residual_scale * X + gate * norm(branch; post_scale, post_bias),
+ *   Y = norm(H; pre_scale, pre_bias).
+ * norm(z; w, b) = z / sqrt(mean(z^2) + epsilon) * w + b, with `layer` of
+ * z - mean(z).  Row r takes row r / (rows / gate_rows) of the gate: one for
+ * all, for each sequence, or for each token.  H before its rounding is what Y
+ * is made from.
+ *
+ *   X, branch    device, rows x cols, dtype.
+ *   gate         device, gate_rows x cols, contiguous, gate_dtype; NULL with
+ *                gate_rows 0 (a factor of 1).
+ *   post_scale, post_bias, pre_scale, pre_bias
+ *                device (cols), param_dtype.  post_scale NULL: the branch is
+ *                not normalised; pre_scale NULL: no Y.  A bias may be NULL
+ *                (zeros); it needs its scale.
+ *   H            device, rows x cols, dtype.
+ *   Y            device, rows x cols, dtype; NULL without pre_scale.
+ *   stats        device fp32, rows x 4, contiguous: mean and factor
+ *                1 / sqrt(...) of the branch, then of H (means are 0 without
+ *                `layer`); or NULL.
+ *
+ * Errors: GS_ERR_NULL, GS_ERR_SHAPE (an extent negative, cols 0 with rows,
+ * gate_rows that does not divide rows, a negative stride, rows of an output
+ * that overlap), GS_ERR_DTYPE, GS_ERR_ATTR (epsilon negative or not finite,
+ * residual_scale not finite, `layer` not 0 or 1, stats off its 16-byte
+ * alignment), GS_ERR_TOO_LARGE (cols above 16384, rows above 2^31 - 1),
+ * GS_ERR_HIP.
+ */
+int gs_residual_norm(const gs_residual_norm_desc *desc, const void *X, const void *branch, const void *gate,
+                     const void *post_scale, const void *post_bias, const void *pre_scale, const void *pre_bias,
+                     void *H, void *Y, float *stats, void *stream);
+
+/*
+ * Gradients of gs_residual_norm, from those of H and Y, its inputs and the
+ * stats that it wrote (H is made again, unrounded).
+ *
+ *   dH           device, rows x cols, dtype; NULL: zeros.
+ *   dY           device, rows x cols, dtype; NULL without pre_scale.
+ *   dX, dbranch  device, rows x cols, dtype.
+ *   dgate        device, gate_rows x cols, gate_dtype; NULL where it is not
+ *                wanted.
+ *   dpost_scale, dpost_bias, dpre_scale, dpre_bias
+ *                device (cols), param_dtype; each NULL where it is not wanted.
+ *                They and dgate are overwritten (rows = 0 writes zeros to
+ *                those of the parameters, and leaves dgate).
+ *   workspace    device, 256-byte aligned, at least
+ *                gs_residual_norm_backward_workspace_size() bytes; needed
+ *                where a gradient of the gate or a parameter is wanted.
+ *
+ * Errors: as gs_residual_norm; GS_ERR_NULL for a missing workspace,
+ * GS_ERR_ATTR for one that is too small or misaligned.
+ */
+int gs_residual_norm_backward(const gs_residual_norm_desc *desc, const void *dH, const void *dY, const void *X,
+                              const void *branch, const void *gate, const void *post_scale, const void *post_bias,
+                              const void *pre_scale, const float *stats, void *dX, void *dbranch, void *dgate,
+                              void *dpost_scale, void *dpost_bias, void *dpre_scale, void *dpre_bias, void *workspace,
+                              int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that gs_residual_norm_backward needs for this descriptor,
+ * written to *bytes (host). */
+int gs_residual_norm_backward_workspace_size(const gs_residual_norm_desc *desc, int64_t *bytes);
+
+/* ------------------------------------------------------------------------
+ * Gated linear recurrence
+ * --------------------------------------------------------------------- */
+
+/* Steps between two states that gs_gated_recurrence saves. */
+#define GS_RECURRENCE_CHUNK 128
+
+/*
+ * One call.  Element (b, t, c) of a tensor with strides s lies at
+ * b * s[0] + t * s[1] + c.
+ */
+typedef struct {
+    int dtype;             /* of X, G, Y and their gradients: GS_F32, GS_F16, GS_BF16 */
+    int64_t batch, length, channels;
+    int64_t x_stride[2], g_stride[2], y_stride[2];
+    int64_t dy_stride[2], dx_stride[2], dg_stride[2]; /* backward only */
+} gs_recurrence_desc;
+
+/*
+ * For each sequence and channel, from the state h_-1 that it begins at:
+ *   a_t = 1 / (1 + exp(-G_t)),  h_t = a_t * h_(t-1) + (1 - a_t) * X_t,  Y_t = h_t.
+ * Gates and states are fp32; Y is rounded once.
+ *
+ *   X, G         device (batch, length, channels), dtype.
+ *   state        device fp32 (batch, channels): h_-1; NULL: zeros.
+ *   lengths      device int32 (batch): tokens of each sequence, held to
+ *                0 .. length; NULL: length.  What lies at and past a
+ *                sequence's length is not read; Y is 0 there.
+ *   Y            device (batch, length, channels), dtype.
+ *   last         device fp32 (batch, channels): the state after each
+ *                sequence's last token (h_-1 of one without any); or NULL.
+ *                May be `state` itself (a state kept from call to call).
+ *   saved        device fp32 (batch, ceil(length / GS_RECURRENCE_CHUNK),
+ *                channels), contiguous: the state before every chunk of
+ *                GS_RECURRENCE_CHUNK steps that a sequence reaches, which the
+ *                backward pass takes; or NULL.
+ *   workspace    device, 256-byte aligned, of
+ *                gs_gated_recurrence_workspace_size() bytes; without it (NULL,
+ *                0), or with less, long sequences of few channels are not
+ *                split over thread blocks: slower, and the sums in another
+ *                order.
+ *
+ * Errors: GS_ERR_NULL, GS_ERR_SHAPE (an extent negative, a negative stride,
+ * one of Y below channels along an axis of more than one element),
+ * GS_ERR_DTYPE, GS_ERR_ATTR (a workspace that is misaligned or of negative
+ * size), GS_ERR_TOO_LARGE (length or channels above 2^29, batch * channels
+ * above 2^30, 2^22 thread blocks or more: one has 64 or 128 channels of a
+ * sequence), GS_ERR_HIP.
+ */
+int gs_gated_recurrence(const gs_recurrence_desc *desc, const void *X, const void *G, const float *state,
+                        const int32_t *lengths, void *Y, float *last, float *saved, void *workspace,
+                        int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that gs_gated_recurrence uses for this descriptor (0:
+ * none), written to *bytes (host). */
+int gs_gated_recurrence_workspace_size(const gs_recurrence_desc *desc, int64_t *bytes);
+
+/*
+ * Gradients of gs_gated_recurrence, from those of Y and of the last state, its
+ * inputs and the states that it saved.  With D_t the whole gradient of h_t,
+ *   D_t = dY_t + a_(t+1) D_(t+1),  dX_t = (1 - a_t) D_t,
+ *   dG_t = D_t (h_(t-1) - X_t) a_t (1 - a_t).
+ *
+ *   dlast        device fp32 (batch, channels); NULL: zeros.
+ *   dX, dG       device (batch, length, channels), dtype; 0 at and past a
+ *                sequence's length.
+ *   dstate       device fp32 (batch, channels): the gradient of h_-1; or NULL.
+ *                May be `dlast` itself.
+ *   workspace    as in gs_gated_recurrence, of
+ *                gs_gated_recurrence_backward_workspace_size() bytes.
+ *
+ * Errors: as gs_gated_recurrence.
+ */
+int gs_gated_recurrence_backward(const gs_recurrence_desc *desc, const void *dY, const void *X, const void *G,
+                                 const float *saved, const float *dlast, const int32_t *lengths, void *dX, void *dG,
+                                 float *dstate, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that gs_gated_recurrence_backward uses for this
+ * descriptor (0: none), written to *bytes (host). */
+int gs_gated_recurrence_backward_workspace_size(const gs_recurrence_desc *desc, int64_t *bytes);
 
 #ifdef __cplusplus
 }

@@ -3,8 +3,9 @@
 Python face of libgsample (include/gsample.h): the grid generator
 (AffineGrid), the sampler (GridSample) of any rank and type, their fused
 composition, Resize and DeformConv; and, on the sampled maps read as tokens
-(include/gsample_tokens.h), layer normalisation, dropout and attention with a
-relative position bias, forward and backward.  All are computed by
+(include/gsample_tokens.h), layer normalisation, dropout, attention with a
+relative position bias, gated feed-forward projections, the norms around a
+block and a gated linear recurrence, forward and backward.  All are computed by
 hand-written HIP kernels for gfx950.  Tensors are torch GPU tensors; torch
 supplies device memory and streams only.
 
@@ -35,6 +36,15 @@ from ._binding import (  # noqa: F401
     resize_output_shape,
     resize_to,
 )
+from . import blocks  # noqa: F401
+from .blocks import (  # noqa: F401
+    gated_linear,
+    gated_linear_backward,
+    gated_recurrence,
+    gated_recurrence_backward,
+    residual_norm,
+    residual_norm_backward,
+)
 from ._tokens import (  # noqa: F401
     AttentionDesc,
     attention,
@@ -51,4 +61,4 @@ __all__ = ["affine_grid", "grid_sample", "affine_grid_sample_fused", "resize",
            "deform_conv_output_shape",
            "deform_conv_workspace_size", "dtype_code", "grid_sample_2d_workspace_size",
            "layer_norm", "layer_norm_backward", "dropout", "attention", "attention_backward",
-           "relative_bucket", "GSError", "lib"]
+           "relative_bucket", "blocks", "GSError", "lib"]

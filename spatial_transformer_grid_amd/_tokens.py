@@ -50,6 +50,18 @@ TOKEN_SIGNATURES = {
     "gs_attention_workspace_size": ([_PDESC, _PI64], _I),
     "gs_attention_backward": ([_PDESC] + [_P] * 13 + [_I64, _P], _I),
     "gs_attention_backward_workspace_size": ([_PDESC, _PI64], _I),
+    # (blocks; descriptors are passed by reference)
+    "gs_gated_linear": ([_P, _I] + [_I64] * 4 + [_P, _P, _I, _P, _I64, _P, _P, _I64, _P], _I),
+    "gs_gated_linear_workspace_size": ([_I, _I64, _I64, _I64, _PI64], _I),
+    "gs_gated_linear_backward": ([_P, _P, _I] + [_I64] * 5 + [_P, _P, _I, _P, _P, _I64, _P, _P, _P, _I64, _P], _I),
+    "gs_gated_linear_backward_workspace_size": ([_I, _I64, _I64, _I64, _PI64], _I),
+    "gs_residual_norm": ([_P] * 12, _I),
+    "gs_residual_norm_backward": ([_P] * 18 + [_I64, _P], _I),
+    "gs_residual_norm_backward_workspace_size": ([_P, _PI64], _I),
+    "gs_gated_recurrence": ([_P] * 9 + [_I64, _P], _I),
+    "gs_gated_recurrence_workspace_size": ([_P, _PI64], _I),
+    "gs_gated_recurrence_backward": ([_P] * 11 + [_I64, _P], _I),
+    "gs_gated_recurrence_backward_workspace_size": ([_P, _PI64], _I),
 }
 
 _typed = None

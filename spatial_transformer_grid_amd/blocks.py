@@ -1,0 +1,346 @@
+"""ctypes binding of libgsample's operators around a block of a token model
+(include/gsample_tokens.h): gated feed-forward projections, the norms before and
+after a block joined with its gate and residual, and a gated linear recurrence,
+forward and backward.
+
+Argument marshalling only, as in _tokens: tensors may be strided where the
+library takes strides, results take part in no autograd graph, and a training
+step calls the _backward functions itself.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+
+from ._binding import GS_F32, _check, _device_tensor, _I, _on_stream, _torch, dtype_code
+from ._tokens import (_address, _I64, _like, _output, _rows, _stream_handle, _tensor, _workspace, token_lib)
+
+__all__ = ["gated_linear", "gated_linear_backward", "residual_norm", "residual_norm_backward", "gated_recurrence",
+           "gated_recurrence_backward"]
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+NORMS = {"rms": 0, "layer": 1}
+RECURRENCE_CHUNK = 128  # GS_RECURRENCE_CHUNK
+
+_S2 = _I64 * 2
+
+
+class ResidualNormDesc(ctypes.Structure):
+    """gs_residual_norm_desc"""
+
+    _fields_ = ([(n, _I) for n in ("dtype", "param_dtype", "gate_dtype", "layer")]
+                + [(n, _I64) for n in ("rows", "cols", "gate_rows")]
+                + [(n + "_stride", _I64) for n in ("x", "branch", "h", "y", "dh", "dy", "dx", "dbranch")]
+                + [("epsilon", ctypes.c_float), ("residual_scale", ctypes.c_float)])
+
+
+class RecurrenceDesc(ctypes.Structure):
+    """gs_recurrence_desc"""
+
+    _fields_ = ([("dtype", _I)] + [(n, _I64) for n in ("batch", "length", "channels")]
+                + [(n + "_stride", _S2) for n in ("x", "g", "y", "dy", "dx", "dg")])
+
+
+def _named(value, names, what):
+    code = names.get(value) if isinstance(value, str) else None
+    if code is None:
+        raise ValueError("%s must be one of %s" % (what, ", ".join(names)))
+    return code
+
+
+def _call(name, device, *args):
+    """The entry point on the device's current stream, with that device as the current one."""
+    torch = _torch()
+    fn = getattr(token_lib(), name)
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream_handle(device))
+    else:
+        status = fn(*args, _stream_handle(device))
+    if status:
+        _check(status, name)
+
+
+def _need(name, *args):
+    """Bytes of workspace that the library asks for."""
+    need = _I64(0)
+    _check(getattr(token_lib(), name)(*args, ctypes.byref(need)), name)
+    return need.value
+
+
+# ------------------------------------------------------- gated projections
+
+def _projections(X, gate_weight, up_weight, activation):
+    X = _tensor(X, "X")
+    if X.dim() < 1:
+        raise ValueError("X needs an axis")
+    device, width = X.get_device(), X.shape[-1]
+    if gate_weight.dim() != 2 or gate_weight.shape[1] != width or up_weight.shape != gate_weight.shape:
+        raise ValueError("gate_weight and up_weight must have one shape (hidden, %d)" % width)
+    gate_weight, up_weight = _device_tensor(gate_weight, "gate_weight", device), _device_tensor(up_weight, "up_weight",
+                                                                                                device)
+    if gate_weight.dtype != X.dtype or up_weight.dtype != X.dtype:
+        raise TypeError("gate_weight and up_weight must have X's element type")
+    return X, gate_weight, up_weight, math.prod(X.shape[:-1]), _named(activation, ACTIVATIONS, "activation")
+
+
+def gated_linear(X, gate_weight, up_weight, activation: str = "silu", return_saved: bool = False, out=None,
+                 stream=None, workspace=None):
+    """activation(X gate_weight^T) * (X up_weight^T) in one pass (gs_gated_linear).
+
+    X (..., width); the weights (hidden, width), as a linear layer holds them,
+    of X's element type.  `activation`: "silu", "gelu", "gelu_tanh" or "relu".
+    With `return_saved` both projections before the activation are returned too
+    (float32, (2, ..., hidden)): gated_linear_backward takes them."""
+    if stream is not None:
+        return _on_stream(stream, gated_linear, X, gate_weight, up_weight, activation, return_saved, out,
+                          workspace=workspace)
+    torch = _torch()
+    X, gate_weight, up_weight, rows, act = _projections(X, gate_weight, up_weight, activation)
+    width, hidden, device = X.shape[-1], gate_weight.shape[0], X.device
+    x, xs = _rows(X)
+    shape = (*X.shape[:-1], hidden)
+    if out is None:
+        Y = torch.empty(shape, dtype=X.dtype, device=device)
+    else:
+        if (tuple(out.shape) != shape or out.dtype != X.dtype or out.get_device() != X.get_device()
+                or not out.is_contiguous()):
+            raise ValueError("out must be a contiguous %s tensor of shape %s on X's GPU" % (X.dtype, shape))
+        Y = out
+    saved = torch.empty((2, *shape), dtype=torch.float32, device=device) if return_saved else None
+    code = dtype_code(X)
+    need = 0 if workspace is not None else _need("gs_gated_linear_workspace_size", code, rows, width, hidden)
+    workspace, ws, ws_bytes = _workspace(workspace, need, device)
+    _call("gs_gated_linear", device, x.data_ptr(), code, rows, width, hidden, xs, gate_weight.data_ptr(),
+          up_weight.data_ptr(), act, Y.data_ptr(), hidden, _address(saved), ws, ws_bytes)
+    return (Y, saved) if return_saved else Y
+
+
+def gated_linear_backward(dY, X, gate_weight, up_weight, saved, activation: str = "silu", stream=None,
+                          workspace=None):
+    """Gradients (dX, dgate_weight, dup_weight) of gated_linear (gs_gated_linear_backward)."""
+    if stream is not None:
+        return _on_stream(stream, gated_linear_backward, dY, X, gate_weight, up_weight, saved, activation,
+                          workspace=workspace)
+    torch = _torch()
+    X, gate_weight, up_weight, rows, act = _projections(X, gate_weight, up_weight, activation)
+    width, hidden, device = X.shape[-1], gate_weight.shape[0], X.device
+    shape = (*X.shape[:-1], hidden)
+    dY = _tensor(dY, "dY", X.get_device(), X.dtype, shape)
+    saved = _tensor(saved, "saved", X.get_device(), torch.float32, (2, *shape)).contiguous()
+    x, xs = _rows(X)
+    dy, dys = _rows(dY)
+    dX = torch.empty(X.shape, dtype=X.dtype, device=device)
+    dgate, dup = torch.empty_like(gate_weight), torch.empty_like(up_weight)
+    code = dtype_code(X)
+    need = 0 if workspace is not None else _need("gs_gated_linear_backward_workspace_size", code, rows, width, hidden)
+    workspace, ws, ws_bytes = _workspace(workspace, need, device)
+    _call("gs_gated_linear_backward", device, dy.data_ptr(), x.data_ptr(), code, rows, width, hidden, dys, xs,
+          gate_weight.data_ptr(), up_weight.data_ptr(), act, saved.data_ptr(), dX.data_ptr(), width, dgate.data_ptr(),
+          dup.data_ptr(), ws, ws_bytes)
+    return dX, dgate, dup
+
+
+# --------------------------------------------------- norms around a block
+
+def _join(X, branch, post_scale, post_bias, pre_scale, pre_bias, gate, residual_scale, epsilon, norm):
+    """Checked tensors of a call and its descriptor, without the outputs' strides."""
+    torch = _torch()
+    X = _tensor(X, "X")
+    if X.dim() < 1:
+        raise ValueError("X needs an axis")
+    device, cols = X.get_device(), X.shape[-1]
+    branch = _tensor(branch, "branch", device, X.dtype, X.shape)
+    params, kind = [], None
+    for name, t in (("post_scale", post_scale), ("post_bias", post_bias), ("pre_scale", pre_scale),
+                    ("pre_bias", pre_bias)):
+        if t is not None:
+            t = _device_tensor(t, name, device)
+            if tuple(t.shape) != (cols,):
+                raise ValueError("%s must have shape (%d,)" % (name, cols))
+            if t.dtype != X.dtype and t.dtype != torch.float32:
+                raise TypeError("%s must have X's element type or float32" % name)
+            if kind is not None and t.dtype != kind:
+                raise TypeError("scales and biases must have one element type")
+            kind = t.dtype
+        params.append(t)
+    for scale, bias in (0, 1), (2, 3):
+        if params[bias] is not None and params[scale] is None:
+            raise ValueError("a bias needs its scale")
+    d = ResidualNormDesc()
+    d.dtype = dtype_code(X)
+    d.param_dtype = d.dtype if kind is None or kind == X.dtype else GS_F32
+    d.gate_dtype = d.dtype
+    d.layer = _named(norm, NORMS, "norm")
+    d.rows, d.cols = math.prod(X.shape[:-1]), cols
+    if gate is not None:
+        gate = _device_tensor(gate, "gate", device)
+        lead = gate.dim() - 1
+        if lead < 0 or lead >= X.dim() or tuple(gate.shape) != (*X.shape[:lead], cols):
+            raise ValueError("gate must have the shape of X's first axes and its last one")
+        if gate.dtype != X.dtype and gate.dtype != torch.float32:
+            raise TypeError("gate must have X's element type or float32")
+        d.gate_rows, d.gate_dtype = math.prod(gate.shape[:-1]), dtype_code(gate)
+    d.epsilon, d.residual_scale = epsilon, residual_scale
+    x, d.x_stride = _rows(X)
+    f, d.branch_stride = _rows(branch)
+    d.h_stride = d.y_stride = d.dh_stride = d.dy_stride = d.dx_stride = d.dbranch_stride = cols
+    return X, x, f, params, gate, d
+
+
+def residual_norm(X, branch, post_scale=None, pre_scale=None, post_bias=None, pre_bias=None, gate=None,
+                  residual_scale: float = 1.0, epsilon: float = 1e-5, norm: str = "rms", return_stats: bool = False,
+                  stream=None):
+    """(H, Y): the stream H = residual_scale * X + gate * norm(branch) and what
+    the next block reads, Y = norm(H), in one pass (gs_residual_norm).
+
+    X and branch (..., channels).  `norm`: "rms" (root mean square) or "layer".
+    post_scale and post_bias belong to the branch's norm (post_scale None: the
+    branch as it is), pre_scale and pre_bias to that of H (pre_scale None: Y is
+    None).  `gate`: the shape of X's first axes and its last one, (channels,)
+    for all tokens, (batch, channels) for each sequence, X's own for each token.
+    With `return_stats` the norms' statistics are returned too (float32, X's
+    shape with 4 as its last axis): residual_norm_backward takes them."""
+    if stream is not None:
+        return _on_stream(stream, residual_norm, X, branch, post_scale, pre_scale, post_bias, pre_bias, gate,
+                          residual_scale, epsilon, norm, return_stats)
+    torch = _torch()
+    X, x, f, params, gate, d = _join(X, branch, post_scale, post_bias, pre_scale, pre_bias, gate, residual_scale,
+                                     epsilon, norm)
+    H = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    Y = torch.empty_like(H) if pre_scale is not None else None
+    stats = torch.empty((*X.shape[:-1], 4), dtype=torch.float32, device=X.device) if return_stats else None
+    _call("gs_residual_norm", X.device, ctypes.byref(d), x.data_ptr(), f.data_ptr(), _address(gate),
+          *(_address(t) for t in params), H.data_ptr(), _address(Y), _address(stats))
+    return (H, Y, stats) if return_stats else (H, Y)
+
+
+def residual_norm_backward(dH, dY, X, branch, stats, post_scale=None, pre_scale=None, post_bias=None, pre_bias=None,
+                           gate=None, residual_scale: float = 1.0, epsilon: float = 1e-5, norm: str = "rms",
+                           stream=None, workspace=None):
+    """Gradients (dX, dbranch, dgate, dpost_scale, dpost_bias, dpre_scale,
+    dpre_bias) of residual_norm (gs_residual_norm_backward), from those of H
+    (None: nothing else reads the stream) and of Y (None without pre_scale).
+
+    None stands for the gradient of what the call does not have; with
+    norm="layer" the biases' gradients are there wherever the scales are."""
+    if stream is not None:
+        return _on_stream(stream, residual_norm_backward, dH, dY, X, branch, stats, post_scale, pre_scale, post_bias,
+                          pre_bias, gate, residual_scale, epsilon, norm, workspace=workspace)
+    torch = _torch()
+    X, x, f, params, gate, d = _join(X, branch, post_scale, post_bias, pre_scale, pre_bias, gate, residual_scale,
+                                     epsilon, norm)
+    device = X.device
+    stats = _tensor(stats, "stats", X.get_device(), torch.float32, (*X.shape[:-1], 4)).contiguous()
+    dh = dy = None
+    if dH is not None:
+        dh, d.dh_stride = _rows(_tensor(dH, "dH", X.get_device(), X.dtype, X.shape))
+    if (dY is None) != (pre_scale is None):
+        raise ValueError("dY is given exactly where pre_scale is")
+    if dY is not None:
+        dy, d.dy_stride = _rows(_tensor(dY, "dY", X.get_device(), X.dtype, X.shape))
+    dX = torch.empty(X.shape, dtype=X.dtype, device=device)
+    dbranch = torch.empty_like(dX)
+    dgate = None
+    if gate is not None:
+        dgate = torch.empty_like(gate) if d.rows else torch.zeros_like(gate)
+    post, post_b, pre, pre_b = params
+    grads = [None if t is None else torch.empty_like(t) for t in (
+        post, post if norm == "layer" else post_b, pre, pre if norm == "layer" else pre_b)]
+    need = 0
+    if workspace is None:
+        need = _need("gs_residual_norm_backward_workspace_size", ctypes.byref(d))
+    workspace, ws, ws_bytes = _workspace(workspace, need, device)
+    _call("gs_residual_norm_backward", device, ctypes.byref(d), _address(dh), _address(dy), x.data_ptr(), f.data_ptr(),
+          _address(gate), _address(post), _address(post_b), _address(pre), stats.data_ptr(), dX.data_ptr(),
+          dbranch.data_ptr(), _address(dgate), *(_address(t) for t in grads), ws, ws_bytes)
+    return dX, dbranch, dgate, *grads
+
+
+# ------------------------------------------------------- gated recurrence
+
+def _strides2(t):
+    # the stride of an axis of one element addresses nothing
+    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
+def _recurrence(X, G, lengths):
+    torch = _torch()
+    if X.dim() != 3:
+        raise ValueError("X must have shape (batch, length, channels)")
+    X = _tensor(X, "X")
+    G = _tensor(G, "G", X.get_device(), X.dtype, X.shape)
+    if lengths is not None:
+        lengths = _tensor(lengths, "lengths", X.get_device(), torch.int32, X.shape[:1]).contiguous()
+    d = RecurrenceDesc()
+    d.dtype = dtype_code(X)
+    d.batch, d.length, d.channels = X.shape
+    d.x_stride, d.g_stride = _strides2(X), _strides2(G)
+    return X, G, lengths, d
+
+
+def _state(t, name, X):
+    if t is None:
+        return None
+    return _tensor(t, name, X.get_device(), _torch().float32, (X.shape[0], X.shape[2])).contiguous()
+
+
+def gated_recurrence(X, G, state=None, lengths=None, return_saved: bool = False, last=None, out=None, stream=None,
+                     workspace=None):
+    """(Y, last): h_t = a_t h_(t-1) + (1 - a_t) X_t along the tokens, with the
+    gates a_t = sigmoid(G_t), and the state after each sequence's last token
+    (gs_gated_recurrence).
+
+    X and G (batch, length, channels), of any strides with a contiguous last
+    axis.  `state` (float32, batch x channels): what the sequences begin at, or
+    None for zeros.  `lengths` (int32, batch): tokens that each sequence holds; Y is 0
+    past them.  `last`: where the last state is written, `state` itself if a
+    state is kept from call to call.  With `return_saved` the states that
+    gated_recurrence_backward takes are returned too."""
+    if stream is not None:
+        return _on_stream(stream, gated_recurrence, X, G, state, lengths, return_saved, last, out, workspace=workspace)
+    torch = _torch()
+    X, G, lengths, d = _recurrence(X, G, lengths)
+    same = last is not None and last is state
+    state = _state(state, "state", X)
+    if last is None:
+        last = torch.empty((X.shape[0], X.shape[2]), dtype=torch.float32, device=X.device)
+    elif (last.get_device() != X.get_device() or last.dtype != torch.float32 or not last.is_contiguous()
+          or tuple(last.shape) != (X.shape[0], X.shape[2])):
+        raise ValueError("last must be a contiguous float32 tensor of shape (batch, channels) on X's GPU")
+    elif same:
+        state = last
+    Y = _output(out, X, False)
+    d.y_stride = _strides2(Y)
+    saved = None
+    if return_saved:
+        chunks = -(-X.shape[1] // RECURRENCE_CHUNK)
+        saved = torch.empty((X.shape[0], chunks, X.shape[2]), dtype=torch.float32, device=X.device)
+    need = 0 if workspace is not None else _need("gs_gated_recurrence_workspace_size", ctypes.byref(d))
+    workspace, ws, ws_bytes = _workspace(workspace, need, X.device)
+    _call("gs_gated_recurrence", X.device, ctypes.byref(d), X.data_ptr(), G.data_ptr(), _address(state),
+          _address(lengths), Y.data_ptr(), last.data_ptr(), _address(saved), ws, ws_bytes)
+    return (Y, last, saved) if return_saved else (Y, last)
+
+
+def gated_recurrence_backward(dY, X, G, saved, dlast=None, lengths=None, stream=None, workspace=None):
+    """Gradients (dX, dG, dstate) of gated_recurrence (gs_gated_recurrence_backward), from those of Y and
+    of the last state (None: zeros)."""
+    if stream is not None:
+        return _on_stream(stream, gated_recurrence_backward, dY, X, G, saved, dlast, lengths, workspace=workspace)
+    torch = _torch()
+    X, G, lengths, d = _recurrence(X, G, lengths)
+    dY = _tensor(dY, "dY", X.get_device(), X.dtype, X.shape)
+    chunks = -(-X.shape[1] // RECURRENCE_CHUNK)
+    saved = _tensor(saved, "saved", X.get_device(), torch.float32, (X.shape[0], chunks, X.shape[2])).contiguous()
+    dlast = _state(dlast, "dlast", X)
+    dX, dG = _like(X), _like(G)
+    dstate = torch.empty((X.shape[0], X.shape[2]), dtype=torch.float32, device=X.device)
+    d.dy_stride, d.dx_stride, d.dg_stride = _strides2(dY), _strides2(dX), _strides2(dG)
+    need = 0 if workspace is not None else _need("gs_gated_recurrence_backward_workspace_size", ctypes.byref(d))
+    workspace, ws, ws_bytes = _workspace(workspace, need, X.device)
+    _call("gs_gated_recurrence_backward", X.device, ctypes.byref(d), dY.data_ptr(), X.data_ptr(), G.data_ptr(),
+          saved.data_ptr(), _address(dlast), _address(lengths), dX.data_ptr(), dG.data_ptr(), dstate.data_ptr(), ws,
+          ws_bytes)
+    return dX, dG, dstate

@@ -1,0 +1,471 @@
+// gs_blocks_api.cpp -- C ABI of the gated projections, the norms around a block
+// and the gated recurrence (gsample_tokens.h): argument validation and kernel
+// dispatch.  As in gs_api.cpp every check runs before any launch, and nothing is
+// allocated or kept.
+#include "gsample_tokens.h"
+#include "gs_tokens.hpp"
+
+#include <math.h>
+#include <stdint.h>
+
+namespace {
+
+constexpr int64_t kInt32Max = 0x7fffffff;
+constexpr int64_t kMaxBlocks = int64_t(1) << 22;    // of up to 1024 threads, whose number has to stay below 2^32
+constexpr uintptr_t kWsAlign = 256;
+
+bool data_dtype(int d) { return d == GS_F32 || d == GS_F16 || d == GS_BF16; }
+int dtype_bytes(int d) { return d == GS_F32 ? 4 : 2; }
+int64_t round_ws(int64_t b) { return (b + 255) / 256 * 256; }
+int hip_status(int rc) { return rc == 0 ? GS_OK : GS_ERR_HIP; }
+bool aligned(const void *p, int bytes) { return (uintptr_t)p % bytes == 0; }
+bool bad_workspace(const void *w, int64_t bytes) { return bytes < 0 || (w && (uintptr_t)w % kWsAlign); }
+
+// ------------------------------------------------------ gated projections
+
+constexpr int64_t kMaxExtent = int64_t(1) << 22, kMaxProduct = int64_t(1) << 36;
+
+int gated_extents(int dtype, int64_t rows, int64_t width, int64_t hidden) {
+    if (rows < 0 || width < 0 || hidden < 0) return GS_ERR_SHAPE;
+    if (!data_dtype(dtype)) return GS_ERR_DTYPE;
+    if (width == 0 && rows > 0 && hidden > 0) return GS_ERR_SHAPE;
+    if (rows > kMaxExtent || width > kMaxExtent || hidden > kMaxExtent || rows * hidden > kMaxProduct)
+        return GS_ERR_TOO_LARGE;
+    if (gs::gated_blocks(gs::kGatedForward, dtype, rows, hidden, width) >= kMaxBlocks ||
+        gs::gated_blocks(gs::kGatedInput, dtype, rows, width, hidden) >= kMaxBlocks ||
+        gs::gated_blocks(gs::kGatedWeights, dtype, hidden, width, rows) >= kMaxBlocks)
+        return GS_ERR_TOO_LARGE;
+    return GS_OK;
+}
+
+bool gated_activation(int a) { return a >= GS_ACT_SILU && a <= GS_ACT_RELU; }
+
+// How tiles of an operand are loaded (see gs_gated.hip): `contiguous` elements of
+// a row of its storage, rows `stride` apart.  An asynchronous load reaches the 256
+// rows of a tile by a 32-bit offset.
+int load_mode(int dtype, const void *p, const void *q, int64_t contiguous, int64_t stride) {
+    const int bytes = dtype_bytes(dtype);
+    if (stride * bytes >= (int64_t(1) << 23)) return 2;
+    for (int mode = 0; mode < 2; ++mode) {
+        const int unit = mode == 0 ? 16 : 4;
+        if (contiguous * bytes % unit == 0 && stride * bytes % unit == 0 && aligned(p, unit) && aligned(q, unit))
+            return mode;
+    }
+    return 2;
+}
+
+bool rows_vec(int dtype, const void *p, int64_t stride) {
+    return stride * dtype_bytes(dtype) % 16 == 0 && aligned(p, 16);
+}
+
+// Workspace of a backward call: da, db in rows of whole chunks of eight, then the
+// parts' sums of one product or the other.
+struct GatedSpace {
+    int64_t db, partial, bytes;
+};
+
+GatedSpace gated_space(int dtype, int64_t rows, int64_t width, int64_t hidden) {
+    GatedSpace s;
+    const int64_t plane = round_ws(rows * ((hidden + 7) / 8 * 8) * dtype_bytes(dtype));
+    const int64_t a = gs::gated_partial_floats(gs::kGatedInput, dtype, rows, width, hidden);
+    const int64_t b = gs::gated_partial_floats(gs::kGatedWeights, dtype, hidden, width, rows);
+    s.db = plane;
+    s.partial = 2 * plane;
+    s.bytes = s.partial + round_ws((a > b ? a : b) * 4);
+    return s;
+}
+
+// -------------------------------------------------- norms around a block
+
+bool rows_apart(int64_t rows, int64_t stride, int64_t cols) { return rows <= 1 || stride >= cols; }
+
+int join_setup(const gs_residual_norm_desc *d, bool backward, gs::JoinParams &p) {
+    if (!d) return GS_ERR_NULL;
+    if (!data_dtype(d->dtype)) return GS_ERR_DTYPE;
+    if (d->param_dtype != d->dtype && d->param_dtype != GS_F32) return GS_ERR_DTYPE;
+    if (d->gate_rows != 0 && d->gate_dtype != d->dtype && d->gate_dtype != GS_F32) return GS_ERR_DTYPE;
+    if (d->rows < 0 || d->cols < 0 || d->gate_rows < 0) return GS_ERR_SHAPE;
+    if (d->rows > 0 && d->cols == 0) return GS_ERR_SHAPE;
+    if (d->gate_rows > 0 && d->rows % d->gate_rows != 0) return GS_ERR_SHAPE;
+    if (d->x_stride < 0 || d->branch_stride < 0) return GS_ERR_SHAPE;
+    if (backward ? d->dh_stride < 0 || d->dy_stride < 0 || !rows_apart(d->rows, d->dx_stride, d->cols) ||
+                       !rows_apart(d->rows, d->dbranch_stride, d->cols)
+                 : !rows_apart(d->rows, d->h_stride, d->cols) || !rows_apart(d->rows, d->y_stride, d->cols))
+        return GS_ERR_SHAPE;
+    if (!(d->epsilon >= 0.0f) || !isfinite(d->epsilon) || !isfinite(d->residual_scale)) return GS_ERR_ATTR;
+    if (d->layer != 0 && d->layer != 1) return GS_ERR_ATTR;
+    if (d->cols > 16384 || d->rows > kInt32Max) return GS_ERR_TOO_LARGE;
+    p = gs::JoinParams{};
+    p.rows = d->rows;
+    p.cols = (int)d->cols;
+    p.x_stride = d->x_stride;
+    p.branch_stride = d->branch_stride;
+    p.h_stride = d->h_stride;
+    p.y_stride = d->y_stride;
+    p.dh_stride = d->dh_stride;
+    p.dy_stride = d->dy_stride;
+    p.dx_stride = d->dx_stride;
+    p.dbranch_stride = d->dbranch_stride;
+    p.layer = d->layer;
+    p.param_f32 = d->param_dtype == GS_F32;
+    p.gate_f32 = d->gate_dtype == GS_F32;
+    p.epsilon = d->epsilon;
+    p.alpha = d->residual_scale;
+    p.group = d->gate_rows > 0 && d->rows > 0 ? d->rows / d->gate_rows : 1;
+    return GS_OK;
+}
+
+bool all_aligned(const void *const *v, int n) {
+    for (int i = 0; i < n; ++i)
+        if (!aligned(v[i], 16)) return false;
+    return true;
+}
+
+// ------------------------------------------------------- gated recurrence
+
+int scan_setup(const gs_recurrence_desc *d, bool backward, gs::ScanParams &p) {
+    if (!d) return GS_ERR_NULL;
+    if (!data_dtype(d->dtype)) return GS_ERR_DTYPE;
+    if (d->batch < 0 || d->length < 0 || d->channels < 0) return GS_ERR_SHAPE;
+    const int64_t *const in[] = {d->x_stride, d->g_stride, d->dy_stride}, *const fwd[] = {d->y_stride},
+                  *const bwd[] = {d->dx_stride, d->dg_stride};
+    for (int i = 0; i < (backward ? 3 : 2); ++i)
+        if (in[i][0] < 0 || in[i][1] < 0) return GS_ERR_SHAPE;
+    if (d->length > (int64_t(1) << 29) || d->channels > (int64_t(1) << 29) || d->batch > (int64_t(1) << 30) ||
+        d->batch * d->channels > (int64_t(1) << 30) || d->batch * ((d->channels + 63) / 64) >= kMaxBlocks)
+        return GS_ERR_TOO_LARGE;
+    p = gs::ScanParams{};
+    p.pairwise = d->channels % 2 == 0;
+    for (int i = 0; i < (backward ? 2 : 1); ++i) {
+        const int64_t *s = backward ? bwd[i] : fwd[i];
+        if (d->batch * d->length * d->channels > 0 &&
+            ((d->batch > 1 && s[0] < d->channels) || (d->length > 1 && s[1] < d->channels)))
+            return GS_ERR_SHAPE;
+        if (s[0] % 2 || s[1] % 2) p.pairwise = 0;
+    }
+    for (int i = 0; i < (backward ? 3 : 2); ++i)
+        if (in[i][0] % 2 || in[i][1] % 2) p.pairwise = 0;
+    for (int i = 0; i < 2; ++i) {
+        p.xs[i] = d->x_stride[i];
+        p.gs[i] = d->g_stride[i];
+        p.ys[i] = d->y_stride[i];
+        p.dys[i] = d->dy_stride[i];
+        p.dxs[i] = d->dx_stride[i];
+        p.dgs[i] = d->dg_stride[i];
+    }
+    p.batch = (int)d->batch;
+    p.length = (int)d->length;
+    p.channels = (int)d->channels;
+    return GS_OK;
+}
+
+// Bytes for `parts` pairs a channel and the copy of what the call begins at.
+int64_t scan_bytes(const gs::ScanParams &p, int parts) {
+    return parts > 1 ? round_ws((2 * (int64_t)parts + 1) * p.batch * p.channels * 4) : 0;
+}
+
+// The workspace is the same whether two channels share a lane or not, so that it
+// does not depend on pointers: as many as the larger of both.
+int64_t scan_space(const gs::ScanParams &p) {
+    const int64_t one = scan_bytes(p, gs::recurrence_parts(p.batch, p.length, p.channels, false));
+    const int64_t two = scan_bytes(p, gs::recurrence_parts(p.batch, p.length, p.channels, true));
+    return one > two ? one : two;
+}
+
+void scan_split(gs::ScanParams &p, void *workspace, int64_t bytes) {
+    p.parts = gs::recurrence_parts(p.batch, p.length, p.channels, p.pairwise != 0);
+    if (!workspace || bytes < scan_bytes(p, p.parts)) p.parts = 1;
+    p.copy = (float *)workspace;
+    p.pairs = p.copy ? p.copy + (int64_t)p.batch * p.channels : nullptr;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gs_gated_linear_workspace_size(int dtype, int64_t rows, int64_t width, int64_t hidden, int64_t *bytes) {
+    if (!bytes) return GS_ERR_NULL;
+    const int rc = gated_extents(dtype, rows, width, hidden);
+    if (rc != GS_OK) return rc;
+    *bytes = round_ws(gs::gated_partial_floats(gs::kGatedForward, dtype, rows, hidden, width) * 4);
+    return GS_OK;
+}
+
+int gs_gated_linear(const void *X, int dtype, int64_t rows, int64_t width, int64_t hidden, int64_t x_stride,
+                    const void *Wg, const void *Wu, int activation, void *Y, int64_t y_stride, float *saved,
+                    void *workspace, int64_t workspace_bytes, void *stream) {
+    const int rc = gated_extents(dtype, rows, width, hidden);
+    if (rc != GS_OK) return rc;
+    if (x_stride < 0 || !rows_apart(rows, y_stride, hidden)) return GS_ERR_SHAPE;
+    if (!gated_activation(activation) || bad_workspace(workspace, workspace_bytes)) return GS_ERR_ATTR;
+    if (rows == 0 || hidden == 0) return GS_OK;
+    if (!X || !Wg || !Wu || !Y) return GS_ERR_NULL;
+    gs::GatedParams p = {};
+    p.m0 = X;
+    p.n0 = Wg;
+    p.n1 = Wu;
+    p.out0 = Y;
+    p.saved = saved;
+    p.m_stride = x_stride;
+    p.n_stride = width;
+    p.out_stride = y_stride;
+    p.m = (int)rows;
+    p.n = (int)hidden;
+    p.k = (int)width;
+    p.m_mode = load_mode(dtype, X, X, width, x_stride);
+    p.n_mode = load_mode(dtype, Wg, Wu, width, width);
+    p.out_vec = rows_vec(dtype, Y, y_stride);
+    p.saved_vec = rows_vec(GS_F32, saved, hidden);
+    p.activation = activation;
+    const int64_t need = gs::gated_partial_floats(gs::kGatedForward, dtype, rows, hidden, width) * 4;
+    p.partial = need > 0 && workspace && workspace_bytes >= need ? (float *)workspace : nullptr;
+    return hip_status(gs::launch_gated(p, gs::kGatedForward, dtype, (hipStream_t)stream));
+}
+
+int gs_gated_linear_backward_workspace_size(int dtype, int64_t rows, int64_t width, int64_t hidden, int64_t *bytes) {
+    if (!bytes) return GS_ERR_NULL;
+    const int rc = gated_extents(dtype, rows, width, hidden);
+    if (rc != GS_OK) return rc;
+    *bytes = gated_space(dtype, rows, width, hidden).bytes;
+    return GS_OK;
+}
+
+int gs_gated_linear_backward(const void *dY, const void *X, int dtype, int64_t rows, int64_t width, int64_t hidden,
+                             int64_t dy_stride, int64_t x_stride, const void *Wg, const void *Wu, int activation,
+                             const float *saved, void *dX, int64_t dx_stride, void *dWg, void *dWu, void *workspace,
+                             int64_t workspace_bytes, void *stream) {
+    const int rc = gated_extents(dtype, rows, width, hidden);
+    if (rc != GS_OK) return rc;
+    if (dy_stride < 0 || x_stride < 0 || (dX && !rows_apart(rows, dx_stride, width))) return GS_ERR_SHAPE;
+    if (!gated_activation(activation) || workspace_bytes < 0) return GS_ERR_ATTR;
+    if ((dWg == nullptr) != (dWu == nullptr)) return GS_ERR_NULL;
+    const bool input = dX && rows > 0 && width > 0, weights = dWg && hidden > 0 && width > 0;
+    if (!input && !weights) return GS_OK;
+    const bool both = rows > 0 && hidden > 0;
+    if (both && (!dY || !saved || (weights && !X) || (input && (!Wg || !Wu)))) return GS_ERR_NULL;
+    const GatedSpace space = gated_space(dtype, rows, width, hidden);
+    if (space.bytes > 0) {
+        if (!workspace) return GS_ERR_NULL;
+        if (workspace_bytes < space.bytes || (uintptr_t)workspace % kWsAlign) return GS_ERR_ATTR;
+    }
+    char *const ws = (char *)workspace;
+    void *const da = ws, *const db = ws + space.db;
+    float *const partial = (float *)(ws + space.partial);
+    const int64_t padded = (hidden + 7) / 8 * 8;
+    if (both) {
+        gs::GatedParams p = {};
+        p.dy = dY;
+        p.dy_stride = dy_stride;
+        p.saved = const_cast<float *>(saved);
+        p.saved_vec = rows_vec(GS_F32, saved, hidden);
+        p.out_vec = rows_vec(dtype, dY, dy_stride) && hidden % 8 == 0;
+        p.out0 = da;
+        p.out1 = db;
+        p.m = (int)rows;
+        p.n = (int)hidden;
+        p.activation = activation;
+        const int e = gs::launch_gated(p, gs::kGatedGradients, dtype, (hipStream_t)stream);
+        if (e) return hip_status(e);
+    }
+    if (input) {
+        gs::GatedParams p = {};
+        p.m0 = da;
+        p.m1 = db;
+        p.n0 = Wg;
+        p.n1 = Wu;
+        p.out0 = dX;
+        p.m_stride = padded;
+        p.n_stride = width;
+        p.out_stride = dx_stride;
+        p.m = (int)rows;
+        p.n = (int)width;
+        p.k = (int)hidden;
+        p.m_mode = load_mode(dtype, da, db, padded, padded);
+        p.n_mode = load_mode(dtype, Wg, Wu, width, width);
+        p.out_vec = rows_vec(dtype, dX, dx_stride);
+        p.partial = gs::gated_partial_floats(gs::kGatedInput, dtype, rows, width, hidden) > 0 ? partial : nullptr;
+        const int e = gs::launch_gated(p, gs::kGatedInput, dtype, (hipStream_t)stream);
+        if (e) return hip_status(e);
+    }
+    if (weights) {
+        gs::GatedParams p = {};
+        p.m0 = da;
+        p.m1 = db;
+        p.n0 = X;
+        p.n1 = X;
+        p.out0 = dWg;
+        p.out1 = dWu;
+        p.m_stride = padded;
+        p.n_stride = x_stride;
+        p.out_stride = width;
+        p.m = (int)hidden;
+        p.n = (int)width;
+        p.k = (int)rows;
+        p.m_mode = load_mode(dtype, da, db, padded, padded);
+        p.n_mode = load_mode(dtype, X, X, width, x_stride);
+        p.out_vec = rows_vec(dtype, dWg, width) && aligned(dWu, 16);
+        p.partial = gs::gated_partial_floats(gs::kGatedWeights, dtype, hidden, width, rows) > 0 ? partial : nullptr;
+        return hip_status(gs::launch_gated(p, gs::kGatedWeights, dtype, (hipStream_t)stream));
+    }
+    return GS_OK;
+}
+
+int gs_residual_norm(const gs_residual_norm_desc *desc, const void *X, const void *branch, const void *gate,
+                     const void *post_scale, const void *post_bias, const void *pre_scale, const void *pre_bias,
+                     void *H, void *Y, float *stats, void *stream) {
+    gs::JoinParams p;
+    const int rc = join_setup(desc, false, p);
+    if (rc != GS_OK) return rc;
+    if (p.rows == 0) return GS_OK;
+    if (!X || !branch || !H || (desc->gate_rows > 0 && !gate) || (pre_scale && !Y) || (post_bias && !post_scale) ||
+        (pre_bias && !pre_scale))
+        return GS_ERR_NULL;
+    p.x = X;
+    p.branch = branch;
+    p.gate = desc->gate_rows > 0 ? gate : nullptr;
+    p.post = post_scale;
+    p.post_bias = post_bias;
+    p.pre = pre_scale;
+    p.pre_bias = pre_bias;
+    p.h = H;
+    p.y = Y;
+    p.stats = stats;
+    if (!aligned(stats, 16)) return GS_ERR_ATTR;
+    const int epc = 16 / dtype_bytes(desc->dtype);
+    const void *const v[] = {X, branch, p.gate, post_scale, post_bias, pre_scale, pre_bias, H, Y};
+    p.vec = p.cols % 8 == 0 && p.x_stride % epc == 0 && p.branch_stride % epc == 0 && p.h_stride % epc == 0 &&
+            p.y_stride % epc == 0 && all_aligned(v, 9);
+    return hip_status(gs::launch_residual_norm(p, desc->dtype, (hipStream_t)stream));
+}
+
+int gs_residual_norm_backward_workspace_size(const gs_residual_norm_desc *desc, int64_t *bytes) {
+    if (!bytes) return GS_ERR_NULL;
+    gs::JoinParams p;
+    const int rc = join_setup(desc, true, p);
+    if (rc != GS_OK) return rc;
+    // four parameters' sums, and the gate's where its rows are cut into parts
+    const gs::JoinPlan plan = gs::plan_residual_norm(p.rows, p.cols, desc->gate_rows);
+    *bytes = round_ws((int64_t)plan.blocks * 5 * p.cols * 4);
+    return GS_OK;
+}
+
+int gs_residual_norm_backward(const gs_residual_norm_desc *desc, const void *dH, const void *dY, const void *X,
+                              const void *branch, const void *gate, const void *post_scale, const void *post_bias,
+                              const void *pre_scale, const float *stats, void *dX, void *dbranch, void *dgate,
+                              void *dpost_scale, void *dpost_bias, void *dpre_scale, void *dpre_bias, void *workspace,
+                              int64_t workspace_bytes, void *stream) {
+    gs::JoinParams p;
+    const int rc = join_setup(desc, true, p);
+    if (rc != GS_OK) return rc;
+    if (workspace_bytes < 0) return GS_ERR_ATTR;
+    if ((post_bias && !post_scale) || (!post_scale && (dpost_scale || dpost_bias)) ||
+        (!pre_scale && (dpre_scale || dpre_bias)) || (desc->gate_rows == 0 && dgate))
+        return GS_ERR_NULL;
+    if (p.cols == 0) return GS_OK;
+    if (p.rows > 0 && (!X || !branch || !stats || !dX || !dbranch || (desc->gate_rows > 0 && !gate) || (pre_scale && !dY)))
+        return GS_ERR_NULL;
+    if (!aligned(stats, 16)) return GS_ERR_ATTR;
+    const gs::JoinPlan plan = gs::plan_residual_norm(p.rows, p.cols, desc->gate_rows);
+    p.groups = plan.groups;
+    p.span = plan.span;
+    p.parts = plan.parts;
+    p.blocks = plan.blocks;
+    p.by_token = plan.by_token;
+    const int params = (dpost_scale != nullptr) + (dpost_bias != nullptr) + (dpre_scale != nullptr) + (dpre_bias != nullptr);
+    p.vectors = params + (dgate && !p.by_token && p.parts > 1);
+    const int64_t need = (int64_t)p.blocks * p.vectors * p.cols * 4;
+    if (need > 0) {
+        if (!workspace) return GS_ERR_NULL;
+        if (workspace_bytes < need || (uintptr_t)workspace % kWsAlign) return GS_ERR_ATTR;
+    }
+    if (p.rows == 0 && params == 0) return GS_OK;
+    p.x = X;
+    p.branch = branch;
+    p.gate = desc->gate_rows > 0 ? gate : nullptr;
+    p.post = post_scale;
+    p.post_bias = post_bias;
+    p.pre = pre_scale;
+    p.stats = const_cast<float *>(stats);
+    p.d_h = dH;
+    p.d_y = dY;
+    p.dx = dX;
+    p.dbranch = dbranch;
+    p.dgate = dgate;
+    p.dpost = dpost_scale;
+    p.dpost_bias = dpost_bias;
+    p.dpre = dpre_scale;
+    p.dpre_bias = dpre_bias;
+    p.partial = (float *)workspace;
+    const int epc = 16 / dtype_bytes(desc->dtype);
+    const void *const v[] = {X, branch, p.gate, post_scale, post_bias, pre_scale, dH, dY, dX, dbranch, dgate};
+    p.vec = p.cols % 8 == 0 && p.x_stride % epc == 0 && p.branch_stride % epc == 0 && p.dh_stride % epc == 0 &&
+            p.dy_stride % epc == 0 && p.dx_stride % epc == 0 && p.dbranch_stride % epc == 0 && all_aligned(v, 11);
+    return hip_status(gs::launch_residual_norm_backward(p, desc->dtype, (hipStream_t)stream));
+}
+
+int gs_gated_recurrence_workspace_size(const gs_recurrence_desc *desc, int64_t *bytes) {
+    if (!bytes) return GS_ERR_NULL;
+    gs::ScanParams p;
+    const int rc = scan_setup(desc, false, p);
+    if (rc != GS_OK) return rc;
+    *bytes = scan_space(p);
+    return GS_OK;
+}
+
+int gs_gated_recurrence(const gs_recurrence_desc *desc, const void *X, const void *G, const float *state,
+                        const int32_t *lengths, void *Y, float *last, float *saved, void *workspace,
+                        int64_t workspace_bytes, void *stream) {
+    gs::ScanParams p;
+    const int rc = scan_setup(desc, false, p);
+    if (rc != GS_OK) return rc;
+    if (bad_workspace(workspace, workspace_bytes)) return GS_ERR_ATTR;
+    if (p.batch == 0 || p.channels == 0) return GS_OK;
+    if (p.length > 0 && (!X || !G || !Y)) return GS_ERR_NULL;
+    p.x = X;
+    p.g = G;
+    p.y = Y;
+    p.state = state;
+    p.lengths = lengths;
+    p.last = last;
+    p.saved = saved;
+    const int pair = 2 * dtype_bytes(desc->dtype);
+    p.pairwise = p.pairwise && aligned(X, pair) && aligned(G, pair) && aligned(Y, pair);
+    scan_split(p, workspace, workspace_bytes);
+    return hip_status(gs::launch_recurrence(p, desc->dtype, false, (hipStream_t)stream));
+}
+
+int gs_gated_recurrence_backward_workspace_size(const gs_recurrence_desc *desc, int64_t *bytes) {
+    if (!bytes) return GS_ERR_NULL;
+    gs::ScanParams p;
+    const int rc = scan_setup(desc, true, p);
+    if (rc != GS_OK) return rc;
+    *bytes = scan_space(p);
+    return GS_OK;
+}
+
+int gs_gated_recurrence_backward(const gs_recurrence_desc *desc, const void *dY, const void *X, const void *G,
+                                 const float *saved, const float *dlast, const int32_t *lengths, void *dX, void *dG,
+                                 float *dstate, void *workspace, int64_t workspace_bytes, void *stream) {
+    gs::ScanParams p;
+    const int rc = scan_setup(desc, true, p);
+    if (rc != GS_OK) return rc;
+    if (bad_workspace(workspace, workspace_bytes)) return GS_ERR_ATTR;
+    if (p.batch == 0 || p.channels == 0) return GS_OK;
+    if (p.length > 0 && (!dY || !X || !G || !saved || !dX || !dG)) return GS_ERR_NULL;
+    p.dy = dY;
+    p.x = X;
+    p.g = G;
+    p.saved = const_cast<float *>(saved);
+    p.dlast = dlast;
+    p.lengths = lengths;
+    p.dx = dX;
+    p.dg = dG;
+    p.dstate = dstate;
+    const int pair = 2 * dtype_bytes(desc->dtype);
+    p.pairwise = p.pairwise && aligned(X, pair) && aligned(G, pair) && aligned(dY, pair) && aligned(dX, pair) &&
+                 aligned(dG, pair);
+    scan_split(p, workspace, workspace_bytes);
+    return hip_status(gs::launch_recurrence(p, desc->dtype, true, (hipStream_t)stream));
+}
+
+}  // extern "C"

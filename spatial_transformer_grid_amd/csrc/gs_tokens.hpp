@@ -1,6 +1,7 @@
 // gs_tokens.hpp -- shared parts of the token operators (layer norm, dropout,
-// attention): launch parameters, the counter-based generator, 8-element
-// fragments of the matrix cores.
+// attention, gated projections, norms around a block, the gated recurrence):
+// launch parameters, the counter-based generator, 8-element fragments of the
+// matrix cores.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -73,6 +74,63 @@ struct AttnPlan {
 AttnPlan plan_forward(const AttnParams &p, int dtype, bool workspace);
 AttnPlan plan_backward_q(const AttnParams &p, int dtype);
 AttnPlan plan_backward_kv(const AttnParams &p, int dtype);
+
+// One product of the gated projections, out[m][n] = sum over k of M(m, k) N(n, k),
+// or its elementwise step (see gs_gated.hip).  kGatedForward: m rows, n hidden
+// units, k the width; kGatedInput: m rows, n the width, k the hidden units;
+// kGatedWeights: m hidden units, n the width, k rows; kGatedGradients: m rows,
+// n hidden units.
+enum { kGatedForward = 0, kGatedInput = 1, kGatedWeights = 2, kGatedGradients = 3 };
+struct GatedParams {
+    const void *m0, *m1, *n0, *n1, *dy;
+    void *out0, *out1;
+    float *saved;             // a, b: two planes of rows x hidden
+    float *partial;           // sums of the parts of k; null: k is not cut
+    int64_t m_stride, n_stride, out_stride, dy_stride;
+    int m, n, k;
+    int m_mode, n_mode;       // how tiles of the operands are loaded: by 16 bytes, by 4, by element
+    int out_vec, saved_vec;   // rows of out (of dy) and of `saved` allow 16-byte accesses
+    int activation;
+    int tiles_m, tiles_n, parts, blocks;
+};
+int64_t gated_partial_floats(int mode, int dtype, int64_t m, int64_t n, int64_t k);
+int64_t gated_blocks(int mode, int dtype, int64_t m, int64_t n, int64_t k);
+int launch_gated(const GatedParams &p, int mode, int dtype, hipStream_t stream);
+
+struct JoinParams {
+    const void *x, *branch, *gate, *post, *post_bias, *pre, *pre_bias, *d_h, *d_y;
+    void *h, *y, *dx, *dbranch, *dgate, *dpost, *dpost_bias, *dpre, *dpre_bias;
+    float *stats;             // (rows, 4): mean and factor of the branch, then of H
+    float *partial;           // backward: (blocks, vectors, cols) sums
+    int64_t rows, x_stride, branch_stride, h_stride, y_stride, dh_stride, dy_stride, dx_stride, dbranch_stride;
+    int64_t group;            // rows that share a row of the gate
+    int64_t groups, span;     // backward: groups of `span` rows, each cut into `parts`
+    int cols, layer, param_f32, gate_f32, by_token, vec;
+    int parts, blocks, vectors;
+    float epsilon, alpha;
+};
+struct JoinPlan {
+    int64_t groups, span;
+    int parts, blocks, by_token;
+};
+JoinPlan plan_residual_norm(int64_t rows, int64_t cols, int64_t gate_rows);
+int launch_residual_norm(const JoinParams &p, int dtype, hipStream_t stream);
+int launch_residual_norm_backward(const JoinParams &p, int dtype, hipStream_t stream);
+
+struct ScanParams {
+    const void *x, *g, *dy;
+    void *y, *dx, *dg;
+    const float *state, *dlast;
+    float *last, *dstate, *saved;
+    const int32_t *lengths;
+    float *pairs;             // (parts, 2, batch, channels): product of the gates, state from zero
+    float *copy;              // (batch, channels): the state, or its gradient, that the call was given
+    int64_t xs[2], gs[2], ys[2], dys[2], dxs[2], dgs[2];
+    int batch, length, channels, parts;
+    int pairwise;             // a lane has two channels
+};
+int recurrence_parts(int64_t batch, int64_t length, int64_t channels, bool pairwise);
+int launch_recurrence(const ScanParams &p, int dtype, bool backward, hipStream_t stream);
 
 // Launchers; 0 or the hipError_t of the launch.  `dtype` 0 f32, 1 f16, 2 bf16.
 int launch_layer_norm(const NormParams &p, int dtype, hipStream_t stream);
