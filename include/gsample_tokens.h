@@ -389,7 +389,7 @@ int gs_residual_norm_backward_workspace_size(const gs_residual_norm_desc *desc, 
  * --------------------------------------------------------------------- */
 
 /* Steps between two states that gs_gated_recurrence saves. */
-#define GS_RECURRENCE_CHUNK 128
+#define GS_RECURRENCE_CHUNK 64
 
 /*
  * One call.  Element (b, t, c) of a tensor with strides s lies at
@@ -430,8 +430,8 @@ typedef struct {
  * one of Y below channels along an axis of more than one element),
  * GS_ERR_DTYPE, GS_ERR_ATTR (a workspace that is misaligned or of negative
  * size), GS_ERR_TOO_LARGE (length or channels above 2^29, batch * channels
- * above 2^30, 2^22 thread blocks or more: one has 64 or 128 channels of a
- * sequence), GS_ERR_HIP.
+ * above 2^30, tokens 2^25 bytes or more apart, 2^22 thread blocks or more: one
+ * has eight channels of a sequence at least), GS_ERR_HIP.
  */
 int gs_gated_recurrence(const gs_recurrence_desc *desc, const void *X, const void *G, const float *state,
                         const int32_t *lengths, void *Y, float *last, float *saved, void *workspace,

@@ -21,7 +21,7 @@ __all__ = ["gated_linear", "gated_linear_backward", "residual_norm", "residual_n
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 NORMS = {"rms": 0, "layer": 1}
-RECURRENCE_CHUNK = 128  # GS_RECURRENCE_CHUNK
+RECURRENCE_CHUNK = 64  # GS_RECURRENCE_CHUNK
 
 _S2 = _I64 * 2
 

@@ -132,8 +132,14 @@ int scan_setup(const gs_recurrence_desc *d, bool backward, gs::ScanParams &p) {
     for (int i = 0; i < (backward ? 3 : 2); ++i)
         if (in[i][0] < 0 || in[i][1] < 0) return GS_ERR_SHAPE;
     if (d->length > (int64_t(1) << 29) || d->channels > (int64_t(1) << 29) || d->batch > (int64_t(1) << 30) ||
-        d->batch * d->channels > (int64_t(1) << 30) || d->batch * ((d->channels + 63) / 64) >= kMaxBlocks)
+        d->batch * d->channels > (int64_t(1) << 30) || d->batch * ((d->channels + 7) / 8) >= kMaxBlocks)
         return GS_ERR_TOO_LARGE;
+    // a wave reaches the 64 steps it has at most by a 32-bit offset
+    const int64_t furthest = (int64_t(1) << 25) / dtype_bytes(d->dtype);
+    for (int i = 0; i < (backward ? 3 : 2); ++i)
+        if (d->length > 1 && in[i][1] >= furthest) return GS_ERR_TOO_LARGE;
+    for (int i = 0; i < (backward ? 2 : 1); ++i)
+        if (d->length > 1 && (backward ? bwd[i] : fwd[i])[1] >= furthest) return GS_ERR_TOO_LARGE;
     p = gs::ScanParams{};
     p.pairwise = d->channels % 2 == 0;
     for (int i = 0; i < (backward ? 2 : 1); ++i) {
@@ -166,15 +172,21 @@ int64_t scan_bytes(const gs::ScanParams &p, int parts) {
 
 // The workspace is the same whether two channels share a lane or not, so that it
 // does not depend on pointers: as many as the larger of both.
-int64_t scan_space(const gs::ScanParams &p) {
-    const int64_t one = scan_bytes(p, gs::recurrence_parts(p.batch, p.length, p.channels, false));
-    const int64_t two = scan_bytes(p, gs::recurrence_parts(p.batch, p.length, p.channels, true));
-    return one > two ? one : two;
+int64_t scan_space(const gs::ScanParams &p, bool backward) {
+    int64_t most = 0;
+    for (int pairwise = 0; pairwise < 2; ++pairwise) {
+        const int64_t n = scan_bytes(p, gs::plan_recurrence(p.batch, p.length, p.channels, pairwise, backward, true).parts);
+        if (n > most) most = n;
+    }
+    return most;
 }
 
-void scan_split(gs::ScanParams &p, void *workspace, int64_t bytes) {
-    p.parts = gs::recurrence_parts(p.batch, p.length, p.channels, p.pairwise != 0);
-    if (!workspace || bytes < scan_bytes(p, p.parts)) p.parts = 1;
+void scan_split(gs::ScanParams &p, bool backward, void *workspace, int64_t bytes) {
+    gs::ScanPlan plan = gs::plan_recurrence(p.batch, p.length, p.channels, p.pairwise != 0, backward, workspace != nullptr);
+    if (bytes < scan_bytes(p, plan.parts))
+        plan = gs::plan_recurrence(p.batch, p.length, p.channels, p.pairwise != 0, backward, false);
+    p.parts = plan.parts;
+    p.lanes = plan.lanes;
     p.copy = (float *)workspace;
     p.pairs = p.copy ? p.copy + (int64_t)p.batch * p.channels : nullptr;
 }
@@ -408,7 +420,7 @@ int gs_gated_recurrence_workspace_size(const gs_recurrence_desc *desc, int64_t *
     gs::ScanParams p;
     const int rc = scan_setup(desc, false, p);
     if (rc != GS_OK) return rc;
-    *bytes = scan_space(p);
+    *bytes = scan_space(p, false);
     return GS_OK;
 }
 
@@ -430,7 +442,7 @@ int gs_gated_recurrence(const gs_recurrence_desc *desc, const void *X, const voi
     p.saved = saved;
     const int pair = 2 * dtype_bytes(desc->dtype);
     p.pairwise = p.pairwise && aligned(X, pair) && aligned(G, pair) && aligned(Y, pair);
-    scan_split(p, workspace, workspace_bytes);
+    scan_split(p, false, workspace, workspace_bytes);
     return hip_status(gs::launch_recurrence(p, desc->dtype, false, (hipStream_t)stream));
 }
 
@@ -439,7 +451,7 @@ int gs_gated_recurrence_backward_workspace_size(const gs_recurrence_desc *desc, 
     gs::ScanParams p;
     const int rc = scan_setup(desc, true, p);
     if (rc != GS_OK) return rc;
-    *bytes = scan_space(p);
+    *bytes = scan_space(p, true);
     return GS_OK;
 }
 
@@ -464,7 +476,7 @@ int gs_gated_recurrence_backward(const gs_recurrence_desc *desc, const void *dY,
     const int pair = 2 * dtype_bytes(desc->dtype);
     p.pairwise = p.pairwise && aligned(X, pair) && aligned(G, pair) && aligned(dY, pair) && aligned(dX, pair) &&
                  aligned(dG, pair);
-    scan_split(p, workspace, workspace_bytes);
+    scan_split(p, true, workspace, workspace_bytes);
     return hip_status(gs::launch_recurrence(p, desc->dtype, true, (hipStream_t)stream));
 }
 

@@ -2,34 +2,36 @@
 // backward:  h_t = a_t h_(t-1) + (1 - a_t) x_t,  a_t = 1 / (1 + exp(-g_t)).
 //
 // n steps are one step with the product of their a and the state that they
-// reach from zero.  A block has 64 lanes of channels and W waves of S steps
-// each: every wave makes its steps' pair from the registers that hold them, the
-// pairs go through LDS, each wave folds those before its own onto the state that
-// the tile began at, and walks its steps again from there: everything is read
-// once.  The order of the folds is fixed, so the same call gives the same bits.
+// reach from zero.  A wave's 64 lanes are CL lanes of V channels each by 64 / CL
+// runs of S neighbouring steps, and a block has W waves, one after another along
+// the tokens.  Every lane makes its run's pair from the registers that hold it;
+// the pairs are folded over a wave's runs by exchanges between lanes and over
+// the waves through LDS, and each lane walks its run again from the state that
+// it begins at: everything is read once.  The order of the folds is fixed, so the
+// same call gives the same bits.
 //
 // Backward: U_t = a_t D_t, the gradient that leaves step t towards h_(t-1), is
 // the same recurrence the other way, U_t = a_t (dY_t + U_(t+1)).  The states are
-// made again, a tile at a time, from those that the forward pass saved before
-// every tile (a state a channel for kTile steps), in fp32: the rounded Y would
-// carry its rounding into dG where h and x are close.
+// made again from those that the forward pass saved before every kChunk steps,
+// in fp32: the rounded Y would carry its rounding into dG where h and x are close.
 //
-// Where there are too few channels for the chip, the tokens are split in parts
-// over blocks: a first kernel makes each part's pair, and the blocks of the
-// second one fold the pairs of the parts before theirs.
+// Where there are too few channels for the chip even with few lanes a run, the
+// tokens are split in parts over blocks: a first kernel makes each part's pair,
+// and the blocks of the second one fold the pairs of the parts before theirs.
 #include "gs_tokens.hpp"
 
 namespace gs {
 
 namespace {
 
-constexpr int kTile = 128;             // steps of a tile: of a saved state
+constexpr int kChunk = 64;             // steps between two saved states
 constexpr int kMaxParts = 256;
 
 // a and 1 - a of a gate, neither from the other: both keep their relative
 // precision.  e = exp(-|g|) is made in base 2, where fp32's product g log2(e)
-// is rounded; with CORRECT (fp32 data) its remainder is put back.  The reciprocal
-// takes one Newton step, since the error of a product of many a adds up.
+// is rounded.  With CORRECT (fp32 data) its remainder is put back, and the
+// reciprocal, good to a unit of its last place, takes one Newton step, since the
+// error of a product of many a adds up.
 template <bool CORRECT>
 __device__ __forceinline__ void gate_of(float g, float &a, float &rest) {
     const float n = -fabsf(g), z = n * kLog2e;
@@ -38,78 +40,99 @@ __device__ __forceinline__ void gate_of(float g, float &a, float &rest) {
         const float low = fmaf(n, 1.925963033500801e-8f, fmaf(n, kLog2e, -z));
         e = z > -120.0f ? fmaf(e * kLn2, low, e) : e;
     }
-    const float d = 1.0f + e, r0 = __builtin_amdgcn_rcpf(d), r = fmaf(fmaf(-d, r0, 1.0f), r0, r0), er = e * r;
+    const float d = 1.0f + e;
+    float r = __builtin_amdgcn_rcpf(d);
+    if constexpr (CORRECT) r = fmaf(fmaf(-d, r, 1.0f), r, r);
+    const float er = e * r;
     a = g < 0.0f ? er : r;
     rest = g < 0.0f ? r : er;
 }
 
-// V neighbouring channels of a step, as they lie in memory.
+// V neighbouring channels of a step, as they lie in memory: 2, 4 or 8 bytes.
+template <int BYTES> struct Packed;
+template <> struct Packed<2> { typedef uint16_t type; };
+template <> struct Packed<4> { typedef uint32_t type; };
+template <> struct Packed<8> { typedef uint64_t type; };
 template <typename T, int V>
-struct Raw {
-    typename T::raw_t v[V];
+using raw_of = typename Packed<V * T::bytes>::type;
+
+template <typename T, int V>
+__device__ __forceinline__ float channel(raw_of<T, V> r, int j) {
+    return T::from_raw((typename T::raw_t)(r >> (8 * T::bytes * j)));
+}
+
+// A wave's steps of a tensor: `base` its first step, a lane's run and channels
+// `at` bytes from there, its steps `step` bytes apart.  `room` is the number of
+// the lane's steps before the end: a step past it takes an offset that is out of
+// range, by the sign of what is left, and so reads 0 or is dropped.  No branch
+// surrounds an access, so that the loads of the next tile are waited for by their
+// number and not together with the stores behind them.
+template <typename T, int V>
+struct Steps {
+    rsrc_t rsrc;
+    int step;
+    __device__ __forceinline__ Steps(const void *base, int64_t elements, int64_t stride)
+        : rsrc(__builtin_amdgcn_make_buffer_rsrc((void *)((const typename T::raw_t *)base + elements), 0, 0x7fffffff,
+                                                 kRsrcWord3)),
+          step((int)stride * T::bytes) {}
+    __device__ __forceinline__ static uint32_t held(uint32_t at, int room, int i) {
+        return at | ((uint32_t)(room - 1 - i) & GS_OOB);
+    }
+    __device__ __forceinline__ raw_of<T, V> load(uint32_t at, int room, int i) const {
+        at = held(at, room, i);
+        if constexpr (V * T::bytes == 2) return __builtin_amdgcn_raw_buffer_load_b16(rsrc, (int)at, i * step, 0);
+        else if constexpr (V * T::bytes == 4) return __builtin_amdgcn_raw_buffer_load_b32(rsrc, (int)at, i * step, 0);
+        else return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(rsrc, (int)at, i * step, 0));
+    }
+    // zeros from step `full` on
+    __device__ __forceinline__ void store(const float *v, uint32_t at, int room, int full, int i) const {
+        at = held(at, room, i);
+        raw_of<T, V> r = to_bits<T>(v[0]);
+        if constexpr (V == 2) r |= (raw_of<T, V>)to_bits<T>(v[1]) << (8 * T::bytes);
+        r &= (raw_of<T, V>)(int64_t)((i - full) >> 31);
+        if constexpr (V * T::bytes == 2) __builtin_amdgcn_raw_buffer_store_b16(r, rsrc, (int)at, i * step, 0);
+        else if constexpr (V * T::bytes == 4) __builtin_amdgcn_raw_buffer_store_b32(r, rsrc, (int)at, i * step, 0);
+        else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, r), rsrc, (int)at, i * step, 0);
+    }
 };
-
-template <typename T, int V>
-__device__ __forceinline__ Raw<T, V> load_raw(const typename T::raw_t *src) {
-    Raw<T, V> r;
-    if constexpr (V * T::bytes == 2) r.v[0] = src[0];
-    else if constexpr (V * T::bytes == 4) __builtin_memcpy(&r, (const uint32_t *)src, 4);
-    else {
-        const u32x2 w = *(const u32x2 *)src;
-        __builtin_memcpy(&r, &w, 8);
-    }
-    return r;
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void store_raw(typename T::raw_t *dst, const float *v) {
-    Raw<T, V> r;
-#pragma unroll
-    for (int i = 0; i < V; ++i) r.v[i] = to_bits<T>(v[i]);
-    if constexpr (V * T::bytes == 2) dst[0] = r.v[0];
-    else if constexpr (V * T::bytes == 4) {
-        uint32_t w;
-        __builtin_memcpy(&w, &r, 4);
-        *(uint32_t *)dst = w;
-    } else {
-        u32x2 w;
-        __builtin_memcpy(&w, &r, 8);
-        *(u32x2 *)dst = w;
-    }
-}
 
 template <int V>
 struct Floats {
     float v[V];
 };
 
-// The sequence, channels and part of a block, and a lane's first channel.
+// The sequence, part and steps of a block, and a lane's first channel.
 struct Place {
     int b, part, c, len;
     bool on;                                         // the lane has channels
     int t0, t1;                                      // steps of the part
+    int run;                                         // the lane's run of a wave's
 };
 
-template <int V>
+template <int V, int CL, int TILE>
 __device__ __forceinline__ Place place(const ScanParams &p) {
     Place s;
-    const int groups = (p.channels + 64 * V - 1) / (64 * V);
-    int n = (int)blockIdx.x;
+    const int groups = (p.channels + CL * V - 1) / (CL * V), lane = threadIdx.x & 63;
+    // Neighbouring channels of a token are read by neighbours of one XCD's L2.
+    const int per = (p.blocks + 7) >> 3;
+    int n = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
+    s.run = lane / CL;
+    s.c = (n % groups * CL + lane % CL) * V;
+    n /= groups;
     s.part = n % p.parts;
-    n /= p.parts;
-    s.c = (n % groups * 64 + (int)(threadIdx.x & 63)) * V;
-    s.b = n / groups;
-    s.on = s.c < p.channels;
+    s.b = n / p.parts;
+    s.on = s.c < p.channels && s.b < p.batch;
+    s.b = min(s.b, p.batch - 1);                     // (a block past the last one does nothing that is seen)
     s.len = p.lengths ? min(max(p.lengths[s.b], 0), p.length) : p.length;
-    const int tiles = (p.length + kTile - 1) / kTile;
-    s.t0 = (int)((int64_t)tiles * s.part / p.parts) * kTile;
-    s.t1 = min((int)((int64_t)tiles * (s.part + 1) / p.parts) * kTile, p.length);
+    const int tiles = (p.length + TILE - 1) / TILE;
+    s.t0 = (int)((int64_t)tiles * s.part / p.parts) * TILE;
+    s.t1 = min((int)((int64_t)tiles * (s.part + 1) / p.parts) * TILE, p.length);
     return s;
 }
 
-// The state (or gradient) that a part begins at: `first` through the pairs of
-// the parts before it, in the order that `from` and `step` say, a range of them
-// a wave.  All of a block's threads take part.
+// The state (or gradient) that a part begins at: 0 through the pairs of the parts
+// before it, in the order that `from` and `step` say, a range of them a wave.
+// All of a block's threads take part.
 template <int V, int W>
 __device__ __forceinline__ void fold_parts(const ScanParams &p, const Place &s, int count, int from, int step, float *u,
                                            Floats<V> (*lds)[2][64]) {
@@ -137,6 +160,7 @@ __device__ __forceinline__ void fold_parts(const ScanParams &p, const Place &s, 
     for (int i = 0; i < V; ++i) {
         lds[wave][0][lane].v[i] = P[i];
         lds[wave][1][lane].v[i] = H[i];
+        u[i] = 0.0f;
     }
     __syncthreads();
 #pragma unroll 1
@@ -158,111 +182,152 @@ __device__ __forceinline__ void store_state(float *dst, int64_t at, const float 
     for (int i = 0; i < V; ++i) dst[at + i] = u[i];
 }
 
+// Pairs of a wave's runs, folded: P and H become those of the lane's run and the
+// ones before it (BACK: after it), and P1, H1 those without its own (1 and 0
+// where there is none).
+template <int V, int CL, bool BACK>
+__device__ __forceinline__ void fold_runs(int run, float *P, float *H, float *P1, float *H1) {
+    constexpr int RUNS = 64 / CL;
+    const int lane = threadIdx.x & 63;
+    const int place = BACK ? RUNS - 1 - run : run;
+#pragma unroll
+    for (int d = 1; d < RUNS; d <<= 1) {
+        const int from = BACK ? lane + d * CL : lane - d * CL;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float p = __shfl(P[j], from & 63), h = __shfl(H[j], from & 63);
+            if (place >= d) {
+                H[j] = fmaf(P[j], h, H[j]);
+                P[j] *= p;
+            }
+        }
+    }
+    const int from = (BACK ? lane + CL : lane - CL) & 63;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        P1[j] = H1[j] = 0.0f;
+        if constexpr (RUNS > 1) {
+            P1[j] = __shfl(P[j], from);
+            H1[j] = __shfl(H[j], from);
+        }
+        if (place == 0) {
+            P1[j] = 1.0f;
+            H1[j] = 0.0f;
+        }
+    }
+}
+
 // Forward.  PAIRS: only the part's pair (the product of its gates, the state that
 // it reaches) goes to the workspace; part 0 begins at the given state, which is
 // copied, since the other kernel may write the last state over it.
-template <typename T, int V, int W, bool PAIRS>
+template <typename T, int V, int CL, int W, int S, bool PAIRS>
 __global__ __launch_bounds__(64 * W) void recurrence_forward(ScanParams p) {
-    typedef typename T::raw_t raw_t;
-    constexpr int S = kTile / W;
+    constexpr int RUNS = 64 / CL, WAVE = RUNS * S, TILE = W * WAVE;   // steps of a wave and of a tile
+    static_assert(TILE % kChunk == 0 && kChunk % WAVE == 0, "a wave's steps lie in one chunk");
     __shared__ Floats<V> lds[2][W][2][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Place s = place<V>(p);
+    const Place s = place<V, CL, TILE>(p);
     if (PAIRS && s.part == p.parts - 1) return;      // nothing follows it
     const int64_t width = (int64_t)p.batch * p.channels, at = (int64_t)s.b * p.channels + s.c;
     float u[V], product[V];
     const bool split = p.parts > 1;
     load_state<V>(!PAIRS && split ? p.copy : (s.part == 0 ? p.state : nullptr), s, p.channels, u);
-    if (PAIRS && s.part == 0 && wave == 0 && s.on) store_state<V>(p.copy, at, u);
-    if (!PAIRS && split) {
-        // part 0's pair holds the first state already
-        float first[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            first[i] = u[i];
-            u[i] = 0.0f;
-        }
-        fold_parts<V, W>(p, s, s.part, 0, 1, u, lds[0]);
-        if (s.part == 0)
-#pragma unroll
-            for (int i = 0; i < V; ++i) u[i] = first[i];
-    }
+    if (PAIRS && s.part == 0 && wave == 0 && s.run == 0 && s.on) store_state<V>(p.copy, at, u);
+    if (!PAIRS && s.part > 0) fold_parts<V, W>(p, s, s.part, 0, 1, u, lds[0]);  // part 0's pair holds the first state
 #pragma unroll
     for (int i = 0; i < V; ++i) product[i] = 1.0f;
-    const raw_t *const x = (const raw_t *)p.x + (int64_t)s.b * p.xs[0] + s.c;
-    const raw_t *const g = (const raw_t *)p.g + (int64_t)s.b * p.gs[0] + s.c;
-    raw_t *const y = (raw_t *)p.y + (int64_t)s.b * p.ys[0] + s.c;
-    const int chunks = (p.length + kTile - 1) / kTile;
+    const int own = s.run * S;                       // first step of the lane's run in its wave's
+    const auto lane_at = [&](int64_t stride) { return s.on ? (uint32_t)(own * (int)stride + s.c) * T::bytes : GS_OOB; };
+    const uint32_t xat = lane_at(p.xs[1]), gat = lane_at(p.gs[1]), yat = lane_at(p.ys[1]);
+    const int chunks = (p.length + kChunk - 1) / kChunk, held = min(s.len, s.t1);
     int turn = 0;
-    Raw<T, V> xr[S], gr[S];
+    raw_of<T, V> xn[S], gn[S];
     const auto fetch = [&](int t0) {
+        t0 += wave * WAVE;
+        const Steps<T, V> x(p.x, s.b * p.xs[0] + t0 * p.xs[1], p.xs[1]), g(p.g, s.b * p.gs[0] + t0 * p.gs[1], p.gs[1]);
+        const int room = held - t0 - own;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            const int t = t0 + wave * S + i;
-            xr[i] = gr[i] = Raw<T, V>{};
-            if (t < s.len && t < s.t1 && s.on) {
-                xr[i] = load_raw<T, V>(x + t * p.xs[1]);
-                gr[i] = load_raw<T, V>(g + t * p.gs[1]);
-            }
+            xn[i] = x.load(xat, room, i);
+            gn[i] = g.load(gat, room, i);
         }
     };
     fetch(s.t0);
-    for (int t0 = s.t0; t0 < s.t1; t0 += kTile) {
-        float a[S][V], b[S][V], P[V], H[V];
+    for (int t0 = s.t0; t0 < s.t1; t0 += TILE) {
+        const int t = t0 + wave * WAVE;              // the wave's first step
+        float a[S][V], b[S][V], P[V], H[V], P1[V], H1[V];
+        raw_of<T, V> xr[S], gr[S];
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            xr[i] = xn[i];
+            gr[i] = gn[i];
+        }
+        fetch(t0 + TILE);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             P[i] = 1.0f;
             H[i] = 0.0f;
         }
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-            const bool held = t0 + wave * S + i < s.len;
+        for (int i = 0; i < S; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 float rest;
-                gate_of<T::bytes == 4>(T::from_raw(gr[i].v[j]), a[i][j], rest);
-                b[i][j] = rest * T::from_raw(xr[i].v[j]);
-                a[i][j] = held ? a[i][j] : 1.0f;     // past its length a sequence keeps its state
-                b[i][j] = held ? b[i][j] : 0.0f;
+                gate_of<T::bytes == 4>(channel<T, V>(gr[i], j), a[i][j], rest);
+                b[i][j] = rest * channel<T, V>(xr[i], j);
+            }
+        if (t + WAVE > held) {                       // past its length a sequence keeps its state
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    a[i][j] = t + own + i < held ? a[i][j] : 1.0f;
+                    b[i][j] = t + own + i < held ? b[i][j] : 0.0f;
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
                 P[j] *= a[i][j];
                 H[j] = fmaf(a[i][j], H[j], b[i][j]);
             }
-        }
-        fetch(t0 + kTile);
+        fold_runs<V, CL, false>(s.run, P, H, P1, H1);
+        if (s.run == RUNS - 1)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            lds[turn][wave][0][lane].v[j] = P[j];
-            lds[turn][wave][1][lane].v[j] = H[j];
-        }
+            for (int j = 0; j < V; ++j) {
+                lds[turn][wave][0][lane % CL].v[j] = P[j];
+                lds[turn][wave][1][lane % CL].v[j] = H[j];
+            }
         __syncthreads();
-        if (!PAIRS && p.saved && wave == 0 && s.on && t0 < s.len)
-            store_state<V>(p.saved, ((int64_t)s.b * chunks + t0 / kTile) * p.channels + s.c, u);
         float h[V];
 #pragma unroll
         for (int w = 0; w < W; ++w)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 if (w == wave) h[j] = u[j];
-                const float q = lds[turn][w][0][lane].v[j];
-                u[j] = fmaf(q, u[j], lds[turn][w][1][lane].v[j]);
+                const float q = lds[turn][w][0][lane % CL].v[j];
+                u[j] = fmaf(q, u[j], lds[turn][w][1][lane % CL].v[j]);
                 if (PAIRS) product[j] *= q;
             }
         turn ^= 1;                                   // the next tile's pairs do not wait for this one's readers
         if constexpr (!PAIRS) {
 #pragma unroll
-            for (int i = 0; i < S; ++i) {
-                const int t = t0 + wave * S + i;
-                float out[V];
+            for (int j = 0; j < V; ++j) h[j] = fmaf(P1[j], h[j], H1[j]);
+            if (p.saved) {                           // (a wave's steps lie in one chunk)
+                const Steps<F32, V> to(p.saved, ((int64_t)s.b * chunks + t / kChunk) * p.channels, 0);
+                to.store(h, s.on && (t + own) % kChunk == 0 ? (uint32_t)s.c * 4 : GS_OOB, s.len - t - own, 1, 0);
+            }
+            const Steps<T, V> y(p.y, s.b * p.ys[0] + t * p.ys[1], p.ys[1]);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    h[j] = fmaf(a[i][j], h[j], b[i][j]);
-                    out[j] = t < s.len ? h[j] : 0.0f;
-                }
-                if (t < s.t1 && s.on) store_raw<T, V>(y + t * p.ys[1], out);
+            for (int i = 0; i < S; ++i) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) h[j] = fmaf(a[i][j], h[j], b[i][j]);
+                y.store(h, yat, s.t1 - t - own, s.len - t - own, i);
             }
         }
     }
-    if (wave || !s.on) return;
+    if (wave || s.run || !s.on) return;
     if (PAIRS) {
         float *pair = p.pairs + (int64_t)s.part * 2 * width;
         store_state<V>(pair, at, product);
@@ -274,91 +339,117 @@ __global__ __launch_bounds__(64 * W) void recurrence_forward(ScanParams p) {
 
 // Backward.  PAIRS: only the part's pair, in the other direction; the last part
 // begins at dlast, which is copied for the same reason.
-template <typename T, int V, int W, bool PAIRS>
+template <typename T, int V, int CL, int W, int S, bool PAIRS>
 __global__ __launch_bounds__(64 * W) void recurrence_backward(ScanParams p) {
-    typedef typename T::raw_t raw_t;
-    constexpr int S = kTile / W, N = PAIRS ? 2 : 3;
-    __shared__ Floats<V> lds[2][W][N][64];
+    constexpr int RUNS = 64 / CL, WAVE = RUNS * S, TILE = W * WAVE;
+    constexpr int TOGETHER = WAVE < kChunk ? kChunk / WAVE : 1;       // waves of a chunk: they share its state
+    static_assert(TILE % kChunk == 0 && WAVE <= kChunk, "a wave's steps lie in one chunk");
+    __shared__ Floats<V> lds[2][W][2][64];
+    __shared__ Floats<V> heads[2][TOGETHER > 1 ? W : 1][2][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Place s = place<V>(p);
+    const Place s = place<V, CL, TILE>(p);
     if (PAIRS && s.part == 0) return;                // nothing follows it
     const int64_t width = (int64_t)p.batch * p.channels, at = (int64_t)s.b * p.channels + s.c;
     const int final_part = p.parts - 1;
     const bool split = p.parts > 1;
     float u[V], product[V];
     load_state<V>(!PAIRS && split ? p.copy : (s.part == final_part ? p.dlast : nullptr), s, p.channels, u);
-    if (PAIRS && s.part == final_part && wave == 0 && s.on) store_state<V>(p.copy, at, u);
-    if (!PAIRS && split) {
-        float first[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            first[i] = u[i];
-            u[i] = 0.0f;
-        }
-        fold_parts<V, W>(p, s, final_part - s.part, final_part, -1, u, (Floats<V>(*)[2][64])lds);
-        if (s.part == final_part)
-#pragma unroll
-            for (int i = 0; i < V; ++i) u[i] = first[i];
-    }
+    if (PAIRS && s.part == final_part && wave == 0 && s.run == 0 && s.on) store_state<V>(p.copy, at, u);
+    if (!PAIRS && s.part < final_part) fold_parts<V, W>(p, s, final_part - s.part, final_part, -1, u, lds[0]);
 #pragma unroll
     for (int i = 0; i < V; ++i) product[i] = 1.0f;
-    const raw_t *const x = (const raw_t *)p.x + (int64_t)s.b * p.xs[0] + s.c;
-    const raw_t *const g = (const raw_t *)p.g + (int64_t)s.b * p.gs[0] + s.c;
-    const raw_t *const dy = (const raw_t *)p.dy + (int64_t)s.b * p.dys[0] + s.c;
-    raw_t *const dx = (raw_t *)p.dx + (int64_t)s.b * p.dxs[0] + s.c;
-    raw_t *const dg = (raw_t *)p.dg + (int64_t)s.b * p.dgs[0] + s.c;
-    const int chunks = (p.length + kTile - 1) / kTile;
+    const int own = s.run * S;
+    const auto lane_at = [&](int64_t stride) { return s.on ? (uint32_t)(own * (int)stride + s.c) * T::bytes : GS_OOB; };
+    const uint32_t xat = lane_at(p.xs[1]), gat = lane_at(p.gs[1]), dyat = lane_at(p.dys[1]), dxat = lane_at(p.dxs[1]),
+                   dgat = lane_at(p.dgs[1]);
+    const int chunks = (p.length + kChunk - 1) / kChunk, held = min(s.len, s.t1);
     int turn = 0;
-    Raw<T, V> xn[S], gn[S], dn[S];
+    raw_of<T, V> xn[S], gn[S], dn[S];
     const auto fetch = [&](int t0) {
+        t0 += wave * WAVE;
+        const Steps<T, V> x(p.x, s.b * p.xs[0] + t0 * p.xs[1], p.xs[1]), g(p.g, s.b * p.gs[0] + t0 * p.gs[1], p.gs[1]);
+        const Steps<T, V> dy(p.dy, s.b * p.dys[0] + t0 * p.dys[1], p.dys[1]);
+        const int room = held - t0 - own;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            const int t = t0 + wave * S + i;
-            xn[i] = gn[i] = dn[i] = Raw<T, V>{};
-            if (t < s.len && t >= s.t0 && t < s.t1 && s.on) {
-                if (!PAIRS) xn[i] = load_raw<T, V>(x + t * p.xs[1]);
-                gn[i] = load_raw<T, V>(g + t * p.gs[1]);
-                dn[i] = load_raw<T, V>(dy + t * p.dys[1]);
-            }
+            if (!PAIRS) xn[i] = x.load(xat, room, i);
+            gn[i] = g.load(gat, room, i);
+            dn[i] = dy.load(dyat, room, i);
         }
     };
-    const int last_tile = s.t1 > s.t0 ? s.t0 + (s.t1 - 1 - s.t0) / kTile * kTile : s.t0 - kTile;
-    fetch(last_tile);
-    for (int t0 = last_tile; t0 >= s.t0; t0 -= kTile) {
-        Raw<T, V> xr[S], dr[S];
-        float a[S][V], rest[S][V], P[V], H[V], U[V], h[V];
-        if (!PAIRS) load_state<V>(p.saved ? p.saved + (int64_t)(t0 / kTile + s.b * (chunks - 1)) * p.channels : nullptr, s,
-                                  p.channels, h);
+    const int tiles = (s.t1 - s.t0 + TILE - 1) / TILE;
+    fetch(tiles > 0 ? s.t0 + (tiles - 1) * TILE : s.t1);   // (at and past t1 nothing is read)
+    for (int n = tiles - 1; n >= 0; --n) {
+        const int t0 = s.t0 + n * TILE;
+        const int t = t0 + wave * WAVE;
+        raw_of<T, V> xr[S], gr[S], dr[S];
+        float a[S][V], rest[S][V], P[V], U[V], P1[V], U1[V], h[V];
+        // the state before the chunk's first step
+        if (!PAIRS) {
+            const Steps<F32, V> from(p.saved, ((int64_t)s.b * chunks + t / kChunk) * p.channels, 0);
+            const raw_of<F32, V> r = from.load(s.on ? (uint32_t)s.c * 4 : GS_OOB, s.len - t, 0);
+#pragma unroll
+            for (int j = 0; j < V; ++j) h[j] = channel<F32, V>(r, j);
+        }
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            xr[i] = xn[i];
+            gr[i] = gn[i];
+            dr[i] = dn[i];
+        }
+        fetch(n > 0 ? t0 - TILE : s.t1);
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) gate_of<T::bytes == 4>(channel<T, V>(gr[i], j), a[i][j], rest[i][j]);
+        if (t + WAVE > held) {
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    a[i][j] = t + own + i < held ? a[i][j] : 1.0f;
+                    rest[i][j] = t + own + i < held ? rest[i][j] : 0.0f;
+                }
+        }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             P[j] = 1.0f;
-            H[j] = U[j] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < S; ++i) {
-            const bool held = t0 + wave * S + i < s.len;
-            xr[i] = xn[i];
-            dr[i] = dn[i];
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                gate_of<T::bytes == 4>(T::from_raw(gn[i].v[j]), a[i][j], rest[i][j]);
-                a[i][j] = held ? a[i][j] : 1.0f;
-                rest[i][j] = held ? rest[i][j] : 0.0f;
-                P[j] *= a[i][j];
-                if (!PAIRS) H[j] = fmaf(a[i][j], H[j], rest[i][j] * T::from_raw(xr[i].v[j]));
-            }
+            U[j] = 0.0f;
         }
 #pragma unroll
         for (int i = S - 1; i >= 0; --i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) U[j] = a[i][j] * (T::from_raw(dr[i].v[j]) + U[j]);
-        fetch(t0 - kTile);
+            for (int j = 0; j < V; ++j) {
+                P[j] *= a[i][j];
+                U[j] = a[i][j] * (channel<T, V>(dr[i], j) + U[j]);
+            }
+        float Q1[V], H1[V];                          // the pair of the wave's runs before this one
+        if constexpr (!PAIRS) {
+            float Q[V], H[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            lds[turn][wave][0][lane].v[j] = P[j];
-            lds[turn][wave][1][lane].v[j] = U[j];
-            if (!PAIRS) lds[turn][wave][N - 1][lane].v[j] = H[j];
+            for (int j = 0; j < V; ++j) {
+                Q[j] = P[j];
+                H[j] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) H[j] = fmaf(a[i][j], H[j], rest[i][j] * channel<T, V>(xr[i], j));
+            fold_runs<V, CL, false>(s.run, Q, H, Q1, H1);
+            if (TOGETHER > 1 && s.run == RUNS - 1)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    heads[turn][wave % W][0][lane % CL].v[j] = Q[j];
+                    heads[turn][wave % W][1][lane % CL].v[j] = H[j];
+                }
         }
+        fold_runs<V, CL, true>(s.run, P, U, P1, U1);
+        if (s.run == 0)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                lds[turn][wave][0][lane % CL].v[j] = P[j];
+                lds[turn][wave][1][lane % CL].v[j] = U[j];
+            }
         __syncthreads();
         float mine[V];
 #pragma unroll
@@ -366,45 +457,52 @@ __global__ __launch_bounds__(64 * W) void recurrence_backward(ScanParams p) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 if (w == wave) mine[j] = u[j];
-                const float q = lds[turn][w][0][lane].v[j];
-                u[j] = fmaf(q, u[j], lds[turn][w][1][lane].v[j]);
+                const float q = lds[turn][w][0][lane % CL].v[j];
+                u[j] = fmaf(q, u[j], lds[turn][w][1][lane % CL].v[j]);
                 if (PAIRS) product[j] *= q;
             }
         if constexpr (!PAIRS) {
+            if constexpr (TOGETHER > 1) {
 #pragma unroll
-            for (int w = 0; w < W - 1; ++w)
+                for (int w = 0; w < TOGETHER - 1; ++w)
+                    if (w < wave % TOGETHER)
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (w < wave) h[j] = fmaf(lds[turn][w][0][lane].v[j], h[j], lds[turn][w][N - 1][lane].v[j]);
+                        for (int j = 0; j < V; ++j)
+                            h[j] = fmaf(heads[turn][wave / TOGETHER * TOGETHER + w][0][lane % CL].v[j], h[j],
+                                        heads[turn][wave / TOGETHER * TOGETHER + w][1][lane % CL].v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                h[j] = fmaf(Q1[j], h[j], H1[j]);
+                mine[j] = fmaf(P1[j], mine[j], U1[j]);
+            }
             float before[S][V];
 #pragma unroll
             for (int i = 0; i < S; ++i)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     before[i][j] = h[j];
-                    h[j] = fmaf(a[i][j], h[j], rest[i][j] * T::from_raw(xr[i].v[j]));
+                    h[j] = fmaf(a[i][j], h[j], rest[i][j] * channel<T, V>(xr[i], j));
                 }
+            const Steps<T, V> dx(p.dx, s.b * p.dxs[0] + t * p.dxs[1], p.dxs[1]);
+            const Steps<T, V> dg(p.dg, s.b * p.dgs[0] + t * p.dgs[1], p.dgs[1]);
 #pragma unroll
             for (int i = S - 1; i >= 0; --i) {
-                const int t = t0 + wave * S + i;
                 float ox[V], og[V];
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float D = T::from_raw(dr[i].v[j]) + mine[j];
-                    const bool held = t < s.len;
-                    ox[j] = held ? rest[i][j] * D : 0.0f;
-                    og[j] = held ? D * (before[i][j] - T::from_raw(xr[i].v[j])) * (a[i][j] * rest[i][j]) : 0.0f;
+                    const float D = channel<T, V>(dr[i], j) + mine[j], d = rest[i][j] * D;
                     mine[j] = a[i][j] * D;
+                    ox[j] = d;
+                    og[j] = mine[j] * rest[i][j] * (before[i][j] - channel<T, V>(xr[i], j));
                 }
-                if (t < s.t1 && s.on) {
-                    store_raw<T, V>(dx + t * p.dxs[1], ox);
-                    store_raw<T, V>(dg + t * p.dgs[1], og);
-                }
+                dx.store(ox, dxat, s.t1 - t - own, s.len - t - own, i);
+                dg.store(og, dgat, s.t1 - t - own, s.len - t - own, i);
             }
         }
         turn ^= 1;
     }
-    if (wave || !s.on) return;
+    if (wave || s.run || !s.on) return;
     if (PAIRS) {
         float *pair = p.pairs + (int64_t)s.part * 2 * width;
         store_state<V>(pair, at, product);
@@ -416,39 +514,68 @@ __global__ __launch_bounds__(64 * W) void recurrence_backward(ScanParams p) {
 
 // --------------------------------------------------------------- launches
 
-constexpr int kWaves = 8, kBackwardWaves = 16;
+constexpr int kWaves = 8, kSteps = 8;
 
-template <typename T, int V>
-int launch(const ScanParams &p, bool backward, hipStream_t stream) {
-    const int64_t units = (int64_t)p.batch * ((p.channels + 64 * V - 1) / (64 * V));
-    const dim3 grid((unsigned)(units * p.parts)), fwd(64 * kWaves), bwd(64 * kBackwardWaves);
+template <typename T, int V, int CL>
+int launch(const ScanParams &q, bool backward, hipStream_t stream) {
+    ScanParams p = q;
+    const int64_t units = (int64_t)p.batch * ((p.channels + CL * V - 1) / (CL * V));
+    p.blocks = (int)(units * p.parts);
+    const dim3 grid((unsigned)((p.blocks + 7) / 8 * 8)), block(64 * kWaves);
     if (p.parts > 1) {
-        if (backward) hipLaunchKernelGGL((recurrence_backward<T, V, kBackwardWaves, true>), grid, bwd, 0, stream, p);
-        else hipLaunchKernelGGL((recurrence_forward<T, V, kWaves, true>), grid, fwd, 0, stream, p);
+        if (backward) hipLaunchKernelGGL((recurrence_backward<T, V, CL, kWaves, kSteps, true>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((recurrence_forward<T, V, CL, kWaves, kSteps, true>), grid, block, 0, stream, p);
         if (const int e = (int)hipGetLastError()) return e;
     }
-    if (backward) hipLaunchKernelGGL((recurrence_backward<T, V, kBackwardWaves, false>), grid, bwd, 0, stream, p);
-    else hipLaunchKernelGGL((recurrence_forward<T, V, kWaves, false>), grid, fwd, 0, stream, p);
+    if (backward) hipLaunchKernelGGL((recurrence_backward<T, V, CL, kWaves, kSteps, false>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((recurrence_forward<T, V, CL, kWaves, kSteps, false>), grid, block, 0, stream, p);
     return (int)hipGetLastError();
+}
+
+template <typename T, int V>
+int by_lanes(const ScanParams &p, bool backward, hipStream_t stream) {
+    switch (p.lanes) {
+        case 64: return launch<T, V, 64>(p, backward, stream);
+        case 16: return launch<T, V, 16>(p, backward, stream);
+        default: return launch<T, V, 8>(p, backward, stream);
+    }
 }
 
 template <typename T>
 int pick(const ScanParams &p, bool backward, hipStream_t stream) {
-    return p.pairwise ? launch<T, 2>(p, backward, stream) : launch<T, 1>(p, backward, stream);
+    return p.pairwise ? by_lanes<T, 2>(p, backward, stream) : by_lanes<T, 1>(p, backward, stream);
 }
 
 }  // namespace
 
-// Parts of the tokens: as many as give every compute unit two blocks, of four
-// tiles at least.
-int recurrence_parts(int64_t batch, int64_t length, int64_t channels, bool pairwise) {
-    const int64_t lanes = pairwise ? 128 : 64, units = batch * ((channels + lanes - 1) / lanes);
-    if (units == 0 || units >= 256) return 1;
-    const int64_t tiles = (length + kTile - 1) / kTile;
-    int64_t parts = 512 / units;
-    if (parts > tiles / 4) parts = tiles / 4;
-    if (parts > kMaxParts) parts = kMaxParts;
-    return parts < 2 ? 1 : (int)parts;
+// Lanes of a run and parts of the tokens.  One reading, with as many lanes a run
+// as still give every compute unit a block, where the tokens are few or those
+// blocks enough; else 64 lanes (rows of 128 bytes and more) and as many parts as
+// give every compute unit two blocks, of two tiles at least, whose tokens are read
+// twice.  us of both, forward and backward, bf16:
+//   4 x 2048 x 190     15 + 23 in one reading, 15 + 17 in parts
+//   4 x 8192 x 190     51 + 81                 23 + 34
+//   1 x 32768 x 256   167 + 263                31 + 41
+//   4 x 4096 x 1024    29 + 44                 37 + 55
+//   4 x 8192 x 1024    53 + 128                62 + 96
+//   16 x 8192 x 512   109 + 183               123 + 195
+ScanPlan plan_recurrence(int64_t batch, int64_t length, int64_t channels, bool pairwise, bool backward, bool workspace) {
+    const int v = pairwise ? 2 : 1;
+    const auto units = [&](int cl) { return batch * ((channels + cl * v - 1) / (cl * v)); };
+    const int64_t most = units(8);
+    ScanPlan s = {8, 1};
+    if (workspace && most > 0 && ((length > 2048 && most < 256) || (backward && length > 4096 && most < 512))) {
+        s.lanes = channels > 16 * v ? 64 : channels > 8 * v ? 16 : 8;
+        const int64_t tile = kWaves * kSteps * (64 / s.lanes), tiles = (length + tile - 1) / tile;
+        int64_t parts = 512 / units(s.lanes);
+        if (parts > tiles / 2) parts = tiles / 2;
+        if (parts > kMaxParts) parts = kMaxParts;
+        s.parts = (int)parts;
+        if (parts >= 2) return s;
+    }
+    s.parts = 1;
+    s.lanes = units(64) >= 256 ? 64 : units(16) >= 256 ? 16 : 8;
+    return s;
 }
 
 int launch_recurrence(const ScanParams &p, int dtype, bool backward, hipStream_t stream) {

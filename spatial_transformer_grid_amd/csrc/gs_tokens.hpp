@@ -126,10 +126,14 @@ struct ScanParams {
     float *pairs;             // (parts, 2, batch, channels): product of the gates, state from zero
     float *copy;              // (batch, channels): the state, or its gradient, that the call was given
     int64_t xs[2], gs[2], ys[2], dys[2], dxs[2], dgs[2];
-    int batch, length, channels, parts;
+    int batch, length, channels, parts, blocks;
     int pairwise;             // a lane has two channels
+    int lanes;                // of a run of steps
 };
-int recurrence_parts(int64_t batch, int64_t length, int64_t channels, bool pairwise);
+struct ScanPlan {
+    int lanes, parts;
+};
+ScanPlan plan_recurrence(int64_t batch, int64_t length, int64_t channels, bool pairwise, bool backward, bool workspace);
 int launch_recurrence(const ScanParams &p, int dtype, bool backward, hipStream_t stream);
 
 // Launchers; 0 or the hipError_t of the launch.  `dtype` 0 f32, 1 f16, 2 bf16.
