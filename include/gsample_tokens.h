@@ -254,16 +254,18 @@ typedef enum {
  *   saved        device fp32, 2 x rows x hidden, contiguous: a and b, which
  *                the backward pass takes; or NULL.
  *   workspace    device, 256-byte aligned, of gs_gated_linear_workspace_size()
- *                bytes; without it (NULL, 0), or with less, a long width of
- *                few rows is not split over thread blocks: slower, and the
- *                sums in another order.
+ *                bytes.  Without it (NULL, 0), or with less, a long width of
+ *                few rows is not split over thread blocks, and a width that is
+ *                not whole 16-byte chunks takes the kernel for few rows: both
+ *                slower, and the sums in another order.  So does an X or a
+ *                weight off its 16-byte alignment (pointer or rows).
  *
  * Errors: GS_ERR_NULL, GS_ERR_SHAPE (an extent negative, width 0 with rows
  * and hidden, x_stride negative, rows of Y that overlap), GS_ERR_DTYPE,
  * GS_ERR_ATTR (activation, a workspace that is misaligned or of negative
- * size), GS_ERR_TOO_LARGE (rows, width or hidden above 2^22, rows * hidden
- * above 2^36, 2^22 thread blocks or more of the call or of its gradients: a
- * block has 128 rows of the output or more), GS_ERR_HIP.
+ * size), GS_ERR_TOO_LARGE (rows, width or hidden above 2^20, rows * hidden
+ * above 2^36, 2^22 thread blocks or more of a product of the call or of its
+ * gradients: a block has 128 by 128 elements or more of an output), GS_ERR_HIP.
  */
 int gs_gated_linear(const void *X, int dtype, int64_t rows, int64_t width, int64_t hidden, int64_t x_stride,
                     const void *Wg, const void *Wu, int activation, void *Y, int64_t y_stride, float *saved,

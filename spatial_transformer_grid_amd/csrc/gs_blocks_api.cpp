@@ -23,7 +23,7 @@ bool bad_workspace(const void *w, int64_t bytes) { return bytes < 0 || (w && (ui
 
 // ------------------------------------------------------ gated projections
 
-constexpr int64_t kMaxExtent = int64_t(1) << 22, kMaxProduct = int64_t(1) << 36;
+constexpr int64_t kMaxExtent = int64_t(1) << 20, kMaxProduct = int64_t(1) << 36;   // 256 rows of a tile within 2^31 bytes
 
 int gated_extents(int dtype, int64_t rows, int64_t width, int64_t hidden) {
     if (rows < 0 || width < 0 || hidden < 0) return GS_ERR_SHAPE;
@@ -33,44 +33,57 @@ int gated_extents(int dtype, int64_t rows, int64_t width, int64_t hidden) {
         return GS_ERR_TOO_LARGE;
     if (gs::gated_blocks(gs::kGatedForward, dtype, rows, hidden, width) >= kMaxBlocks ||
         gs::gated_blocks(gs::kGatedInput, dtype, rows, width, hidden) >= kMaxBlocks ||
-        gs::gated_blocks(gs::kGatedWeights, dtype, hidden, width, rows) >= kMaxBlocks)
+        gs::gated_blocks(gs::kGatedWeights, dtype, hidden, width, rows) >= kMaxBlocks ||
+        gs::gated_flips(rows, hidden, width) >= 4 * kMaxBlocks)
         return GS_ERR_TOO_LARGE;
     return GS_OK;
 }
 
 bool gated_activation(int a) { return a >= GS_ACT_SILU && a <= GS_ACT_RELU; }
 
-// How tiles of an operand are loaded (see gs_gated.hip): `contiguous` elements of
-// a row of its storage, rows `stride` apart.  An asynchronous load reaches the 256
-// rows of a tile by a 32-bit offset.
-int load_mode(int dtype, const void *p, const void *q, int64_t contiguous, int64_t stride) {
+// Whether rows of `n` elements, `stride` apart, allow 16-byte accesses.  (Tiles are
+// loaded by 32-bit offsets, 256 rows of them.)
+bool rows_vec(int dtype, const void *p, int64_t n, int64_t stride) {
     const int bytes = dtype_bytes(dtype);
-    if (stride * bytes >= (int64_t(1) << 23)) return 2;
-    for (int mode = 0; mode < 2; ++mode) {
-        const int unit = mode == 0 ? 16 : 4;
-        if (contiguous * bytes % unit == 0 && stride * bytes % unit == 0 && aligned(p, unit) && aligned(q, unit))
-            return mode;
-    }
-    return 2;
+    return n * bytes % 16 == 0 && stride * bytes % 16 == 0 && stride * bytes < (int64_t(1) << 23) && stride >= n && aligned(p, 16);
 }
 
-bool rows_vec(int dtype, const void *p, int64_t stride) {
-    return stride * dtype_bytes(dtype) % 16 == 0 && aligned(p, 16);
+int64_t whole(int64_t n) { return (n + 7) / 8 * 8; }
+
+// Workspace of a forward call: the parts' sums, then X and the weights in whole
+// chunks where the width has none (or where a caller's rows are off them).
+struct GatedForwardSpace {
+    int64_t partial, packed;
+};
+
+GatedForwardSpace gated_forward_space(int dtype, int64_t rows, int64_t width, int64_t hidden) {
+    GatedForwardSpace s;
+    s.partial = round_ws(gs::gated_partial_floats(gs::kGatedForward, dtype, rows, hidden, width) * 4);
+    s.packed = hidden > 0 && gs::gated_packs(rows) ? round_ws((rows + 2 * hidden) * whole(width) * dtype_bytes(dtype)) : 0;
+    return s;
 }
 
-// Workspace of a backward call: da, db in rows of whole chunks of eight, then the
-// parts' sums of one product or the other.
+// Workspace of a backward call (see FlipParams), then the parts' sums of one
+// product or the other.
 struct GatedSpace {
-    int64_t db, partial, bytes;
+    int64_t da, db, da_t, db_t, wg_t, wu_t, x_t, partial, bytes;
 };
 
 GatedSpace gated_space(int dtype, int64_t rows, int64_t width, int64_t hidden) {
     GatedSpace s;
-    const int64_t plane = round_ws(rows * ((hidden + 7) / 8 * 8) * dtype_bytes(dtype));
+    const int size = dtype_bytes(dtype);
     const int64_t a = gs::gated_partial_floats(gs::kGatedInput, dtype, rows, width, hidden);
     const int64_t b = gs::gated_partial_floats(gs::kGatedWeights, dtype, hidden, width, rows);
+    const int64_t plane = round_ws(rows * whole(hidden) * size), turned = round_ws(hidden * whole(rows) * size);
+    const int64_t weight = round_ws(width * whole(hidden) * size);
+    s.da = 0;
     s.db = plane;
-    s.partial = 2 * plane;
+    s.da_t = 2 * plane;
+    s.db_t = s.da_t + turned;
+    s.wg_t = s.db_t + turned;
+    s.wu_t = s.wg_t + weight;
+    s.x_t = s.wu_t + weight;
+    s.partial = s.x_t + round_ws(width * whole(rows) * size);
     s.bytes = s.partial + round_ws((a > b ? a : b) * 4);
     return s;
 }
@@ -199,7 +212,8 @@ int gs_gated_linear_workspace_size(int dtype, int64_t rows, int64_t width, int64
     if (!bytes) return GS_ERR_NULL;
     const int rc = gated_extents(dtype, rows, width, hidden);
     if (rc != GS_OK) return rc;
-    *bytes = round_ws(gs::gated_partial_floats(gs::kGatedForward, dtype, rows, hidden, width) * 4);
+    const GatedForwardSpace s = gated_forward_space(dtype, rows, width, hidden);
+    *bytes = s.partial + (width * dtype_bytes(dtype) % 16 ? s.packed : 0);
     return GS_OK;
 }
 
@@ -224,13 +238,15 @@ int gs_gated_linear(const void *X, int dtype, int64_t rows, int64_t width, int64
     p.m = (int)rows;
     p.n = (int)hidden;
     p.k = (int)width;
-    p.m_mode = load_mode(dtype, X, X, width, x_stride);
-    p.n_mode = load_mode(dtype, Wg, Wu, width, width);
-    p.out_vec = rows_vec(dtype, Y, y_stride);
-    p.saved_vec = rows_vec(GS_F32, saved, hidden);
+    p.m_vec = rows_vec(dtype, X, width, rows > 1 ? x_stride : width);
+    p.n_vec = rows_vec(dtype, Wg, width, width) && aligned(Wu, 16);
+    p.out_vec = y_stride * dtype_bytes(dtype) % 16 == 0 && aligned(Y, 16);
+    p.saved_vec = hidden % 4 == 0 && aligned(saved, 16);
     p.activation = activation;
-    const int64_t need = gs::gated_partial_floats(gs::kGatedForward, dtype, rows, hidden, width) * 4;
-    p.partial = need > 0 && workspace && workspace_bytes >= need ? (float *)workspace : nullptr;
+    const GatedForwardSpace space = gated_forward_space(dtype, rows, width, hidden);
+    const int64_t room = workspace ? workspace_bytes : 0;
+    p.partial = space.partial > 0 && room >= space.partial ? (float *)workspace : nullptr;
+    p.packed = space.packed > 0 && room >= space.partial + space.packed ? (char *)workspace + space.partial : nullptr;
     return hip_status(gs::launch_gated(p, gs::kGatedForward, dtype, (hipStream_t)stream));
 }
 
@@ -261,62 +277,69 @@ int gs_gated_linear_backward(const void *dY, const void *X, int dtype, int64_t r
         if (workspace_bytes < space.bytes || (uintptr_t)workspace % kWsAlign) return GS_ERR_ATTR;
     }
     char *const ws = (char *)workspace;
-    void *const da = ws, *const db = ws + space.db;
-    float *const partial = (float *)(ws + space.partial);
-    const int64_t padded = (hidden + 7) / 8 * 8;
+    const int64_t np = whole(hidden), mp = whole(rows);
     if (both) {
-        gs::GatedParams p = {};
+        gs::FlipParams p = {};
         p.dy = dY;
+        p.x = X;
+        p.wg = Wg;
+        p.wu = Wu;
+        p.saved = saved;
+        if (input) {
+            p.da = ws + space.da;
+            p.db = ws + space.db;
+            p.wg_t = ws + space.wg_t;
+            p.wu_t = ws + space.wu_t;
+        }
+        if (weights) {
+            p.da_t = ws + space.da_t;
+            p.db_t = ws + space.db_t;
+            p.x_t = ws + space.x_t;
+        }
         p.dy_stride = dy_stride;
-        p.saved = const_cast<float *>(saved);
-        p.saved_vec = rows_vec(GS_F32, saved, hidden);
-        p.out_vec = rows_vec(dtype, dY, dy_stride) && hidden % 8 == 0;
-        p.out0 = da;
-        p.out1 = db;
+        p.x_stride = x_stride;
         p.m = (int)rows;
         p.n = (int)hidden;
+        p.k = (int)width;
         p.activation = activation;
-        const int e = gs::launch_gated(p, gs::kGatedGradients, dtype, (hipStream_t)stream);
+        const int size = dtype_bytes(dtype);
+        p.dy_vec = hidden * size % 16 == 0 && dy_stride * size % 16 == 0 && aligned(dY, 16);
+        p.saved_vec = hidden % 4 == 0 && aligned(saved, 16);
+        p.x_vec = width * size % 16 == 0 && x_stride * size % 16 == 0 && aligned(X, 16);
+        p.w_vec = width * size % 16 == 0 && aligned(Wg, 16) && aligned(Wu, 16);
+        const int e = gs::launch_gated_prepare(p, dtype, (hipStream_t)stream);
         if (e) return hip_status(e);
     }
+    gs::GatedParams p = {};
     if (input) {
-        gs::GatedParams p = {};
-        p.m0 = da;
-        p.m1 = db;
-        p.n0 = Wg;
-        p.n1 = Wu;
+        p.m0 = ws + space.da;
+        p.m1 = ws + space.db;
+        p.n0 = ws + space.wg_t;
+        p.n1 = ws + space.wu_t;
         p.out0 = dX;
-        p.m_stride = padded;
-        p.n_stride = width;
+        p.m_stride = p.n_stride = np;
         p.out_stride = dx_stride;
         p.m = (int)rows;
         p.n = (int)width;
         p.k = (int)hidden;
-        p.m_mode = load_mode(dtype, da, db, padded, padded);
-        p.n_mode = load_mode(dtype, Wg, Wu, width, width);
-        p.out_vec = rows_vec(dtype, dX, dx_stride);
-        p.partial = gs::gated_partial_floats(gs::kGatedInput, dtype, rows, width, hidden) > 0 ? partial : nullptr;
+        p.out_vec = dx_stride * dtype_bytes(dtype) % 16 == 0 && aligned(dX, 16);
+        p.partial = gs::gated_partial_floats(gs::kGatedInput, dtype, rows, width, hidden) > 0 ? (float *)(ws + space.partial) : nullptr;
         const int e = gs::launch_gated(p, gs::kGatedInput, dtype, (hipStream_t)stream);
         if (e) return hip_status(e);
     }
     if (weights) {
-        gs::GatedParams p = {};
-        p.m0 = da;
-        p.m1 = db;
-        p.n0 = X;
-        p.n1 = X;
+        p.m0 = ws + space.da_t;
+        p.m1 = ws + space.db_t;
+        p.n0 = p.n1 = ws + space.x_t;
         p.out0 = dWg;
         p.out1 = dWu;
-        p.m_stride = padded;
-        p.n_stride = x_stride;
+        p.m_stride = p.n_stride = mp;
         p.out_stride = width;
         p.m = (int)hidden;
         p.n = (int)width;
         p.k = (int)rows;
-        p.m_mode = load_mode(dtype, da, db, padded, padded);
-        p.n_mode = load_mode(dtype, X, X, width, x_stride);
-        p.out_vec = rows_vec(dtype, dWg, width) && aligned(dWu, 16);
-        p.partial = gs::gated_partial_floats(gs::kGatedWeights, dtype, hidden, width, rows) > 0 ? partial : nullptr;
+        p.out_vec = width * dtype_bytes(dtype) % 16 == 0 && aligned(dWg, 16) && aligned(dWu, 16);
+        p.partial = gs::gated_partial_floats(gs::kGatedWeights, dtype, hidden, width, rows) > 0 ? (float *)(ws + space.partial) : nullptr;
         return hip_status(gs::launch_gated(p, gs::kGatedWeights, dtype, (hipStream_t)stream));
     }
     return GS_OK;

@@ -2,15 +2,21 @@
 // Y = act(X Wg^T) * (X Wu^T).
 //
 // Every product is one kernel on 32 x 32 matrix instructions, out[m][n] = sum
-// over k of M(m, k) N(n, k), whose operands lie in memory along k (kAlongK) or
-// across it (kAcross; read from LDS transposed):
-//   forward   M = X rows        N = Wg and Wu rows, half a tile of each, so that
-//             a lane holds a and b of the same element and Y needs no second pass
-//   dX        M = da, then db   N = Wg, then Wu across: one sum over both
-//   dWg, dWu  M = da, db across N = X across
+// over k of M(m, k) N(n, k), both operands lying along k in memory:
+//   forward   M = X            N = Wg and Wu, half a tile of each, so that a wave
+//             holds a and b of the same elements and Y needs no second pass
+//   dX        M = da, then db  N = Wg^T, then Wu^T: one sum over both
+//   dWg, dWu  M = da^T, db^T   N = X^T
+// The transposed copies are made by the pass over dY that makes da and db, tile by
+// tile through LDS.  (Reading the tiles of the products transposed instead saves
+// that traffic, but the compiler waits for every load under way before each
+// transposing read of LDS: 600 + 614 us for dX and the weights' gradients of 8192 x
+// 2048 -> 8192 in bf16.)
+// Operands that are off their 16-byte alignment are copied into rows that are not.
+//
 // N is the A operand of the instructions with its rows permuted (a_row), so that
 // a lane has eight neighbouring columns of an output row.  Tiles come by
-// asynchronous loads into LDS, the next one while this one is multiplied.  A
+// asynchronous loads into LDS, several ahead of the one that is multiplied.  A
 // long sum of few tiles is cut into parts over blocks, whose fp32 sums a second
 // kernel adds in order.
 //
@@ -58,104 +64,51 @@ __device__ __forceinline__ float activation(int kind, float a, float &slope) {
 
 // ---------------------------------------------------------------- operands
 
-// How a tile's rows are brought into LDS: 16 bytes a lane, four bytes a lane
-// (rows that are only so aligned), or element by element through registers.
-enum { kWide = 0, kNarrow = 1, kElements = 2 };
-
+// Steps of the contracted axis a tile, and tiles in LDS.  16-bit types: 64 bytes a
+// row and four tiles, three of them on their way; fp32, whose products take eight
+// times as long, 128 bytes and two.
 template <typename T>
 struct K {
-    static constexpr int BK = 128 / T::bytes;        // of the contracted axis a tile
+    static constexpr int BK = (T::bytes == 4 ? 128 : 64) / T::bytes;
+    static constexpr int DEPTH = T::bytes == 4 ? 2 : 4;
     static constexpr int EPC = 16 / T::bytes;
 };
 
-// One operand's tile of ROWS rows of the output by BK of the contracted axis.
-// ALONG: LDS rows are the output's, BK columns each.  Else LDS rows are the
-// contracted axis', 128 columns each, in ROWS / 128 such blocks one after another.
-template <typename T, int ROWS, bool ALONG, int NT>
+// One operand's tile: ROWS rows of BK, loaded by NT threads.
+template <typename T, int ROWS, int NT>
 struct Operand {
     typedef typename T::raw_t raw_t;
-    static constexpr int BK = K<T>::BK, EPC = K<T>::EPC, DP = ALONG ? BK : 128;
-    static constexpr int CHUNKS = ROWS * BK / EPC, CPR = DP / EPC;
-    typedef Tile<T, DP> L;
-    static_assert(CHUNKS % NT == 0 && NT % 64 == 0, "whole waves, whole steps");
+    static constexpr int BK = K<T>::BK, EPC = K<T>::EPC, CPR = BK / EPC;
+    static constexpr int LOADS = ROWS * CPR / NT;    // of a thread
+    static constexpr int STEP = NT / CPR;            // rows of one load of all threads
+    typedef Tile<T, BK> L;
+    static_assert(NT % CPR == 0 && STEP % 16 == 0, "the order of a row's chunks repeats every 16 rows");
 
-    // row and column of LDS chunk c's source, relative to the tile
-    __device__ __forceinline__ static void source(int c, int &row, int &k, int part) {
-        if constexpr (ALONG) {
-            const int r = c / CPR;
-            row = r;
-            k = ((c - r * CPR) ^ L::turn(r)) * EPC + part;
-        } else {
-            const int block = c / (BK * CPR), q = c - block * (BK * CPR), r = q / CPR;
-            k = r;
-            row = block * 128 + ((q - r * CPR) ^ L::turn(r)) * EPC + part;
-        }
-    }
-
-    // The tile at output row row0 and contracted index k0.  `base` is the operand's
-    // first element; a row of its storage is `stride` elements.  HALVES: the upper
-    // half of the tile's rows is the same rows of `base2`.
-    template <bool HALVES>
+    // Part PART of PARTS of the tile at row row0 of `rows` and contracted index k0 of
+    // ks, `stride` elements a row (whole 16-byte chunks, as is what lies past ks).
+    // HALVES: the upper half of the tile's rows is the same rows of `base2`.  Rows past
+    // the last one lie past the descriptor's range, which ends with the last one's last
+    // chunk; chunks past ks take an offset that is out of range.  (The offset is whole in
+    // the vector register: the range is checked against that.)
+    template <bool HALVES, int PART, int PARTS>
     __device__ __forceinline__ static void load(raw_t *lds, const raw_t *base, const raw_t *base2, int64_t stride,
-                                                int row0, int rows, int k0, int ks, int mode, int t) {
+                                                int row0, int rows, int k0, int ks, int t) {
         constexpr int H = HALVES ? ROWS / 2 : ROWS;
-        const int64_t first = ALONG ? row0 * stride + k0 : k0 * stride + row0;
-        if (mode != kElements) {
-            const __amdgpu_buffer_rsrc_t r1 =
-                __builtin_amdgcn_make_buffer_rsrc((void *)(base + first), 0, 0x7fffffff, 0x00027000);
-            const __amdgpu_buffer_rsrc_t r2 = HALVES
-                ? __builtin_amdgcn_make_buffer_rsrc((void *)(base2 + first), 0, 0x7fffffff, 0x00027000) : r1;
-            if (mode == kWide) {
+        const int64_t first = row0 * stride + k0;
+        const int64_t range = ((int64_t)(rows - row0 - 1) * stride + (ks - k0 + EPC - 1) / EPC * EPC) * T::bytes;
+        const int bytes = rows <= row0 || ks <= k0 ? 0 : (int)(range < 0x7fffffff ? range : 0x7fffffff);
+        const rsrc_t r1 = __builtin_amdgcn_make_buffer_rsrc((void *)(base + first), 0, bytes, kRsrcWord3);
+        const rsrc_t r2 = HALVES ? __builtin_amdgcn_make_buffer_rsrc((void *)(base2 + first), 0, bytes, kRsrcWord3) : r1;
+        const int line = t / CPR, col = ((t - line * CPR) ^ L::turn(line)) * EPC;
+        const uint32_t at = col < ks - k0 ? (uint32_t)(line * (int)stride + col) * T::bytes : GS_OOB;
 #pragma unroll
-                for (int n = 0; n < CHUNKS / NT; ++n) {
-                    int row, k;
-                    source(t + n * NT, row, k, 0);
-                    const bool upper = HALVES && n >= CHUNKS / NT / 2;
-                    if (upper) row -= H;
-                    const bool in = row0 + row < rows && k0 + k < ks;
-                    const uint32_t at = in ? (uint32_t)(ALONG ? row * (int)stride + k : k * (int)stride + row) * T::bytes
-                                           : 0x80000000u;
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                        upper ? r2 : r1, (__attribute__((address_space(3))) void *)(lds + ((t & ~63) + n * NT) * EPC), 16,
-                        (int)at, 0, 0, 0);
-                }
-            } else {
-                constexpr int PER = 4 / T::bytes;
-#pragma unroll 4
-                for (int n = 0; n < 4 * CHUNKS / NT; ++n) {
-                    int row, k;
-                    const int word = t + n * NT;
-                    source(word >> 2, row, k, (word & 3) * PER);
-                    const bool upper = HALVES && n >= 4 * CHUNKS / NT / 2;
-                    if (upper) row -= H;
-                    const bool in = row0 + row < rows && k0 + k < ks;
-                    const uint32_t at = in ? (uint32_t)(ALONG ? row * (int)stride + k : k * (int)stride + row) * T::bytes
-                                           : 0x80000000u;
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                        upper ? r2 : r1, (__attribute__((address_space(3))) void *)(lds + ((t & ~63) + n * NT) * PER), 4,
-                        (int)at, 0, 0, 0);
-                }
-            }
-            return;
-        }
-#pragma unroll 1
-        for (int n = 0; n < CHUNKS / NT; ++n) {
-            raw_t e[EPC];
-#pragma unroll
-            for (int j = 0; j < EPC; ++j) {
-                int row, k;
-                source(t + n * NT, row, k, j);
-                const raw_t *from = base + first;
-                if (HALVES && row >= H) {
-                    row -= H;
-                    from = base2 + first;
-                }
-                const bool in = row0 + row < rows && k0 + k < ks;
-                e[j] = in ? from[ALONG ? row * stride + k : k * stride + row] : raw_t(0);
-            }
-            u32x4 v;
-            __builtin_memcpy(&v, e, 16);
-            *(u32x4 *)(lds + (t + n * NT) * EPC) = v;
+        for (int n = LOADS * PART / PARTS; n < LOADS * (PART + 1) / PARTS; ++n) {
+            const int l = n * STEP;
+            const bool upper = HALVES && l >= H;
+            const uint32_t off = at + (uint32_t)((upper ? l - H : l) * (int)stride) * T::bytes;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                upper ? r2 : r1, (__attribute__((address_space(3))) void *)(lds + ((t & ~63) + n * NT) * EPC), 16, (int)off, 0,
+                0, 0);
         }
     }
 
@@ -163,25 +116,7 @@ struct Operand {
     // PERMUTED rows as a_row says, else in order.
     template <bool PERMUTED>
     __device__ __forceinline__ static Frag<T> read(const raw_t *lds, int row, int k, int lane) {
-        if constexpr (ALONG) {
-            return frag_lds<T, DP>(lds, row + (PERMUTED ? a_row(lane & 31) : lane & 31), k + 8 * (lane >> 5));
-        } else {
-            const raw_t *block = lds + row / 128 * (128 * BK);
-            row &= 127;
-            if constexpr (!PERMUTED) {
-                return frag_lds_transposed<T, DP>(block, k, row, lane);
-            } else if constexpr (T::bytes == 4) {
-                Frag<T> f;
-                const int col = row + a_row(lane & 31);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f.w[j >> 2][j & 3] = block[L::chunk(k + 8 * (lane >> 5) + j, col) + (col & 3)];
-                return f;
-            } else {
-                // of the four groups of four columns a transposing read names, the middle two change places
-                const int group = lane & 3, named = (group & 1) << 1 | group >> 1;
-                return frag_lds_transposed<T, DP>(block, k, row, (lane & ~3) | named);
-            }
-        }
+        return frag_lds<T, BK>(lds, row + (PERMUTED ? a_row(lane & 31) : lane & 31), k + 8 * (lane >> 5));
     }
 };
 
@@ -216,13 +151,44 @@ __device__ __forceinline__ void store_gated(const GatedParams &p, int m, int n, 
     store8<T>((raw_t *)p.out0 + m * p.out_stride, n, p.n, p.out_vec, y);
 }
 
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
+// Everything this wave has asked for but the last N asynchronous loads is there.
+template <int N>
+__device__ __forceinline__ void await() {
+    static_assert(N < 64, "six bits");
+    __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// A barrier that nothing is moved across.
+[[maybe_unused]] __device__ __forceinline__ void meet() {
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+}
+
+// The order of a step: its reads of LDS and loads spread between its products.
+template <int PRODUCTS, int READS, int LOADS, int GROUPS, int G = 0>
+__device__ __forceinline__ void interleave() {
+    if constexpr (G < GROUPS) {
+        constexpr int reads = READS * (G + 1) / GROUPS - READS * G / GROUPS, loads = LOADS * (G + 1) / GROUPS - LOADS * G / GROUPS;
+        if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+        if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, PRODUCTS / GROUPS, 0);
+        interleave<PRODUCTS, READS, LOADS, GROUPS, G + 1>();
+    }
+}
+
 template <typename T, int MODE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void gated_product(GatedParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
     typedef typename T::raw_t raw_t;
     constexpr int NT = 64 * WM * WN, TM = BM / WM / 32, TN = BN / WN / 32, BK = K<T>::BK;
-    typedef Operand<T, BM, MODE != kWeights, NT> OM;
-    typedef Operand<T, BN, MODE == kForward, NT> ON;
-    constexpr int STAGE = (BM + BN) * BK;
+    typedef Operand<T, BM, NT> OM;
+    typedef Operand<T, BN, NT> ON;
+    constexpr int STAGE = (BM + BN) * BK, DEPTH = K<T>::DEPTH, STEPS = BK / 16;
     constexpr int COLS = MODE == kForward ? BN / 2 : BN;    // of the output
     extern __shared__ __align__(16) unsigned char smem[];
     raw_t *const lds = (raw_t *)smem;
@@ -245,12 +211,14 @@ __global__ __launch_bounds__(64 * WM * WN) void gated_product(GatedParams p) {
     // the contracted axis in tiles: all of da and Wg, then all of db and Wu
     const int per_half = (p.k + BK - 1) / BK, all = MODE == kInput ? 2 * per_half : per_half;
     const int s0 = (int)((int64_t)all * part / p.parts), s1 = (int)((int64_t)all * (part + 1) / p.parts);
-    const auto load = [&](int s, raw_t *to) {
+    const auto load = [&](int s, auto part) {
+        constexpr int PART = decltype(part)::value;
+        raw_t *const to = lds + (unsigned)(s - s0) % DEPTH * STAGE;
         const int half = MODE == kInput && s >= per_half ? 1 : 0, k0 = (s - half * per_half) * BK;
         const raw_t *const mb = (const raw_t *)(MODE == kWeights ? (which ? p.m1 : p.m0) : half ? p.m1 : p.m0);
-        OM::template load<false>(to, mb, mb, p.m_stride, m0, p.m, k0, p.k, p.m_mode, t);
+        OM::template load<false, PART, STEPS>(to, mb, mb, p.m_stride, m0, p.m, k0, p.k, t);
         const raw_t *const nb = (const raw_t *)(half ? p.n1 : p.n0);
-        ON::template load<MODE == kForward>(to + BM * BK, nb, (const raw_t *)p.n1, p.n_stride, n0, p.n, k0, p.k, p.n_mode, t);
+        ON::template load<MODE == kForward, PART, STEPS>(to + BM * BK, nb, (const raw_t *)p.n1, p.n_stride, n0, p.n, k0, p.k, t);
     };
     f32x16 acc[TM][TN];
 #pragma unroll
@@ -264,56 +232,129 @@ __global__ __launch_bounds__(64 * WM * WN) void gated_product(GatedParams p) {
         if (MODE == kForward) return (j < TN / 2 ? 0 : BN / 2) + (wn * (TN / 2) + j % (TN / 2)) * 32;
         return (wn * TN + j) * 32;
     };
-    if (s0 < s1) load(s0, lds);
-    for (int s = s0; s < s1; ++s) {
-        const raw_t *const tile = lds + ((s - s0) & 1) * STAGE;
-        async_wait();
-        __syncthreads();
-        if (s + 1 < s1) load(s + 1, lds + ((s + 1 - s0) & 1) * STAGE);
+    // A step's operands are read while the one before is multiplied, a tile's first
+    // ones while the last step of the tile before is.  The loads of the tile DEPTH - 1
+    // further on are spread over the steps: a wave that sent them all at once would
+    // wait for the memory unit to take them, its products behind them.  At the end of
+    // a tile the next one is waited for, and everybody has read this one, whose place
+    // is the next to be filled.  (Past the last tile zeros are loaded that nobody
+    // reads, so that the number of loads under way stays the same.)
+    static_assert(STEPS % 2 == 0, "a step's registers follow from its number");
+    constexpr bool ORDERED = T::bytes == 2;
+    constexpr int TILE_LOADS = OM::LOADS + ON::LOADS, UNDER_WAY = (DEPTH - 2) * TILE_LOADS;
+    Frag<T> a[2][TN], b[2][TM];
+    const auto read = [&](const raw_t *tile, int step) {
 #pragma unroll
-        for (int k = 0; k < BK; k += 16) {
-            Frag<T> a[TN], b[TM];
+        for (int j = 0; j < TN; ++j) a[step & 1][j] = ON::template read<true>(tile + BM * BK, n_row(j), 16 * step, lane);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) a[j] = ON::template read<true>(tile + BM * BK, n_row(j), k, lane);
+        for (int i = 0; i < TM; ++i) b[step & 1][i] = OM::template read<false>(tile, (wm * TM + i) * 32, 16 * step, lane);
+    };
+    const auto multiply = [&](int step) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i) b[i] = OM::template read<false>(tile, (wm * TM + i) * 32, k, lane);
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+            for (int j = 0; j < TN; ++j) mma<T>(acc[i][j], a[step & 1][j], b[step & 1][i]);
+    };
+    const auto load_all = [&](int s) {
+        load(s, Int<0>{});
+        if constexpr (STEPS > 1) load(s, Int<1>{});
+        static_assert(STEPS == 2, "all parts");
+    };
+    if (s0 < s1) {
 #pragma unroll
-                for (int j = 0; j < TN; ++j) mma<T>(acc[i][j], a[j], b[i]);
-        }
+        for (int d = 0; d + 1 < DEPTH; ++d) load_all(s0 + d);
+        await<UNDER_WAY>();
+        meet();
+        read(lds, 0);
     }
+    for (int s = s0; s < s1; ++s) {
+        const raw_t *const tile = lds + (unsigned)(s - s0) % DEPTH * STAGE, *const next = lds + (unsigned)(s - s0 + 1) % DEPTH * STAGE;
+        load(s + DEPTH - 1, Int<0>{});
+        read(tile, 1);
+        multiply(0);
+        if constexpr (ORDERED) interleave<TM * TN, TM + TN, TILE_LOADS / STEPS, TM + TN>();
+        if constexpr (DEPTH == 2) load(s + 1, Int<1>{});
+        await<DEPTH == 2 ? 0 : UNDER_WAY - TILE_LOADS / 2>();
+        meet();
+        if constexpr (DEPTH > 2) load(s + DEPTH - 1, Int<1>{});
+        read(next, 0);
+        multiply(1);
+        if constexpr (ORDERED) interleave<TM * TN, TM + TN, TILE_LOADS / STEPS, TM + TN>();
+    }
+    await<0>();
+    __syncthreads();
 
-    constexpr int HALF = MODE == kForward ? TN / 2 : TN;
+    if constexpr (MODE == kForward) {
+        // Through LDS, 32 rows of a wave at a time: the activation is a small loop, and
+        // rows are stored whole.
+        constexpr int HALF = TN / 2, WIDTH = 32 * HALF, PITCH = WIDTH + 4;
+        float *const mine = (float *)smem + wave * (2 * 32 * PITCH);
+        static_assert(WM * WN * 2 * 32 * PITCH * 4 <= 2 * 2 * BM * 128, "room");
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int m = m0 + (wm * TM + i) * 32 + (lane & 31);
-        if (m >= p.m) continue;
+        for (int i = 0; i < TM; ++i) {
 #pragma unroll
-        for (int j = 0; j < HALF; ++j)
+            for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int n = n0 + (wn * HALF + j) * 32 + 16 * u + 8 * (lane >> 5);
+                for (int u = 0; u < 4; ++u) {
+                    // results 4 u .. 4 u + 3 are neighbours
+                    const int col = (j % HALF) * 32 + 16 * (u >> 1) + 8 * (lane >> 5) + 4 * (u & 1);
+                    *(tokens_f32x4 *)(mine + (j / HALF) * 32 * PITCH + (lane & 31) * PITCH + col) = tokens_f32x4{
+                        acc[i][j][4 * u], acc[i][j][4 * u + 1], acc[i][j][4 * u + 2], acc[i][j][4 * u + 3]};
+                }
+            tile_sync<true>();
+#pragma unroll 1
+            for (int c = lane; c < 32 * WIDTH / 8; c += 64) {
+                const int row = c / (WIDTH / 8), col = (c - row * (WIDTH / 8)) * 8;
+                const int m = m0 + (wm * TM + i) * 32 + row, n = n0 + wn * WIDTH + col;
                 float v[8], w[8];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    v[r] = acc[i][j][8 * u + r];
-                    w[r] = MODE == kForward ? acc[i][j + HALF][8 * u + r] : 0.0f;
+                for (int q = 0; q < 2; ++q) {
+                    const tokens_f32x4 x = *(const tokens_f32x4 *)(mine + row * PITCH + col + 4 * q);
+                    const tokens_f32x4 y = *(const tokens_f32x4 *)(mine + 32 * PITCH + row * PITCH + col + 4 * q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[4 * q + e] = x[e];
+                        w[4 * q + e] = y[e];
+                    }
                 }
-                if (n >= p.n) continue;
+                if (m >= p.m || n >= p.n) continue;
                 if (p.parts > 1) {
                     // rows of partial sums are padded to eight columns
-                    const int64_t width = (p.n + 7) / 8 * 8, plane = (int64_t)p.m * width, planes = MODE == kInput ? 1 : 2;
-                    float *to = p.partial + (part * planes + which) * plane + m * width;
+                    const int64_t width = (p.n + 7) / 8 * 8, plane = (int64_t)p.m * width;
+                    float *to = p.partial + part * 2 * plane + m * width;
                     store8<F32>((uint32_t *)to, n, (int)width, true, v);
-                    if (MODE == kForward) store8<F32>((uint32_t *)to + plane, n, (int)width, true, w);
-                } else if (MODE == kForward) {
-                    store_gated<T>(p, m, n, v, w);
+                    store8<F32>((uint32_t *)to + plane, n, (int)width, true, w);
                 } else {
-                    store8<T>((raw_t *)(which ? p.out1 : p.out0) + m * p.out_stride, n, p.n, p.out_vec, v);
+                    store_gated<T>(p, m, n, v, w);
                 }
             }
+            tile_sync<true>();
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int m = m0 + (wm * TM + i) * 32 + (lane & 31);
+            if (m >= p.m) continue;
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int n = n0 + (wn * TN + j) * 32 + 16 * u + 8 * (lane >> 5);
+                    float v[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) v[r] = acc[i][j][8 * u + r];
+                    if (n >= p.n) continue;
+                    if (p.parts > 1) {
+                        const int64_t width = (p.n + 7) / 8 * 8, plane = (int64_t)p.m * width;
+                        constexpr int planes = MODE == kInput ? 1 : 2;
+                        store8<F32>((uint32_t *)p.partial + (part * planes + which) * plane + m * width, n, (int)width, true, v);
+                    } else {
+                        store8<T>((raw_t *)(which ? p.out1 : p.out0) + m * p.out_stride, n, p.n, p.out_vec, v);
+                    }
+                }
+        }
     }
+#endif
 }
 
 // The parts' sums, in order, and what follows them.
@@ -344,33 +385,139 @@ __global__ __launch_bounds__(256) void gated_join(GatedParams p) {
     }
 }
 
-// ------------------------------------------------------- gradients of a, b
+// -------------------------------------------------- what the products read
+
+// Eight elements from column col of a row (zeros past `cols`), by 16 bytes where
+// `vec` says that rows allow it.
+template <typename T>
+__device__ __forceinline__ void load8(const typename T::raw_t *row, int col, int cols, bool vec, float *v) {
+    const Frag<T> f = frag_global<T>(row, col, cols, true, vec);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = frag_get<T>(f, j);
+}
+
+// Rows of X, Wg, Wu copied into rows of whole chunks of eight, the rest zero.
+template <typename T>
+__global__ __launch_bounds__(256) void gated_pack(GatedParams p) {
+    typedef typename T::raw_t raw_t;
+    const int chunks = (p.k + 7) / 8;
+    const int64_t width = (int64_t)chunks * 8, lines = (int64_t)p.m + 2 * (int64_t)p.n, items = lines * chunks;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
+        const int64_t line = i / chunks;
+        const int col = (int)(i - line * chunks) * 8;
+        const raw_t *row = (const raw_t *)p.m0 + line * p.m_stride;
+        if (line >= p.m) {
+            const int64_t unit = line - p.m;
+            row = unit < p.n ? (const raw_t *)p.n0 + unit * p.n_stride : (const raw_t *)p.n1 + (unit - p.n) * p.n_stride;
+        }
+        float v[8];
+        load8<T>(row, col, p.k, false, v);
+        store8<T>((raw_t *)p.out0 + line * width, col, (int)width, true, v);
+    }
+}
+
+constexpr int kFlip = 64;              // rows and columns of a tile of the pass below
+
+// A tile in LDS whose columns become rows of the output: `cols` rows of `stride`
+// elements (whole chunks of eight, `rows` of them used, zeros past them).
+template <typename T>
+__device__ __forceinline__ void store_flipped(const typename T::raw_t (*tile)[kFlip + 4 / T::bytes], void *out, int64_t stride,
+                                              int row0, int rows, int col0, int cols, int t) {
+    typedef typename T::raw_t raw_t;
+#pragma unroll
+    for (int c = t; c < kFlip * kFlip / 8; c += 256) {
+        const int col = c / (kFlip / 8), row = (c - col * (kFlip / 8)) * 8;
+        if (col0 + col >= cols || row0 + row >= rows) continue;
+        raw_t e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = tile[row + j][col];
+        raw_t *const to = (raw_t *)out + (col0 + col) * stride + row0 + row;
+#pragma unroll
+        for (int i = 0; i < T::bytes / 2; ++i) {
+            u32x4 v;
+            __builtin_memcpy(&v, e + i * (16 / T::bytes), 16);
+            *(u32x4 *)(to + i * (16 / T::bytes)) = v;
+        }
+    }
+}
 
 // da = dY b act'(a) and db = dY act(a), rounded to T, in rows of whole chunks of
-// eight whose rest is zero.
+// eight whose rest is zero, and transposed; and Wg, Wu and X transposed.  A block
+// takes one tile of one of them.
 template <typename T>
-__global__ __launch_bounds__(256) void gated_gradients(GatedParams p) {
+__global__ __launch_bounds__(256) void gated_prepare(FlipParams p) {
     typedef typename T::raw_t raw_t;
-    const int64_t width = (p.n + 7) / 8 * 8, chunks = width / 8, items = (int64_t)p.m * chunks;
-    const int64_t plane = (int64_t)p.m * p.n;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
-        const int64_t m = i / chunks;
-        const int n = (int)(i - m * chunks) * 8;
-        const uint32_t *const a = (const uint32_t *)p.saved + m * p.n;
-        const Frag<T> g = frag_global<T>((const raw_t *)p.dy + m * p.dy_stride, n, p.n, true, p.out_vec);
-        const Frag<F32> fa = frag_global<F32>(a, n, p.n, true, p.saved_vec);
-        const Frag<F32> fb = frag_global<F32>(a + plane, n, p.n, true, p.saved_vec);
-        float da[8], db[8];
+    __shared__ raw_t tile[2][kFlip][kFlip + 4 / T::bytes];
+    const int t = threadIdx.x;
+    int id = (int)blockIdx.x;
+    const int flips_n = (p.n + kFlip - 1) / kFlip, flips_k = (p.k + kFlip - 1) / kFlip, flips_m = (p.m + kFlip - 1) / kFlip;
+    const int64_t np = ((int64_t)p.n + 7) / 8 * 8, mp = ((int64_t)p.m + 7) / 8 * 8;
+    if (id < flips_m * flips_n) {
+        const int row0 = id / flips_n * kFlip, col0 = id % flips_n * kFlip;
+        const int64_t plane = (int64_t)p.m * p.n;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float slope;
-            const float d = frag_get<T>(g, j), f = activation(p.activation, frag_get<F32>(fa, j), slope);
-            da[j] = n + j < p.n ? d * frag_get<F32>(fb, j) * slope : 0.0f;
-            db[j] = n + j < p.n ? d * f : 0.0f;
+        for (int c = t; c < kFlip * kFlip / 8; c += 256) {
+            const int r = c / (kFlip / 8), m = row0 + r, q = (c - r * (kFlip / 8)) * 8, n = col0 + q;
+            float da[8] = {}, db[8] = {};
+            if (m < p.m && n < p.n) {
+                float d[8], a[8], b[8];
+                load8<T>((const raw_t *)p.dy + m * p.dy_stride, n, p.n, p.dy_vec, d);
+                load8<F32>((const uint32_t *)p.saved + (int64_t)m * p.n, n, p.n, p.saved_vec, a);
+                load8<F32>((const uint32_t *)p.saved + plane + (int64_t)m * p.n, n, p.n, p.saved_vec, b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float slope;
+                    const float f = activation(p.activation, a[j], slope);
+                    da[j] = n + j < p.n ? d[j] * b[j] * slope : 0.0f;
+                    db[j] = n + j < p.n ? d[j] * f : 0.0f;
+                }
+                if (p.da) {
+                    store8<T>((raw_t *)p.da + m * np, n, (int)np, true, da);
+                    store8<T>((raw_t *)p.db + m * np, n, (int)np, true, db);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                tile[0][r][q + j] = to_bits<T>(da[j]);
+                tile[1][r][q + j] = to_bits<T>(db[j]);
+            }
         }
-        store8<T>((raw_t *)p.out0 + m * width, n, (int)width, true, da);
-        store8<T>((raw_t *)p.out1 + m * width, n, (int)width, true, db);
+        if (!p.da_t) return;
+        __syncthreads();
+        store_flipped<T>(tile[0], p.da_t, mp, row0, (int)mp, col0, p.n, t);
+        store_flipped<T>(tile[1], p.db_t, mp, row0, (int)mp, col0, p.n, t);
+        return;
     }
+    id -= flips_m * flips_n;
+    const void *src = p.x;
+    void *dst = p.x_t;
+    int64_t stride = p.x_stride, out = mp;
+    int rows = p.m, vec = p.x_vec;
+    if (id < 2 * flips_n * flips_k) {
+        const int which = id / (flips_n * flips_k);
+        id -= which * flips_n * flips_k;
+        src = which ? p.wu : p.wg;
+        dst = which ? p.wu_t : p.wg_t;
+        stride = p.k;
+        out = np;
+        rows = p.n;
+        vec = p.w_vec;
+    } else {
+        id -= 2 * flips_n * flips_k;
+    }
+    if (!dst) return;
+    const int row0 = id / flips_k * kFlip, col0 = id % flips_k * kFlip;
+#pragma unroll
+    for (int c = t; c < kFlip * kFlip / 8; c += 256) {
+        const int r = c / (kFlip / 8), q = (c - r * (kFlip / 8)) * 8;
+        float v[8] = {};
+        if (row0 + r < rows && col0 + q < p.k)
+            load8<T>((const raw_t *)src + (row0 + r) * stride, col0 + q, p.k, vec, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tile[0][r][q + j] = to_bits<T>(v[j]);
+    }
+    __syncthreads();
+    store_flipped<T>(tile[0], dst, out, row0, (int)out, col0, p.k, t);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -404,14 +551,14 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gated_skinny(GatedParams p)
     typedef typename T::raw_t raw_t;
     __shared__ f32x4_t part[kSkinnyWaves][2 * RG][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = (int)blockIdx.x * 16, row = lane & 15, steps = (p.k + 31) / 32;
+    const int n0 = (int)blockIdx.x * 16, row0 = (int)blockIdx.y * (16 * RG), row = lane & 15, steps = (p.k + 31) / 32;
     const bool on = n0 + row < p.n;
     const raw_t *const wg = (const raw_t *)p.n0 + (int64_t)(n0 + row) * p.k;
     const raw_t *const wu = (const raw_t *)p.n1 + (int64_t)(n0 + row) * p.k;
     f32x4_t acc[2 * RG];
 #pragma unroll
     for (int i = 0; i < 2 * RG; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const bool nvec = p.n_mode == kWide, mvec = p.m_mode == kWide;
+    const bool nvec = p.n_vec, mvec = p.m_vec;
     for (int s0 = wave; s0 < steps; s0 += kSkinnyWaves * kSkinnyAhead) {
         Frag<T> g[kSkinnyAhead], u[kSkinnyAhead];
 #pragma unroll
@@ -425,7 +572,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gated_skinny(GatedParams p)
             const int k = (s0 + j * kSkinnyWaves) * 32 + 8 * (lane >> 4);
 #pragma unroll
             for (int i = 0; i < RG; ++i) {
-                const int m = 16 * i + row;
+                const int m = row0 + 16 * i + row;
                 const Frag<T> x = frag_global<T>((const raw_t *)p.m0 + m * p.m_stride, k, p.k, m < p.m, mvec);
                 acc[2 * i] = mma16<T>(acc[2 * i], g[j], x);
                 acc[2 * i + 1] = mma16<T>(acc[2 * i + 1], u[j], x);
@@ -437,12 +584,12 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gated_skinny(GatedParams p)
     __syncthreads();
     // one element of Y a thread: row m of X, hidden unit n
     for (int i = threadIdx.x; i < 256 * RG; i += 64 * kSkinnyWaves) {
-        const int m = i >> 4, n = i & 15, from = (n >> 2) * 16 + (m & 15);
+        const int r = i >> 4, m = row0 + r, n = i & 15, from = (n >> 2) * 16 + (r & 15);
         float a = 0.0f, b = 0.0f, slope;
 #pragma unroll
         for (int w = 0; w < kSkinnyWaves; ++w) {
-            a += part[w][2 * (m >> 4)][from][n & 3];
-            b += part[w][2 * (m >> 4) + 1][from][n & 3];
+            a += part[w][2 * (r >> 4)][from][n & 3];
+            b += part[w][2 * (r >> 4) + 1][from][n & 3];
         }
         if (m >= p.m || n0 + n >= p.n) continue;
         const int64_t at = (int64_t)m * p.n + n0 + n;
@@ -477,22 +624,24 @@ Shape shape_of(int mode, int dtype, int64_t m, int64_t n, int64_t k) {
         s.blocks = (int64_t)planes * s.tiles_m * s.tiles_n;
         if (s.big == 0 || s.blocks >= 200) break;
     }
-    const int64_t steps = (int64_t)tiles_of(k, dtype == 0 ? 32 : 64) * (mode == kInput ? 2 : 1);
+    const int64_t steps = (int64_t)tiles_of(k, 32) * (mode == kInput ? 2 : 1);
     s.parts = 1;
     if (s.blocks < 192) {
         int64_t parts = 512 / s.blocks;
-        if (parts > steps / 4) parts = steps / 4;
+        if (parts > steps / 8) parts = steps / 8;
         if (parts > 64) parts = 64;
         if (parts > 1) s.parts = (int)parts;
     }
     s.blocks *= s.parts;
+    (void)dtype;
     return s;
 }
 
-template <typename T, int MODE, int SIZE, int WM, int WN>
+template <typename T, int MODE, int SIZE>
 int launch_tiles(const GatedParams &p, hipStream_t stream) {
+    constexpr int WM = 2, WN = 2;
     const auto fn = gated_product<T, MODE, SIZE, SIZE, WM, WN>;
-    const int smem = 2 * 2 * SIZE * 128;
+    const int smem = 2 * 2 * SIZE * 128;             // the tiles of both operands
     const hipError_t e = hipFuncSetAttribute((const void *)fn, hipFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != hipSuccess) return (int)e;
     hipLaunchKernelGGL(fn, dim3((unsigned)((p.blocks + 7) / 8 * 8)), dim3(64 * WM * WN), smem, stream, p);
@@ -506,7 +655,7 @@ int product(GatedParams p, int dtype, hipStream_t stream) {
     p.tiles_n = s.tiles_n;
     p.parts = p.partial ? s.parts : 1;
     p.blocks = (int)(s.blocks / s.parts * p.parts);
-    const int e = s.big ? launch_tiles<T, MODE, 256, 2, 4>(p, stream) : launch_tiles<T, MODE, 128, 2, 2>(p, stream);
+    const int e = s.big ? launch_tiles<T, MODE, 256>(p, stream) : launch_tiles<T, MODE, 128>(p, stream);
     if (e || p.parts == 1) return e;
     const int64_t items = (MODE == kWeights ? 2 : 1) * (int64_t)p.m * ((p.n + 7) / 8), blocks = (items + 255) / 256;
     hipLaunchKernelGGL((gated_join<T, MODE>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, p);
@@ -514,22 +663,45 @@ int product(GatedParams p, int dtype, hipStream_t stream) {
 }
 
 template <typename T>
-int run(const GatedParams &p, int mode, int dtype, hipStream_t stream) {
-    if (mode == kGatedForward) {
-        if (p.m <= kSkinnyRows) {
-            const dim3 grid((unsigned)tiles_of(p.n, 16)), block(64 * kSkinnyWaves);
-            if (p.m <= 16) hipLaunchKernelGGL((gated_skinny<T, 1>), grid, block, 0, stream, p);
-            else if (p.m <= 32) hipLaunchKernelGGL((gated_skinny<T, 2>), grid, block, 0, stream, p);
-            else hipLaunchKernelGGL((gated_skinny<T, 4>), grid, block, 0, stream, p);
-            return (int)hipGetLastError();
-        }
-        return product<T, kForward>(p, dtype, stream);
-    }
-    if (mode == kGatedInput) return product<T, kInput>(p, dtype, stream);
-    if (mode == kGatedWeights) return product<T, kWeights>(p, dtype, stream);
-    const int64_t items = (int64_t)p.m * ((p.n + 7) / 8), blocks = (items + 255) / 256;
-    hipLaunchKernelGGL(gated_gradients<T>, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, stream, p);
+int few_rows(const GatedParams &p, hipStream_t stream) {
+    const dim3 grid((unsigned)tiles_of(p.n, 16), (unsigned)tiles_of(p.m, kSkinnyRows)), block(64 * kSkinnyWaves);
+    if (p.m <= 16) hipLaunchKernelGGL((gated_skinny<T, 1>), grid, block, 0, stream, p);
+    else if (p.m <= 32) hipLaunchKernelGGL((gated_skinny<T, 2>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((gated_skinny<T, 4>), grid, block, 0, stream, p);
     return (int)hipGetLastError();
+}
+
+template <typename T>
+int forward(GatedParams p, int dtype, hipStream_t stream) {
+    const bool aligned = p.n_vec && p.m_vec;
+    if (p.m <= kSkinnyRows || (!aligned && !p.packed)) return few_rows<T>(p, stream);
+    if (!aligned) {
+        GatedParams q = p;
+        q.out0 = p.packed;
+        const int64_t items = ((int64_t)p.m + 2 * (int64_t)p.n) * ((p.k + 7) / 8), blocks = (items + 255) / 256;
+        hipLaunchKernelGGL(gated_pack<T>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, q);
+        if (const int e = (int)hipGetLastError()) return e;
+        const int64_t width = ((int64_t)p.k + 7) / 8 * 8;
+        p.m0 = p.packed;
+        p.n0 = (typename T::raw_t *)p.packed + p.m * width;
+        p.n1 = (typename T::raw_t *)p.packed + (p.m + (int64_t)p.n) * width;
+        p.m_stride = p.n_stride = width;
+    }
+    return product<T, kForward>(p, dtype, stream);
+}
+
+template <typename T>
+int prepare(const FlipParams &p, hipStream_t stream) {
+    const int64_t m = tiles_of(p.m, kFlip), n = tiles_of(p.n, kFlip), k = tiles_of(p.k, kFlip);
+    hipLaunchKernelGGL(gated_prepare<T>, dim3((unsigned)(m * n + 2 * n * k + (p.x_t ? m * k : 0))), dim3(256), 0, stream, p);
+    return (int)hipGetLastError();
+}
+
+template <typename T>
+int run(const GatedParams &p, int mode, int dtype, hipStream_t stream) {
+    if (mode == kGatedForward) return forward<T>(p, dtype, stream);
+    if (mode == kGatedInput) return product<T, kInput>(p, dtype, stream);
+    return product<T, kWeights>(p, dtype, stream);
 }
 
 }  // namespace
@@ -538,18 +710,30 @@ int run(const GatedParams &p, int mode, int dtype, hipStream_t stream) {
 int64_t gated_partial_floats(int mode, int dtype, int64_t m, int64_t n, int64_t k) {
     if (m == 0 || n == 0 || (mode == kGatedForward && m <= kSkinnyRows)) return 0;
     const Shape s = shape_of(mode, dtype, m, n, k);
-    if (s.parts == 1) return 0;
-    return (int64_t)s.parts * (mode == kGatedInput ? 1 : 2) * m * ((n + 7) / 8 * 8);
+    return s.parts == 1 ? 0 : (int64_t)s.parts * (mode == kGatedInput ? 1 : 2) * m * ((n + 7) / 8 * 8);
 }
+
+bool gated_packs(int64_t rows) { return rows > kSkinnyRows; }
 
 int64_t gated_blocks(int mode, int dtype, int64_t m, int64_t n, int64_t k) {
     return m == 0 || n == 0 ? 0 : shape_of(mode, dtype, m, n, k).blocks;
+}
+
+int64_t gated_flips(int64_t m, int64_t n, int64_t k) {
+    const int64_t a = tiles_of(m, kFlip), b = tiles_of(n, kFlip), c = tiles_of(k, kFlip);
+    return a * b + 2 * b * c + a * c;
 }
 
 int launch_gated(const GatedParams &p, int mode, int dtype, hipStream_t stream) {
     if (dtype == 0) return run<F32>(p, mode, dtype, stream);
     if (dtype == 1) return run<F16>(p, mode, dtype, stream);
     return run<BF16>(p, mode, dtype, stream);
+}
+
+int launch_gated_prepare(const FlipParams &p, int dtype, hipStream_t stream) {
+    if (dtype == 0) return prepare<F32>(p, stream);
+    if (dtype == 1) return prepare<F16>(p, stream);
+    return prepare<BF16>(p, stream);
 }
 
 }  // namespace gs

@@ -75,27 +75,40 @@ AttnPlan plan_forward(const AttnParams &p, int dtype, bool workspace);
 AttnPlan plan_backward_q(const AttnParams &p, int dtype);
 AttnPlan plan_backward_kv(const AttnParams &p, int dtype);
 
-// One product of the gated projections, out[m][n] = sum over k of M(m, k) N(n, k),
-// or its elementwise step (see gs_gated.hip).  kGatedForward: m rows, n hidden
-// units, k the width; kGatedInput: m rows, n the width, k the hidden units;
-// kGatedWeights: m hidden units, n the width, k rows; kGatedGradients: m rows,
-// n hidden units.
-enum { kGatedForward = 0, kGatedInput = 1, kGatedWeights = 2, kGatedGradients = 3 };
+// One product of the gated projections, out[m][n] = sum over k of M(m, k) N(n, k)
+// (see gs_gated.hip).  kGatedForward: m rows, n hidden units, k the width;
+// kGatedInput: m rows, n the width, k the hidden units; kGatedWeights: m hidden
+// units, n the width, k rows.
+enum { kGatedForward = 0, kGatedInput = 1, kGatedWeights = 2 };
 struct GatedParams {
-    const void *m0, *m1, *n0, *n1, *dy;
+    const void *m0, *m1, *n0, *n1;
     void *out0, *out1;
     float *saved;             // a, b: two planes of rows x hidden
     float *partial;           // sums of the parts of k; null: k is not cut
-    int64_t m_stride, n_stride, out_stride, dy_stride;
+    void *packed;             // forward: X, Wg, Wu in rows of whole chunks of eight
+    int64_t m_stride, n_stride, out_stride;
     int m, n, k;
-    int m_mode, n_mode;       // how tiles of the operands are loaded: by 16 bytes, by 4, by element
-    int out_vec, saved_vec;   // rows of out (of dy) and of `saved` allow 16-byte accesses
+    int m_vec, n_vec;         // forward: rows of X, of Wg and Wu allow 16-byte accesses
+    int out_vec, saved_vec;   // rows of out and of `saved` do
     int activation;
     int tiles_m, tiles_n, parts, blocks;
 };
+// The pass over dY: da, db and the transposed operands (null: not wanted), rows of
+// whole chunks of eight.  m rows, n hidden units, k the width.
+struct FlipParams {
+    const void *dy, *x, *wg, *wu;
+    const float *saved;
+    void *da, *db, *da_t, *db_t, *wg_t, *wu_t, *x_t;
+    int64_t dy_stride, x_stride;
+    int m, n, k, activation;
+    int dy_vec, saved_vec, x_vec, w_vec;
+};
 int64_t gated_partial_floats(int mode, int dtype, int64_t m, int64_t n, int64_t k);
 int64_t gated_blocks(int mode, int dtype, int64_t m, int64_t n, int64_t k);
+int64_t gated_flips(int64_t m, int64_t n, int64_t k);
+bool gated_packs(int64_t rows);
 int launch_gated(const GatedParams &p, int mode, int dtype, hipStream_t stream);
+int launch_gated_prepare(const FlipParams &p, int dtype, hipStream_t stream);
 
 struct JoinParams {
     const void *x, *branch, *gate, *post, *post_bias, *pre, *pre_bias, *d_h, *d_y;

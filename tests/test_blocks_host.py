@@ -129,9 +129,9 @@ def test_gated_linear_refuses(tk):
     bad = [(dict(x=None), 1), (dict(wg=None), 1), (dict(wu=None), 1), (dict(y=None), 1), (dict(rows=-1), 2),
            (dict(width=-1), 2), (dict(hidden=-1), 2), (dict(width=0), 2), (dict(xs=-1), 2), (dict(ys=15), 2),
            (dict(dtype=3), 3), (dict(dtype=-1), 3), (dict(act=4), 4), (dict(act=-1), 4), (dict(n=-1), 4),
-           (dict(ws=ctypes.c_void_p(0x1010), n=512), 4), (dict(rows=2 ** 22 + 1), 6), (dict(width=2 ** 22 + 1), 6),
-           (dict(hidden=2 ** 22 + 1, ys=2 ** 23), 6), (dict(rows=2 ** 20, hidden=2 ** 17, ys=2 ** 17), 6),
-           (dict(hidden=2 ** 22, width=2 ** 22, ys=2 ** 22), 6)]
+           (dict(ws=ctypes.c_void_p(0x1010), n=512), 4), (dict(rows=2 ** 20 + 1), 6), (dict(width=2 ** 20 + 1), 6),
+           (dict(hidden=2 ** 20 + 1, ys=2 ** 23), 6), (dict(rows=2 ** 20, hidden=2 ** 17, ys=2 ** 17), 6),
+           (dict(hidden=2 ** 20, width=2 ** 20, rows=2 ** 16, ys=2 ** 20), 6)]
     for kw, status in bad:
         assert fwd(**kw) == status, kw
     assert fwd(rows=0, x=None, y=None) == 0 and fwd(hidden=0, wg=None, wu=None, y=None) == 0
