@@ -265,7 +265,7 @@ typedef enum {
  * GS_ERR_ATTR (activation, a workspace that is misaligned or of negative
  * size), GS_ERR_TOO_LARGE (rows, width or hidden above 2^20, rows * hidden
  * above 2^36, 2^22 thread blocks or more of a product of the call or of its
- * gradients: a block has 128 by 128 elements or more of an output), GS_ERR_HIP.
+ * gradients: a block has 64 by 64 elements or more of an output), GS_ERR_HIP.
  */
 int gs_gated_linear(const void *X, int dtype, int64_t rows, int64_t width, int64_t hidden, int64_t x_stride,
                     const void *Wg, const void *Wu, int activation, void *Y, int64_t y_stride, float *saved,

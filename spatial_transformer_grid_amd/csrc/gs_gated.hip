@@ -257,7 +257,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gated_product(GatedParams p) {
     // reads, so that the number of loads under way stays the same.)
     static_assert(STEPS % 2 == 0, "a step's registers follow from its number");
     constexpr bool ORDERED = T::bytes == 2;
-    constexpr int TILE_LOADS = OM::LOADS + ON::LOADS, UNDER_WAY = (DEPTH - 2) * TILE_LOADS;
+    // Loads of a tile, and those that may still be under way: when the first tile is
+    // awaited, all but its own; when the next one is, those of the tiles after it, of
+    // the last of which only the first part has been sent.
+    constexpr int TILE_LOADS = OM::LOADS + ON::LOADS, FIRST_PART = OM::LOADS / STEPS + ON::LOADS / STEPS;
+    constexpr int AFTER_FIRST = (DEPTH - 2) * TILE_LOADS, AFTER_NEXT = (DEPTH - 3) * TILE_LOADS + FIRST_PART;
     Frag<T> a[2][TN], b[2][TM];
     const auto read = [&](const raw_t *tile, int step) {
 #pragma unroll
@@ -279,7 +283,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gated_product(GatedParams p) {
     if (s0 < s1) {
 #pragma unroll
         for (int d = 0; d + 1 < DEPTH; ++d) load_all(s0 + d);
-        await<UNDER_WAY>();
+        await<AFTER_FIRST>();
         meet();
         read(lds, 0);
     }
@@ -288,14 +292,14 @@ __global__ __launch_bounds__(64 * WM * WN) void gated_product(GatedParams p) {
         load(s + DEPTH - 1, Int<0>{});
         read(tile, 1);
         multiply(0);
-        if constexpr (ORDERED) interleave<TM * TN, TM + TN, TILE_LOADS / STEPS, TM + TN>();
+        if constexpr (ORDERED) interleave<TM * TN, TM + TN, TILE_LOADS / STEPS, TM * TN % (TM + TN) ? TM * TN : TM + TN>();
         if constexpr (DEPTH == 2) load(s + 1, Int<1>{});
-        await<DEPTH == 2 ? 0 : UNDER_WAY - TILE_LOADS / 2>();
+        await<DEPTH == 2 ? 0 : AFTER_NEXT>();
         meet();
         if constexpr (DEPTH > 2) load(s + DEPTH - 1, Int<1>{});
         read(next, 0);
         multiply(1);
-        if constexpr (ORDERED) interleave<TM * TN, TM + TN, TILE_LOADS / STEPS, TM + TN>();
+        if constexpr (ORDERED) interleave<TM * TN, TM + TN, TILE_LOADS / STEPS, TM * TN % (TM + TN) ? TM * TN : TM + TN>();
     }
     await<0>();
     __syncthreads();
@@ -623,22 +627,21 @@ constexpr int kSkinnyRows = 64;
 
 int tiles_of(int64_t n, int size) { return (int)((n + size - 1) / size); }
 
-// Tiles of the output of a product, 256 or 128 rows and columns each, and the
-// parts of its sum.
+// Tiles of the output of a product, `size` rows and columns each, and the parts of
+// its sum.
 struct Shape {
-    int big, tiles_m, tiles_n, parts;
+    int size, tiles_m, tiles_n, parts;
     int64_t blocks;
 };
 
 Shape shape_of(int mode, int dtype, int64_t m, int64_t n, int64_t k) {
     Shape s = {};
     const int planes = mode == kWeights ? 2 : 1;
-    for (s.big = 1; s.big >= 0; --s.big) {
-        const int size = s.big ? 256 : 128;
-        s.tiles_m = tiles_of(m, size);
-        s.tiles_n = tiles_of(n, mode == kForward ? size / 2 : size);
+    for (s.size = 256;; s.size /= 2) {
+        s.tiles_m = tiles_of(m, s.size);
+        s.tiles_n = tiles_of(n, mode == kForward ? s.size / 2 : s.size);
         s.blocks = (int64_t)planes * s.tiles_m * s.tiles_n;
-        if (s.big == 0 || s.blocks >= 200) break;
+        if (s.size == 64 || s.blocks >= 200) break;
     }
     const int64_t steps = (int64_t)tiles_of(k, 32) * (mode == kInput ? 2 : 1);
     s.parts = 1;
@@ -655,7 +658,8 @@ Shape shape_of(int mode, int dtype, int64_t m, int64_t n, int64_t k) {
 
 template <typename T, int MODE, int SIZE>
 int launch_tiles(const GatedParams &p, hipStream_t stream) {
-    constexpr int WM = 2, WN = SIZE == 256 ? 4 : 2;
+    // (of a forward tile of 64 a wave has 32 columns of Wg and the same of Wu)
+    constexpr int WM = 2, WN = SIZE == 256 ? 4 : SIZE == 64 && MODE == kForward ? 1 : 2;
     const auto fn = gated_product<T, MODE, SIZE, SIZE, WM, WN>;
     const int smem = 2 * 2 * SIZE * 128;             // the tiles of both operands
     const hipError_t e = hipFuncSetAttribute((const void *)fn, hipFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -671,7 +675,8 @@ int product(GatedParams p, int dtype, hipStream_t stream) {
     p.tiles_n = s.tiles_n;
     p.parts = p.partial ? s.parts : 1;
     p.blocks = (int)(s.blocks / s.parts * p.parts);
-    const int e = s.big ? launch_tiles<T, MODE, 256>(p, stream) : launch_tiles<T, MODE, 128>(p, stream);
+    const int e = s.size == 256   ? launch_tiles<T, MODE, 256>(p, stream)
+                  : s.size == 128 ? launch_tiles<T, MODE, 128>(p, stream) : launch_tiles<T, MODE, 64>(p, stream);
     if (e || p.parts == 1) return e;
     const int64_t items = (MODE == kWeights ? 2 : 1) * (int64_t)p.m * ((p.n + 7) / 8), blocks = (items + 255) / 256;
     hipLaunchKernelGGL((gated_join<T, MODE>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, p);
