@@ -25,31 +25,53 @@ constexpr int kThreads = 512;         // of a block whose rows take fewer
 
 constexpr int join_threads(int nt) { return nt < kThreads ? kThreads : nt; }
 
-// Two sums over the NT threads of a row; `red` has room for the waves of a
-// block, twice, and `turn` says which half is used: one barrier a sum, since
-// the other half's readers have passed it.
-template <int NT>
-__device__ __forceinline__ void join_totals(float &a, float &b, float *red, int &turn) {
-    a = lanes_total<(NT < 64 ? NT : 64)>(a);
-    b = lanes_total<(NT < 64 ? NT : 64)>(b);
+// Sums of N values over the NT threads of a row; `red` has room for the waves of a
+// block, two values and twice, and `turn` says which half is used: one barrier a
+// sum, since the other half's readers have passed it.
+template <int NT, int N>
+__device__ __forceinline__ void join_totals(float (&v)[N], float *red, int &turn) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = lanes_sum<(NT < 64 ? NT : 64)>(v[n]);
     if constexpr (NT > 64) {
         constexpr int W = NT / 64, ALL = join_threads(NT) / 64;
         float *at = red + turn * 2 * ALL;
         turn ^= 1;
         const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) {
-            at[wave] = a;
-            at[ALL + wave] = b;
-        }
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int n = 0; n < N; ++n) at[n * ALL + wave] = v[n];
         __syncthreads();
         const int first = wave / W * W;
-        a = b = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            a += at[first + w];
-            b += at[ALL + first + w];
+        for (int n = 0; n < N; ++n) {
+            v[n] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) v[n] += at[n * ALL + first + w];
         }
     }
+}
+
+template <int NT>
+__device__ __forceinline__ float join_total(float v, float *red, int &turn) {
+    float one[1] = {v};
+    join_totals<NT, 1>(one, red, turn);
+    return one[0];
+}
+
+// The means of g and of g z over a row, as their gradients take them off: without
+// `layer` that of g is left out.
+template <int NT>
+__device__ __forceinline__ void gradient_means(float &g, float &gz, int layer, int cols, float *red, int &turn) {
+    if (layer) {
+        float both[2] = {g, gz};
+        join_totals<NT, 2>(both, red, turn);
+        g = both[0] / (float)cols;
+        gz = both[1];
+    } else {
+        g = 0.0f;
+        gz = join_total<NT>(gz, red, turn);
+    }
+    gz /= (float)cols;
 }
 
 // Mean and factor of a row's values v (zeros past its end), which come out as
@@ -57,21 +79,19 @@ __device__ __forceinline__ void join_totals(float &a, float &b, float *red, int 
 template <int NT, int E, bool VEC>
 __device__ __forceinline__ void row_stats(float *v, int layer, int cols, int t, float epsilon, float *red, int &turn,
                                           float &mean, float &inv) {
-    float s = 0.0f, none = 0.0f;
+    float s = 0.0f;
     mean = 0.0f;
     if (layer) {
 #pragma unroll
         for (int e = 0; e < E; ++e) s += v[e];
-        join_totals<NT>(s, none, red, turn);
-        mean = s / (float)cols;
-        s = none = 0.0f;
+        mean = join_total<NT>(s, red, turn) / (float)cols;
+        s = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = column<NT, VEC>(t, e) < cols ? v[e] - mean : 0.0f;
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) s = fmaf(v[e], v[e], s);
-    join_totals<NT>(s, none, red, turn);
-    inv = 1.0f / sqrtf(s / (float)cols + epsilon);
+    inv = 1.0f / sqrtf(join_total<NT>(s, red, turn) / (float)cols + epsilon);
 }
 
 // A row of the gate: ones where there is none.
@@ -87,27 +107,101 @@ __device__ __forceinline__ void load_gate(const JoinParams &p, int64_t row, int 
     }
 }
 
+// A thread's elements of a row as they lie in memory, so that the next row's can be
+// under way while this one is worked on.
+template <typename T, int E, bool VEC>
+struct Held {
+    Frag<T> f[E / 8];
+};
+template <typename T, int E>
+struct Held<T, E, false> {
+    uint32_t e[E];                                   // (half words would be kept in memory)
+};
+
+template <typename T, int NT, int E, bool VEC>
+__device__ __forceinline__ void hold_row(const typename T::raw_t *row, int cols, int t, Held<T, E, VEC> &h) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int e = 0; e < E; e += 8) {
+            const int c = column<NT, true>(t, e);
+            h.f[e / 8] = frag_global<T>(row, c, cols, c < cols, true);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int c = column<NT, false>(t, e);
+            h.e[e] = c < cols ? row[c] : 0;
+        }
+    }
+}
+
+template <typename T, int E, bool VEC>
+__device__ __forceinline__ void held_row(const Held<T, E, VEC> &h, float *v) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = frag_get<T>(h.f[e / 8], e % 8);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = T::from_raw((typename T::raw_t)h.e[e]);
+    }
+}
+
+// What belongs to the columns: kept in registers from row to row where a thread has
+// eight elements, else read for every row.
+template <typename T, int NT, int E, bool VEC>
+struct Columns {
+    static constexpr bool KEPT = E == 8;
+    float v[KEPT ? E : 1];
+    __device__ __forceinline__ void start(const JoinParams &p, const void *src, int t) {
+        if constexpr (KEPT) load_params<T, NT, E, VEC>(src, p.param_f32, p.cols, t, v);
+    }
+    __device__ __forceinline__ void get(const JoinParams &p, const void *src, int t, float *w) const {
+        if constexpr (KEPT) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) w[e] = v[e];
+        } else {
+            load_params<T, NT, E, VEC>(src, p.param_f32, p.cols, t, w);
+        }
+    }
+};
+
 template <typename T, int NT, int E, bool VEC>
 __global__ __launch_bounds__(join_threads(NT)) void residual_norm_rows(JoinParams p) {
     typedef typename T::raw_t raw_t;
     constexpr int ROWS = join_threads(NT) / NT;
+    constexpr bool AHEAD = E == 8;                   // (sixteen elements leave no registers for the next row)
     __shared__ float red[NT > 64 ? 4 * join_threads(NT) / 64 : 1];
     int turn = 0;
-    const int t = threadIdx.x % NT, cols = p.cols;
-    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < p.rows; r0 += (int64_t)gridDim.x * ROWS) {
-        const int64_t r = r0 + threadIdx.x / NT;
-        const bool live = r < p.rows;                // (a block's rows meet the same barriers)
-        const int64_t at = live ? r : p.rows - 1;
+    const int t = threadIdx.x % NT, slot = threadIdx.x / NT, cols = p.cols;
+    Columns<T, NT, E, VEC> post, post_b, pre, pre_b;
+    post.start(p, p.post, t);
+    post_b.start(p, p.post_bias, t);
+    pre.start(p, p.pre, t);
+    pre_b.start(p, p.pre_bias, t);
+    Held<T, E, VEC> nf, nx;
+    const int64_t move = (int64_t)gridDim.x * ROWS;
+    const auto fetch = [&](int64_t r) {
+        if (r >= p.rows) r = p.rows - 1;             // (a block's rows meet the same barriers)
+        hold_row<T, NT, E, VEC>((const raw_t *)p.branch + r * p.branch_stride, cols, t, nf);
+        hold_row<T, NT, E, VEC>((const raw_t *)p.x + r * p.x_stride, cols, t, nx);
+    };
+    int64_t r0 = (int64_t)blockIdx.x * ROWS;
+    if (AHEAD) fetch(r0 + slot);
+    for (; r0 < p.rows; r0 += move) {
+        const int64_t r = r0 + slot;
+        const bool live = r < p.rows;
         float f[E], x[E], m[E];
-        load_row<T, NT, E, VEC>((const raw_t *)p.branch + at * p.branch_stride, cols, t, f);
-        load_row<T, NT, E, VEC>((const raw_t *)p.x + at * p.x_stride, cols, t, x);
-        load_gate<T, NT, E, VEC>(p, p.gate ? at / p.group : 0, t, m);
+        if (!AHEAD) fetch(r);
+        held_row<T, E, VEC>(nf, f);
+        held_row<T, E, VEC>(nx, x);
+        load_gate<T, NT, E, VEC>(p, p.gate ? (live ? r : p.rows - 1) / p.group : 0, t, m);
+        if (AHEAD && r0 + move < p.rows) fetch(r + move);
         float mean_f = 0.0f, inv_f = 1.0f, mean_h = 0.0f, inv_h = 1.0f;
         if (p.post) {
-            float w[E], b[E];
-            load_params<T, NT, E, VEC>(p.post, p.param_f32, cols, t, w);
-            load_params<T, NT, E, VEC>(p.post_bias, p.param_f32, cols, t, b);
             row_stats<NT, E, VEC>(f, p.layer, cols, t, p.epsilon, red, turn, mean_f, inv_f);
+            float w[E], b[E];
+            post.get(p, p.post, t, w);
+            post_b.get(p, p.post_bias, t, b);
 #pragma unroll
             for (int e = 0; e < E; ++e) f[e] = fmaf(f[e] * inv_f, w[e], b[e]);
         }
@@ -115,12 +209,12 @@ __global__ __launch_bounds__(join_threads(NT)) void residual_norm_rows(JoinParam
         for (int e = 0; e < E; ++e) x[e] = fmaf(p.alpha, x[e], m[e] * f[e]);
         if (live) store_row<T, NT, E, VEC>((raw_t *)p.h + r * p.h_stride, cols, t, x);
         if (p.pre) {
-            float w[E], b[E];
-            load_params<T, NT, E, VEC>(p.pre, p.param_f32, cols, t, w);
-            load_params<T, NT, E, VEC>(p.pre_bias, p.param_f32, cols, t, b);
 #pragma unroll
             for (int e = 0; e < E; ++e) x[e] = column<NT, VEC>(t, e) < cols ? x[e] : 0.0f;
             row_stats<NT, E, VEC>(x, p.layer, cols, t, p.epsilon, red, turn, mean_h, inv_h);
+            float w[E], b[E];
+            pre.get(p, p.pre, t, w);
+            pre_b.get(p, p.pre_bias, t, b);
 #pragma unroll
             for (int e = 0; e < E; ++e) x[e] = fmaf(x[e] * inv_h, w[e], b[e]);
             if (live) store_row<T, NT, E, VEC>((raw_t *)p.y + r * p.y_stride, cols, t, x);
@@ -160,126 +254,155 @@ __device__ __forceinline__ void slot_sums(const float *v, float *sums, int t, in
 }
 
 // A block takes whole groups of rows that share a row of the gate, or (parts > 1)
-// one part of one group.
-template <typename T, int NT, int E, bool VEC>
+// one part of one group.  BIAS: the biases' gradients are wanted.
+template <typename T, int NT, int E, bool VEC, bool BIAS>
 __global__ __launch_bounds__(join_threads(NT)) void residual_norm_backward_rows(JoinParams p) {
     typedef typename T::raw_t raw_t;
     constexpr int BT = join_threads(NT), ROWS = BT / NT;
+    constexpr bool AHEAD = E == 8;
     __shared__ float red[NT > 64 ? 4 * BT / 64 : 1];
     __shared__ float sums[ROWS > 1 ? BT * 8 : 1];
     int turn = 0;
     const int t = threadIdx.x % NT, slot = threadIdx.x / NT, cols = p.cols;
-    float s_post[E], s_post_b[E], s_pre[E], s_pre_b[E], s_gate[E];
+    float s_post[E], s_post_b[BIAS ? E : 1], s_pre[E], s_pre_b[BIAS ? E : 1], s_gate[E], m[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_post[e] = s_post_b[e] = s_pre[e] = s_pre_b[e] = 0.0f;
+    for (int e = 0; e < E; ++e) s_post[e] = s_pre[e] = s_gate[e] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < (BIAS ? E : 1); ++e) s_post_b[e] = s_pre_b[e] = 0.0f;
+    Columns<T, NT, E, VEC> post, post_b, pre;
+    post.start(p, p.post, t);
+    post_b.start(p, p.post_bias, t);
+    pre.start(p, p.pre, t);
     const int64_t g0 = p.parts > 1 ? blockIdx.x / p.parts : p.groups * (int64_t)blockIdx.x / gridDim.x;
     const int64_t g1 = p.parts > 1 ? g0 + 1 : p.groups * (int64_t)(blockIdx.x + 1) / gridDim.x;
     const int part = p.parts > 1 ? blockIdx.x % p.parts : 0;
-    for (int64_t g = g0; g < g1; ++g) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) s_gate[e] = 0.0f;
-        const int64_t first = g * p.span + p.span * part / p.parts, end = g * p.span + p.span * (part + 1) / p.parts;
-        for (int64_t r0 = first; r0 < end; r0 += ROWS) {
-            const int64_t r = r0 + slot;
-            const bool live = r < end;
-            const int64_t at = live ? r : end - 1;
-            float f[E], h[E], m[E], d[E], fp[E];
-            const tokens_f32x4 st = *(const tokens_f32x4 *)(p.stats + 4 * at);
-            load_row<T, NT, E, VEC>((const raw_t *)p.branch + at * p.branch_stride, cols, t, f);
-            load_row<T, NT, E, VEC>((const raw_t *)p.x + at * p.x_stride, cols, t, h);
-            load_gate<T, NT, E, VEC>(p, p.gate ? at / p.group : 0, t, m);
-            if (p.d_h) {
-                load_row<T, NT, E, VEC>((const raw_t *)p.d_h + at * p.dh_stride, cols, t, d);
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) d[e] = 0.0f;
-            }
-            // f: normalised branch; fp: what the gate multiplies
-            if (p.post) {
-                float w[E], b[E];
-                load_params<T, NT, E, VEC>(p.post, p.param_f32, cols, t, w);
-                load_params<T, NT, E, VEC>(p.post_bias, p.param_f32, cols, t, b);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    f[e] = column<NT, VEC>(t, e) < cols ? (f[e] - st[0]) * st[1] : 0.0f;
-                    fp[e] = fmaf(f[e], w[e], b[e]);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) fp[e] = f[e];
-            }
-            if (p.pre) {
-                float y[E], w[E], a = 0.0f, c = 0.0f;
-                load_row<T, NT, E, VEC>((const raw_t *)p.d_y + at * p.dy_stride, cols, t, y);
-                load_params<T, NT, E, VEC>(p.pre, p.param_f32, cols, t, w);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float z = fmaf(p.alpha, h[e], m[e] * fp[e]);
-                    h[e] = column<NT, VEC>(t, e) < cols ? (z - st[2]) * st[3] : 0.0f;
-                    if (live) {
-                        s_pre[e] = fmaf(y[e], h[e], s_pre[e]);
-                        s_pre_b[e] += y[e];
-                    }
-                    y[e] *= w[e];
-                    a += y[e];
-                    c = fmaf(y[e], h[e], c);
-                }
-                join_totals<NT>(a, c, red, turn);
-                a = p.layer ? a / (float)cols : 0.0f;
-                c /= (float)cols;
-#pragma unroll
-                for (int e = 0; e < E; ++e) d[e] += st[3] * (y[e] - a - h[e] * c);
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) h[e] = p.alpha * d[e];
-            if (live) store_row<T, NT, E, VEC>((raw_t *)p.dx + r * p.dx_stride, cols, t, h);
-            if (p.dgate) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) h[e] = d[e] * fp[e];
-                if (p.by_token) {
-                    if (live && p.gate_f32)
-                        store_row<F32, NT, E, VEC>((uint32_t *)p.dgate + r * cols, cols, t, h);
-                    else if (live)
-                        store_row<T, NT, E, VEC>((raw_t *)p.dgate + r * cols, cols, t, h);
-                } else if (live) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) s_gate[e] += h[e];
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) d[e] *= m[e];
-            if (p.post) {
-                float w[E], a = 0.0f, c = 0.0f;
-                load_params<T, NT, E, VEC>(p.post, p.param_f32, cols, t, w);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    if (live) {
-                        s_post[e] = fmaf(d[e], f[e], s_post[e]);
-                        s_post_b[e] += d[e];
-                    }
-                    d[e] = column<NT, VEC>(t, e) < cols ? d[e] * w[e] : 0.0f;
-                    a += d[e];
-                    c = fmaf(d[e], f[e], c);
-                }
-                join_totals<NT>(a, c, red, turn);
-                a = p.layer ? a / (float)cols : 0.0f;
-                c /= (float)cols;
-#pragma unroll
-                for (int e = 0; e < E; ++e) d[e] = st[1] * (d[e] - a - f[e] * c);
-            }
-            if (live) store_row<T, NT, E, VEC>((raw_t *)p.dbranch + r * p.dbranch_stride, cols, t, d);
+    const auto first_of = [&](int64_t g) { return g * p.span + p.span * part / p.parts; };
+    const auto end_of = [&](int64_t g) { return g * p.span + p.span * (part + 1) / p.parts; };
+    Held<T, E, VEC> nf, nx, nd, ny;
+    tokens_f32x4 nst;
+    const auto fetch = [&](int64_t first, int64_t end) {
+        const int64_t at = first + slot < end ? first + slot : end - 1;   // (a block's rows meet the same barriers)
+        nst = *(const tokens_f32x4 *)(p.stats + 4 * at);
+        hold_row<T, NT, E, VEC>((const raw_t *)p.branch + at * p.branch_stride, cols, t, nf);
+        hold_row<T, NT, E, VEC>((const raw_t *)p.x + at * p.x_stride, cols, t, nx);
+        if (p.d_h) hold_row<T, NT, E, VEC>((const raw_t *)p.d_h + at * p.dh_stride, cols, t, nd);
+        if (p.pre) hold_row<T, NT, E, VEC>((const raw_t *)p.d_y + at * p.dy_stride, cols, t, ny);
+    };
+    int64_t g = g0, r0 = first_of(g), end = end_of(g);
+    if (g < g1) {
+        if (AHEAD) fetch(r0, end);
+        if (!p.by_token) load_gate<T, NT, E, VEC>(p, g, t, m);
+    }
+    while (g < g1) {
+        int64_t next_g = g, next_r = r0 + ROWS, next_end = end;
+        if (next_r >= end && ++next_g < g1) {
+            next_r = first_of(next_g);
+            next_end = end_of(next_g);
         }
-        if (p.dgate && !p.by_token) {
-            if (p.parts > 1) {
-                float *const out = p.partial + ((int64_t)blockIdx.x * p.vectors + p.vectors - 1) * cols;
-                slot_sums<NT, E, VEC>(s_gate, sums, t, slot, cols, [&](int c, float s) { out[c] = s; });
-            } else {
-                slot_sums<NT, E, VEC>(s_gate, sums, t, slot, cols, [&](int c, float s) {
-                    if (p.gate_f32) ((float *)p.dgate)[g * cols + c] = s;
-                    else ((raw_t *)p.dgate)[g * cols + c] = to_bits<T>(s);
-                });
+        const int64_t r = r0 + slot;
+        const bool live = r < end;
+        if (!AHEAD) fetch(r0, end);
+        const tokens_f32x4 st = nst;
+        float f[E], h[E], d[E], fp[E], y[E];
+        held_row<T, E, VEC>(nf, f);
+        held_row<T, E, VEC>(nx, h);
+        held_row<T, E, VEC>(ny, y);
+        if (p.d_h) {
+            held_row<T, E, VEC>(nd, d);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) d[e] = 0.0f;
+        }
+        if (p.by_token) load_gate<T, NT, E, VEC>(p, live ? r : end - 1, t, m);
+        if (AHEAD && next_g < g1) fetch(next_r, next_end);
+        // f: normalised branch; fp: what the gate multiplies
+        if (p.post) {
+            float w[E], b[E];
+            post.get(p, p.post, t, w);
+            post_b.get(p, p.post_bias, t, b);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                f[e] = column<NT, VEC>(t, e) < cols ? (f[e] - st[0]) * st[1] : 0.0f;
+                fp[e] = fmaf(f[e], w[e], b[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) fp[e] = f[e];
+        }
+        if (p.pre) {
+            float w[E], a = 0.0f, c = 0.0f;
+            pre.get(p, p.pre, t, w);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float z = fmaf(p.alpha, h[e], m[e] * fp[e]);
+                h[e] = column<NT, VEC>(t, e) < cols ? (z - st[2]) * st[3] : 0.0f;
+                if (live) {
+                    s_pre[e] = fmaf(y[e], h[e], s_pre[e]);
+                    if constexpr (BIAS) s_pre_b[e] += y[e];
+                }
+                y[e] *= w[e];
+                a += y[e];
+                c = fmaf(y[e], h[e], c);
+            }
+            gradient_means<NT>(a, c, p.layer, cols, red, turn);
+#pragma unroll
+            for (int e = 0; e < E; ++e) d[e] += st[3] * (y[e] - a - h[e] * c);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) h[e] = p.alpha * d[e];
+        if (live) store_row<T, NT, E, VEC>((raw_t *)p.dx + r * p.dx_stride, cols, t, h);
+        if (p.dgate) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) h[e] = d[e] * fp[e];
+            if (p.by_token) {
+                if (live && p.gate_f32)
+                    store_row<F32, NT, E, VEC>((uint32_t *)p.dgate + r * cols, cols, t, h);
+                else if (live)
+                    store_row<T, NT, E, VEC>((raw_t *)p.dgate + r * cols, cols, t, h);
+            } else if (live) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) s_gate[e] += h[e];
             }
         }
+#pragma unroll
+        for (int e = 0; e < E; ++e) d[e] *= m[e];
+        if (p.post) {
+            float w[E], a = 0.0f, c = 0.0f;
+            post.get(p, p.post, t, w);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (live) {
+                    s_post[e] = fmaf(d[e], f[e], s_post[e]);
+                    if constexpr (BIAS) s_post_b[e] += d[e];
+                }
+                d[e] = column<NT, VEC>(t, e) < cols ? d[e] * w[e] : 0.0f;
+                a += d[e];
+                c = fmaf(d[e], f[e], c);
+            }
+            gradient_means<NT>(a, c, p.layer, cols, red, turn);
+#pragma unroll
+            for (int e = 0; e < E; ++e) d[e] = st[1] * (d[e] - a - f[e] * c);
+        }
+        if (live) store_row<T, NT, E, VEC>((raw_t *)p.dbranch + r * p.dbranch_stride, cols, t, d);
+        if (next_g != g) {
+            if (p.dgate && !p.by_token) {
+                if (p.parts > 1) {
+                    float *const out = p.partial + ((int64_t)blockIdx.x * p.vectors + p.vectors - 1) * cols;
+                    slot_sums<NT, E, VEC>(s_gate, sums, t, slot, cols, [&](int c, float s) { out[c] = s; });
+                } else {
+                    slot_sums<NT, E, VEC>(s_gate, sums, t, slot, cols, [&](int c, float s) {
+                        if (p.gate_f32) ((float *)p.dgate)[g * cols + c] = s;
+                        else ((raw_t *)p.dgate)[g * cols + c] = to_bits<T>(s);
+                    });
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) s_gate[e] = 0.0f;
+            }
+            if (!p.by_token && next_g < g1) load_gate<T, NT, E, VEC>(p, next_g, t, m);
+        }
+        g = next_g;
+        r0 = next_r;
+        end = next_end;
     }
     float *out = p.partial + (int64_t)blockIdx.x * p.vectors * cols;
     const auto put = [&](const float *v, const void *wanted) {
@@ -288,9 +411,9 @@ __global__ __launch_bounds__(join_threads(NT)) void residual_norm_backward_rows(
         out += cols;
     };
     put(s_post, p.dpost);
-    put(s_post_b, p.dpost_bias);
+    if constexpr (BIAS) put(s_post_b, p.dpost_bias);
     put(s_pre, p.dpre);
-    put(s_pre_b, p.dpre_bias);
+    if constexpr (BIAS) put(s_pre_b, p.dpre_bias);
 }
 
 // Sums of the parts: 64 columns a block, sixteen waves with a range of the parts
@@ -302,8 +425,6 @@ __global__ __launch_bounds__(1024) void residual_norm_sums(JoinParams p) {
     __shared__ float red[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = (int)blockIdx.x * 64 + lane;
-    const int wide = (p.cols + 63) / 64;
-    (void)wide;
     void *const outs[4] = {p.dpost, p.dpost_bias, p.dpre, p.dpre_bias};
     int which = 0, left = (int)blockIdx.y;
     for (; which < 4; ++which) {
@@ -347,14 +468,14 @@ __global__ __launch_bounds__(1024) void residual_norm_sums(JoinParams p) {
 
 // --------------------------------------------------------------- launches
 
-// Threads of a row: eight elements each up to 8192 columns.
+// Threads of a row: eight elements each up to 4096 columns, then sixteen.
 int row_threads(int64_t cols) {
     if (cols <= 64) return 8;
     if (cols <= 256) return 32;
     if (cols <= 512) return 64;
     if (cols <= 1024) return 128;
     if (cols <= 2048) return 256;
-    return cols <= 4096 ? 512 : 1024;
+    return cols <= 8192 ? 512 : 1024;
 }
 
 int block_rows(int64_t cols) { return join_threads(row_threads(cols)) / row_threads(cols); }
@@ -365,8 +486,11 @@ template <typename T, int NT, int E>
 void rows_form(const JoinParams &p, bool backward, hipStream_t stream) {
     constexpr int BT = join_threads(NT);
     if (backward) {
-        if (p.vec) hipLaunchKernelGGL((residual_norm_backward_rows<T, NT, E, true>), dim3(p.blocks), dim3(BT), 0, stream, p);
-        else hipLaunchKernelGGL((residual_norm_backward_rows<T, NT, E, false>), dim3(p.blocks), dim3(BT), 0, stream, p);
+        const bool bias = p.dpost_bias || p.dpre_bias;
+        const dim3 grid(p.blocks), block(BT);
+        if (p.vec && bias) hipLaunchKernelGGL((residual_norm_backward_rows<T, NT, E, true, true>), grid, block, 0, stream, p);
+        else if (p.vec) hipLaunchKernelGGL((residual_norm_backward_rows<T, NT, E, true, false>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((residual_norm_backward_rows<T, NT, E, false, true>), grid, block, 0, stream, p);
         return;
     }
     const int64_t blocks = (p.rows + BT / NT - 1) / (BT / NT);
@@ -383,10 +507,11 @@ int rows_launch(const JoinParams &p, bool backward, hipStream_t stream) {
         case 64: rows_form<T, 64, 8>(p, backward, stream); break;
         case 128: rows_form<T, 128, 8>(p, backward, stream); break;
         case 256: rows_form<T, 256, 8>(p, backward, stream); break;
-        case 512: rows_form<T, 512, 8>(p, backward, stream); break;
-        default:
-            if (p.cols <= 8192) rows_form<T, 1024, 8>(p, backward, stream);
-            else rows_form<T, 1024, 16>(p, backward, stream);
+        case 512:
+            if (p.cols <= 4096) rows_form<T, 512, 8>(p, backward, stream);
+            else rows_form<T, 512, 16>(p, backward, stream);
+            break;
+        default: rows_form<T, 1024, 16>(p, backward, stream);
     }
     return (int)hipGetLastError();
 }

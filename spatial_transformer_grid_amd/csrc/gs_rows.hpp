@@ -13,6 +13,30 @@ __device__ __forceinline__ float lanes_total(float v) {
     return v;
 }
 
+// The same sums, bit for bit, without a way through LDS: neighbours, pairs, halves
+// of eight and of sixteen lanes by the lane permutations of an addition (a mirrored
+// lane's partial sum is that of the lane across), then halves of 32 and of the wave.
+template <int CTRL>
+__device__ __forceinline__ float plus_lane(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+template <int N>
+__device__ __forceinline__ float lanes_sum(float v) {
+    static_assert(N == 8 || N == 32 || N == 64, "widths of a row's lanes");
+    v = plus_lane<0xB1>(v);                          // quad_perm [1, 0, 3, 2]
+    v = plus_lane<0x4E>(v);                          // quad_perm [2, 3, 0, 1]
+    v = plus_lane<0x141>(v);                         // row_half_mirror
+    if constexpr (N > 8) {
+        v = plus_lane<0x140>(v);                     // row_mirror
+        const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v),
+                                                        false, false);
+        v = __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+    }
+    if constexpr (N > 32) v += other_half(v);
+    return v;
+}
+
 // Sums over the NT threads of a row, two at once; `red` holds 2 NT / 64 floats
 // where they are more than a wave.
 template <int NT>
