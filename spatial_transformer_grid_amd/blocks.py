@@ -11,6 +11,7 @@ step calls the _backward functions itself.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 from ._binding import GS_F32, _check, _device_tensor, _I, _on_stream, _torch, dtype_code
@@ -53,7 +54,7 @@ def _call(name, device, *args):
     """The entry point on the device's current stream, with that device as the current one."""
     torch = _torch()
     fn = getattr(token_lib(), name)
-    if torch.cuda.current_device() != device.index:
+    if torch._C._cuda_getDevice() != device.index:
         with torch.cuda.device(device):
             status = fn(*args, _stream_handle(device))
     else:
@@ -69,6 +70,34 @@ def _need(name, *args):
     return need.value
 
 
+@functools.lru_cache(maxsize=1024)
+def _need_of(name, *extents):
+    """_need of whole numbers alone, on which it depends: a call of a few microseconds does not ask twice."""
+    return _need(name, *extents)
+
+
+def _parameter(t, name, device):
+    """`t`, contiguous, on GPU `device`, of a small call's checks in few steps."""
+    if t.get_device() != device or not t.is_contiguous():
+        return _device_tensor(t, name, device)
+    return t
+
+
+def _beside(t, name, X, device):
+    """`t` as _tensor(t, name, device, X.dtype, X.shape): in few steps where it is dense."""
+    if t.is_contiguous() and t.get_device() == device and t.dtype == X.dtype and t.shape == X.shape:
+        return t
+    return _tensor(t, name, device, X.dtype, X.shape)
+
+
+def _state(t, name, X, device):
+    if t is None:
+        return None
+    if t.is_contiguous() and t.get_device() == device and t.dtype == _torch().float32 and t.shape == (X.shape[0], X.shape[2]):
+        return t
+    return _tensor(t, name, device, _torch().float32, (X.shape[0], X.shape[2])).contiguous()
+
+
 # ------------------------------------------------------- gated projections
 
 def _projections(X, gate_weight, up_weight, activation):
@@ -78,11 +107,12 @@ def _projections(X, gate_weight, up_weight, activation):
     device, width = X.get_device(), X.shape[-1]
     if gate_weight.dim() != 2 or gate_weight.shape[1] != width or up_weight.shape != gate_weight.shape:
         raise ValueError("gate_weight and up_weight must have one shape (hidden, %d)" % width)
-    gate_weight, up_weight = _device_tensor(gate_weight, "gate_weight", device), _device_tensor(up_weight, "up_weight",
-                                                                                                device)
+    gate_weight = _parameter(gate_weight, "gate_weight", device)
+    up_weight = _parameter(up_weight, "up_weight", device)
     if gate_weight.dtype != X.dtype or up_weight.dtype != X.dtype:
         raise TypeError("gate_weight and up_weight must have X's element type")
-    return X, gate_weight, up_weight, math.prod(X.shape[:-1]), _named(activation, ACTIVATIONS, "activation")
+    rows = X.numel() // width if width else math.prod(X.shape[:-1])
+    return X, gate_weight, up_weight, rows, _named(activation, ACTIVATIONS, "activation")
 
 
 def gated_linear(X, gate_weight, up_weight, activation: str = "silu", return_saved: bool = False, out=None,
@@ -110,7 +140,7 @@ def gated_linear(X, gate_weight, up_weight, activation: str = "silu", return_sav
         Y = out
     saved = torch.empty((2, *shape), dtype=torch.float32, device=device) if return_saved else None
     code = dtype_code(X)
-    need = 0 if workspace is not None else _need("gs_gated_linear_workspace_size", code, rows, width, hidden)
+    need = 0 if workspace is not None else _need_of("gs_gated_linear_workspace_size", code, rows, width, hidden)
     workspace, ws, ws_bytes = _workspace(workspace, need, device)
     _call("gs_gated_linear", device, x.data_ptr(), code, rows, width, hidden, xs, gate_weight.data_ptr(),
           up_weight.data_ptr(), act, Y.data_ptr(), hidden, _address(saved), ws, ws_bytes)
@@ -134,7 +164,8 @@ def gated_linear_backward(dY, X, gate_weight, up_weight, saved, activation: str 
     dX = torch.empty(X.shape, dtype=X.dtype, device=device)
     dgate, dup = torch.empty_like(gate_weight), torch.empty_like(up_weight)
     code = dtype_code(X)
-    need = 0 if workspace is not None else _need("gs_gated_linear_backward_workspace_size", code, rows, width, hidden)
+    need = 0 if workspace is not None else _need_of("gs_gated_linear_backward_workspace_size", code, rows, width,
+                                                       hidden)
     workspace, ws, ws_bytes = _workspace(workspace, need, device)
     _call("gs_gated_linear_backward", device, dy.data_ptr(), x.data_ptr(), code, rows, width, hidden, dys, xs,
           gate_weight.data_ptr(), up_weight.data_ptr(), act, saved.data_ptr(), dX.data_ptr(), width, dgate.data_ptr(),
@@ -151,41 +182,38 @@ def _join(X, branch, post_scale, post_bias, pre_scale, pre_bias, gate, residual_
     if X.dim() < 1:
         raise ValueError("X needs an axis")
     device, cols = X.get_device(), X.shape[-1]
-    branch = _tensor(branch, "branch", device, X.dtype, X.shape)
-    params, kind = [], None
-    for name, t in (("post_scale", post_scale), ("post_bias", post_bias), ("pre_scale", pre_scale),
-                    ("pre_bias", pre_bias)):
+    branch = _beside(branch, "branch", X, device)
+    params, kind = (post_scale, post_bias, pre_scale, pre_bias), None
+    for n, t in enumerate(params):
         if t is not None:
-            t = _device_tensor(t, name, device)
-            if tuple(t.shape) != (cols,):
+            name = ("post_scale", "post_bias", "pre_scale", "pre_bias")[n]
+            u = _parameter(t, name, device)
+            if u is not t:
+                params = (*params[:n], u, *params[n + 1:])
+            if t.dim() != 1 or t.shape[0] != cols:
                 raise ValueError("%s must have shape (%d,)" % (name, cols))
             if t.dtype != X.dtype and t.dtype != torch.float32:
                 raise TypeError("%s must have X's element type or float32" % name)
             if kind is not None and t.dtype != kind:
                 raise TypeError("scales and biases must have one element type")
             kind = t.dtype
-        params.append(t)
-    for scale, bias in (0, 1), (2, 3):
-        if params[bias] is not None and params[scale] is None:
-            raise ValueError("a bias needs its scale")
-    d = ResidualNormDesc()
-    d.dtype = dtype_code(X)
-    d.param_dtype = d.dtype if kind is None or kind == X.dtype else GS_F32
-    d.gate_dtype = d.dtype
-    d.layer = _named(norm, NORMS, "norm")
-    d.rows, d.cols = math.prod(X.shape[:-1]), cols
+    if (post_bias is not None and post_scale is None) or (pre_bias is not None and pre_scale is None):
+        raise ValueError("a bias needs its scale")
+    code, gate_rows = dtype_code(X), 0
+    gate_code = code
     if gate is not None:
-        gate = _device_tensor(gate, "gate", device)
+        gate = _parameter(gate, "gate", device)
         lead = gate.dim() - 1
         if lead < 0 or lead >= X.dim() or tuple(gate.shape) != (*X.shape[:lead], cols):
             raise ValueError("gate must have the shape of X's first axes and its last one")
         if gate.dtype != X.dtype and gate.dtype != torch.float32:
             raise TypeError("gate must have X's element type or float32")
-        d.gate_rows, d.gate_dtype = math.prod(gate.shape[:-1]), dtype_code(gate)
-    d.epsilon, d.residual_scale = epsilon, residual_scale
-    x, d.x_stride = _rows(X)
-    f, d.branch_stride = _rows(branch)
-    d.h_stride = d.y_stride = d.dh_stride = d.dy_stride = d.dx_stride = d.dbranch_stride = cols
+        gate_rows, gate_code = math.prod(gate.shape[:-1]), dtype_code(gate)
+    x, xs = _rows(X)
+    f, fs = _rows(branch)
+    d = ResidualNormDesc(code, code if kind is None or kind == X.dtype else GS_F32, gate_code,
+                         _named(norm, NORMS, "norm"), X.numel() // cols if cols else math.prod(X.shape[:-1]), cols,
+                         gate_rows, xs, fs, cols, cols, cols, cols, cols, cols, epsilon, residual_scale)
     return X, x, f, params, gate, d
 
 
@@ -235,11 +263,11 @@ def residual_norm_backward(dH, dY, X, branch, stats, post_scale=None, pre_scale=
     stats = _tensor(stats, "stats", X.get_device(), torch.float32, (*X.shape[:-1], 4)).contiguous()
     dh = dy = None
     if dH is not None:
-        dh, d.dh_stride = _rows(_tensor(dH, "dH", X.get_device(), X.dtype, X.shape))
+        dh, d.dh_stride = _rows(_beside(dH, "dH", X, X.get_device()))
     if (dY is None) != (pre_scale is None):
         raise ValueError("dY is given exactly where pre_scale is")
     if dY is not None:
-        dy, d.dy_stride = _rows(_tensor(dY, "dY", X.get_device(), X.dtype, X.shape))
+        dy, d.dy_stride = _rows(_beside(dY, "dY", X, X.get_device()))
     dX = torch.empty(X.shape, dtype=X.dtype, device=device)
     dbranch = torch.empty_like(dX)
     dgate = None
@@ -262,6 +290,9 @@ def residual_norm_backward(dH, dY, X, branch, stats, post_scale=None, pre_scale=
 
 def _strides2(t):
     # the stride of an axis of one element addresses nothing
+    if t.is_contiguous():
+        _, n, c = t.shape
+        return n * c, c
     return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
 
 
@@ -270,20 +301,11 @@ def _recurrence(X, G, lengths):
     if X.dim() != 3:
         raise ValueError("X must have shape (batch, length, channels)")
     X = _tensor(X, "X")
-    G = _tensor(G, "G", X.get_device(), X.dtype, X.shape)
+    G = _beside(G, "G", X, X.get_device())
     if lengths is not None:
         lengths = _tensor(lengths, "lengths", X.get_device(), torch.int32, X.shape[:1]).contiguous()
-    d = RecurrenceDesc()
-    d.dtype = dtype_code(X)
-    d.batch, d.length, d.channels = X.shape
-    d.x_stride, d.g_stride = _strides2(X), _strides2(G)
+    d = RecurrenceDesc(dtype_code(X), *X.shape, _strides2(X), _strides2(G))
     return X, G, lengths, d
-
-
-def _state(t, name, X):
-    if t is None:
-        return None
-    return _tensor(t, name, X.get_device(), _torch().float32, (X.shape[0], X.shape[2])).contiguous()
 
 
 def gated_recurrence(X, G, state=None, lengths=None, return_saved: bool = False, last=None, out=None, stream=None,
@@ -303,7 +325,7 @@ def gated_recurrence(X, G, state=None, lengths=None, return_saved: bool = False,
     torch = _torch()
     X, G, lengths, d = _recurrence(X, G, lengths)
     same = last is not None and last is state
-    state = _state(state, "state", X)
+    state = _state(state, "state", X, X.get_device())
     if last is None:
         last = torch.empty((X.shape[0], X.shape[2]), dtype=torch.float32, device=X.device)
     elif (last.get_device() != X.get_device() or last.dtype != torch.float32 or not last.is_contiguous()
@@ -311,13 +333,15 @@ def gated_recurrence(X, G, state=None, lengths=None, return_saved: bool = False,
         raise ValueError("last must be a contiguous float32 tensor of shape (batch, channels) on X's GPU")
     elif same:
         state = last
-    Y = _output(out, X, False)
+    Y = torch.empty_like(X) if out is None and X.is_contiguous() else _output(out, X, False)
     d.y_stride = _strides2(Y)
     saved = None
     if return_saved:
         chunks = -(-X.shape[1] // RECURRENCE_CHUNK)
         saved = torch.empty((X.shape[0], chunks, X.shape[2]), dtype=torch.float32, device=X.device)
-    need = 0 if workspace is not None else _need("gs_gated_recurrence_workspace_size", ctypes.byref(d))
+    # (a sequence of at most 2048 tokens is not split)
+    need = 0 if workspace is not None or X.shape[1] <= 2048 else _need("gs_gated_recurrence_workspace_size",
+                                                                       ctypes.byref(d))
     workspace, ws, ws_bytes = _workspace(workspace, need, X.device)
     _call("gs_gated_recurrence", X.device, ctypes.byref(d), X.data_ptr(), G.data_ptr(), _address(state),
           _address(lengths), Y.data_ptr(), last.data_ptr(), _address(saved), ws, ws_bytes)
@@ -331,14 +355,16 @@ def gated_recurrence_backward(dY, X, G, saved, dlast=None, lengths=None, stream=
         return _on_stream(stream, gated_recurrence_backward, dY, X, G, saved, dlast, lengths, workspace=workspace)
     torch = _torch()
     X, G, lengths, d = _recurrence(X, G, lengths)
-    dY = _tensor(dY, "dY", X.get_device(), X.dtype, X.shape)
+    dY = _beside(dY, "dY", X, X.get_device())
     chunks = -(-X.shape[1] // RECURRENCE_CHUNK)
     saved = _tensor(saved, "saved", X.get_device(), torch.float32, (X.shape[0], chunks, X.shape[2])).contiguous()
-    dlast = _state(dlast, "dlast", X)
-    dX, dG = _like(X), _like(G)
+    dlast = _state(dlast, "dlast", X, X.get_device())
+    dX = torch.empty_like(X) if X.is_contiguous() else _like(X)
+    dG = torch.empty_like(G) if G.is_contiguous() else _like(G)
     dstate = torch.empty((X.shape[0], X.shape[2]), dtype=torch.float32, device=X.device)
     d.dy_stride, d.dx_stride, d.dg_stride = _strides2(dY), _strides2(dX), _strides2(dG)
-    need = 0 if workspace is not None else _need("gs_gated_recurrence_backward_workspace_size", ctypes.byref(d))
+    need = 0 if workspace is not None or X.shape[1] <= 2048 else _need("gs_gated_recurrence_backward_workspace_size",
+                                                                       ctypes.byref(d))
     workspace, ws, ws_bytes = _workspace(workspace, need, X.device)
     _call("gs_gated_recurrence_backward", X.device, ctypes.byref(d), dY.data_ptr(), X.data_ptr(), G.data_ptr(),
           saved.data_ptr(), _address(dlast), _address(lengths), dX.data_ptr(), dG.data_ptr(), dstate.data_ptr(), ws,
