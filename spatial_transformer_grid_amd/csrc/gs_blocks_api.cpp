@@ -42,10 +42,10 @@ int gated_extents(int dtype, int64_t rows, int64_t width, int64_t hidden) {
 bool gated_activation(int a) { return a >= GS_ACT_SILU && a <= GS_ACT_RELU; }
 
 // Whether rows of `n` elements, `stride` apart, allow 16-byte accesses.  (Tiles are
-// loaded by 32-bit offsets, 256 rows of them.)
+// loaded by 32-bit offsets, 256 rows of them: 2^30 bytes.)
 bool rows_vec(int dtype, const void *p, int64_t n, int64_t stride) {
     const int bytes = dtype_bytes(dtype);
-    return n * bytes % 16 == 0 && stride * bytes % 16 == 0 && stride * bytes < (int64_t(1) << 23) && stride >= n && aligned(p, 16);
+    return n * bytes % 16 == 0 && stride * bytes % 16 == 0 && stride * bytes <= (int64_t(1) << 22) && stride >= n && aligned(p, 16);
 }
 
 int64_t whole(int64_t n) { return (n + 7) / 8 * 8; }
@@ -66,7 +66,8 @@ GatedForwardSpace gated_forward_space(int dtype, int64_t rows, int64_t width, in
 // Workspace of a backward call (see FlipParams), then the parts' sums of one
 // product or the other.
 struct GatedSpace {
-    int64_t da, db, da_t, db_t, wg_t, wu_t, x_t, partial, bytes;
+    int64_t da, db, da_t, db_t, rest, wg_t, wu_t, x_t, partial, bytes;   // rest: da .. db_t once more
+    bool precise;
 };
 
 GatedSpace gated_space(int dtype, int64_t rows, int64_t width, int64_t hidden) {
@@ -80,7 +81,9 @@ GatedSpace gated_space(int dtype, int64_t rows, int64_t width, int64_t hidden) {
     s.db = plane;
     s.da_t = 2 * plane;
     s.db_t = s.da_t + turned;
-    s.wg_t = s.db_t + turned;
+    s.rest = s.db_t + turned;
+    s.precise = gs::gated_precise(dtype, rows, width, hidden);
+    s.wg_t = s.precise ? 2 * s.rest : s.rest;
     s.wu_t = s.wg_t + weight;
     s.x_t = s.wu_t + weight;
     s.partial = s.x_t + round_ws(width * whole(rows) * size);
@@ -277,6 +280,7 @@ int gs_gated_linear_backward(const void *dY, const void *X, int dtype, int64_t r
         if (workspace_bytes < space.bytes || (uintptr_t)workspace % kWsAlign) return GS_ERR_ATTR;
     }
     char *const ws = (char *)workspace;
+    char *const rest = space.precise ? ws + space.rest : nullptr;
     const int64_t np = whole(hidden), mp = whole(rows);
     if (both) {
         gs::FlipParams p = {};
@@ -290,12 +294,17 @@ int gs_gated_linear_backward(const void *dY, const void *X, int dtype, int64_t r
             p.db = ws + space.db;
             p.wg_t = ws + space.wg_t;
             p.wu_t = ws + space.wu_t;
+            p.da_rest = rest ? rest + space.da : nullptr;
+            p.db_rest = rest ? rest + space.db : nullptr;
         }
         if (weights) {
             p.da_t = ws + space.da_t;
             p.db_t = ws + space.db_t;
             p.x_t = ws + space.x_t;
+            p.da_t_rest = rest ? rest + space.da_t : nullptr;
+            p.db_t_rest = rest ? rest + space.db_t : nullptr;
         }
+        p.precise = rest != nullptr;
         p.dy_stride = dy_stride;
         p.x_stride = x_stride;
         p.m = (int)rows;
@@ -314,6 +323,8 @@ int gs_gated_linear_backward(const void *dY, const void *X, int dtype, int64_t r
     if (input) {
         p.m0 = ws + space.da;
         p.m1 = ws + space.db;
+        p.m0_rest = rest ? rest + space.da : nullptr;
+        p.m1_rest = rest ? rest + space.db : nullptr;
         p.n0 = ws + space.wg_t;
         p.n1 = ws + space.wu_t;
         p.out0 = dX;
@@ -330,6 +341,8 @@ int gs_gated_linear_backward(const void *dY, const void *X, int dtype, int64_t r
     if (weights) {
         p.m0 = ws + space.da_t;
         p.m1 = ws + space.db_t;
+        p.m0_rest = rest ? rest + space.da_t : nullptr;
+        p.m1_rest = rest ? rest + space.db_t : nullptr;
         p.n0 = p.n1 = ws + space.x_t;
         p.out0 = dWg;
         p.out1 = dWu;

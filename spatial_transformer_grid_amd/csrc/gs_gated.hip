@@ -7,6 +7,7 @@
 //             holds a and b of the same elements and Y needs no second pass
 //   dX        M = da, then db  N = Wg^T, then Wu^T: one sum over both
 //   dWg, dWu  M = da^T, db^T   N = X^T
+// (small ones once more with what the rounding of da and db left, see `precise`).
 // The transposed copies are made by the pass over dY that makes da and db, tile by
 // tile through LDS.  (Reading the tiles of the products transposed instead saves
 // that traffic, but the compiler waits for every load under way before each
@@ -100,28 +101,40 @@ struct Operand {
     typedef Tile<T, BK> L;
     static_assert(NT % CPR == 0 && STEP % 16 == 0, "the order of a row's chunks repeats every 16 rows");
 
-    // Part PART of PARTS of the tile at row row0 of `rows` and contracted index k0 of
-    // ks, `stride` elements a row (whole 16-byte chunks, as is what lies past ks).
+    // What stays from tile to tile: rows of `stride` elements from row row0 of `rows`
+    // (whole 16-byte chunks, 2^22 bytes at most, as is what lies past the contracted
+    // axis' end); a thread's first chunk.
+    struct Rows {
+        int reach, step, col;                        // bytes to the last row; of STEP rows; the chunk's column
+        uint32_t at;
+    };
+    __device__ __forceinline__ static Rows rows_of(int64_t stride, int row0, int rows, int t) {
+        const int64_t reach = (int64_t)(rows - row0 - 1) * stride * T::bytes;
+        const int line = t / CPR, col = ((t - line * CPR) ^ L::turn(line)) * EPC;
+        return {(int)(reach < kReach ? reach : kReach), STEP * (int)stride * T::bytes, col,
+                (uint32_t)(line * (int)stride + col) * T::bytes};
+    }
+    static constexpr int64_t kReach = (1 << 30) + (1 << 23);   // past any row of a tile
+
+    // Part PART of PARTS of the tile at contracted index k0 of ks; `base` is row row0.
     // HALVES: the upper half of the tile's rows is the same rows of `base2`.  Rows past
     // the last one lie past the descriptor's range, which ends with the last one's last
     // chunk; chunks past ks take an offset that is out of range.  (The offset is whole in
     // the vector register: the range is checked against that.)
     template <bool HALVES, int PART, int PARTS>
-    __device__ __forceinline__ static void load(raw_t *lds, const raw_t *base, const raw_t *base2, int64_t stride,
-                                                int row0, int rows, int k0, int ks, int t) {
+    __device__ __forceinline__ static void load(raw_t *lds, const raw_t *base, const raw_t *base2, const Rows &w, int k0,
+                                                int ks, int t) {
         constexpr int H = HALVES ? ROWS / 2 : ROWS;
-        const int64_t first = row0 * stride + k0;
-        const int64_t range = ((int64_t)(rows - row0 - 1) * stride + (ks - k0 + EPC - 1) / EPC * EPC) * T::bytes;
-        const int bytes = rows <= row0 || ks <= k0 ? 0 : (int)(range < 0x7fffffff ? range : 0x7fffffff);
-        const rsrc_t r1 = __builtin_amdgcn_make_buffer_rsrc((void *)(base + first), 0, bytes, kRsrcWord3);
-        const rsrc_t r2 = HALVES ? __builtin_amdgcn_make_buffer_rsrc((void *)(base2 + first), 0, bytes, kRsrcWord3) : r1;
-        const int line = t / CPR, col = ((t - line * CPR) ^ L::turn(line)) * EPC;
-        const uint32_t at = col < ks - k0 ? (uint32_t)(line * (int)stride + col) * T::bytes : GS_OOB;
+        static_assert(!HALVES || H % STEP == 0, "a load lies in one half");
+        const int bytes = ks <= k0 || w.reach < 0 ? 0 : w.reach + (ks - k0 + EPC - 1) / EPC * EPC * T::bytes;
+        const rsrc_t r1 = __builtin_amdgcn_make_buffer_rsrc((void *)(base + k0), 0, bytes, kRsrcWord3);
+        const rsrc_t r2 = HALVES ? __builtin_amdgcn_make_buffer_rsrc((void *)(base2 + k0), 0, bytes, kRsrcWord3) : r1;
+        const uint32_t at = w.col < ks - k0 ? w.at : GS_OOB;
 #pragma unroll
         for (int n = LOADS * PART / PARTS; n < LOADS * (PART + 1) / PARTS; ++n) {
-            const int l = n * STEP;
-            const bool upper = HALVES && l >= H;
-            const uint32_t off = at + (uint32_t)((upper ? l - H : l) * (int)stride) * T::bytes;
+            constexpr int HALF_LOADS = H / STEP;
+            const bool upper = HALVES && n >= HALF_LOADS;
+            const uint32_t off = at + (uint32_t)((upper ? n - HALF_LOADS : n) * w.step);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 upper ? r2 : r1, (__attribute__((address_space(3))) void *)(lds + ((t & ~63) + n * NT) * EPC), 16, (int)off, 0,
                 0, 0);
@@ -224,17 +237,37 @@ __global__ __launch_bounds__(64 * WM * WN) void gated_product(GatedParams p) {
     id -= group * 8 * p.tiles_n;
     const int m0 = (first + id % high) * BM, n0 = id / high * COLS;
 
-    // the contracted axis in tiles: all of da and Wg, then all of db and Wu
-    const int per_half = (p.k + BK - 1) / BK, all = MODE == kInput ? 2 * per_half : per_half;
+    // The contracted axis in tiles, pair after pair of operands: da and Wg, db and Wu
+    // (dX), then the remainders of da and db with the same where there are any.
+    const int per_pair = (p.k + BK - 1) / BK, all = p.pairs * per_pair;
     const int s0 = (int)((int64_t)all * part / p.parts), s1 = (int)((int64_t)all * (part + 1) / p.parts);
-    const auto load = [&](int s, auto part) {
+    // The tile that is loaded next: its place in LDS, its pair of operands and its
+    // first index.  Past the last tile the index lies past the axis' end.
+    const typename OM::Rows mrows = OM::rows_of(p.m_stride, m0, p.m, t);
+    const typename ON::Rows nrows = ON::rows_of(p.n_stride, n0, p.n, t);
+    const raw_t *mb, *nb, *nb2 = (const raw_t *)p.n1 + n0 * p.n_stride;
+    int slot = 0, pair = per_pair > 0 ? s0 / per_pair : 0, k0 = (s0 - pair * per_pair) * BK;
+    const auto choose = [&]() {
+        const bool second = MODE == kWeights ? which == 1 : MODE == kInput && (pair & 1) == 1;
+        const bool rest = MODE == kWeights ? pair == 1 : MODE == kInput && pair > 1;
+        mb = (const raw_t *)(second ? (rest ? p.m1_rest : p.m1) : (rest ? p.m0_rest : p.m0)) + m0 * p.m_stride;
+        nb = (const raw_t *)(MODE == kInput && second ? p.n1 : p.n0) + n0 * p.n_stride;
+    };
+    choose();
+    const auto load = [&](auto part) {
         constexpr int PART = decltype(part)::value;
-        raw_t *const to = lds + (unsigned)(s - s0) % DEPTH * STAGE;
-        const int half = MODE == kInput && s >= per_half ? 1 : 0, k0 = (s - half * per_half) * BK;
-        const raw_t *const mb = (const raw_t *)(MODE == kWeights ? (which ? p.m1 : p.m0) : half ? p.m1 : p.m0);
-        OM::template load<false, PART, STEPS>(to, mb, mb, p.m_stride, m0, p.m, k0, p.k, t);
-        const raw_t *const nb = (const raw_t *)(half ? p.n1 : p.n0);
-        ON::template load<MODE == kForward, PART, STEPS>(to + BM * BK, nb, (const raw_t *)p.n1, p.n_stride, n0, p.n, k0, p.k, t);
+        raw_t *const to = lds + slot * STAGE;
+        OM::template load<false, PART, STEPS>(to, mb, mb, mrows, k0, p.k, t);
+        ON::template load<MODE == kForward, PART, STEPS>(to + BM * BK, nb, nb2, nrows, k0, p.k, t);
+        if constexpr (PART + 1 == STEPS) {
+            slot = (slot + 1) % DEPTH;
+            k0 += BK;
+            if (MODE != kForward && k0 >= p.k && pair + 1 < p.pairs) {
+                k0 = 0;
+                ++pair;
+                choose();
+            }
+        }
     };
     f32x16 acc[TM][TN];
 #pragma unroll
@@ -275,28 +308,30 @@ __global__ __launch_bounds__(64 * WM * WN) void gated_product(GatedParams p) {
 #pragma unroll
             for (int j = 0; j < TN; ++j) mma<T>(acc[i][j], a[step & 1][j], b[step & 1][i]);
     };
-    const auto load_all = [&](int s) {
-        load(s, Int<0>{});
-        if constexpr (STEPS > 1) load(s, Int<1>{});
-        static_assert(STEPS == 2, "all parts");
-    };
+    static_assert(STEPS == 2, "a tile is loaded in two parts");
     if (s0 < s1) {
 #pragma unroll
-        for (int d = 0; d + 1 < DEPTH; ++d) load_all(s0 + d);
+        for (int d = 0; d + 1 < DEPTH; ++d) {
+            load(Int<0>{});
+            load(Int<1>{});
+        }
         await<AFTER_FIRST>();
         meet();
         read(lds, 0);
     }
+    int at = 0;
     for (int s = s0; s < s1; ++s) {
-        const raw_t *const tile = lds + (unsigned)(s - s0) % DEPTH * STAGE, *const next = lds + (unsigned)(s - s0 + 1) % DEPTH * STAGE;
-        load(s + DEPTH - 1, Int<0>{});
+        const raw_t *const tile = lds + at * STAGE;
+        at = (at + 1) % DEPTH;
+        const raw_t *const next = lds + at * STAGE;
+        load(Int<0>{});
         read(tile, 1);
         multiply(0);
         if constexpr (ORDERED) interleave<TM * TN, TM + TN, TILE_LOADS / STEPS, TM * TN % (TM + TN) ? TM * TN : TM + TN>();
-        if constexpr (DEPTH == 2) load(s + 1, Int<1>{});
+        if constexpr (DEPTH == 2) load(Int<1>{});
         await<DEPTH == 2 ? 0 : AFTER_NEXT>();
         meet();
-        if constexpr (DEPTH > 2) load(s + DEPTH - 1, Int<1>{});
+        if constexpr (DEPTH > 2) load(Int<1>{});
         read(next, 0);
         multiply(1);
         if constexpr (ORDERED) interleave<TM * TN, TM + TN, TILE_LOADS / STEPS, TM * TN % (TM + TN) ? TM * TN : TM + TN>();
@@ -475,37 +510,51 @@ __global__ __launch_bounds__(256) void gated_prepare(FlipParams p) {
     if (id < flips_m * flips_n) {
         const int row0 = id / flips_n * kFlip, col0 = id % flips_n * kFlip;
         const int64_t plane = (int64_t)p.m * p.n;
+        constexpr int CHUNKS = kFlip * kFlip / 8 / 256;
+        float da[CHUNKS][8], db[CHUNKS][8];
 #pragma unroll
-        for (int c = t; c < kFlip * kFlip / 8; c += 256) {
-            const int r = c / (kFlip / 8), m = row0 + r, q = (c - r * (kFlip / 8)) * 8, n = col0 + q;
-            float da[8] = {}, db[8] = {};
-            if (m < p.m && n < p.n) {
-                float d[8], a[8], b[8];
-                load8<T>((const raw_t *)p.dy + m * p.dy_stride, n, p.n, p.dy_vec, d);
-                load8<F32>((const uint32_t *)p.saved + (int64_t)m * p.n, n, p.n, p.saved_vec, a);
-                load8<F32>((const uint32_t *)p.saved + plane + (int64_t)m * p.n, n, p.n, p.saved_vec, b);
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int c = t + i * 256, r = c / (kFlip / 8), m = row0 + r, n = col0 + (c - r * (kFlip / 8)) * 8;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float slope;
-                    const float f = activation(p.activation, a[j], slope);
-                    da[j] = n + j < p.n ? d[j] * b[j] * slope : 0.0f;
-                    db[j] = n + j < p.n ? d[j] * f : 0.0f;
-                }
-                if (p.da) {
-                    store8<T>((raw_t *)p.da + m * np, n, (int)np, true, da);
-                    store8<T>((raw_t *)p.db + m * np, n, (int)np, true, db);
-                }
-            }
+            for (int j = 0; j < 8; ++j) da[i][j] = db[i][j] = 0.0f;
+            if (m >= p.m || n >= p.n) continue;
+            float d[8], a[8], b[8];
+            load8<T>((const raw_t *)p.dy + m * p.dy_stride, n, p.n, p.dy_vec, d);
+            load8<F32>((const uint32_t *)p.saved + (int64_t)m * p.n, n, p.n, p.saved_vec, a);
+            load8<F32>((const uint32_t *)p.saved + plane + (int64_t)m * p.n, n, p.n, p.saved_vec, b);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                tile[0][r][q + j] = to_bits<T>(da[j]);
-                tile[1][r][q + j] = to_bits<T>(db[j]);
+                float slope;
+                const float f = activation(p.activation, a[j], slope);
+                da[i][j] = n + j < p.n ? d[j] * b[j] * slope : 0.0f;
+                db[i][j] = n + j < p.n ? d[j] * f : 0.0f;
             }
         }
-        if (!p.da_t) return;
-        __syncthreads();
-        store_flipped<T>(tile[0], p.da_t, mp, row0, (int)mp, col0, p.n, t);
-        store_flipped<T>(tile[1], p.db_t, mp, row0, (int)mp, col0, p.n, t);
+        // first the rounded values, then, where they are wanted, what the rounding left
+        for (int rest = 0; rest < (p.precise ? 2 : 1); ++rest) {
+            void *const to_a = rest ? p.da_rest : p.da, *const to_b = rest ? p.db_rest : p.db;
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+                const int c = t + i * 256, r = c / (kFlip / 8), m = row0 + r, q = (c - r * (kFlip / 8)) * 8, n = col0 + q;
+                if (to_a && m < p.m && n < p.n) {
+                    store8<T>((raw_t *)to_a + m * np, n, (int)np, true, da[i]);
+                    store8<T>((raw_t *)to_b + m * np, n, (int)np, true, db[i]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const raw_t ra = to_bits<T>(da[i][j]), rb = to_bits<T>(db[i][j]);
+                    tile[0][r][q + j] = ra;
+                    tile[1][r][q + j] = rb;
+                    da[i][j] -= T::from_raw(ra);
+                    db[i][j] -= T::from_raw(rb);
+                }
+            }
+            if (!p.da_t) continue;
+            __syncthreads();
+            store_flipped<T>(tile[0], rest ? p.da_t_rest : p.da_t, mp, row0, (int)mp, col0, p.n, t);
+            store_flipped<T>(tile[1], rest ? p.db_t_rest : p.db_t, mp, row0, (int)mp, col0, p.n, t);
+            __syncthreads();
+        }
         return;
     }
     id -= flips_m * flips_n;
@@ -634,6 +683,23 @@ struct Shape {
     int64_t blocks;
 };
 
+// Whether da and db carry the remainder of their rounding into the products, as
+// pairs of operands of their own.  Rounded once they add an error of the size of
+// the outputs' own rounding (1.4 times it together) where sums and outputs are many;
+// where they are few, that is 1.4 times on average only, and the products take little
+// longer with twice the operands (bf16, backward: 33 x 136 -> 72 30 us, without 29;
+// 128 x 256 -> 512 35 and 33).
+bool precise(int dtype, int64_t rows, int64_t width, int64_t hidden) {
+    return dtype != 0 && (rows * hidden <= 65536 || rows * width <= 4096 || hidden * width <= 4096);
+}
+
+// Pairs of operands of a product.
+int pairs_of(int mode, int dtype, int64_t m, int64_t n, int64_t k) {
+    if (mode == kForward) return 1;
+    if (mode == kInput) return precise(dtype, m, n, k) ? 4 : 2;
+    return precise(dtype, k, n, m) ? 2 : 1;
+}
+
 Shape shape_of(int mode, int dtype, int64_t m, int64_t n, int64_t k) {
     Shape s = {};
     const int planes = mode == kWeights ? 2 : 1;
@@ -643,7 +709,7 @@ Shape shape_of(int mode, int dtype, int64_t m, int64_t n, int64_t k) {
         s.blocks = (int64_t)planes * s.tiles_m * s.tiles_n;
         if (s.size == 64 || s.blocks >= 200) break;
     }
-    const int64_t steps = (int64_t)tiles_of(k, 32) * (mode == kInput ? 2 : 1);
+    const int64_t steps = (int64_t)tiles_of(k, 32) * pairs_of(mode, dtype, m, n, k);
     s.parts = 1;
     if (s.blocks < 192) {
         int64_t parts = 512 / s.blocks;
@@ -652,7 +718,6 @@ Shape shape_of(int mode, int dtype, int64_t m, int64_t n, int64_t k) {
         if (parts > 1) s.parts = (int)parts;
     }
     s.blocks *= s.parts;
-    (void)dtype;
     return s;
 }
 
@@ -673,6 +738,7 @@ int product(GatedParams p, int dtype, hipStream_t stream) {
     const Shape s = shape_of(MODE, dtype, p.m, p.n, p.k);
     p.tiles_m = s.tiles_m;
     p.tiles_n = s.tiles_n;
+    p.pairs = pairs_of(MODE, dtype, p.m, p.n, p.k);
     p.parts = p.partial ? s.parts : 1;
     p.blocks = (int)(s.blocks / s.parts * p.parts);
     const int e = s.size == 256   ? launch_tiles<T, MODE, 256>(p, stream)
@@ -735,6 +801,7 @@ int64_t gated_partial_floats(int mode, int dtype, int64_t m, int64_t n, int64_t 
 }
 
 bool gated_packs(int64_t rows) { return rows > kSkinnyRows; }
+bool gated_precise(int dtype, int64_t rows, int64_t width, int64_t hidden) { return precise(dtype, rows, width, hidden); }
 
 int64_t gated_blocks(int mode, int dtype, int64_t m, int64_t n, int64_t k) {
     return m == 0 || n == 0 ? 0 : shape_of(mode, dtype, m, n, k).blocks;

@@ -82,6 +82,7 @@ AttnPlan plan_backward_kv(const AttnParams &p, int dtype);
 enum { kGatedForward = 0, kGatedInput = 1, kGatedWeights = 2 };
 struct GatedParams {
     const void *m0, *m1, *n0, *n1;
+    const void *m0_rest, *m1_rest;   // what the rounding of da, db left
     void *out0, *out1;
     float *saved;             // a, b: two planes of rows x hidden
     float *partial;           // sums of the parts of k; null: k is not cut
@@ -91,7 +92,7 @@ struct GatedParams {
     int m_vec, n_vec;         // forward: rows of X, of Wg and Wu allow 16-byte accesses
     int out_vec, saved_vec;   // rows of out and of `saved` do
     int activation;
-    int tiles_m, tiles_n, parts, blocks;
+    int tiles_m, tiles_n, parts, blocks, pairs;
 };
 // The pass over dY: da, db and the transposed operands (null: not wanted), rows of
 // whole chunks of eight.  m rows, n hidden units, k the width.
@@ -99,14 +100,16 @@ struct FlipParams {
     const void *dy, *x, *wg, *wu;
     const float *saved;
     void *da, *db, *da_t, *db_t, *wg_t, *wu_t, *x_t;
+    void *da_rest, *db_rest, *da_t_rest, *db_t_rest;   // `precise`: what the rounding left
     int64_t dy_stride, x_stride;
     int m, n, k, activation;
-    int dy_vec, saved_vec, x_vec, w_vec;
+    int dy_vec, saved_vec, x_vec, w_vec, precise;
 };
 int64_t gated_partial_floats(int mode, int dtype, int64_t m, int64_t n, int64_t k);
 int64_t gated_blocks(int mode, int dtype, int64_t m, int64_t n, int64_t k);
 int64_t gated_flips(int64_t m, int64_t n, int64_t k);
 bool gated_packs(int64_t rows);
+bool gated_precise(int dtype, int64_t rows, int64_t width, int64_t hidden);
 int launch_gated(const GatedParams &p, int mode, int dtype, hipStream_t stream);
 int launch_gated_prepare(const FlipParams &p, int dtype, hipStream_t stream);
 
