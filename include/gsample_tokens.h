@@ -432,9 +432,9 @@ typedef struct {
  * Errors: GS_ERR_NULL, GS_ERR_SHAPE (an extent negative, a negative stride,
  * one of Y below channels along an axis of more than one element),
  * GS_ERR_DTYPE, GS_ERR_ATTR (a workspace that is misaligned or of negative
- * size), GS_ERR_TOO_LARGE (length or channels above 2^29, batch * channels
- * above 2^30, tokens 2^25 bytes or more apart, 2^22 thread blocks or more: one
- * has eight channels of a sequence at least), GS_ERR_HIP.
+ * size), GS_ERR_TOO_LARGE (length above 2^29, channels above 2^22, batch above
+ * 2^30, tokens 2^25 bytes or more apart, 2^22 thread blocks or more: one has
+ * eight channels of a sequence at least), GS_ERR_HIP.
  */
 int gs_gated_recurrence(const gs_recurrence_desc *desc, const void *X, const void *G, const float *state,
                         const int32_t *lengths, void *Y, float *last, float *saved, void *workspace,

@@ -83,6 +83,14 @@ def _parameter(t, name, device):
     return t
 
 
+def _aligned(t, stride, width):
+    """`t`, a copy of it where its rows, `stride` elements apart, are off the 16 bytes that their width is whole of."""
+    size = t.element_size()
+    if width * size % 16 == 0 and (t.data_ptr() % 16 or stride * size % 16 or stride < width):
+        return t.clone(memory_format=_torch().contiguous_format), width
+    return t, stride
+
+
 def _beside(t, name, X, device):
     """`t` as _tensor(t, name, device, X.dtype, X.shape): in few steps where it is dense."""
     if t.is_contiguous() and t.get_device() == device and t.dtype == X.dtype and t.shape == X.shape:
@@ -130,6 +138,9 @@ def gated_linear(X, gate_weight, up_weight, activation: str = "silu", return_sav
     X, gate_weight, up_weight, rows, act = _projections(X, gate_weight, up_weight, activation)
     width, hidden, device = X.shape[-1], gate_weight.shape[0], X.device
     x, xs = _rows(X)
+    if rows > 64:  # (few rows are read once, as they lie)
+        x, xs = _aligned(x, xs, width)
+        gate_weight, up_weight = _aligned(gate_weight, width, width)[0], _aligned(up_weight, width, width)[0]
     shape = (*X.shape[:-1], hidden)
     if out is None:
         Y = torch.empty(shape, dtype=X.dtype, device=device)

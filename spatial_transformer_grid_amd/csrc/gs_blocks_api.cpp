@@ -147,10 +147,11 @@ int scan_setup(const gs_recurrence_desc *d, bool backward, gs::ScanParams &p) {
                   *const bwd[] = {d->dx_stride, d->dg_stride};
     for (int i = 0; i < (backward ? 3 : 2); ++i)
         if (in[i][0] < 0 || in[i][1] < 0) return GS_ERR_SHAPE;
-    if (d->length > (int64_t(1) << 29) || d->channels > (int64_t(1) << 29) || d->batch > (int64_t(1) << 30) ||
-        d->batch * d->channels > (int64_t(1) << 30) || d->batch * ((d->channels + 7) / 8) >= kMaxBlocks)
+    // A wave reaches the channels of the 64 steps that it has at most by offsets below
+    // 2^31 - 1: 63 rows of less than 2^25 bytes, and channels of at most 2^24.
+    if (d->length > (int64_t(1) << 29) || d->channels > (int64_t(1) << 22) || d->batch > (int64_t(1) << 30) ||
+        d->batch * ((d->channels + 7) / 8) >= kMaxBlocks)
         return GS_ERR_TOO_LARGE;
-    // a wave reaches the 64 steps it has at most by a 32-bit offset
     const int64_t furthest = (int64_t(1) << 25) / dtype_bytes(d->dtype);
     for (int i = 0; i < (backward ? 3 : 2); ++i)
         if (d->length > 1 && in[i][1] >= furthest) return GS_ERR_TOO_LARGE;

@@ -239,8 +239,9 @@ def test_gated_recurrence_refuses(tk):
     sizes = (lib.gs_gated_recurrence_workspace_size, lib.gs_gated_recurrence_backward_workspace_size)
     for over, status in [(dict(dtype=3), 3), (dict(batch=-1), 2), (dict(length=-1), 2), (dict(channels=-1), 2),
                          (dict(x_stride=(-1, 8)), 2), (dict(g_stride=(40, -8)), 2), (dict(length=2 ** 29 + 1), 6),
-                         (dict(channels=2 ** 29 + 1), 6), (dict(batch=2 ** 30 + 1), 6),
-                         (dict(batch=2 ** 16, channels=2 ** 15), 6), (dict(batch=2 ** 22, channels=1), 6)]:
+                         (dict(channels=2 ** 22 + 1), 6), (dict(batch=2 ** 30 + 1), 6),
+                         (dict(batch=2 ** 16, channels=2 ** 15), 6), (dict(batch=2 ** 22, channels=1), 6),
+                         (dict(x_stride=(0, 2 ** 23)), 6), (dict(dtype=2, g_stride=(0, 2 ** 24)), 6)]:
         d = scan_desc(**over)
         assert fwd(d) == status and bwd(d) == status, over
         assert [size_of(s, d) for s in sizes] == [-status] * 2, over
