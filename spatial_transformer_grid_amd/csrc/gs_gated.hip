@@ -81,15 +81,19 @@ __device__ __forceinline__ float activation(int kind, float a, float &slope) {
 
 // ---------------------------------------------------------------- operands
 
-// Steps of the contracted axis a tile, and tiles in LDS.  16-bit types: 64 bytes a
-// row and four tiles, three of them on their way; fp32, whose products take eight
-// times as long, 128 bytes and two.
+// Steps of the contracted axis a tile.  16-bit types: 64 bytes a row and four tiles
+// in LDS, three of them on their way; fp32, whose products take eight times as long,
+// 128 bytes and two tiles, of 64 rows four (577 x 203 -> 531, the three products:
+// with two 18 + 13 + 14 us).
 template <typename T>
 struct K {
     static constexpr int BK = (T::bytes == 4 ? 128 : 64) / T::bytes;
-    static constexpr int DEPTH = T::bytes == 4 ? 2 : 4;
     static constexpr int EPC = 16 / T::bytes;
 };
+template <typename T, int SIZE>
+constexpr int tiles_held() {
+    return T::bytes == 4 && SIZE > 64 ? 2 : 4;
+}
 
 // One operand's tile: ROWS rows of BK, loaded by NT threads.
 template <typename T, int ROWS, int NT>
@@ -217,7 +221,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gated_product(GatedParams p) {
     constexpr int NT = 64 * WM * WN, TM = BM / WM / 32, TN = BN / WN / 32, BK = K<T>::BK;
     typedef Operand<T, BM, NT> OM;
     typedef Operand<T, BN, NT> ON;
-    constexpr int STAGE = (BM + BN) * BK, DEPTH = K<T>::DEPTH, STEPS = BK / 16;
+    constexpr int STAGE = (BM + BN) * BK, DEPTH = tiles_held<T, BM>(), STEPS = BK / 16;
     constexpr int COLS = MODE == kForward ? BN / 2 : BN;    // of the output
     extern __shared__ __align__(16) unsigned char smem[];
     raw_t *const lds = (raw_t *)smem;
@@ -344,7 +348,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gated_product(GatedParams p) {
         // rows are stored whole.
         constexpr int HALF = TN / 2, WIDTH = 32 * HALF, PITCH = WIDTH + 4;
         float *const mine = (float *)smem + wave * (2 * 32 * PITCH);
-        static_assert(WM * WN * 2 * 32 * PITCH * 4 <= 2 * 2 * BM * 128, "room");
+        static_assert(WM * WN * 2 * 32 * PITCH * 4 <= DEPTH * STAGE * T::bytes, "room");
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -700,25 +704,46 @@ int pairs_of(int mode, int dtype, int64_t m, int64_t n, int64_t k) {
     return precise(dtype, k, n, m) ? 2 : 1;
 }
 
+// The size and the parts whose estimated time is least.  A compute unit holds one
+// block of 256, two of 128 or four of 64, and the launch takes as many rounds as that
+// needs.  32 of the contracted axis take a block `step` us (measured in 16-bit types at
+// 8192 x 2048 -> 8192: 256 0.85; at 2048 x 1024 -> 4096 the forward product takes 45 us by
+// 256, 57 by 128; fp32 by 128 as fast as by 256 for its size), one that is alone there
+// no less than `alone`, and a round `start` to fill and to store.  Parts cost their sums' way through memory
+// and a launch.  (4097 x 1024 -> 2736 backward, fp16 and fp32: 242 and 955 us; by the
+// largest size that fills the chip, without a count of rounds, 293 and 1279.)
 Shape shape_of(int mode, int dtype, int64_t m, int64_t n, int64_t k) {
-    Shape s = {};
-    const int planes = mode == kWeights ? 2 : 1;
-    for (s.size = 256;; s.size /= 2) {
-        s.tiles_m = tiles_of(m, s.size);
-        s.tiles_n = tiles_of(n, mode == kForward ? s.size / 2 : s.size);
-        s.blocks = (int64_t)planes * s.tiles_m * s.tiles_n;
-        if (s.size == 64 || s.blocks >= 200) break;
+    Shape best = {};
+    double least = 0.0;
+    const int planes = mode == kWeights ? 2 : 1, sums = mode == kInput ? 1 : 2;
+    const int64_t steps = (int64_t)tiles_of(k, 32) * pairs_of(mode, dtype, m, n, k), cols = n;
+    for (int size = 256; size >= 64; size /= 2) {
+        Shape s = {};
+        s.size = size;
+        s.tiles_m = tiles_of(m, size);
+        s.tiles_n = tiles_of(n, mode == kForward ? size / 2 : size);
+        const int64_t blocks = (int64_t)planes * s.tiles_m * s.tiles_n, held = 256 / size, slots = 256 * held;
+        const double step = dtype == 0 ? (size == 256 ? 8.2 : size == 128 ? 2.05 : 0.6) : (size == 256 ? 0.85 : size == 128 ? 0.27 : 0.1);
+        const double alone = dtype == 0 ? (size == 256 ? 8.2 : 1.4 * step) : 0.25;
+        const double start = size == 256 ? 12.0 : size == 128 ? 8.0 : 6.0;
+        const auto round = [&](int64_t n) {          // of n blocks, 32 of the axis
+            const double t = step * (double)((n + 255) / 256);
+            return n == 0 ? 0.0 : t > alone ? t : alone;
+        };
+        for (int parts = 1; parts <= 32 && (parts == 1 || steps >= 8 * parts); ++parts) {
+            const int64_t n = blocks * parts, full = n / slots, rest = n % slots;
+            const double join = parts == 1 ? 0.0 : 5.0 + 2e-6 * parts * sums * (double)m * (double)cols;
+            const double time = ((double)full * round(slots) + round(rest)) * (double)((steps + parts - 1) / parts) +
+                                (double)(full + (rest > 0)) * start + join;
+            if (best.size == 0 || time < least) {
+                least = time;
+                best = s;
+                best.parts = parts;
+                best.blocks = blocks * parts;
+            }
+        }
     }
-    const int64_t steps = (int64_t)tiles_of(k, 32) * pairs_of(mode, dtype, m, n, k);
-    s.parts = 1;
-    if (s.blocks < 192) {
-        int64_t parts = 512 / s.blocks;
-        if (parts > steps / 8) parts = steps / 8;
-        if (parts > 64) parts = 64;
-        if (parts > 1) s.parts = (int)parts;
-    }
-    s.blocks *= s.parts;
-    return s;
+    return best;
 }
 
 template <typename T, int MODE, int SIZE>
@@ -726,7 +751,7 @@ int launch_tiles(const GatedParams &p, hipStream_t stream) {
     // (of a forward tile of 64 a wave has 32 columns of Wg and the same of Wu)
     constexpr int WM = 2, WN = SIZE == 256 ? 4 : SIZE == 64 && MODE == kForward ? 1 : 2;
     const auto fn = gated_product<T, MODE, SIZE, SIZE, WM, WN>;
-    const int smem = 2 * 2 * SIZE * 128;             // the tiles of both operands
+    const int smem = tiles_held<T, SIZE>() * 2 * SIZE * K<T>::BK * T::bytes;   // the tiles of both operands
     const hipError_t e = hipFuncSetAttribute((const void *)fn, hipFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != hipSuccess) return (int)e;
     hipLaunchKernelGGL(fn, dim3((unsigned)((p.blocks + 7) / 8 * 8)), dim3(64 * WM * WN), smem, stream, p);
