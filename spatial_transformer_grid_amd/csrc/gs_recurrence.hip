@@ -551,7 +551,7 @@ int pick(const ScanParams &p, bool backward, hipStream_t stream) {
 // Lanes of a run and parts of the tokens.  One reading, with as many lanes a run
 // as still give every compute unit a block, where the tokens are few or those
 // blocks enough; else 64 lanes (rows of 128 bytes and more) and as many parts as
-// give every compute unit two blocks, of two tiles at least, whose tokens are read
+// give every compute unit a block, of two tiles at least, whose tokens are read
 // twice.  us of both, forward and backward, bf16:
 //   4 x 2048 x 190     15 + 23 in one reading, 15 + 17 in parts
 //   4 x 8192 x 190     51 + 81                 23 + 34
@@ -567,7 +567,7 @@ ScanPlan plan_recurrence(int64_t batch, int64_t length, int64_t channels, bool p
     if (workspace && most > 0 && ((length > 2048 && most < 256) || (backward && length > 4096 && most < 512))) {
         s.lanes = channels > 16 * v ? 64 : channels > 8 * v ? 16 : 8;
         const int64_t tile = kWaves * kSteps * (64 / s.lanes), tiles = (length + tile - 1) / tile;
-        int64_t parts = 512 / units(s.lanes);
+        int64_t parts = 256 / units(s.lanes);
         if (parts > tiles / 2) parts = tiles / 2;
         if (parts > kMaxParts) parts = kMaxParts;
         s.parts = (int)parts;

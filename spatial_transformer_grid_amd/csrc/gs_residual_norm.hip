@@ -61,17 +61,23 @@ __device__ __forceinline__ float join_total(float v, float *red, int &turn) {
 // The means of g and of g z over a row, as their gradients take them off: without
 // `layer` that of g is left out.
 template <int NT>
-__device__ __forceinline__ void gradient_means(float &g, float &gz, int layer, int cols, float *red, int &turn) {
+__device__ __forceinline__ void gradient_means(float &g, float &gz, int layer, float inv_n, float *red, int &turn) {
     if (layer) {
         float both[2] = {g, gz};
         join_totals<NT, 2>(both, red, turn);
-        g = both[0] / (float)cols;
+        g = both[0] * inv_n;
         gz = both[1];
     } else {
         g = 0.0f;
         gz = join_total<NT>(gz, red, turn);
     }
-    gz /= (float)cols;
+    gz *= inv_n;
+}
+
+// Whether a thread's element lies in the row: of a chunk of eight all do, or none.
+template <int NT, bool VEC>
+__device__ __forceinline__ bool inside(int t, int e, int cols) {
+    return column<NT, VEC>(t, VEC ? e & ~7 : e) < cols;
 }
 
 // Mean and factor of a row's values v (zeros past its end), which come out as
@@ -87,11 +93,11 @@ __device__ __forceinline__ void row_stats(float *v, int layer, int cols, int t, 
         mean = join_total<NT>(s, red, turn) / (float)cols;
         s = 0.0f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = column<NT, VEC>(t, e) < cols ? v[e] - mean : 0.0f;
+        for (int e = 0; e < E; ++e) v[e] = inside<NT, VEC>(t, e, cols) ? v[e] - mean : 0.0f;
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) s = fmaf(v[e], v[e], s);
-    inv = 1.0f / sqrtf(join_total<NT>(s, red, turn) / (float)cols + epsilon);
+    inv = 1.0f / sqrtf(join_total<NT>(s, red, turn) * (1.0f / (float)cols) + epsilon);
 }
 
 // A row of the gate: ones where there is none.
@@ -209,8 +215,6 @@ __global__ __launch_bounds__(join_threads(NT)) void residual_norm_rows(JoinParam
         for (int e = 0; e < E; ++e) x[e] = fmaf(p.alpha, x[e], m[e] * f[e]);
         if (live) store_row<T, NT, E, VEC>((raw_t *)p.h + r * p.h_stride, cols, t, x);
         if (p.pre) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = column<NT, VEC>(t, e) < cols ? x[e] : 0.0f;
             row_stats<NT, E, VEC>(x, p.layer, cols, t, p.epsilon, red, turn, mean_h, inv_h);
             float w[E], b[E];
             pre.get(p, p.pre, t, w);
@@ -264,6 +268,7 @@ __global__ __launch_bounds__(join_threads(NT)) void residual_norm_backward_rows(
     __shared__ float sums[ROWS > 1 ? BT * 8 : 1];
     int turn = 0;
     const int t = threadIdx.x % NT, slot = threadIdx.x / NT, cols = p.cols;
+    const float inv_n = 1.0f / (float)cols;
     float s_post[E], s_post_b[BIAS ? E : 1], s_pre[E], s_pre_b[BIAS ? E : 1], s_gate[E], m[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) s_post[e] = s_pre[e] = s_gate[e] = 0.0f;
@@ -322,7 +327,7 @@ __global__ __launch_bounds__(join_threads(NT)) void residual_norm_backward_rows(
             post_b.get(p, p.post_bias, t, b);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                f[e] = column<NT, VEC>(t, e) < cols ? (f[e] - st[0]) * st[1] : 0.0f;
+                f[e] = inside<NT, VEC>(t, e, cols) ? (f[e] - st[0]) * st[1] : 0.0f;
                 fp[e] = fmaf(f[e], w[e], b[e]);
             }
         } else {
@@ -335,7 +340,7 @@ __global__ __launch_bounds__(join_threads(NT)) void residual_norm_backward_rows(
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const float z = fmaf(p.alpha, h[e], m[e] * fp[e]);
-                h[e] = column<NT, VEC>(t, e) < cols ? (z - st[2]) * st[3] : 0.0f;
+                h[e] = inside<NT, VEC>(t, e, cols) ? (z - st[2]) * st[3] : 0.0f;
                 if (live) {
                     s_pre[e] = fmaf(y[e], h[e], s_pre[e]);
                     if constexpr (BIAS) s_pre_b[e] += y[e];
@@ -344,7 +349,7 @@ __global__ __launch_bounds__(join_threads(NT)) void residual_norm_backward_rows(
                 a += y[e];
                 c = fmaf(y[e], h[e], c);
             }
-            gradient_means<NT>(a, c, p.layer, cols, red, turn);
+            gradient_means<NT>(a, c, p.layer, inv_n, red, turn);
 #pragma unroll
             for (int e = 0; e < E; ++e) d[e] += st[3] * (y[e] - a - h[e] * c);
         }
@@ -375,11 +380,11 @@ __global__ __launch_bounds__(join_threads(NT)) void residual_norm_backward_rows(
                     s_post[e] = fmaf(d[e], f[e], s_post[e]);
                     if constexpr (BIAS) s_post_b[e] += d[e];
                 }
-                d[e] = column<NT, VEC>(t, e) < cols ? d[e] * w[e] : 0.0f;
+                d[e] *= w[e];                        // 0 past the row's end, with w
                 a += d[e];
                 c = fmaf(d[e], f[e], c);
             }
-            gradient_means<NT>(a, c, p.layer, cols, red, turn);
+            gradient_means<NT>(a, c, p.layer, inv_n, red, turn);
 #pragma unroll
             for (int e = 0; e < E; ++e) d[e] = st[1] * (d[e] - a - f[e] * c);
         }
