@@ -18,6 +18,11 @@
 // Where there are too few channels for the chip even with few lanes a run, the
 // tokens are split in parts over blocks: a first kernel makes each part's pair,
 // and the blocks of the second one fold the pairs of the parts before theirs.
+//
+// Bound by memory where there are tokens enough: 4 x 16384 x 1024 bf16, pairs and
+// states, forward 64 + 82 us (4.2 and 4.9 TB/s; one reading 149), backward 61 + 137
+// (4.4 and 4.9 TB/s; one reading 249, at first 65 + 913); 1 x 65536 x 256 fp16 forward
+// 16 + 26.
 #include "gs_tokens.hpp"
 
 namespace gs {
@@ -552,19 +557,21 @@ int pick(const ScanParams &p, bool backward, hipStream_t stream) {
 // as still give every compute unit a block, where the tokens are few or those
 // blocks enough; else 64 lanes (rows of 128 bytes and more) and as many parts as
 // give every compute unit a block, of two tiles at least, whose tokens are read
-// twice.  us of both, forward and backward, bf16:
-//   4 x 2048 x 190     15 + 23 in one reading, 15 + 17 in parts
-//   4 x 8192 x 190     51 + 81                 23 + 34
-//   1 x 32768 x 256   167 + 263                31 + 41
-//   4 x 4096 x 1024    29 + 44                 37 + 55
-//   4 x 8192 x 1024    53 + 128                62 + 96
-//   16 x 8192 x 512   109 + 183               123 + 195
+// twice.  us of forward + backward, bf16, batch x tokens x channels:
+//   4 x 2304 x 190     18 + 28 in one reading, 15 + 18 in parts
+//   4 x 8192 x 190     52 + 81                 24 + 30
+//   1 x 32768 x 256   167 + 262                28 + 32
+//   64 x 4096 x 24     23 + 31                 24 + 30
+//   4 x 4096 x 1024    29 + 45                 39 + 49
+//   4 x 8192 x 1024    53 + 128                66 + 94
+//   4 x 16384 x 1024  149 + 249               133 + 196
+//   16 x 8192 x 512   106 + 183               129 + 186
 ScanPlan plan_recurrence(int64_t batch, int64_t length, int64_t channels, bool pairwise, bool backward, bool workspace) {
     const int v = pairwise ? 2 : 1;
     const auto units = [&](int cl) { return batch * ((channels + cl * v - 1) / (cl * v)); };
     const int64_t most = units(8);
     ScanPlan s = {8, 1};
-    if (workspace && most > 0 && ((length > 2048 && most < 256) || (backward && length > 4096 && most < 512))) {
+    if (workspace && most > 0 && ((length > 2048 && most < 256) || (length > (backward ? 4096 : 12288) && most < 512))) {
         s.lanes = channels > 16 * v ? 64 : channels > 8 * v ? 16 : 8;
         const int64_t tile = kWaves * kSteps * (64 / s.lanes), tiles = (length + tile - 1) / tile;
         int64_t parts = 256 / units(s.lanes);

@@ -18,7 +18,7 @@
 //
 // Bound by memory: the next row's loads are under way while one is worked on, what
 // belongs to a column stays in registers, a row's sums go over the lanes by
-// permutations (through LDS their latency took 13 us of the backward pass below), and
+// permutations (through LDS their latency took 12 us of the backward pass below), and
 // a block holds one wide row, so that no two wait for one another (two: 31 us for
 // 24 at 4101 x 777 fp32 backward, the same at the size below).  16384 x 2048 bf16
 // with fp32 parameters and a gate for each channel: forward 54 us (5.0 TB/s),
