@@ -84,9 +84,10 @@ def _parameter(t, name, device):
 
 
 def _aligned(t, stride, width):
-    """`t`, a copy of it where its rows, `stride` elements apart, are off the 16 bytes that their width is whole of."""
+    """`t`, a copy of it where its rows, `stride` elements apart, are off the 16 bytes that their width is whole of,
+    or further apart than a tile's offsets reach."""
     size = t.element_size()
-    if width * size % 16 == 0 and (t.data_ptr() % 16 or stride * size % 16 or stride < width):
+    if width * size % 16 == 0 and (t.data_ptr() % 16 or stride * size % 16 or stride < width or stride * size > 1 << 22):
         return t.clone(memory_format=_torch().contiguous_format), width
     return t, stride
 

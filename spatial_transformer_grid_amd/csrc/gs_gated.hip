@@ -52,8 +52,7 @@ __device__ __forceinline__ float activation(int kind, float a, float &slope) {
     if (kind == 1) {
         // Phi by erfc(x) = exp(-x^2) t P(t), t = 1 / (1 + x / 2): P of degree 8 fitted to
         // exp(x^2) erfc(x) / t on 0 .. 14 for the least relative error, 3.2e-7 in fp32.
-        // (By erfcf a training step's forward product of 4097 x 1024 -> 2736 took twice
-        // as long.)
+        // (4097 x 1024 -> 2736 fp16 forward 88 us, by erfcf 93; 8192 x 512 -> 2048 60, 68.)
         const float x = 0.70710678118654752f * fabsf(a), t = __builtin_amdgcn_rcpf(fmaf(0.5f, x, 1.0f));
         float q = -0.059386398643f;
         q = fmaf(q, t, 0.286123692989f);
@@ -500,6 +499,14 @@ __device__ __forceinline__ void store_flipped(const typename T::raw_t (*tile)[kF
     }
 }
 
+// What the rounding of v to r left: nothing of an infinity, whose difference from
+// itself would make a NaN of every sum that it is in.
+template <typename T>
+__device__ __forceinline__ float left_of(float v, typename T::raw_t r) {
+    const float f = T::from_raw(r);
+    return fabsf(f) == INFINITY ? 0.0f : v - f;
+}
+
 // da = dY b act'(a) and db = dY act(a), rounded to T, in rows of whole chunks of
 // eight whose rest is zero, and transposed; and Wg, Wu and X transposed.  A block
 // takes one tile of one of them.
@@ -549,8 +556,8 @@ __global__ __launch_bounds__(256) void gated_prepare(FlipParams p) {
                     const raw_t ra = to_bits<T>(da[i][j]), rb = to_bits<T>(db[i][j]);
                     tile[0][r][q + j] = ra;
                     tile[1][r][q + j] = rb;
-                    da[i][j] -= T::from_raw(ra);
-                    db[i][j] -= T::from_raw(rb);
+                    da[i][j] = left_of<T>(da[i][j], ra);
+                    db[i][j] = left_of<T>(db[i][j], rb);
                 }
             }
             if (!p.da_t) continue;
@@ -676,6 +683,11 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gated_skinny(GatedParams p)
 
 // --------------------------------------------------------------- launches
 
+// Rows up to which the weights are read straight into registers instead of in tiles.
+// us forward, bf16 (fp32), straight and in tiles:
+//   16 x 1024 -> 4096    5 (10) and 14 (26)      64 x 1024 -> 4096    9 (20) and 14 (27)
+//   16 x 2048 -> 8192   15 (28) and 18 (74)      64 x 2048 -> 8192   27 (69) and 24 (75)
+//   128 x 1024 -> 4096  16 (38) and 15 (43)     128 x 2048 -> 8192   52 (134) and 33 (137)
 constexpr int kSkinnyRows = 64;
 
 int tiles_of(int64_t n, int size) { return (int)((n + size - 1) / size); }
@@ -690,9 +702,9 @@ struct Shape {
 // Whether da and db carry the remainder of their rounding into the products, as
 // pairs of operands of their own.  Rounded once they add an error of the size of
 // the outputs' own rounding (1.4 times it together) where sums and outputs are many;
-// where they are few, that is 1.4 times on average only, and the products take little
-// longer with twice the operands (bf16, backward: 33 x 136 -> 72 30 us, without 29;
-// 128 x 256 -> 512 35 and 33).
+// where they are few, that is 1.4 times on average only, and twice the operands cost
+// a few us (bf16, backward: 33 x 136 -> 72 15.0 us, without 12.3; 128 x 256 -> 512 20.9
+// and 17.3; 16 x 1024 -> 4096 38 and 37).
 bool precise(int dtype, int64_t rows, int64_t width, int64_t hidden) {
     return dtype != 0 && (rows * hidden <= 65536 || rows * width <= 4096 || hidden * width <= 4096);
 }

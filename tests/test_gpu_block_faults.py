@@ -317,3 +317,32 @@ def test_gated_linear_past_2_to_the_31(gs):
     dx, dg, du = gs.gated_linear_backward(y, x, w, u, saved)
     close(dx[ends], *want["dx"], "dx")
     assert dg.isfinite().all() and du.isfinite().all()
+
+
+def test_gated_linear_rows_further_apart_than_a_tiles_offsets(gs):
+    """Rows of a wide buffer, more than 4 MiB apart, give the bits of the same rows side by side."""
+    apart = (1 << 21) + 8
+    x = torch.randn(66, 64, device="cuda").to(torch.bfloat16)
+    wide = torch.zeros(66 * apart, dtype=torch.bfloat16, device="cuda").as_strided((66, 64), (apart, 1))
+    wide.copy_(x)
+    wg, wu = (torch.randn(48, 64, device="cuda").to(torch.bfloat16) for _ in range(2))
+    y, saved = gs.gated_linear(x, wg, wu, return_saved=True)
+    z, again = gs.gated_linear(wide, wg, wu, return_saved=True)
+    assert torch.equal(z, y) and torch.equal(again, saved)
+    for p, q in zip(gs.gated_linear_backward(y, wide, wg, wu, saved), gs.gated_linear_backward(y, x, wg, wu, saved)):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 66])
+def test_gated_linear_gradients_of_infinities(gs, rows, dtype):
+    """With positive operands an infinite dY gives infinite gradients, no NaN, also where what the rounding of da and
+    db left is multiplied too; so does one whose da passes the element type's range."""
+    t = TYPES[dtype]
+    x, w = torch.ones(rows, 16, device="cuda", dtype=t), torch.full((24, 16), 0.25, device="cuda", dtype=t)
+    y, saved = gs.gated_linear(x, w, w, return_saved=True)
+    for value in (math.inf, 0.9 * torch.finfo(t).max):
+        dy = torch.zeros(rows, 24, device="cuda", dtype=t)
+        dy[0] = value
+        for v in gs.gated_linear_backward(dy, x, w, w, saved):
+            assert torch.isposinf(v[0]).all() and not torch.isnan(v).any()
