@@ -20,9 +20,9 @@
 // and the blocks of the second one fold the pairs of the parts before theirs.
 //
 // Bound by memory where there are tokens enough: 4 x 16384 x 1024 bf16, pairs and
-// states, forward 64 + 82 us (4.2 and 4.9 TB/s; one reading 149), backward 61 + 137
-// (4.4 and 4.9 TB/s; one reading 249, at first 65 + 913); 1 x 65536 x 256 fp16 forward
-// 16 + 26.
+// states, forward 61 + 80 us (4.4 and 5.0 TB/s; one reading 149), backward 60 + 126
+// (4.5 and 5.3 TB/s; one reading 249, at first 65 + 913); 1 x 65536 x 256 fp16 forward
+// 16 + 24.
 #include "gs_tokens.hpp"
 
 namespace gs {
