@@ -258,7 +258,8 @@ typedef enum {
  *                few rows is not split over thread blocks, and a width that is
  *                not whole 16-byte chunks takes the kernel for few rows: both
  *                slower, and the sums in another order.  So does an X or a
- *                weight off its 16-byte alignment (pointer or rows).
+ *                weight off its 16-byte alignment (pointer or rows), or an X
+ *                whose rows overlap or lie more than 4 MiB apart.
  *
  * Errors: GS_ERR_NULL, GS_ERR_SHAPE (an extent negative, width 0 with rows
  * and hidden, x_stride negative, rows of Y that overlap), GS_ERR_DTYPE,
